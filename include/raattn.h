@@ -340,6 +340,118 @@ ra_status_t ra_attention_bwd_noalloc(const void* q, const void* k, const void* v
                                      ra_dtype_t in_dtype, ra_dtype_t o_dtype, ra_dtype_t grad_dtype,
                                      void* stream);
 
+/*
+ * Positions, key/value caches and single-token attention.
+ *
+ * ra_norm_t -- normalisation of a query or key row over its D elements:
+ *   RA_NORM_NONE   none (no weights, no biases);
+ *   RA_NORM_LAYER  (x - mean) / sqrt(var + eps) * weight + bias (biased variance; biases may be NULL);
+ *   RA_NORM_RMS    x / sqrt(mean(x^2) + eps) * weight (no biases).
+ */
+typedef enum { RA_NORM_NONE = 0, RA_NORM_LAYER = 1, RA_NORM_RMS = 2 } ra_norm_t;
+
+/*
+ * ra_qk_norm_rope_fwd -- q, k and v of every head from the packed projection: per-head
+ * normalisation of q and k and rotation by position, in one pass.
+ *   qkv           [B, N, (H_Q + 2 H_KV) D] of dtype: a token's query heads, key heads, value
+ *                 heads.  batch_stride and token_stride in elements (multiples of 16 bytes); a
+ *                 token's elements are contiguous.
+ *   q_weight, q_bias, k_weight, k_bias   [D] of dtype, as `norm` asks.
+ *   sections, axes   axes (0..4) host ints >= 1: how many pairs of dimensions each position axis
+ *                 turns; R = their sum, 2 R <= D.  axes = 0: no rotation.  Dimensions from 2 R on
+ *                 stay as they are.
+ *   interleaved   0: pair i is (i, i + R), and R must be a multiple of 8; else (2 i, 2 i + 1).
+ *   frequencies   [R] doubles in device memory, radians per position.
+ *   positions     int32: token n of sequence b has position
+ *                 positions[axis * pos_axis_stride + b * pos_batch_stride + n] on an axis (a
+ *                 stride of 0 shares them).  Any int32; angles keep fp32 accuracy at all of them.
+ *   q             [B, H_Q, N, D] (written).
+ *   k, v          start NULL (then count NULL, capacity 0): [B, H_KV, N, D] (written).
+ *                 Otherwise a cache [B, H_KV, capacity, D]: token n of sequence b goes to slot
+ *                 start[b] + n, for n < count[b] (count NULL: all N) and slots in [0, capacity);
+ *                 nothing else of the cache is touched, and start is not changed.
+ *   dtype         RA_F32 or RA_BF16; arithmetic in fp32, each output rounded once.  v is copied.
+ * Outputs must not overlap inputs.  Errors: RA_ERR_ARG for null or misaligned pointers, sizes
+ * < 1, B N (H_Q + 2 H_KV) or B H_KV capacity beyond int32, weights that do not go with `norm`, a
+ * bad enum, eps or section; RA_ERR_UNSUPPORTED for D outside {16, 32, 64, 128}, more than
+ * four axes, or an R that is no multiple of 8 when not interleaved; RA_ERR_LAUNCH.
+ */
+ra_status_t ra_qk_norm_rope_fwd(const void* qkv, int64_t batch_stride, int64_t token_stride, const void* q_weight,
+                                const void* q_bias, const void* k_weight, const void* k_bias, ra_norm_t norm,
+                                float eps, const double* frequencies, const int32_t* positions,
+                                int64_t pos_axis_stride, int64_t pos_batch_stride, const int32_t* sections, int axes,
+                                int interleaved, void* q, void* k, void* v, const int32_t* start,
+                                const int32_t* count, int capacity, int B, int N, int H_Q, int H_KV, int D,
+                                ra_dtype_t dtype, void* stream);
+
+/*
+ * ra_qk_norm_rope_bwd -- gradients of sum(dq q) + sum(dk k) + sum(dv v) for the q, k, v that
+ * ra_qk_norm_rope_fwd (start NULL) gives.
+ *   dq, dk, dv    [B, H_Q, N, D], [B, H_KV, N, D] x2 of dtype.
+ *   dqkv          [B, N, (H_Q + 2 H_KV) D] of dtype, dense (written).
+ *   dparams       [4][D] float (written unless norm is RA_NORM_NONE, then it may be NULL): the
+ *                 gradients of q_weight, q_bias, k_weight, k_bias.  The bias rows are the
+ *                 gradients that biases would have where there are none.
+ *   workspace     ra_qk_norm_rope_bwd_workspace_size(D) bytes, 16-byte aligned, contents on entry
+ *                 irrelevant (NULL allowed with RA_NORM_NONE).
+ * Results do not depend on scheduling (no floating-point atomics).  Other arguments and errors as
+ * the forward; the size query returns 0 for an unsupported D.
+ */
+size_t ra_qk_norm_rope_bwd_workspace_size(int D);
+ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t token_stride, const void* q_weight,
+                                const void* q_bias, const void* k_weight, const void* k_bias, ra_norm_t norm,
+                                float eps, const double* frequencies, const int32_t* positions,
+                                int64_t pos_axis_stride, int64_t pos_batch_stride, const int32_t* sections, int axes,
+                                int interleaved, const void* dq, const void* dk, const void* dv, void* dqkv,
+                                float* dparams, void* workspace, int B, int N, int H_Q, int H_KV, int D,
+                                ra_dtype_t dtype, void* stream);
+
+/*
+ * ra_attention_decode -- ra_attention of one query token per sequence: over a prefix of P keys
+ * that every sequence of the batch shares, and the first length[b] keys of its own cache.
+ *   q             [B, H_Q, D].  H_Q is a multiple of H_KV; query head h reads key head
+ *                 h / (H_Q / H_KV).
+ *   k, v          [B, H_KV, C, D]; entries from length[b] on are never read.
+ *   length        [B] int32 in device memory, read as min(max(length, 0), C).
+ *   prefix_k, prefix_v   [H_KV, P, D]; NULL if and only if P = 0.
+ *   o             [B, H_Q, D] (written).  A sequence with no key at all gives zeros.
+ *   weight        NULL, or [B, H_KV, C] float: weight[b][kv][j] += the attention weights of
+ *                 key j summed over the query heads that read it, for j < length[b].
+ *   workspace     ra_attention_decode_workspace_size() bytes, 16-byte aligned, contents on entry
+ *                 irrelevant.  Calls that may run at the same time need one each.
+ *   scale         score scale; <= 0 means 1/sqrt(D).
+ *   dtype         of q, k, v, prefix and o.  RA_BF16: D in {64, 128}; RA_F32: {16, 32, 64, 128}.
+ * Scores, row maxima, sums and weights are fp32.  Results do not depend on scheduling.
+ * Errors: RA_ERR_ARG for null or misaligned pointers, sizes < 1 (P < 0), H_Q no multiple of
+ * H_KV, B H_Q, B H_KV C or H_KV P beyond int32, a bad enum or scale; RA_ERR_UNSUPPORTED for D outside
+ * the sets above, B > 8192 or more than 1024 query heads per key head; RA_ERR_LAUNCH.  The size
+ * query returns 0 for such sizes.
+ */
+size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D);
+ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, const int32_t* length,
+                                const void* prefix_k, const void* prefix_v, void* o, float* weight, void* workspace,
+                                int B, int H_Q, int H_KV, int C, int P, int D, float scale, ra_dtype_t dtype,
+                                void* stream);
+
+/*
+ * ra_cache_evict -- a cache cut down to its most attended entries.  Per sequence b and key head,
+ * with n = length[b] (read as min(max(length, 0), C)), m = min(n, keep) and l = min(recent, n):
+ * the last l entries stay, and of the others the m - l of the largest weight (of equal weights the
+ * lowest slots; NaN counts as larger than any number).  They are copied, in their order, to the
+ * first m slots of the out cache, whose other slots are left as they are.
+ *   k, v, weight              [B, H_KV, C, D] x2 of dtype, [B, H_KV, C] float.
+ *   k_out, v_out, weight_out  [B, H_KV, C_out, D] x2, [B, H_KV, C_out]; not the inputs.
+ *   length_out    [B] int32 (written): m.
+ *   index         [B, H_KV, keep] int32 (written): the kept slots, ascending, then -1.
+ *   keep, recent  1 <= keep <= C_out, 0 <= recent <= keep.
+ * Errors: RA_ERR_ARG for null, misaligned or equal in and out pointers and sizes outside the above,
+ * B H_KV C or B H_KV C_out beyond int32; RA_ERR_UNSUPPORTED where D elements are no multiple of 16
+ * bytes; RA_ERR_LAUNCH.
+ */
+ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, const int32_t* length, void* k_out,
+                           void* v_out, float* weight_out, int32_t* length_out, int32_t* index, int B, int H_KV,
+                           int C, int C_out, int D, int keep, int recent, ra_dtype_t dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,6 +9,9 @@ Functional API, after the page "Ra-Family: Rational Neural Architecture",
 section 3 "Rational Attention & Softmax":
     ra_softmax(x)                                   last-dim rational soft-argmax
     ra_attention(q, k, v, attn_mask=None, is_causal=False, scale=None)   drop-in for SDPA, autograd-aware
+around it, for positions and for serving (serving.py):
+    ra_qk_norm_rope(qkv, ...)          per-head norm and rotation of q and k, autograd-aware
+    ra_cache_append, ra_attention_decode, ra_cache_evict, RaCache        single tokens against a cache
 plus the explicit forward/backward entry points used by tests and benchmarks.
 """
 from __future__ import annotations
@@ -22,7 +25,8 @@ import torch
 __all__ = [
     "RaError", "lib", "ra_softmax", "ra_softmax_backward", "ra_attention", "ra_attention_forward", "RaAttention",
     "ra_attention_backward", "pack_attn_mask", "device_status", "set_wait_limit_ns", "exported_symbols", "LIB_PATH",
-    "debug_kernel_events",
+    "debug_kernel_events", "ra_rope_frequencies", "ra_qk_norm_rope", "ra_qk_norm_rope_backward", "ra_cache_append",
+    "ra_attention_decode", "ra_cache_evict", "RaCache",
 ]
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -59,6 +63,14 @@ _SIGNATURES = {
                                                _vp], _i32),
     "ra_attention_bwd_masked": ([_vp] * 12 + [_i32, _i32, _i32, _i32, _i32, _f32, _i32, _i32, _i32, _i32, _vp, _vp,
                                                 _i32, _i32, _vp], _i32),
+    "ra_qk_norm_rope_fwd": ([_vp, _i64, _i64] + [_vp] * 4 + [_i32, _f32, _vp, _vp, _i64, _i64, _vp, _i32, _i32]
+                            + [_vp] * 5 + [_i32] * 7 + [_vp], _i32),
+    "ra_qk_norm_rope_bwd_workspace_size": ([_i32], ctypes.c_size_t),
+    "ra_qk_norm_rope_bwd": ([_vp, _i64, _i64] + [_vp] * 4 + [_i32, _f32, _vp, _vp, _i64, _i64, _vp, _i32, _i32]
+                            + [_vp] * 6 + [_i32] * 6 + [_vp], _i32),
+    "ra_attention_decode_workspace_size": ([_i32] * 6, ctypes.c_size_t),
+    "ra_attention_decode": ([_vp] * 9 + [_i32] * 6 + [_f32, _i32, _vp], _i32),
+    "ra_cache_evict": ([_vp] * 9 + [_i32] * 8 + [_vp], _i32),
     "ra_device_status": ([_vp], _i32),
     "ra_set_wait_limit_ns": ([_u64], None),
     "ra_debug_force_timeout": ([_i32], None),
@@ -269,19 +281,28 @@ def ra_attention(q, k, v, attn_mask=None, is_causal=False, scale=None):
     return _RaAttentionFn.apply(q.contiguous(), k.contiguous(), v.contiguous(), bool(is_causal), scale, attn_mask)
 
 
+from .serving import (RaCache, ra_attention_decode, ra_cache_append, ra_cache_evict, ra_qk_norm_rope,  # noqa: E402
+                      ra_qk_norm_rope_backward, ra_rope_frequencies)
+
+
 class RaAttention(torch.nn.Module):
     """Multi-head attention with ra_softmax (page "Ra-Family: Rational Neural Architecture",
     section 3, "ra_attention & RaAttention").
 
     x [B, N, dim] -> one projection to q, k, v of every head ([B, heads, N, dim/heads])
     -> optional layer normalisation of q and k over the head dimension (qk_norm)
+    -> optional rotation of q and k by position (rope_sections: pairs of dimensions per position
+    axis; with it, norm and rotation are one kernel, ra_qk_norm_rope)
     -> ra_attention (this library's kernels, with autograd) -> heads merged -> output
     projection.  The two projections are plain library GEMMs (torch Linear, cuBLAS).
     Dropout is not part of this path: attn_drop and proj_drop must be 0.
+
+    Serving (causal modules): new_cache, then prefill for a prompt and decode for single tokens.
     """
 
     def __init__(self, dim, num_heads=8, qkv_bias=False, qk_norm=False, attn_drop=0.0, proj_drop=0.0,
-                 causal=False, device=None, dtype=None):
+                 causal=False, device=None, dtype=None, rope_sections=None, rope_theta=10000.0,
+                 rope_interleaved=False):
         super().__init__()
         if dim % num_heads != 0:
             raise ValueError("dim must be a multiple of num_heads")
@@ -295,14 +316,92 @@ class RaAttention(torch.nn.Module):
         self.q_norm = torch.nn.LayerNorm(self.head_dim, eps=1e-5, **kw) if qk_norm else None
         self.k_norm = torch.nn.LayerNorm(self.head_dim, eps=1e-5, **kw) if qk_norm else None
         self.proj = torch.nn.Linear(dim, dim, **kw)
+        self.rope_sections = tuple(int(s) for s in rope_sections) if rope_sections else None
+        if self.rope_sections and (min(self.rope_sections) < 1 or 2 * sum(self.rope_sections) > self.head_dim):
+            raise ValueError("rope_sections must be positive pair counts with 2 * sum(rope_sections) <= dim / num_heads")
+        self.rope_theta = float(rope_theta)
+        self.rope_interleaved = bool(rope_interleaved)
+        # float64 whatever the module's dtype becomes, so not a buffer; made on a device's first call
+        self._frequencies = {}
 
-    def forward(self, x):
+    def _how(self, positions):
+        """ra_qk_norm_rope's keyword arguments for this module."""
+        how = {"norm": "none"}
+        if self.q_norm is not None:
+            how = {"norm": "layer", "q_weight": self.q_norm.weight, "q_bias": self.q_norm.bias,
+                   "k_weight": self.k_norm.weight, "k_bias": self.k_norm.bias, "eps": self.q_norm.eps}
+        if self.rope_sections:
+            device = self.proj.weight.device
+            if device not in self._frequencies:
+                self._frequencies[device] = ra_rope_frequencies(self.rope_sections, self.rope_theta, device=device)
+            how.update(frequencies=self._frequencies[device], sections=self.rope_sections, positions=positions,
+                       interleaved=self.rope_interleaved)
+        return how
+
+    def _merge(self, o):
+        B, _, N, _ = o.shape
+        return self.proj(o.transpose(1, 2).reshape(B, N, self.num_heads * self.head_dim))
+
+    def forward(self, x, positions=None):
+        """positions (with rope_sections): integer [N], [B, N] or [axes, B, N]; 0 .. N - 1 when not given."""
         B, N, C = x.shape
+        if self.rope_sections:
+            if positions is None:
+                positions = torch.arange(N, device=x.device, dtype=torch.int32)
+            q, k, v = ra_qk_norm_rope(self.qkv(x), self.num_heads, **self._how(positions))
+            return self._merge(ra_attention(q, k, v, is_causal=self.causal))
+        if positions is not None:
+            raise ValueError("positions need rope_sections")
         q, k, v = self.qkv(x).reshape(B, N, 3, self.num_heads, self.head_dim).permute(2, 0, 3, 1, 4).unbind(0)
         if self.q_norm is not None:
             q, k = self.q_norm(q), self.k_norm(k)
         o = ra_attention(q, k, v, is_causal=self.causal)
         return self.proj(o.transpose(1, 2).reshape(B, N, C))
+
+    def new_cache(self, batch, capacity, *, prefix=None, track_weight=False):
+        """An empty RaCache for this module."""
+        return RaCache(batch, self.num_heads, capacity, self.head_dim, prefix=prefix, track_weight=track_weight,
+                       device=self.proj.weight.device, dtype=self.proj.weight.dtype)
+
+    @torch.no_grad()
+    def prefill(self, x, cache, positions=None, count=None):
+        """forward of a prompt x [B, N, dim] whose keys and values go into an empty cache; returns y.
+        count: optional int32 [B], the tokens of a padded batch (rows of y behind them mean nothing).
+        Behind a prefix the prompt attends to it too (bf16 only: a masked attention call)."""
+        if not self.causal:
+            raise ValueError("serving needs a causal module")
+        if cache.bound:
+            raise ValueError("prefill needs an empty cache")
+        B, N, _ = x.shape
+        cache.require_room(N)
+        P = cache.prefix_length
+        if P and x.dtype != torch.bfloat16:
+            raise NotImplementedError("prefill behind a prefix takes bf16 modules only")
+        if self.rope_sections and positions is None:
+            positions = torch.arange(P, P + N, device=x.device, dtype=torch.int32)
+        q, k, v = ra_qk_norm_rope(self.qkv(x), self.num_heads, **self._how(positions))
+        cache.k[:, :, :N].copy_(k)
+        cache.v[:, :, :N].copy_(v)
+        cache.advance(N, count)
+        if not P:
+            return self._merge(ra_attention(q, k, v, is_causal=True))
+        k = torch.cat([cache.prefix_k.expand(B, -1, -1, -1), k], 2)
+        v = torch.cat([cache.prefix_v.expand(B, -1, -1, -1), v], 2)
+        seen = torch.ones(N, P + N, dtype=torch.bool, device=x.device).tril(P)
+        return self._merge(ra_attention(q, k, v, attn_mask=seen))
+
+    @torch.no_grad()
+    def decode(self, x, cache, positions=None):
+        """One token per sequence, x [B, 1, dim], appended to the cache and attended over all of it;
+        returns y [B, 1, dim].  positions: as in forward; the cache's own when not given."""
+        if not self.causal:
+            raise ValueError("serving needs a causal module")
+        if x.dim() != 3 or x.shape[1] != 1:
+            raise ValueError("decode takes one token per sequence: x [B, 1, dim]")
+        if self.rope_sections and positions is None:
+            positions = cache.position.view(1, -1, 1)
+        q = cache.append(self.qkv(x), self.num_heads, **self._how(positions))
+        return self._merge(cache.attend(q[:, :, 0]).unsqueeze(2))
 
 
 def device_status(stream=None):

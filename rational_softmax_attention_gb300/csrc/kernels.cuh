@@ -139,4 +139,71 @@ size_t bwd_workspace_bytes(int B, int H, int NQ, int NK, int D, bool f32_inputs)
 cudaError_t launch_attn_bwd_tc(const AttnShape& s, const BwdTcArgs& a, const LaunchCtx& ctx, cudaStream_t st,
                                const KernelEvents& ev);
 
+// Multiprocessors of a GB300: grids and splits are planned for them, so that a workspace's size
+// does not depend on the device that is current when it is asked for.
+constexpr int kSms = 152;
+
+// Per-head normalisation and position rotation (norm_rope.cu).  D in {16, 32, 64, 128}.
+struct NormRopeShape {
+  const void* qkv;              // [B, N, (Hq + 2 Hkv) D] with these strides (elements)
+  int64_t batch_stride, token_stride;
+  const void *qw, *qb, *kw, *kb;   // [D] each; qb, kb may be null; all null without a norm
+  const double* freq;           // [pairs] radians per position
+  const int32_t* pos;           // position of token n of sequence b on an axis:
+  int64_t pos_axis_stride, pos_batch_stride;   //   pos[axis * axis stride + b * batch stride + n]
+  int end[3];                   // one past the last pair of axes 0, 1, 2
+  int pairs, interleaved;
+  int B, N, Hq, Hkv, D;
+  int norm;                     // ra_norm_t
+  float eps;
+  int tile;                     // tokens of a CTA's tile (set by the launcher)
+};
+struct NormRopeFwd {
+  void *q, *k, *v;              // q [B, Hq, N, D]; k, v [B, Hkv, capacity, D]
+  const int32_t* start;         // [B] slot of a sequence's first token, or null: 0
+  const int32_t* count;         // [B] tokens of a sequence that are written, or null: N
+  int capacity;
+};
+struct NormRopeBwd {
+  const void *dq, *dk, *dv;     // [B, Hq or Hkv, N, D]
+  void* dqkv;                   // [B, N, (Hq + 2 Hkv) D] dense
+  float* dparams;               // [4][D]: q weight, q bias, k weight, k bias
+  float* partial;               // [norm_rope_bwd_ctas][4][D]
+};
+int norm_rope_bwd_ctas();
+cudaError_t launch_norm_rope_fwd(NormRopeShape a, const NormRopeFwd& io, bool bf16, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(NormRopeShape a, const NormRopeBwd& io, bool bf16, cudaStream_t st);
+
+// One query token per sequence against its cache and a shared prefix (decode.cu).
+struct DecodeArgs {
+  const void *q, *k, *v, *pk, *pv;   // [B, Hq, D], [B, Hkv, C, D] x2, [Hkv, P, D] x2
+  const int32_t* length;        // [B], read as min(max(length, 0), C)
+  float* weight;                // [B, Hkv, C] or null
+  void* o;                      // [B, Hq, D]
+  float *s_own, *s_pre;         // scores: B Hq rows of own_width and pre_width
+  float *row_max, *part_sum;    // [B Hq][slots]: per item; slots = shared items, then own ones
+  float* part_o;                // [B Hq][slots][D]
+  int B, Hq, Hkv, G, D, C, P;
+  int chunk, own_width;         // keys of an own item; padded length of a row of s_own
+  int pchunk, pchunks, pre_width;
+  int slots;
+  float scale;
+};
+// Fills the split (chunk .. slots) from the sizes; returns the workspace bytes and, with `base`,
+// sets the workspace pointers.
+size_t plan_decode(DecodeArgs* a, char* base);
+cudaError_t launch_decode(const DecodeArgs& a, bool bf16, cudaStream_t st);
+
+// Eviction by accumulated weight (evict.cu).
+struct EvictArgs {
+  const void *k, *v;            // [B, Hkv, C] rows of row_bytes
+  const float* weight;          // [B, Hkv, C]
+  const int32_t* length;        // [B], read as min(max(length, 0), C)
+  void *k_out, *v_out;          // [B, Hkv, C_out] rows
+  float* weight_out;            // [B, Hkv, C_out]
+  int32_t *length_out, *index;  // [B], [B, Hkv, keep]
+  int B, Hkv, C, C_out, row_bytes, keep, recent;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
 }  // namespace raattn

@@ -1,0 +1,251 @@
+"""GPU parity of ra_qk_norm_rope (forward, backward, cache append) against the float64 oracle on the
+same rounded inputs.
+
+Tolerances.  Output rounding: half a step, finfo.eps / 2 of the value (bf16 2^-8, fp32 2^-24).
+Arithmetic: fp32.  A normalised value passes about 20 roundings (two sums over D of at most 4 + 5 levels,
+mean, square root, products) of 2^-24, the rotation two products, a sum, and a cosine and sine within
+2 ulp of an angle within 2^-22 turns of the exact one: together below 64 * 2^-24 of the largest
+value in the row.  A row gradient passes the same twice: 128 * 2^-24, of the row's largest possible
+value r * max|g w| * 3.  A parameter gradient over n rows: (16 + log2 n) * 4 roundings of 2^-24 of the
+sum of the terms' absolute values at most."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ra_serving as S
+import rational_softmax_attention_gb300 as ra
+
+pytestmark = pytest.mark.gpu
+U32 = 2.0 ** -24
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def make(B, N, Hq, Hkv, D, dtype, norm, bias, sections, interleaved, seed, start=0, shared_pos=False):
+    g = torch.Generator().manual_seed(seed)
+    qkv = (torch.randn(B, N, (Hq + 2 * Hkv) * D, generator=g) * 1.5 + 0.2).to(dtype)
+    params = {"q_weight": None, "q_bias": None, "k_weight": None, "k_bias": None}
+    if norm != "none":
+        params["q_weight"], params["k_weight"] = ((torch.rand(D, generator=g) + 0.5).to(dtype) for _ in range(2))
+    if bias:
+        params["q_bias"], params["k_bias"] = ((torch.randn(D, generator=g) * 0.2).to(dtype) for _ in range(2))
+    how = {"norm": norm, "interleaved": interleaved, "sections": sections, "frequencies": None, "positions": None}
+    if sections:
+        how["frequencies"] = ra.ra_rope_frequencies(sections, device="cpu")
+        shape = (1, 1, N) if shared_pos else (len(sections), B, N)
+        how["positions"] = (torch.randint(0, 5000, shape, generator=g) + start).to(torch.int32)
+    return qkv, params, how
+
+
+def cuda(x):
+    return {n: t.cuda() if torch.is_tensor(t) else t for n, t in x.items()}
+
+
+def oracle_how(params, how):
+    return dict(norm=how["norm"], params=tuple(f64(params[n]) for n in ("q_weight", "q_bias", "k_weight", "k_bias")),
+                frequencies=f64(how["frequencies"]), sections=how["sections"],
+                positions=None if how["positions"] is None else how["positions"].numpy(),
+                interleaved=how["interleaved"])
+
+
+def check_rows(got, want, dtype, what):
+    assert got.dtype == dtype
+    got = f64(got)
+    bound = half_step(dtype) * np.abs(want) + 64 * U32 * np.abs(want).max(-1, keepdims=True)
+    worst = np.max(np.abs(got - want) - bound)
+    assert worst <= 0, f"{what}: beyond the bound by {worst:.3e}"
+
+
+CASES = [  # B, N, Hq, Hkv, D, norm, bias, sections, interleaved
+    (2, 128, 12, 12, 64, "layer", True, (32,), False),
+    (1, 1, 1, 1, 64, "rms", False, (8, 24), False),
+    (3, 37, 6, 2, 128, "rms", False, (16, 24, 24), True),
+    (2, 19, 5, 1, 128, "layer", False, (10, 3, 2, 1), False),
+    (1, 67, 3, 3, 16, "layer", True, (8,), False),
+    (2, 33, 4, 2, 32, "none", False, (5, 2), True),
+    (2, 50, 7, 1, 64, "layer", True, None, False),
+    (1, 700, 16, 8, 128, "none", False, (64,), False),
+    (4, 1500, 2, 1, 16, "rms", False, (1, 1), True),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_forward_and_backward_match_the_oracle(case, dtype):
+    B, N, Hq, Hkv, D, norm, bias, sections, inter = case
+    qkv, params, how = make(B, N, Hq, Hkv, D, dtype, norm, bias, sections, inter, seed=N + D)
+    q, k, v = ra.ra_qk_norm_rope(qkv.cuda(), Hq, Hkv, **cuda(params), **cuda(how))
+    torch.cuda.synchronize()
+    oh = oracle_how(params, how)
+    Q, K, V = S.qk_norm_rope(f64(qkv), Hq, Hkv, **oh)
+    check_rows(q, Q, dtype, "q")
+    check_rows(k, K, dtype, "k")
+    assert np.array_equal(f64(v), V)
+
+    g = torch.Generator().manual_seed(5)
+    d = [torch.randn(B, h, N, D, generator=g).to(dtype) for h in (Hq, Hkv, Hkv)]
+    got = ra.ra_qk_norm_rope_backward(qkv.cuda(), *(t.cuda() for t in d), Hq, Hkv, **cuda(params), **cuda(how))
+    torch.cuda.synchronize()
+    DX, DP = S.qk_norm_rope_bwd(f64(qkv), *(f64(t) for t in d), Hq, Hkv, **oh)
+    dx = f64(got[0]).reshape(B, N, -1, D)
+    DX = DX.reshape(B, N, -1, D)
+    if norm == "none":
+        scale = np.ones(DX.shape[:-1] + (1,))
+    else:
+        _, r = S._norm(f64(qkv).reshape(B, N, -1, D)[:, :, :Hq + Hkv], norm, 1e-5)
+        scale = np.concatenate([r, np.ones((B, N, Hkv, 1))], 2) * 1.5
+    dmax = np.concatenate([np.abs(f64(t)).max(-1, keepdims=True).transpose(0, 2, 1, 3) for t in d], 2) * np.sqrt(2)
+    assert np.all(np.abs(dx - DX) <= half_step(dtype) * np.abs(DX) + 128 * U32 * 3 * scale * dmax)
+    assert np.array_equal(dx[:, :, Hq + Hkv:], DX[:, :, Hq + Hkv:])
+    names = ("q_weight", "q_bias", "k_weight", "k_bias")
+    for i, name in enumerate(names):
+        if params[name] is None:
+            assert got[1 + i] is None
+            continue
+        rows = B * N * (Hq if i < 2 else Hkv)
+        # |g| <= sqrt(2) max|d|, |xhat| <= sqrt(D): the terms' sum, by its mean size
+        size = rows * 1.5 * np.abs(f64(d[i // 2])).mean() * (2.0 if i % 2 == 0 else 1.0)
+        assert got[1 + i].dtype == torch.float32
+        err = np.abs(f64(got[1 + i]) - DP[i]).max()
+        assert err <= (16 + np.log2(rows)) * 4 * U32 * size, (name, err)
+
+
+@pytest.mark.parametrize("start", [(1 << 24) + 1, (1 << 31) - 6000, -(1 << 31)])
+def test_far_positions_keep_their_angles(start):
+    """Angles of positions that fp32 cannot hold, against 64 bits; positions shared by axes and batch."""
+    qkv, params, how = make(2, 40, 2, 1, 64, torch.float32, "none", False, (16, 16), False, 3, start, True)
+    q, k, _ = ra.ra_qk_norm_rope(qkv.cuda(), 2, 1, **cuda(params), **cuda(how))
+    Q, K, _ = S.qk_norm_rope(f64(qkv), 2, 1, **oracle_how(params, how))
+    # the frequency's two floats hold 48 bits: at 2^31 / (2 pi) turns 2^-49 of that more, 6e-7 turns
+    more = 2 * np.pi * 2 ** 31 / (2 * np.pi) * 2.0 ** -48 * 2
+    for got, want in ((q, Q), (k, K)):
+        bound = (64 * U32 + more) * np.abs(want).max(-1, keepdims=True) * np.sqrt(2)
+        assert np.all(np.abs(f64(got) - want) <= bound)
+
+
+def test_strided_projection_and_position_forms():
+    """qkv as a slice of a wider row, misaligned slices, [N] and [B, N] and int64 positions: the same results."""
+    B, N, Hq, Hkv, D = 2, 21, 3, 1, 64
+    qkv, params, how = make(B, N, Hq, Hkv, D, torch.bfloat16, "layer", True, (32,), False, 8, 0, True)
+    params, how = cuda(params), cuda(how)
+    ref = ra.ra_qk_norm_rope(qkv.cuda(), Hq, Hkv, **params, **how)
+    wide = torch.full((B, N + 3, qkv.shape[-1] + 72), float("nan"), dtype=qkv.dtype, device="cuda")
+    for off in (8, 3):
+        part = wide[:, 2:2 + N, off:off + qkv.shape[-1]]
+        part.copy_(qkv)
+        for a, b in zip(ref, ra.ra_qk_norm_rope(part, Hq, Hkv, **params, **how)):
+            assert torch.equal(a, b)
+    p = how.pop("positions")
+    for form in (p.view(N), p.view(1, N).expand(B, N), p.view(N).long(), p.expand(1, B, N)):
+        for a, b in zip(ref, ra.ra_qk_norm_rope(qkv.cuda(), Hq, Hkv, **params, **how, positions=form)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N,count", [(1, None), (5, None), (6, [6, 0, 3])])
+def test_append_writes_its_slots_and_nothing_else(N, count):
+    B, Hq, Hkv, D, C = 3, 4, 2, 128, 24
+    qkv, params, how = make(B, N, Hq, Hkv, D, torch.bfloat16, "rms", False, (64,), False, 11)
+    params, how = cuda(params), cuda(how)
+    q, k, v = ra.ra_qk_norm_rope(qkv.cuda(), Hq, Hkv, **params, **how)
+    ck, cv = (torch.full((B, Hkv, C, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    length = torch.tensor([0, C - 2, 9], dtype=torch.int32, device="cuda")    # the second has room for two
+    n = None if count is None else torch.tensor(count, dtype=torch.int32, device="cuda")
+    got = ra.ra_cache_append(qkv.cuda(), ck, cv, length, Hq, Hkv, count=n, **params, **how)
+    assert torch.equal(got, q) and length.tolist() == [0, C - 2, 9]
+    wk, wv = torch.full_like(ck, 7.0), torch.full_like(cv, 7.0)
+    for b, s in enumerate(length.tolist()):
+        m = min(N if count is None else count[b], C - s)
+        wk[b, :, s:s + m], wv[b, :, s:s + m] = k[b, :, :m], v[b, :, :m]
+    assert torch.equal(ck, wk) and torch.equal(cv, wv)
+
+
+def test_append_ignores_slots_outside_the_cache():
+    qkv, params, how = make(3, 2, 1, 1, 64, torch.float32, "none", False, None, False, 12)
+    ck, cv = torch.zeros(3, 1, 4, 64, device="cuda"), torch.zeros(3, 1, 4, 64, device="cuda")
+    length = torch.tensor([-1, 4, (1 << 31) - 1], dtype=torch.int32, device="cuda")
+    ra.ra_cache_append(qkv.cuda(), ck, cv, length, 1, 1, norm="none")
+    assert torch.equal(ck[0, 0, 0], qkv[0, 1, 64:128].cuda()) and not ck[0, 0, 1:].any() and not ck[1:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_autograd(dtype):
+    """The autograd function gives the explicit backward's gradients, for the inputs that ask."""
+    B, N, Hq, Hkv, D = 2, 30, 4, 2, 64
+    qkv, params, how = make(B, N, Hq, Hkv, D, dtype, "layer", True, (16, 16), True, 13)
+    params, how, qkv = cuda(params), cuda(how), qkv.cuda()
+    d = [torch.randn(B, N, h, D, device="cuda").to(dtype).transpose(1, 2) for h in (Hq, Hkv, Hkv)]   # strided
+    want = ra.ra_qk_norm_rope_backward(qkv, *(t.contiguous() for t in d), Hq, Hkv, **params, **how)
+    x = qkv.clone().requires_grad_(True)
+    p = {n: t.clone().requires_grad_(True) for n, t in params.items()}
+    out = ra.ra_qk_norm_rope(x, Hq, Hkv, **p, **how)
+    torch.autograd.backward(out, d)
+    assert torch.equal(x.grad, want[0])
+    for (n, t), w in zip(p.items(), want[1:]):
+        assert t.grad.dtype == dtype and torch.equal(t.grad, w.to(dtype)), n
+    y = qkv.clone().requires_grad_(True)
+    q, _, _ = ra.ra_qk_norm_rope(y, Hq, Hkv, **params, **how)
+    q.sum().backward()                                   # k and v take no part
+    assert not y.grad.view(B, N, -1, D)[:, :, Hq:].any()
+
+
+def test_bit_identical_on_streams_and_in_a_graph():
+    B, N, Hq, Hkv, D = 2, 900, 4, 4, 128
+    qkv, params, how = make(B, N, Hq, Hkv, D, torch.bfloat16, "layer", True, (64,), False, 14)
+    params, how, x = cuda(params), cuda(how), qkv.cuda()
+    d = [torch.randn(B, h, N, D, device="cuda").bfloat16() for h in (Hq, Hkv, Hkv)]
+
+    def both():
+        return (*ra.ra_qk_norm_rope(x, Hq, Hkv, **params, **how),
+                *ra.ra_qk_norm_rope_backward(x, *d, Hq, Hkv, **params, **how))
+    ref = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = both()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        cap = both()
+    for _ in range(2):
+        for t in cap:
+            t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b, c in zip(ref, got, cap):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_refusals():
+    x = torch.zeros(1, 2, 3 * 64, device="cuda")
+    w, f = torch.ones(64, device="cuda"), ra.ra_rope_frequencies((32,))
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    bad = [dict(norm="batch"), dict(norm="layer"), dict(norm="rms", q_weight=w, k_weight=w, q_bias=w),
+           dict(norm="none", q_weight=w), dict(norm="none", sections=(32,)),
+           dict(norm="none", sections=(32,), frequencies=f.float(), positions=pos),
+           dict(norm="none", sections=(33,), frequencies=f, positions=pos),
+           dict(norm="none", sections=(32,), frequencies=f, positions=pos.cpu()),
+           dict(norm="none", sections=(32,), frequencies=f, positions=pos.float()),
+           dict(norm="none", sections=(32,), frequencies=f, positions=pos[:1]),
+           dict(norm="none", sections=(32,), frequencies=f, positions=pos.view(1, 1, 2).expand(3, 1, 2)),
+           dict(norm="none", frequencies=f), dict(norm="layer", q_weight=w.bfloat16(), k_weight=w.bfloat16())]
+    for how in bad:
+        with pytest.raises(ValueError):
+            ra.ra_qk_norm_rope(x, 1, 1, **how)
+    with pytest.raises(ra.RaError) as e:
+        ra.ra_qk_norm_rope(x, 1, 1, norm="none", sections=(4,), frequencies=f[:4].contiguous(), positions=pos)
+    assert e.value.code == 2
+    with pytest.raises(TypeError):
+        ra.ra_qk_norm_rope(x.half(), 1, 1, norm="none")
+    with pytest.raises(ValueError):
+        ra.ra_qk_norm_rope(x, 3, 1, norm="none")      # 192 elements are not 5 heads
+    c = torch.zeros(1, 1, 4, 64, device="cuda")
+    with pytest.raises(ValueError):
+        ra.ra_cache_append(x, c, c.bfloat16(), pos[:1], 1, 1, norm="none")
+    with pytest.raises(ValueError):
+        ra.ra_cache_append(x, c, c, pos[:1].long(), 1, 1, norm="none")
