@@ -422,12 +422,14 @@ ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t t
  *   scale         score scale; <= 0 means 1/sqrt(D).
  *   dtype         of q, k, v, prefix and o.  RA_BF16: D in {64, 128}; RA_F32: {16, 32, 64, 128}.
  * Scores, row maxima, sums and weights are fp32.  Results do not depend on scheduling.
+ * With a prefix and more than 32 query rows per key head (B H_Q / H_KV), bf16 calls use kernels
+ * with bounded waits, whose giving up ra_device_status() reports.
  * Errors: RA_ERR_ARG for null or misaligned pointers, sizes < 1 (P < 0), H_Q no multiple of
  * H_KV, B H_Q, B H_KV C or H_KV P beyond int32, a bad enum or scale; RA_ERR_UNSUPPORTED for D outside
  * the sets above, B > 8192 or more than 1024 query heads per key head; RA_ERR_LAUNCH.  The size
  * query returns 0 for such sizes.
  */
-size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D);
+size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D, ra_dtype_t dtype);
 ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, const int32_t* length,
                                 const void* prefix_k, const void* prefix_v, void* o, float* weight, void* workspace,
                                 int B, int H_Q, int H_KV, int C, int P, int D, float scale, ra_dtype_t dtype,

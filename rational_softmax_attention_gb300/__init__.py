@@ -68,7 +68,7 @@ _SIGNATURES = {
     "ra_qk_norm_rope_bwd_workspace_size": ([_i32], ctypes.c_size_t),
     "ra_qk_norm_rope_bwd": ([_vp, _i64, _i64] + [_vp] * 4 + [_i32, _f32, _vp, _vp, _i64, _i64, _vp, _i32, _i32]
                             + [_vp] * 6 + [_i32] * 6 + [_vp], _i32),
-    "ra_attention_decode_workspace_size": ([_i32] * 6, ctypes.c_size_t),
+    "ra_attention_decode_workspace_size": ([_i32] * 7, ctypes.c_size_t),
     "ra_attention_decode": ([_vp] * 9 + [_i32] * 6 + [_f32, _i32, _vp], _i32),
     "ra_cache_evict": ([_vp] * 9 + [_i32] * 8 + [_vp], _i32),
     "ra_device_status": ([_vp], _i32),

@@ -135,6 +135,11 @@ ra_status_t check_attn_sizes(int B, int H, int NQ, int NK, int D) {
 
 }  // namespace
 
+ra_status_t launch_context(LaunchCtx* ctx) { return make_ctx(ctx); }
+bool tensor_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int D) {
+  return make_map_bf16(map, base, BH, N, D);
+}
+
 size_t fwd_workspace_v_bytes(int B, int H, int NK, int D) {
   return (static_cast<size_t>(B) * H * NK * D * 2 + 255) & ~static_cast<size_t>(255);
 }

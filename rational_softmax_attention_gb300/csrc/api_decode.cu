@@ -138,9 +138,10 @@ ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t t
              : RA_ERR_LAUNCH;
 }
 
-size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D) {
+size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D, ra_dtype_t dtype) {
   DecodeArgs a{};
-  return decode_shape(&a, B, H_Q, H_KV, C, P, D) == RA_OK ? plan_decode(&a, nullptr) : 0;
+  if (!dtype_ok(dtype) || decode_shape(&a, B, H_Q, H_KV, C, P, D) != RA_OK) return 0;
+  return plan_decode(&a, dtype == RA_BF16, nullptr);
 }
 
 ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, const int32_t* length,
@@ -168,8 +169,15 @@ ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, con
   a.weight = weight;
   a.o = o;
   a.scale = scale;
-  plan_decode(&a, static_cast<char*>(workspace));
-  return launch_decode(a, dtype == RA_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
+  plan_decode(&a, dtype == RA_BF16, static_cast<char*>(workspace));
+  PrefixMaps maps;
+  LaunchCtx ctx;
+  if (a.tc && (launch_context(&ctx) != RA_OK || !tensor_map_bf16(&maps.k, prefix_k, H_KV, P, D) ||
+               !tensor_map_bf16(&maps.v, prefix_v, H_KV, P, D)))
+    return RA_ERR_LAUNCH;
+  return launch_decode(a, dtype == RA_BF16, maps, ctx, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? RA_OK
+             : RA_ERR_LAUNCH;
 }
 
 ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, const int32_t* length, void* k_out,

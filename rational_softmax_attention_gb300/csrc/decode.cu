@@ -34,7 +34,7 @@ constexpr int kRows = 16;        // query rows of an item
 constexpr int kBlock = 32;       // keys a warp takes at a time; score rows are padded to whole blocks
 constexpr float kInf = __builtin_huge_valf();
 
-__device__ __forceinline__ float phi_of(float d, float) {   // bf16 inputs: 2 ulp reciprocal, exact 1 at d = 0
+__device__ __forceinline__ float phi_fast(float d) {   // bf16 inputs: 2 ulp reciprocal, exact 1 at d = 0
   const float q = fmaxf(16.0f - d, 0.0f) * rcp_approx(16.0f + d);
   const float q2 = q * q, q4 = q2 * q2;
   return q4 * q4;
@@ -46,8 +46,7 @@ __device__ __forceinline__ float phi_exact(float d) {        // fp32 inputs: IEE
 }
 template <typename T>
 __device__ __forceinline__ float phi_t(float d) {
-  if (sizeof(T) == 2) return phi_of(d, 0.0f);
-  return phi_exact(d);
+  return sizeof(T) == 2 ? phi_fast(d) : phi_exact(d);
 }
 
 struct Item {
@@ -58,14 +57,12 @@ struct Item {
   int row0, rows;       // rows of the block: within the head's G (own) or the batch's B G (shared)
 };
 
-__device__ __forceinline__ int own_length(const DecodeArgs& a, int b) { return min(max(a.length[b], 0), a.C); }
-
 // cum[b] = own chunks of the sequences before b, for b <= B.  All threads.
 __device__ void count_chunks(int* cum, const DecodeArgs& a) {
   __shared__ int sums[kWarps];
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
   int mine = 0;
-  for (int i = 0; i < per && b0 + i < a.B; ++i) mine += (own_length(a, b0 + i) + a.chunk - 1) / a.chunk;
+  for (int i = 0; i < per && b0 + i < a.B; ++i) mine += (decode_own_length(a, b0 + i) + a.chunk - 1) / a.chunk;
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -78,22 +75,24 @@ __device__ void count_chunks(int* cum, const DecodeArgs& a) {
   int run = inc - mine;
   for (int i = 0; i < per && b0 + i < a.B; ++i) {
     cum[b0 + i] = run;
-    run += (own_length(a, b0 + i) + a.chunk - 1) / a.chunk;
+    run += (decode_own_length(a, b0 + i) + a.chunk - 1) / a.chunk;
   }
   if (b0 < a.B && b0 + per >= a.B) cum[a.B] = run;
   __syncthreads();
 }
 
+// Row blocks of the shared keys' items: none where the tensor cores take them.
+__device__ __forceinline__ int shared_blocks(const DecodeArgs& a) { return a.tc ? 0 : (a.B * a.G + kRows - 1) / kRows; }
+
 __device__ __forceinline__ int64_t item_count(const int* cum, const DecodeArgs& a) {
-  const int64_t shared = static_cast<int64_t>(a.Hkv) * a.pchunks * ((a.B * a.G + kRows - 1) / kRows);
-  return shared + static_cast<int64_t>(cum[a.B]) * a.Hkv * ((a.G + kRows - 1) / kRows);
+  return static_cast<int64_t>(a.Hkv) * a.pchunks * shared_blocks(a) + static_cast<int64_t>(cum[a.B]) * a.Hkv * ((a.G + kRows - 1) / kRows);
 }
 
 // Item i: the shared keys' items first (a key range's row blocks together, so that they find it
 // in L2), then the sequences' in order.
 __device__ __forceinline__ Item get_item(int64_t i, const int* cum, const DecodeArgs& a) {
   Item it;
-  const int blocks = (a.B * a.G + kRows - 1) / kRows;
+  const int blocks = shared_blocks(a);
   const int64_t shared = static_cast<int64_t>(a.Hkv) * a.pchunks * blocks;
   if (i < shared) {
     const int rb = static_cast<int>(i % blocks), rest = static_cast<int>(i / blocks);
@@ -121,7 +120,7 @@ __device__ __forceinline__ Item get_item(int64_t i, const int* cum, const Decode
   const int k = c - cum[lo];
   it.slot = a.pchunks + k;
   it.first = k * a.chunk;
-  it.last = min(it.first + a.chunk, own_length(a, lo));
+  it.last = min(it.first + a.chunk, decode_own_length(a, lo));
   it.row0 = rb * kRows;
   it.rows = min(a.G - it.row0, kRows);
   return it;
@@ -202,7 +201,7 @@ __device__ __forceinline__ void item_scores(const Item& it, const DecodeArgs& a,
       }
       const int key = k0 + nb * 8 + 2 * t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = key + (i & 1) < it.last ? s[i] * a.scale : -kInf;
+      for (int i = 0; i < 4; ++i) s[i] = key + (i & 1) < it.last ? s[i] : -kInf;
       m0 = fmaxf(m0, fmaxf(s[0], s[1]));
       m1 = fmaxf(m1, fmaxf(s[2], s[3]));
       if (w0) *reinterpret_cast<float2*>(s0 + key) = make_float2(s[0], s[1]);
@@ -248,7 +247,7 @@ __device__ __forceinline__ void item_scores(const Item& it, const DecodeArgs& a,
         float s = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s = in ? s * a.scale : -kInf;
+        s = in ? s : -kInf;
         best[r] = fmaxf(best[r], s);
         if (gl == 0 && key < end) score_row(it, row_of(it, r, a), a)[key] = s;
       }
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) decode_scores_kernel(const DecodeArg
 // A row's maximum over its shared and own items.  A whole warp.
 __device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row) {
   const int b = row / a.Hq;
-  const int n = a.pchunks + (own_length(a, b) + a.chunk - 1) / a.chunk;
+  const int n = a.pchunks + (decode_own_length(a, b) + a.chunk - 1) / a.chunk;
   float m = -kInf;
   for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.row_max[static_cast<int64_t>(row) * a.slots + i]);
 #pragma unroll
@@ -326,10 +325,10 @@ __device__ __forceinline__ void item_values(const Item& it, const DecodeArgs& a,
         const int key = k0 + h * 16 + e * 8 + 2 * t;
         float2 x = w0 ? *reinterpret_cast<const float2*>(s0 + key) : make_float2(-kInf, -kInf);
         float2 y = w1 ? *reinterpret_cast<const float2*>(s1 + key) : make_float2(-kInf, -kInf);
-        x.x = phi_of(m0 - x.x, 0.0f);
-        x.y = phi_of(m0 - x.y, 0.0f);
-        y.x = phi_of(m1 - y.x, 0.0f);
-        y.y = phi_of(m1 - y.y, 0.0f);
+        x.x = phi_fast((m0 - x.x) * a.scale);
+        x.y = phi_fast((m0 - x.y) * a.scale);
+        y.x = phi_fast((m1 - y.x) * a.scale);
+        y.y = phi_fast((m1 - y.y) * a.scale);
         t0 += x.x + x.y;
         t1 += y.x + y.y;
         live |= x.x > 0.0f || x.y > 0.0f || y.x > 0.0f || y.y > 0.0f;
@@ -408,7 +407,7 @@ __device__ __forceinline__ void item_values(const Item& it, const DecodeArgs& a,
       if (r < it.rows) {
         const float* s = score_row(it, row_of(it, r, a), a);
         for (int i = lane; i < TK; i += 32) {
-          const float f = k0 + i < it.last ? phi_exact(rowm[r] - s[k0 + i]) : 0.0f;
+          const float f = k0 + i < it.last ? phi_exact((rowm[r] - s[k0 + i]) * a.scale) : 0.0f;
           ph[r][i] = f;
           tot[rr] += f;
         }
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(kThreads) decode_values_kernel(const DecodeArg
         const float m = row_maximum(a, row);
         if (lane == 0) {
           rowm[r] = m;
-          if (m - a.row_max[static_cast<int64_t>(row) * a.slots + it.slot] < 16.0f) live = 1;
+          if ((m - a.row_max[static_cast<int64_t>(row) * a.slots + it.slot]) * a.scale < 16.0f) live = 1;
         }
       } else if (lane == 0) {
         rowm[r] = 0.0f;
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) decode_values_kernel(const DecodeArg
 // A row's sum of phi over its items, in a fixed order.  A whole warp.
 __device__ __forceinline__ float row_total(const DecodeArgs& a, int row) {
   const int b = row / a.Hq;
-  const int n = a.pchunks + (own_length(a, b) + a.chunk - 1) / a.chunk;
+  const int n = a.pchunks + (decode_own_length(a, b) + a.chunk - 1) / a.chunk;
   float s = 0.0f;
   for (int i = threadIdx.x & 31; i < n; i += 32) s += a.part_sum[static_cast<int64_t>(row) * a.slots + i];
 #pragma unroll
@@ -530,7 +529,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     constexpr int L = D / 4, KS = kThreads / L;
     __shared__ float4 part[KS][L];
     const int row = blockIdx.x, b = row / a.Hq;
-    const int n = a.pchunks + (own_length(a, b) + a.chunk - 1) / a.chunk;
+    const int n = a.pchunks + (decode_own_length(a, b) + a.chunk - 1) / a.chunk;
     const float total = row_total(a, row);
     const int gl = threadIdx.x % L, ks = threadIdx.x / L;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -571,7 +570,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
   const int64_t x = blockIdx.x - rows;
   const int split = static_cast<int>(x % splits);
   const int bk = static_cast<int>(x / splits), b = bk / a.Hkv, kv = bk - b * a.Hkv;
-  const int first = split * kWeightKeys, last = min(first + kWeightKeys, own_length(a, b));
+  const int first = split * kWeightKeys, last = min(first + kWeightKeys, decode_own_length(a, b));
   if (first >= last) return;
   for (int g = warp; g < a.G; g += kWarps) {
     const int row = b * a.Hq + kv * a.G + g;
@@ -584,27 +583,29 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     float sum = 0.0f;
     for (int g = 0; g < a.G; ++g) {
       const float s = a.s_own[(static_cast<int64_t>(b) * a.Hq + kv * a.G + g) * a.own_width + key];
-      sum += phi_t<T>(ms[g].x - s) / ms[g].y;
+      sum += phi_t<T>((ms[g].x - s) * a.scale) / ms[g].y;
     }
     w[key] += sum;
   }
 }
 
 template <typename T, int D>
-cudaError_t go(const DecodeArgs& a, cudaStream_t st) {
+cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
   const int cum = (a.B + 1) * 4;
   const int smem_values = kWarps * kRows * D * 4 + cum;
+  cudaError_t e = cudaSuccess;
   if (smem_values > 40 * 1024) {   // many sequences: 32 KB of partial sums and up to 32 KB of chunk counts
-    const cudaError_t e = cudaFuncSetAttribute(decode_values_kernel<T, D>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem_values);
+    e = cudaFuncSetAttribute(decode_values_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_values);
     if (e != cudaSuccess) return e;
   }
-  const int64_t shared = static_cast<int64_t>(a.Hkv) * a.pchunks * ((a.B * a.G + kRows - 1) / kRows);
+  const int64_t shared = a.tc ? 0 : static_cast<int64_t>(a.Hkv) * a.pchunks * ((a.B * a.G + kRows - 1) / kRows);
   const int64_t own = static_cast<int64_t>(a.B) * ((a.C + a.chunk - 1) / a.chunk) * a.Hkv *
                       ((a.G + kRows - 1) / kRows);
   const int64_t most = shared + own;
   const int grid = static_cast<int>(most < 3 * kSms ? most : 3 * kSms);
+  if (a.tc && (e = launch_decode_prefix(maps, a, false, ctx, st)) != cudaSuccess) return e;
   decode_scores_kernel<T, D><<<grid, kThreads, cum, st>>>(a);
+  if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
   decode_values_kernel<T, D><<<grid, kThreads, smem_values, st>>>(a);
   const int64_t join = static_cast<int64_t>(a.B) * a.Hq +
                        (a.weight ? static_cast<int64_t>(a.B) * a.Hkv * ((a.C + kWeightKeys - 1) / kWeightKeys) : 0);
@@ -615,22 +616,28 @@ cudaError_t go(const DecodeArgs& a, cudaStream_t st) {
 }  // namespace
 
 // The split of the keys.  Own items of 256 keys, or of 128 where that would leave SMs without an
-// item; the shared keys in as many items as give every SM three, of at least 128 keys.
-size_t plan_decode(DecodeArgs* a, char* base) {
+// item.  Shared keys of more than kTcRows rows per key head go to the tensor cores, in whole
+// tiles of 128, split so that one wave of CTAs takes them; otherwise in as many items as give
+// every SM three, of at least 128 keys.
+constexpr int64_t kTcRows = 32;
+size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
   a->G = a->Hq / a->Hkv;
-  const int64_t own_blocks = (a->G + kRows - 1) / kRows, blocks = (static_cast<int64_t>(a->B) * a->G + kRows - 1) / kRows;
+  const int64_t shared_rows = static_cast<int64_t>(a->B) * a->G;
+  const int64_t own_blocks = (a->G + kRows - 1) / kRows;
   a->chunk = static_cast<int64_t>(a->B) * a->Hkv * own_blocks * ((a->C + 255) / 256) < 2 * kSms ? 128 : 256;
   const int own = (a->C + a->chunk - 1) / a->chunk;
   a->own_width = own * a->chunk;
   a->pchunk = a->pchunks = a->pre_width = 0;
+  a->tc = bf16 && a->P > 0 && shared_rows > kTcRows;
   if (a->P > 0) {
-    const int64_t per = a->Hkv * blocks;
-    const int64_t most = (a->P + 127) / 128, want = (3 * kSms + per - 1) / per;
-    const int n = static_cast<int>(want < most ? want : most);
-    a->pchunk = ((a->P + n - 1) / n + 127) / 128 * 128;
+    const int64_t per = a->Hkv * (a->tc ? (shared_rows + 255) / 256 : (shared_rows + kRows - 1) / kRows);
+    const int64_t tiles = (a->P + 127) / 128;
+    int64_t n = a->tc ? kSms / per : (3 * kSms + per - 1) / per;
+    n = n < 1 ? 1 : n > tiles ? tiles : n;
+    a->pchunk = static_cast<int>((tiles + n - 1) / n * 128);
     a->pchunks = (a->P + a->pchunk - 1) / a->pchunk;
-    a->pre_width = a->pchunks * a->pchunk;
+    a->pre_width = a->tc ? 0 : a->pchunks * a->pchunk;
   }
   a->slots = a->pchunks + own;
   size_t at = 0;
@@ -647,12 +654,13 @@ size_t plan_decode(DecodeArgs* a, char* base) {
   return at;
 }
 
-cudaError_t launch_decode(const DecodeArgs& a, bool bf16, cudaStream_t st) {
-  if (bf16) return a.D == 64 ? go<__nv_bfloat16, 64>(a, st) : go<__nv_bfloat16, 128>(a, st);
-  if (a.D == 16) return go<float, 16>(a, st);
-  if (a.D == 32) return go<float, 32>(a, st);
-  if (a.D == 64) return go<float, 64>(a, st);
-  return go<float, 128>(a, st);
+cudaError_t launch_decode(const DecodeArgs& a, bool bf16, const PrefixMaps& maps, const LaunchCtx& ctx,
+                          cudaStream_t st) {
+  if (bf16) return a.D == 64 ? go<__nv_bfloat16, 64>(a, maps, ctx, st) : go<__nv_bfloat16, 128>(a, maps, ctx, st);
+  if (a.D == 16) return go<float, 16>(a, maps, ctx, st);
+  if (a.D == 32) return go<float, 32>(a, maps, ctx, st);
+  if (a.D == 64) return go<float, 64>(a, maps, ctx, st);
+  return go<float, 128>(a, maps, ctx, st);
 }
 
 }  // namespace raattn

@@ -180,19 +180,44 @@ struct DecodeArgs {
   const int32_t* length;        // [B], read as min(max(length, 0), C)
   float* weight;                // [B, Hkv, C] or null
   void* o;                      // [B, Hq, D]
-  float *s_own, *s_pre;         // scores: B Hq rows of own_width and pre_width
-  float *row_max, *part_sum;    // [B Hq][slots]: per item; slots = shared items, then own ones
+  float *s_own, *s_pre;         // unscaled scores: B Hq rows of own_width and pre_width
+  float *row_max, *part_sum;    // [B Hq][slots]: per item (unscaled); slots = shared items, then own ones
   float* part_o;                // [B Hq][slots][D]
   int B, Hq, Hkv, G, D, C, P;
+  int tc;                       // the shared keys go to the tensor cores (decode_prefix_tc.cu)
   int chunk, own_width;         // keys of an own item; padded length of a row of s_own
   int pchunk, pchunks, pre_width;
   int slots;
   float scale;
 };
-// Fills the split (chunk .. slots) from the sizes; returns the workspace bytes and, with `base`,
-// sets the workspace pointers.
-size_t plan_decode(DecodeArgs* a, char* base);
-cudaError_t launch_decode(const DecodeArgs& a, bool bf16, cudaStream_t st);
+// The cache entries a sequence holds, and the maximum (unscaled) of a row over its shared and own
+// items, read by one thread.
+__device__ __forceinline__ int decode_own_length(const DecodeArgs& a, int b) { return min(max(a.length[b], 0), a.C); }
+__device__ __forceinline__ float decode_row_max(const DecodeArgs& a, int row) {
+  const int n = a.pchunks + (decode_own_length(a, row / a.Hq) + a.chunk - 1) / a.chunk;
+  const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
+  float m = -__builtin_huge_valf();
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) m = fmaxf(m, p[i]);
+  return m;
+}
+// Fills the split (tc, chunk .. slots) from the sizes; returns the workspace bytes and sets the
+// workspace pointers from `base`.
+size_t plan_decode(DecodeArgs* a, bool bf16, char* base);
+// Tensor maps of the prefix [Hkv, P, D] (the tensor-core form only).
+struct PrefixMaps {
+  CUtensorMap k, v;
+};
+cudaError_t launch_decode(const DecodeArgs& a, bool bf16, const PrefixMaps& maps, const LaunchCtx& ctx,
+                          cudaStream_t st);
+// The shared keys' maxima, or their values, on the tensor cores (decode_prefix_tc.cu).
+cudaError_t launch_decode_prefix(const PrefixMaps& maps, const DecodeArgs& a, bool values, const LaunchCtx& ctx,
+                                 cudaStream_t st);
+
+// From api.cu: where a launch reports timeouts, and the tensor map of a [BH, N, D] bf16 tensor
+// (box 64 x 128 rows, 128-byte swizzle).
+ra_status_t launch_context(LaunchCtx* ctx);
+bool tensor_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int D);
 
 // Eviction by accumulated weight (evict.cu).
 struct EvictArgs {

@@ -243,7 +243,7 @@ def ra_attention_decode(q, k, v, length, *, prefix_k=None, prefix_v=None, scale=
         _check_tensor("weight", weight, (B, Hkv, C), torch.float32, device)
     L = lib()
     o = torch.empty_like(q)
-    ws = torch.empty(max(L.ra_attention_decode_workspace_size(B, Hq, Hkv, C, P, D), 16), dtype=torch.uint8,
+    ws = torch.empty(max(L.ra_attention_decode_workspace_size(B, Hq, Hkv, C, P, D, code), 16), dtype=torch.uint8,
                      device=device)
     with _on(device):
         _check("ra_attention_decode", L.ra_attention_decode(

@@ -93,6 +93,13 @@ CASES = [  # B, Hq, Hkv, C, P, D, sigma, lengths
     (40, 4, 2, 48, 600, 64, 1.0, list(range(40))),         # rows of many sequences against the prefix
     (1, 5, 5, 4999, 0, 64, 3.0, [4990]),
     (2, 2, 1, 16, 2, 128, 1.0, [-3, 99]),                  # lengths outside the cache
+    # the shared keys on the tensor cores (bf16, more than 32 rows per key head)
+    (33, 1, 1, 3, 1, 64, 1.0, [i % 4 for i in range(33)]),
+    (70, 8, 2, 20, 129, 128, 1.0, [i % 21 for i in range(70)]),        # 280 rows: a second row pair of 24
+    (100, 3, 1, 40, 2500, 128, 2.0, [i % 41 for i in range(100)]),     # three heads per key head, 300 rows
+    (128, 2, 2, 9, 1024, 64, 1.0, [i % 10 for i in range(128)]),       # exactly one row tile
+    (150, 4, 1, 5, 1000, 64, 3.0, [i % 6 for i in range(150)]),        # 600 rows
+    (36, 8, 8, 700, 2900, 128, 3.0, [700 - i for i in range(36)]),
 ]
 
 
@@ -179,6 +186,35 @@ def test_decode_repeats_streams_and_graphs_agree(dtype):
         torch.cuda.synchronize()
         for g, og, wg in graphs:
             assert torch.equal(og, ref[name][0]) and torch.equal(wg, ref[name][1])
+
+
+def test_decode_shared_keys_beyond_the_support():
+    """Row tiles whose every shared weight is 0 (a far larger own score), mixed with others."""
+    q, k, v, pk, pv = inputs(64, 4, 2, 6, 700, 128, torch.bfloat16, seed=25)
+    k[:32, :, 2] = q[:32, ::2] * 8                # own scores of about 90 for half of the heads
+    check_decode(q, k, v, [6] * 32 + [0] * 32, pk, pv)
+    k[:, :, 2] = (q[:, ::2] + q[:, 1::2]) * 8     # and for all rows of all sequences
+    o = check_decode(q, k, v, [6] * 64, pk, pv)
+    assert torch.isfinite(o.float()).all()
+
+
+def test_decode_wait_timeout_is_reported_and_the_context_survives():
+    q, k, v, pk, pv = inputs(40, 4, 2, 16, 300, 64, torch.bfloat16, seed=26)
+    args = [t.cuda() for t in (q, k, v)] + [torch.full((40,), 16, dtype=torch.int32, device="cuda")]
+    how = dict(prefix_k=pk.cuda(), prefix_v=pv.cuda())
+    assert ra.device_status() == "RA_OK"
+    ra.set_wait_limit_ns(2_000_000)
+    ra.debug_force_timeout(True)
+    try:
+        ra.ra_attention_decode(*args, **how)
+        torch.cuda.synchronize()
+        status = ra.device_status()
+    finally:
+        ra.debug_force_timeout(False)
+        ra.set_wait_limit_ns(0)
+    assert status == "RA_ERR_TIMEOUT"
+    check_decode(q, k, v, [16] * 40, pk, pv)
+    assert ra.device_status() == "RA_OK"
 
 
 def test_decode_refusals():

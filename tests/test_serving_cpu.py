@@ -77,11 +77,11 @@ def test_decode_validation(lib):
 
 def test_decode_workspace_size(lib):
     size = lib.ra_attention_decode_workspace_size
-    assert size(2, 4, 2, 16, 0, 64) > 0 and size(2, 3, 2, 16, 0, 64) == 0 and size(2, 4, 2, 0, 0, 64) == 0
-    assert size(8193, 4, 2, 16, 0, 64) == 0
+    assert size(2, 4, 2, 16, 0, 64, 1) > 0 and size(2, 3, 2, 16, 0, 64, 1) == 0 and size(2, 4, 2, 0, 0, 64, 1) == 0
+    assert size(8193, 4, 2, 16, 0, 64, 1) == 0
     # more keys never need less
-    assert size(2, 4, 2, 70000, 0, 64) >= size(2, 4, 2, 1000, 0, 64)
-    assert size(2, 4, 2, 1000, 70000, 64) >= size(2, 4, 2, 1000, 0, 64)
+    assert size(2, 4, 2, 70000, 0, 64, 1) >= size(2, 4, 2, 1000, 0, 64, 1)
+    assert size(2, 4, 2, 1000, 70000, 64, 1) >= size(2, 4, 2, 1000, 0, 64, 1)
 
 
 def _evict(lib, k=FAKE, ko=OTHER[0], vo=OTHER[1], v=OTHER[2], w=OTHER[3], wo=OTHER[4], n=OTHER[5], no=OTHER[6],
