@@ -9,37 +9,55 @@
 // phi(d + c) is no multiple of phi(d), so a running maximum cannot rescale what was summed
 // before it, as an exponential's can: the maximum comes first.  Three launches, each with its
 // work split over the keys:
-//   scores   the keys are read once; scores go to the workspace in fp32 (4 bytes per query head
-//            against the key's 2 D), with each item's maximum;
-//   values   phi from the scores and the final maximum; the values are read once, and not at
-//            all where every phi of a block is 0; partial sums (fp32) per item.  Sums need no
-//            rescaling: all items share one maximum;
+//   scores   the keys are read once; unscaled scores go to the workspace in fp32 (4 bytes per
+//            query head against the key's 2 D), with each part's maximum;
+//   values   phi from the scores and the final maximum; the values are read once; partial sums
+//            (fp32) per part.  Sums need no rescaling: all parts share one maximum;
 //   join     adds an output row's partial sums in a fixed order, and the weights.
-// An item is a range of keys for a block of up to 16 query rows that share them: the query
-// heads of a key head (own keys), or the whole batch's rows of a key head (shared keys).
-// Every CTA forms the list of items from the lengths by itself: no host copy of them is needed,
-// and a cache much larger than what it holds costs nothing.
+// The shared keys of many rows go to the tensor cores instead (decode_prefix_tc.cu).
 //
-// Bound: HBM, K and V once.  bf16: m16n8k16 products with rows as M; K fragments come
-// straight from global memory (a lane's 16-byte vector is the operand of two products, the
-// query's dimensions permuted alike), V fragments by interleaving two keys' vectors, so
-// neither passes through shared memory.  fp32: FFMA.
-#include "kernels.cuh"
+// The unit of work is a block of keys (kKeys) of one stream: a key head's own keys of one
+// sequence, or its shared keys, for a block of up to 16 query rows that read them.  All blocks of
+// all streams, in order, are cut into equal runs, one per warp of a grid that fills every SM
+// once, so a ragged batch loads all SMs alike however its lengths lie; a stream's part in a run is
+// one partial result.  Every CTA counts the blocks from the lengths by itself: no host copy of
+// them is needed, and a cache much larger than what it holds costs nothing.
+//
+// Each warp works alone, with no barrier beyond its own lanes: it streams its blocks through a
+// small ring in shared memory with asynchronous copies (which also zero the keys past a stream's
+// end, so that nothing in a cache's unused slots can reach a sum).  bf16: m16n8k16 products, query
+// rows as M; the chunks of a row are permuted in shared memory so that the 16-byte fragment reads
+// below meet no bank conflict.  fp32: FFMA.
+//
+// Bound: HBM, K and V once.
+#include "decode_split.cuh"
 
 namespace raattn {
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kRows = 16;        // query rows of an item
-constexpr int kBlock = 32;       // keys a warp takes at a time; score rows are padded to whole blocks
+constexpr int kThreads = kDecodeThreads, kWarps = kThreads / 32, kCtasPerSm = kDecodeCtasPerSm;
+constexpr int kRuns = kDecodeRuns, kRows = kDecodeRows;
+using Split = DecodeSplit;
 constexpr float kInf = __builtin_huge_valf();
 
-__device__ __forceinline__ float phi_fast(float d) {   // bf16 inputs: 2 ulp reciprocal, exact 1 at d = 0
+template <typename T, int D>
+struct Cfg {
+  static constexpr bool BF = sizeof(T) == 2;
+  static constexpr int kKeys = decode_block_keys(BF, D);
+  static constexpr int kChunks = D * static_cast<int>(sizeof(T)) / 16;   // of a key's or value's row
+  static constexpr int kBlockBytes = kKeys * kChunks * 16;
+  static constexpr int kStages = kBlockBytes >= 4096 ? 3 : 4;
+  static constexpr int kScoreStride = kKeys + 8;                         // floats of a row of scores in shared memory
+  static constexpr int kStageK = kBlockBytes;
+  static constexpr int kStageV = kBlockBytes + kRows * kScoreStride * 4;
+};
+
+__device__ __forceinline__ float phi_fast(float d) {   // bf16 inputs: 1 ulp reciprocal, exactly 1 at d = 0
   const float q = fmaxf(16.0f - d, 0.0f) * rcp_approx(16.0f + d);
   const float q2 = q * q, q4 = q2 * q2;
   return q4 * q4;
 }
-__device__ __forceinline__ float phi_exact(float d) {        // fp32 inputs: IEEE division
+__device__ __forceinline__ float phi_exact(float d) {   // fp32 inputs: IEEE division
   const float q = d < 16.0f ? (16.0f - d) / (16.0f + d) : 0.0f;
   const float q2 = q * q, q4 = q2 * q2;
   return q4 * q4;
@@ -49,20 +67,15 @@ __device__ __forceinline__ float phi_t(float d) {
   return sizeof(T) == 2 ? phi_fast(d) : phi_exact(d);
 }
 
-struct Item {
-  int first, last;      // keys [first, last)
-  int slot;             // its place among a row's partial results
-  int kv;               // key head
-  int b;                // sequence, or -1: shared keys
-  int row0, rows;       // rows of the block: within the head's G (own) or the batch's B G (shared)
-};
-
-// cum[b] = own chunks of the sequences before b, for b <= B.  All threads.
-__device__ void count_chunks(int* cum, const DecodeArgs& a) {
+// ---------------------------------------------------------------------------------------------
+// the split
+// ---------------------------------------------------------------------------------------------
+// cum[b] = own blocks per stream of the sequences before b, for b <= B.  All threads.
+__device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a) {
   __shared__ int sums[kWarps];
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
   int mine = 0;
-  for (int i = 0; i < per && b0 + i < a.B; ++i) mine += (decode_own_length(a, b0 + i) + a.chunk - 1) / a.chunk;
+  for (int i = 0; i < per && b0 + i < a.B; ++i) mine += (decode_own_length(a, b0 + i) + a.block - 1) / a.block;
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -75,71 +88,118 @@ __device__ void count_chunks(int* cum, const DecodeArgs& a) {
   int run = inc - mine;
   for (int i = 0; i < per && b0 + i < a.B; ++i) {
     cum[b0 + i] = run;
-    run += (decode_own_length(a, b0 + i) + a.chunk - 1) / a.chunk;
+    run += (decode_own_length(a, b0 + i) + a.block - 1) / a.block;
   }
   if (b0 < a.B && b0 + per >= a.B) cum[a.B] = run;
   __syncthreads();
+  return decode_split(a, cum[a.B]);
 }
 
-// Row blocks of the shared keys' items: none where the tensor cores take them.
-__device__ __forceinline__ int shared_blocks(const DecodeArgs& a) { return a.tc ? 0 : (a.B * a.G + kRows - 1) / kRows; }
+// A stream's part in a run.
+struct Part {
+  int first, count;    // blocks of the stream
+  int keys;            // keys of the stream
+  int slot;            // its place among a row's partial results
+  int kv, b;           // key head; sequence, or -1: shared keys
+  int row0, rows;      // rows: within the head's G (own) or the batch's B G (shared)
+};
 
-__device__ __forceinline__ int64_t item_count(const int* cum, const DecodeArgs& a) {
-  return static_cast<int64_t>(a.Hkv) * a.pchunks * shared_blocks(a) + static_cast<int64_t>(cum[a.B]) * a.Hkv * ((a.G + kRows - 1) / kRows);
-}
-
-// Item i: the shared keys' items first (a key range's row blocks together, so that they find it
-// in L2), then the sequences' in order.
-__device__ __forceinline__ Item get_item(int64_t i, const int* cum, const DecodeArgs& a) {
-  Item it;
-  const int blocks = shared_blocks(a);
-  const int64_t shared = static_cast<int64_t>(a.Hkv) * a.pchunks * blocks;
-  if (i < shared) {
-    const int rb = static_cast<int>(i % blocks), rest = static_cast<int>(i / blocks);
-    it.b = -1;
-    it.kv = rest % a.Hkv;
-    it.slot = rest / a.Hkv;
-    it.first = it.slot * a.pchunk;
-    it.last = min(it.first + a.pchunk, a.P);
-    it.row0 = rb * kRows;
-    it.rows = min(a.B * a.G - it.row0, kRows);
-    return it;
+__device__ __forceinline__ Part get_part(int64_t u, int64_t end, const int* cum, const Split& s, const DecodeArgs& a) {
+  Part p;
+  int64_t stream0;   // the stream's first block among all
+  int blocks;
+  if (u < s.own0) {
+    const int64_t st = u / a.pblocks;
+    const int rb = static_cast<int>(st % a.shared_rowblocks);
+    stream0 = st * a.pblocks;
+    blocks = a.pblocks;
+    p.kv = static_cast<int>(st / a.shared_rowblocks);
+    p.b = -1;
+    p.keys = a.P;
+    p.row0 = rb * kRows;
+    p.rows = min(a.B * a.G - p.row0, kRows);
+    p.slot = 0;
+  } else {
+    const int streams = a.Hkv * a.own_rowblocks;
+    const int64_t x = u - s.own0;
+    const int c = static_cast<int>(x / streams);
+    int lo = 0, hi = a.B - 1;   // the last b with cum[b] <= c: c lies in its blocks
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cum[mid] <= c) lo = mid; else hi = mid - 1;
+    }
+    blocks = cum[lo + 1] - cum[lo];
+    const int64_t seq0 = static_cast<int64_t>(cum[lo]) * streams;
+    const int st = static_cast<int>((x - seq0) / blocks);
+    stream0 = s.own0 + seq0 + static_cast<int64_t>(st) * blocks;
+    p.kv = st / a.own_rowblocks;
+    p.b = lo;
+    p.keys = decode_own_length(a, lo);
+    p.row0 = st % a.own_rowblocks * kRows;
+    p.rows = min(a.G - p.row0, kRows);
+    p.slot = a.pslots;
   }
-  i -= shared;
-  const int own_blocks = (a.G + kRows - 1) / kRows;
-  const int rb = static_cast<int>(i % own_blocks);
-  i /= own_blocks;
-  it.kv = static_cast<int>(i % a.Hkv);
-  const int c = static_cast<int>(i / a.Hkv);
-  int lo = 0, hi = a.B - 1;   // the last b with cum[b] <= c
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cum[mid] <= c) lo = mid; else hi = mid - 1;
-  }
-  it.b = lo;
-  const int k = c - cum[lo];
-  it.slot = a.pchunks + k;
-  it.first = k * a.chunk;
-  it.last = min(it.first + a.chunk, decode_own_length(a, lo));
-  it.row0 = rb * kRows;
-  it.rows = min(a.G - it.row0, kRows);
-  return it;
+  p.first = static_cast<int>(u - stream0);
+  p.count = static_cast<int>(min(static_cast<int64_t>(blocks - p.first), end - u));
+  p.slot += static_cast<int>(u / s.per - stream0 / s.per);
+  return p;
 }
 
-// Row r of an item as an index into [B, H_q].
-__device__ __forceinline__ int row_of(const Item& it, int r, const DecodeArgs& a) {
-  const int x = it.row0 + r;
-  if (it.b >= 0) return it.b * a.Hq + it.kv * a.G + x;
-  return x / a.G * a.Hq + it.kv * a.G + x % a.G;
+// Row r of a part as an index into [B, H_q].
+__device__ __forceinline__ int row_of(const Part& p, int r, const DecodeArgs& a) {
+  const int x = p.row0 + r;
+  if (p.b >= 0) return p.b * a.Hq + p.kv * a.G + x;
+  return x / a.G * a.Hq + p.kv * a.G + x % a.G;
 }
-__device__ __forceinline__ float* score_row(const Item& it, int row, const DecodeArgs& a) {
-  return it.b >= 0 ? a.s_own + static_cast<int64_t>(row) * a.own_width
-                   : a.s_pre + static_cast<int64_t>(row) * a.pre_width;
+__device__ __forceinline__ float* score_row(const Part& p, int row, const DecodeArgs& a) {
+  return p.b >= 0 ? a.s_own + static_cast<int64_t>(row) * a.own_width
+                  : a.s_pre + static_cast<int64_t>(row) * a.pre_width;
 }
-template <typename T>
-__device__ __forceinline__ const T* keys_of(const Item& it, const void* own, const void* pre, const DecodeArgs& a) {
-  return it.b >= 0 ? static_cast<const T*>(own) + (static_cast<int64_t>(it.b) * a.Hkv + it.kv) * a.C * a.D
-                   : static_cast<const T*>(pre) + static_cast<int64_t>(it.kv) * a.P * a.D;
+template <typename T, int D>
+__device__ __forceinline__ const char* stream_of(const Part& p, const void* own, const void* pre, const DecodeArgs& a) {
+  const T* x = p.b >= 0 ? static_cast<const T*>(own) + (static_cast<int64_t>(p.b) * a.Hkv + p.kv) * a.C * D
+                        : static_cast<const T*>(pre) + static_cast<int64_t>(p.kv) * a.P * D;
+  return reinterpret_cast<const char*>(x);
+}
+
+// ---------------------------------------------------------------------------------------------
+// asynchronous copies
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {   // zeros when not in
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where chunk c of row r of a block stands.  K16, V16: the bf16 fragment reads of eight lanes
+// (two keys by four chunks; four keys by two chunks); F32: eight keys by one chunk.
+enum Layout { K16, V16, F32 };
+template <Layout LAY, int CHUNKS>
+__device__ __forceinline__ int place(int r, int c) {
+  if (LAY == K16) return r * CHUNKS + (c ^ ((r & 1) << 2));
+  if (LAY == V16) return r * CHUNKS + (c ^ (((r >> 1) & 3) << 1));
+  return r * CHUNKS + (CHUNKS >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
+}
+
+// One block (keys first .. of a stream of `keys`) into a stage.
+template <int KEYS, int CHUNKS, Layout LAY>
+__device__ __forceinline__ void fetch_block(uint32_t stage, const char* stream, int first, int keys, int lane) {
+#pragma unroll
+  for (int i = 0; i < KEYS * CHUNKS / 32; ++i) {
+    const int x = i * 32 + lane, r = x / CHUNKS, c = x % CHUNKS, key = first + r;
+    const bool in = key < keys;
+    copy16(stage + place<LAY, CHUNKS>(r, c) * 16,
+           stream + (static_cast<int64_t>(in ? key : 0) * CHUNKS + c) * 16, in);
+  }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
+  return u;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -151,57 +211,58 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load_stream(const void* p) {   // read once: past L1
-  uint4 u;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p));
-  return u;
-}
-
 // ---------------------------------------------------------------------------------------------
 // scores
 // ---------------------------------------------------------------------------------------------
-// bf16.  Lane (g, t) = (lane / 4, lane % 4) loads, of key g of a block of eight, the vectors
-// t, t + 4, .. of its row: words 0, 1 of vector c are the B operand of product 2 c, words 2, 3 of
-// product 2 c + 1, and the query's vectors give the A operand in the same order.
+// bf16.  Lane (g, t) = (lane / 4, lane % 4) reads, of key g of a block of eight, the chunks t,
+// t + 4, .. of its row: words 0, 1 of chunk 4 c + t are the B operand of product 2 c, words 2, 3 of
+// product 2 c + 1, and the query's chunks give the A operand in the same order (any order of the
+// D products of a score is the score).
 template <int D>
-__device__ __forceinline__ void item_scores(const Item& it, const DecodeArgs& a, __nv_bfloat16*, float* smax) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  constexpr int NV = D / 32;   // vectors of a lane per key
-  const __nv_bfloat16* keys = keys_of<__nv_bfloat16>(it, a.k, a.pk, a);
+__device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, uint32_t ring, __nv_bfloat16*) {
+  using C = Cfg<__nv_bfloat16, D>;
+  constexpr int NV = D / 32;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const char* keys = stream_of<__nv_bfloat16, D>(p, a.k, a.pk, a);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    if (i < p.count)
+      fetch_block<C::kKeys, C::kChunks, K16>(ring + i * C::kStageK, keys, (p.first + i) * C::kKeys, p.keys, lane);
+    copy_commit();
+  }
   uint4 q0[NV], q1[NV];
-  const int r0 = row_of(it, min(g, it.rows - 1), a), r1 = row_of(it, min(g + 8, it.rows - 1), a);
+  const int r0 = row_of(p, min(g, p.rows - 1), a), r1 = row_of(p, min(g + 8, p.rows - 1), a);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     q0[c] = *reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r0) * D + c * 32 + t * 8);
     q1[c] = *reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r1) * D + c * 32 + t * 8);
   }
-  float* s0 = score_row(it, r0, a);
-  float* s1 = score_row(it, r1, a);
-  const bool w0 = g < it.rows, w1 = g + 8 < it.rows;
+  float* s0 = score_row(p, r0, a);
+  float* s1 = score_row(p, r1, a);
+  const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
   float m0 = -kInf, m1 = -kInf;
-  for (int k0 = it.first + warp * kBlock; k0 < it.last; k0 += kWarps * kBlock) {
-    uint4 kv[4][NV];
+  for (int i = 0; i < p.count; ++i) {
+    copy_wait<C::kStages - 2>();
+    __syncwarp();   // block i has landed for all lanes, and all have read block i - 1
+    const int ahead = i + C::kStages - 1;
+    if (ahead < p.count)
+      fetch_block<C::kKeys, C::kChunks, K16>(ring + ahead % C::kStages * C::kStageK, keys,
+                                             (p.first + ahead) * C::kKeys, p.keys, lane);
+    copy_commit();
+    const uint32_t stage = ring + i % C::kStages * C::kStageK;
 #pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
-      const int key = k0 + nb * 8 + g;
-      const __nv_bfloat16* p = keys + static_cast<int64_t>(key) * D + t * 8;
-#pragma unroll
-      for (int c = 0; c < NV; ++c) kv[nb][c] = key < it.last ? load_stream(p + c * 32) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb) {
+    for (int nb = 0; nb < C::kKeys / 8; ++nb) {
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        mma_bf16(s, q0[c].x, q1[c].x, q0[c].y, q1[c].y, kv[nb][c].x, kv[nb][c].y);
-        mma_bf16(s, q0[c].z, q1[c].z, q0[c].w, q1[c].w, kv[nb][c].z, kv[nb][c].w);
+        const uint4 x = lds128(stage + place<K16, C::kChunks>(nb * 8 + g, c * 4 + t) * 16);
+        mma_bf16(s, q0[c].x, q1[c].x, q0[c].y, q1[c].y, x.x, x.y);
+        mma_bf16(s, q0[c].z, q1[c].z, q0[c].w, q1[c].w, x.z, x.w);
       }
-      const int key = k0 + nb * 8 + 2 * t;
+      const int key = (p.first + i) * C::kKeys + nb * 8 + 2 * t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = key + (i & 1) < it.last ? s[i] : -kInf;
+      for (int e = 0; e < 4; ++e) s[e] = key + (e & 1) < p.keys ? s[e] : -kInf;
       m0 = fmaxf(m0, fmaxf(s[0], s[1]));
       m1 = fmaxf(m1, fmaxf(s[2], s[3]));
       if (w0) *reinterpret_cast<float2*>(s0 + key) = make_float2(s[0], s[1]);
@@ -213,154 +274,198 @@ __device__ __forceinline__ void item_scores(const Item& it, const DecodeArgs& a,
     m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
-  if (t == 0) {
-    smax[warp * kRows + g] = m0;
-    smax[warp * kRows + g + 8] = m1;
-  }
+  if (t == 0 && w0) a.row_max[static_cast<int64_t>(r0) * a.slots + p.slot] = m0;
+  if (t == 0 && w1) a.row_max[static_cast<int64_t>(r1) * a.slots + p.slot] = m1;
 }
 
-// fp32: a key across D / 4 lanes, the block's queries in shared memory.
+// fp32: 32 / kKeys lanes per key.
 template <int D>
-__device__ __forceinline__ void item_scores(const Item& it, const DecodeArgs& a, float*, float* smax) {
-  constexpr int L = D / 4, KS = kThreads / L;
-  __shared__ float4 qs[kRows][L];
-  const int gl = threadIdx.x % L, ks = threadIdx.x / L;
-  for (int i = threadIdx.x; i < it.rows * L; i += kThreads)
-    qs[i / L][i % L] = reinterpret_cast<const float4*>(
-        static_cast<const float*>(a.q) + static_cast<int64_t>(row_of(it, i / L, a)) * D)[i % L];
-  for (int i = threadIdx.x; i < kWarps * kRows; i += kThreads) smax[i] = -kInf;
-  __syncthreads();
-  const float* keys = keys_of<float>(it, a.k, a.pk, a);
-  const int end = it.first + (it.last - it.first + kBlock - 1) / kBlock * kBlock;   // whole blocks: -inf past the last
+__device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, uint32_t ring, float*) {
+  using C = Cfg<float, D>;
+  constexpr int PARTS = 32 / C::kKeys;
+  const int lane = threadIdx.x & 31, kk = lane / PARTS, part = lane % PARTS;
+  const char* keys = stream_of<float, D>(p, a.k, a.pk, a);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    if (i < p.count)
+      fetch_block<C::kKeys, C::kChunks, F32>(ring + i * C::kStageK, keys, (p.first + i) * C::kKeys, p.keys, lane);
+    copy_commit();
+  }
   float best[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) best[r] = -kInf;
-  for (int k0 = it.first; k0 < end; k0 += KS) {
-    const int key = k0 + ks;
-    const bool in = key < it.last;
-    const float4 kv = in ? reinterpret_cast<const float4*>(keys + static_cast<int64_t>(key) * D)[gl]
-                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = 0; i < p.count; ++i) {
+    copy_wait<C::kStages - 2>();
+    __syncwarp();
+    const int ahead = i + C::kStages - 1;
+    if (ahead < p.count)
+      fetch_block<C::kKeys, C::kChunks, F32>(ring + ahead % C::kStages * C::kStageK, keys,
+                                             (p.first + ahead) * C::kKeys, p.keys, lane);
+    copy_commit();
+    const uint32_t stage = ring + i % C::kStages * C::kStageK;
+    float4 kx[C::kChunks / PARTS];
+#pragma unroll
+    for (int c = 0; c < C::kChunks / PARTS; ++c) {
+      const uint4 u = lds128(stage + place<F32, C::kChunks>(kk, c * PARTS + part) * 16);
+      kx[c] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+    }
+    const int key = (p.first + i) * C::kKeys + kk;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      if (r < it.rows) {
-        const float4 q = qs[r][gl];
-        float s = fmaf(q.x, kv.x, fmaf(q.y, kv.y, fmaf(q.z, kv.z, q.w * kv.w)));
+      if (r < p.rows) {
+        const int row = row_of(p, r, a);
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + static_cast<int64_t>(row) * D);
+        float s = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s = in ? s : -kInf;
+        for (int c = 0; c < C::kChunks / PARTS; ++c) {
+          const float4 y = __ldg(q + c * PARTS + part);
+          s = fmaf(y.x, kx[c].x, fmaf(y.y, kx[c].y, s));
+          s2 = fmaf(y.z, kx[c].z, fmaf(y.w, kx[c].w, s2));
+        }
+        s += s2;
+#pragma unroll
+        for (int o = 1; o < PARTS; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s = key < p.keys ? s : -kInf;
         best[r] = fmaxf(best[r], s);
-        if (gl == 0 && key < end) score_row(it, row_of(it, r, a), a)[key] = s;
+        if (part == 0) score_row(p, row, a)[key] = s;
       }
     }
   }
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    float v = best[r];
+    if (r < p.rows) {
+      float v = best[r];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) smax[(threadIdx.x >> 5) * kRows + r] = v;
+      for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      if (lane == 0) a.row_max[static_cast<int64_t>(row_of(p, r, a)) * a.slots + p.slot] = v;
+    }
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_scores_kernel(const DecodeArgs a) {
-  extern __shared__ int cum[];
-  __shared__ float smax[kWarps * kRows];
-  count_chunks(cum, a);
-  const int64_t items = item_count(cum, a);
-  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-    const Item it = get_item(i, cum, a);
-    item_scores<D>(it, a, static_cast<T*>(nullptr), smax);
-    __syncthreads();
-    if (threadIdx.x < static_cast<unsigned>(it.rows)) {
-      float m = smax[threadIdx.x];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, smax[w * kRows + threadIdx.x]);
-      a.row_max[static_cast<int64_t>(row_of(it, threadIdx.x, a)) * a.slots + it.slot] = m;
-    }
-    __syncthreads();
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(const DecodeArgs a) {
+  extern __shared__ uint4 dyn[];
+  int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * Cfg<T, D>::kStages * Cfg<T, D>::kStageK);
+  const uint32_t ring = smem_u32(dyn) + (threadIdx.x >> 5) * Cfg<T, D>::kStages * Cfg<T, D>::kStageK;
+  const Split s = make_split(cum, a);
+  if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
+    for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
+  }
+  // runs go to the CTAs in turn, so that few runs spread over the SMs
+  const int64_t run = (threadIdx.x >> 5) * static_cast<int64_t>(gridDim.x) + blockIdx.x;
+  const int64_t end = min((run + 1) * s.per, s.total);
+  for (int64_t u = run * s.per; u < end;) {
+    const Part p = get_part(u, end, cum, s, a);
+    part_scores<D>(p, a, ring, static_cast<T*>(nullptr));
+    u += p.count;
+    __syncwarp();   // the ring is free
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------------------------
-// A row's maximum over its shared and own items.  A whole warp.
-__device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row) {
+// A row's values v[] over its slots, folded by f over four lanes (lane % 4).
+template <typename F>
+__device__ __forceinline__ float fold_slots(const float* v, int shared, int own, int pslots, int t, float x, F f) {
+  for (int i = t; i < shared; i += 4) x = f(x, v[i]);
+  for (int i = t; i < own; i += 4) x = f(x, v[pslots + i]);
+  x = f(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return f(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float row_maximum(int row, const int* cum, const Split& s, const DecodeArgs& a, int t) {
   const int b = row / a.Hq;
-  const int n = a.pchunks + (decode_own_length(a, b) + a.chunk - 1) / a.chunk;
-  float m = -kInf;
-  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.row_max[static_cast<int64_t>(row) * a.slots + i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  int shared, own;
+  decode_row_slots(row, cum[b], cum[b + 1], s, a, shared, own);
+  return fold_slots(a.row_max + static_cast<int64_t>(row) * a.slots, shared, own, a.pslots, t, -kInf,
+                    [](float x, float y) { return fmaxf(x, y); });
 }
 
-// bf16.  Lane (g, t) loads, of keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of sixteen, the dimensions
+// A block of values and its scores into a stage.
+template <typename T, int D, Layout LAY>
+__device__ __forceinline__ void fetch_values(uint32_t stage, const char* vals, const Part& p, int i, const DecodeArgs& a,
+                                             int lane) {
+  using C = Cfg<T, D>;
+  const int first = (p.first + i) * C::kKeys;
+  fetch_block<C::kKeys, C::kChunks, LAY>(stage, vals, first, p.keys, lane);
+  constexpr int PIECES = C::kKeys / 4;   // 16-byte pieces of a row of scores
+#pragma unroll
+  for (int j = 0; j < (kRows * PIECES + 31) / 32; ++j) {
+    const int x = j * 32 + lane, r = x / PIECES, c = x % PIECES;
+    if (r < p.rows)
+      copy16(stage + C::kBlockBytes + (r * C::kScoreStride + c * 4) * 4,
+             score_row(p, row_of(p, r, a), a) + first + c * 4, true);
+  }
+}
+
+// bf16.  Lane (g, t) reads, of keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of sixteen, the dimensions
 // 8 g .. 8 g + 7 of every 64: words of two keys, interleaved, are the B operand of the product
-// whose column g stands for dimension 8 g + j.  phi of scores at the same keys is the A operand.
+// whose column g stands for dimension 8 g + j.  phi of the scores at the same keys is the A operand.
 template <int D>
-__device__ __forceinline__ void item_values(const Item& it, const DecodeArgs& a, __nv_bfloat16*, const float* rowm,
-                                            float* sums, float* acc_s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
+                                            uint32_t ring, const char* ring_ptr, __nv_bfloat16*) {
+  using C = Cfg<__nv_bfloat16, D>;
   constexpr int NC = D / 64;
-  const __nv_bfloat16* vals = keys_of<__nv_bfloat16>(it, a.v, a.pv, a);
-  const bool w0 = g < it.rows, w1 = g + 8 < it.rows;
-  const float* s0 = score_row(it, row_of(it, min(g, it.rows - 1), a), a);
-  const float* s1 = score_row(it, row_of(it, min(g + 8, it.rows - 1), a), a);
-  const float m0 = rowm[g], m1 = rowm[g + 8];
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const char* vals = stream_of<__nv_bfloat16, D>(p, a.v, a.pv, a);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    if (i < p.count) fetch_values<__nv_bfloat16, D, V16>(ring + i * C::kStageV, vals, p, i, a, lane);
+    copy_commit();
+  }
+  const bool w0 = g < p.rows, w1 = g + 8 < p.rows, upper = p.rows > 8;
+  const int r0 = row_of(p, min(g, p.rows - 1), a), r1 = row_of(p, min(g + 8, p.rows - 1), a);
+  const float m0 = row_maximum(r0, cum, s, a, t), m1 = upper ? row_maximum(r1, cum, s, a, t) : 0.0f;
   float acc[NC][8][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[c][j][0] = acc[c][j][1] = acc[c][j][2] = acc[c][j][3] = 0.0f;
   float t0 = 0.0f, t1 = 0.0f;
-  for (int k0 = it.first + warp * kBlock; k0 < it.last; k0 += kWarps * kBlock) {
-    uint32_t p[2][4];
-    bool live = false;
+  for (int i = 0; i < p.count; ++i) {
+    copy_wait<C::kStages - 2>();
+    __syncwarp();
+    const int ahead = i + C::kStages - 1;
+    if (ahead < p.count)
+      fetch_values<__nv_bfloat16, D, V16>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
+    copy_commit();
+    const uint32_t stage = ring + i % C::kStages * C::kStageV;
+    const float* sc = reinterpret_cast<const float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    float live = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = k0 + h * 16 + e * 8 + 2 * t;
-        float2 x = w0 ? *reinterpret_cast<const float2*>(s0 + key) : make_float2(-kInf, -kInf);
-        float2 y = w1 ? *reinterpret_cast<const float2*>(s1 + key) : make_float2(-kInf, -kInf);
-        x.x = phi_fast((m0 - x.x) * a.scale);
-        x.y = phi_fast((m0 - x.y) * a.scale);
-        y.x = phi_fast((m1 - y.x) * a.scale);
-        y.y = phi_fast((m1 - y.y) * a.scale);
-        t0 += x.x + x.y;
-        t1 += y.x + y.y;
-        live |= x.x > 0.0f || x.y > 0.0f || y.x > 0.0f || y.y > 0.0f;
-        // V is bf16, so phi goes into the product as bf16: 2^-8 relative at most per weight,
-        // like the rounding of the output; the sums above keep all 32 bits
-        p[h][2 * e] = pack_bf16x2(x.x, x.y);
-        p[h][2 * e + 1] = pack_bf16x2(y.x, y.y);
+    for (int e = 0; e < 2; ++e) {
+      // V is bf16, so phi goes into the product as bf16: 2^-8 relative at most per weight, like the
+      // rounding of the output; the sums keep all 32 bits.  Scores past the last key are -inf.
+      if (w0) {
+        const float2 x = *reinterpret_cast<const float2*>(sc + g * C::kScoreStride + e * 8 + 2 * t);
+        const float f0 = phi_fast((m0 - x.x) * a.scale), f1 = phi_fast((m0 - x.y) * a.scale);
+        t0 += f0 + f1;
+        live += f0 + f1;
+        w[2 * e] = pack_bf16x2(f0, f1);
+      }
+      if (w1) {
+        const float2 x = *reinterpret_cast<const float2*>(sc + (g + 8) * C::kScoreStride + e * 8 + 2 * t);
+        const float f0 = phi_fast((m1 - x.x) * a.scale), f1 = phi_fast((m1 - x.y) * a.scale);
+        t1 += f0 + f1;
+        live += f0 + f1;
+        w[2 * e + 1] = pack_bf16x2(f0, f1);
       }
     }
-    if (!__any_sync(0xffffffffu, live)) continue;
+    if (!__any_sync(0xffffffffu, live > 0.0f)) continue;   // every weight is exactly 0
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 v[4][NC];
+    for (int c = 0; c < NC; ++c) {
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = k0 + h * 16 + (i >> 1) * 8 + 2 * t + (i & 1);
-        const __nv_bfloat16* src = vals + static_cast<int64_t>(key) * D + g * 8;
+      for (int e = 0; e < 4; ++e)
+        v[e] = lds128(stage + place<V16, C::kChunks>((e >> 1) * 8 + 2 * t + (e & 1), c * 8 + g) * 16);
+      const uint32_t x0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, x1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+      const uint32_t x2[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, x3[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
-        for (int c = 0; c < NC; ++c) v[i][c] = key < it.last ? load_stream(src + c * 64) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const uint32_t x0[4] = {v[0][c].x, v[0][c].y, v[0][c].z, v[0][c].w};
-        const uint32_t x1[4] = {v[1][c].x, v[1][c].y, v[1][c].z, v[1][c].w};
-        const uint32_t x2[4] = {v[2][c].x, v[2][c].y, v[2][c].z, v[2][c].w};
-        const uint32_t x3[4] = {v[3][c].x, v[3][c].y, v[3][c].z, v[3][c].w};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-          mma_bf16(acc[c][j], p[h][0], p[h][1], p[h][2], p[h][3], __byte_perm(x0[j >> 1], x1[j >> 1], sel),
-                   __byte_perm(x2[j >> 1], x3[j >> 1], sel));
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+        mma_bf16(acc[c][j], w[0], w[1], w[2], w[3], __byte_perm(x0[j >> 1], x1[j >> 1], sel),
+                 __byte_perm(x2[j >> 1], x3[j >> 1], sel));
       }
     }
   }
@@ -369,58 +474,75 @@ __device__ __forceinline__ void item_values(const Item& it, const DecodeArgs& a,
     t0 += __shfl_xor_sync(0xffffffffu, t0, o);
     t1 += __shfl_xor_sync(0xffffffffu, t1, o);
   }
-  if (t == 0) {
-    sums[warp * kRows + g] = t0;
-    sums[warp * kRows + g + 8] = t1;
-  }
+  const int64_t at0 = static_cast<int64_t>(r0) * a.slots + p.slot, at1 = static_cast<int64_t>(r1) * a.slots + p.slot;
+  if (t == 0 && w0) a.part_sum[at0] = t0;
+  if (t == 0 && w1) a.part_sum[at1] = t1;
   // accumulator columns 2 t, 2 t + 1 stand for dimensions 16 t + j and 16 t + 8 + j
-  float* out = acc_s + warp * kRows * D;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int j = 0; j < 8; j += 4)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float4*>(out + (g + (e >> 1) * 8) * D + c * 64 + t * 16 + (e & 1) * 8 + j) =
-            make_float4(acc[c][j][e], acc[c][j + 1][e], acc[c][j + 2][e], acc[c][j + 3][e]);
+        if (e < 2 ? w0 : w1)
+          *reinterpret_cast<float4*>(a.part_o + (e < 2 ? at0 : at1) * D + c * 64 + t * 16 + (e & 1) * 8 + j) =
+              make_float4(acc[c][j][e], acc[c][j + 1][e], acc[c][j + 2][e], acc[c][j + 3][e]);
 }
 
-// fp32: D / 4 lanes across the dimensions; each of the kThreads / (D / 4) lane groups takes every
-// so many keys of a tile whose phi stands in shared memory.
+// fp32: D / 4 lanes across the dimensions, the other lanes over the keys; phi replaces the scores in
+// shared memory.
 template <int D>
-__device__ __forceinline__ void item_values(const Item& it, const DecodeArgs& a, float*, const float* rowm,
-                                            float* sums, float* acc_s) {
-  constexpr int L = D / 4, KS = kThreads / L, TK = 64;
-  __shared__ float ph[kRows][TK];
-  const int gl = threadIdx.x % L, ks = threadIdx.x / L;
-  const float* vals = keys_of<float>(it, a.v, a.pv, a);
+__device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
+                                            uint32_t ring, const char* ring_ptr, float*) {
+  using C = Cfg<float, D>;
+  constexpr int L = D / 4, KS = 32 / L;
+  const int lane = threadIdx.x & 31, gl = lane % L, ks = lane / L;
+  const char* vals = stream_of<float, D>(p, a.v, a.pv, a);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    if (i < p.count) fetch_values<float, D, F32>(ring + i * C::kStageV, vals, p, i, a, lane);
+    copy_commit();
+  }
+  // four lanes per row for phi: lane (g, t) takes rows g and g + 8, keys t, t + 4, ..
+  const int g = lane >> 2, t = lane & 3;
+  const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
+  const float m0 = row_maximum(row_of(p, min(g, p.rows - 1), a), cum, s, a, t);
+  const float m1 = row_maximum(row_of(p, min(g + 8, p.rows - 1), a), cum, s, a, t);
   float acc[kRows][4];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float tot[kRows / kWarps] = {};
-  for (int k0 = it.first; k0 < it.last; k0 += TK) {
-    __syncthreads();
+  float t0 = 0.0f, t1 = 0.0f;
+  for (int i = 0; i < p.count; ++i) {
+    copy_wait<C::kStages - 2>();
+    __syncwarp();
+    const int ahead = i + C::kStages - 1;
+    if (ahead < p.count) fetch_values<float, D, F32>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
+    copy_commit();
+    const uint32_t stage = ring + i % C::kStages * C::kStageV;
+    float* sc = reinterpret_cast<float*>(const_cast<char*>(ring_ptr) + i % C::kStages * C::kStageV + C::kBlockBytes);
 #pragma unroll
-    for (int rr = 0; rr < kRows / kWarps; ++rr) {
-      const int r = warp + rr * kWarps;
-      if (r < it.rows) {
-        const float* s = score_row(it, row_of(it, r, a), a);
-        for (int i = lane; i < TK; i += 32) {
-          const float f = k0 + i < it.last ? phi_exact((rowm[r] - s[k0 + i]) * a.scale) : 0.0f;
-          ph[r][i] = f;
-          tot[rr] += f;
-        }
+    for (int k = 0; k < C::kKeys; k += 4) {
+      if (w0) {
+        float& x = sc[g * C::kScoreStride + k + t];
+        x = phi_exact((m0 - x) * a.scale);
+        t0 += x;
+      }
+      if (w1) {
+        float& x = sc[(g + 8) * C::kScoreStride + k + t];
+        x = phi_exact((m1 - x) * a.scale);
+        t1 += x;
       }
     }
-    __syncthreads();
-    const int n = min(TK, it.last - k0);
-    for (int i = ks; i < n; i += KS) {
-      const float4 v = reinterpret_cast<const float4*>(vals + static_cast<int64_t>(k0 + i) * D)[gl];
+    __syncwarp();
+#pragma unroll 2
+    for (int kk = ks; kk < C::kKeys; kk += KS) {
+      const uint4 u = lds128(stage + place<F32, C::kChunks>(kk, gl) * 16);
+      const float4 v = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                   __uint_as_float(u.w));
 #pragma unroll
       for (int r = 0; r < kRows; ++r)
-        if (r < it.rows) {
-          const float f = ph[r][i];
+        if (r < p.rows) {
+          const float f = sc[r * C::kScoreStride + kk];
           acc[r][0] = fmaf(f, v.x, acc[r][0]);
           acc[r][1] = fmaf(f, v.y, acc[r][1]);
           acc[r][2] = fmaf(f, v.z, acc[r][2]);
@@ -429,121 +551,78 @@ __device__ __forceinline__ void item_values(const Item& it, const DecodeArgs& a,
     }
   }
 #pragma unroll
-  for (int rr = 0; rr < kRows / kWarps; ++rr) {
-    float f = tot[rr];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-    if (lane < kWarps) sums[lane * kRows + warp + rr * kWarps] = lane == 0 ? f : 0.0f;
+  for (int o = 1; o < 4; o <<= 1) {
+    t0 += __shfl_xor_sync(0xffffffffu, t0, o);
+    t1 += __shfl_xor_sync(0xffffffffu, t1, o);
   }
-  // lane groups of one warp first, so that kWarps partial sums remain
+  if (t == 0 && w0) a.part_sum[static_cast<int64_t>(row_of(p, g, a)) * a.slots + p.slot] = t0;
+  if (t == 0 && w1) a.part_sum[static_cast<int64_t>(row_of(p, g + 8, a)) * a.slots + p.slot] = t1;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
+  for (int r = 0; r < kRows; ++r) {
+    if (r < p.rows) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float f = acc[r][e];
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int o = L; o < 32; o <<= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-      if (lane < L) acc_s[(warp * kRows + r) * D + gl * 4 + e] = f;
+        for (int o = L; o < 32; o <<= 1) acc[r][e] += __shfl_xor_sync(0xffffffffu, acc[r][e], o);
+      if (ks == 0)
+        reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, r, a)) * a.slots + p.slot) * D)[gl] =
+            make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
     }
+  }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_values_kernel(const DecodeArgs a) {
-  extern __shared__ float4 dyn4[];
-  float* acc_s = reinterpret_cast<float*>(dyn4);                    // [kWarps][kRows][D]
-  int* cum = reinterpret_cast<int*>(acc_s + kWarps * kRows * D);
-  __shared__ float rowm[kRows], sums[kWarps * kRows];
-  __shared__ int live;
-  count_chunks(cum, a);
-  const int64_t items = item_count(cum, a);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-    const Item it = get_item(i, cum, a);
-    if (threadIdx.x == 0) live = 0;
-    __syncthreads();
-    for (int r = warp; r < kRows; r += kWarps) {
-      if (r < it.rows) {
-        const int row = row_of(it, r, a);
-        const float m = row_maximum(a, row);
-        if (lane == 0) {
-          rowm[r] = m;
-          if ((m - a.row_max[static_cast<int64_t>(row) * a.slots + it.slot]) * a.scale < 16.0f) live = 1;
-        }
-      } else if (lane == 0) {
-        rowm[r] = 0.0f;
-      }
-    }
-    __syncthreads();
-    if (!live) {   // every phi of the item is 0
-      if (threadIdx.x < static_cast<unsigned>(it.rows))
-        a.part_sum[static_cast<int64_t>(row_of(it, threadIdx.x, a)) * a.slots + it.slot] = 0.0f;
-      __syncthreads();
-      continue;
-    }
-    item_values<D>(it, a, static_cast<T*>(nullptr), rowm, sums, acc_s);
-    __syncthreads();
-    if (threadIdx.x < static_cast<unsigned>(it.rows)) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sums[w * kRows + threadIdx.x];
-      a.part_sum[static_cast<int64_t>(row_of(it, threadIdx.x, a)) * a.slots + it.slot] = s;
-    }
-    for (int e = threadIdx.x; e < it.rows * (D / 4); e += kThreads) {
-      const int r = e / (D / 4), c = e % (D / 4);
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 x = reinterpret_cast<const float4*>(acc_s + (w * kRows + r) * D)[c];
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
-      }
-      reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(it, r, a)) * a.slots + it.slot) * D)[c] = s;
-    }
-    __syncthreads();
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(const DecodeArgs a) {
+  extern __shared__ uint4 dyn[];
+  constexpr int kRing = Cfg<T, D>::kStages * Cfg<T, D>::kStageV;
+  int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
+  const char* ring_ptr = reinterpret_cast<const char*>(dyn) + (threadIdx.x >> 5) * kRing;
+  const Split s = make_split(cum, a);
+  const int64_t run = (threadIdx.x >> 5) * static_cast<int64_t>(gridDim.x) + blockIdx.x;
+  const int64_t end = min((run + 1) * s.per, s.total);
+  for (int64_t u = run * s.per; u < end;) {
+    const Part p = get_part(u, end, cum, s, a);
+    part_values<D>(p, a, s, cum, smem_u32(ring_ptr), ring_ptr, static_cast<T*>(nullptr));
+    u += p.count;
+    __syncwarp();
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 // join
 // ---------------------------------------------------------------------------------------------
-// A row's sum of phi over its items, in a fixed order.  A whole warp.
-__device__ __forceinline__ float row_total(const DecodeArgs& a, int row) {
-  const int b = row / a.Hq;
-  const int n = a.pchunks + (decode_own_length(a, b) + a.chunk - 1) / a.chunk;
-  float s = 0.0f;
-  for (int i = threadIdx.x & 31; i < n; i += 32) s += a.part_sum[static_cast<int64_t>(row) * a.slots + i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-constexpr int kWeightKeys = 1024;   // keys of a weight CTA
+constexpr int kWeightKeys = 8 * kThreads;   // keys of a weight CTA
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+  const Split sp = decode_split(a, a.cum[a.B]);   // the counts that the scores kernel left
   if (blockIdx.x < rows) {   // one output row
     constexpr int L = D / 4, KS = kThreads / L;
     __shared__ float4 part[KS][L];
+    __shared__ float sums[KS];
     const int row = blockIdx.x, b = row / a.Hq;
-    const int n = a.pchunks + (decode_own_length(a, b) + a.chunk - 1) / a.chunk;
-    const float total = row_total(a, row);
+    int shared, own;
+    decode_row_slots(row, a.cum[b], a.cum[b + 1], sp, a, shared, own);
     const int gl = threadIdx.x % L, ks = threadIdx.x / L;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = ks; i < n; i += KS) {
-      const int64_t at = static_cast<int64_t>(row) * a.slots + i;
-      if (a.part_sum[at] > 0.0f) {   // 0: the item was skipped and wrote no partial output
-        const float4 x = reinterpret_cast<const float4*>(a.part_o + at * D)[gl];
+    float total = 0.0f;
+#pragma unroll 4
+    for (int i = ks; i < shared + own; i += KS) {
+      const int64_t at = static_cast<int64_t>(row) * a.slots + (i < shared ? i : a.pslots + i - shared);
+      const float f = a.part_sum[at];
+      const float4 x = reinterpret_cast<const float4*>(a.part_o + at * D)[gl];
+      if (f > 0.0f) {   // a part whose weights are all 0 may have written no output
         s.x += x.x;
         s.y += x.y;
         s.z += x.z;
         s.w += x.w;
+        total += f;
       }
     }
     part[ks][gl] = s;
+    if (gl == 0) sums[ks] = total;
     __syncthreads();
     if (ks == 0) {
 #pragma unroll
@@ -553,6 +632,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
         s.y += x.y;
         s.z += x.z;
         s.w += x.w;
+        total += sums[i];
       }
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // no key at all: zeros
       T* o = static_cast<T*>(a.o) + static_cast<int64_t>(row) * D + gl * 4;
@@ -565,46 +645,61 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     return;
   }
   // weights of kWeightKeys keys of one (sequence, key head)
-  extern __shared__ float2 ms[];   // [G] maximum and 1 / sum
+  extern __shared__ float2 stat[];   // [G] maximum, 1 / sum
   const int splits = (a.C + kWeightKeys - 1) / kWeightKeys;
   const int64_t x = blockIdx.x - rows;
   const int split = static_cast<int>(x % splits);
   const int bk = static_cast<int>(x / splits), b = bk / a.Hkv, kv = bk - b * a.Hkv;
-  const int first = split * kWeightKeys, last = min(first + kWeightKeys, decode_own_length(a, b));
-  if (first >= last) return;
-  for (int g = warp; g < a.G; g += kWarps) {
-    const int row = b * a.Hq + kv * a.G + g;
-    const float m = row_maximum(a, row), s = row_total(a, row);
-    if (lane == 0) ms[g] = make_float2(m, s);
+  const int first = split * kWeightKeys + threadIdx.x, last = decode_own_length(a, b);
+  if (split * kWeightKeys >= last) return;
+  for (int g = warp * 8 + (lane >> 2); g < (a.G + 7) / 8 * 8; g += kWarps * 8) {   // four lanes per row
+    const int row = b * a.Hq + kv * a.G + min(g, a.G - 1);
+    int shared, own;
+    decode_row_slots(row, a.cum[b], a.cum[b + 1], sp, a, shared, own);
+    const int64_t at = static_cast<int64_t>(row) * a.slots;
+    const float m = fold_slots(a.row_max + at, shared, own, a.pslots, lane & 3, -kInf,
+                               [](float u, float v) { return fmaxf(u, v); });
+    const float s = fold_slots(a.part_sum + at, shared, own, a.pslots, lane & 3, 0.0f,
+                               [](float u, float v) { return u + v; });
+    if ((lane & 3) == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / s);
   }
   __syncthreads();
-  float* w = a.weight + static_cast<int64_t>(bk) * a.C;
-  for (int key = first + threadIdx.x; key < last; key += kThreads) {
-    float sum = 0.0f;
-    for (int g = 0; g < a.G; ++g) {
-      const float s = a.s_own[(static_cast<int64_t>(b) * a.Hq + kv * a.G + g) * a.own_width + key];
-      sum += phi_t<T>((ms[g].x - s) * a.scale) / ms[g].y;
+  const float* sc = a.s_own + (static_cast<int64_t>(b) * a.Hq + kv * a.G) * a.own_width;
+  float sum[8] = {};
+#pragma unroll 2
+  for (int g = 0; g < a.G; ++g) {
+    const float2 ms = stat[g];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int key = first + i * kThreads;
+      const float s = key < last ? sc[static_cast<int64_t>(g) * a.own_width + key] : -kInf;
+      sum[i] = fmaf(phi_t<T>((ms.x - s) * a.scale), ms.y, sum[i]);
     }
-    w[key] += sum;
   }
+  float* w = a.weight + static_cast<int64_t>(bk) * a.C;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (first + i * kThreads < last) w[first + i * kThreads] += sum[i];
 }
 
 template <typename T, int D>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
+  using C = Cfg<T, D>;
   const int cum = (a.B + 1) * 4;
-  const int smem_values = kWarps * kRows * D * 4 + cum;
-  cudaError_t e = cudaSuccess;
-  if (smem_values > 40 * 1024) {   // many sequences: 32 KB of partial sums and up to 32 KB of chunk counts
+  const int smem_scores = kWarps * C::kStages * C::kStageK + cum;
+  const int smem_values = kWarps * C::kStages * C::kStageV + cum;
+  cudaError_t e = cudaFuncSetAttribute(decode_scores_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_scores);
+  if (e == cudaSuccess)
     e = cudaFuncSetAttribute(decode_values_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_values);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t shared = a.tc ? 0 : static_cast<int64_t>(a.Hkv) * a.pchunks * ((a.B * a.G + kRows - 1) / kRows);
-  const int64_t own = static_cast<int64_t>(a.B) * ((a.C + a.chunk - 1) / a.chunk) * a.Hkv *
-                      ((a.G + kRows - 1) / kRows);
-  const int64_t most = shared + own;
-  const int grid = static_cast<int>(most < 3 * kSms ? most : 3 * kSms);
+  if (e != cudaSuccess) return e;
+  // CTAs for the runs that there can be (each has one run per warp)
+  const int64_t most = (a.tc ? 0 : static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks) +
+                       static_cast<int64_t>(a.B) * (a.own_width / a.block) * a.Hkv * a.own_rowblocks;
+  const int64_t runs = (most + a.min_run - 1) / a.min_run;
+  const int grid = static_cast<int>(runs < kSms * kCtasPerSm ? runs : kSms * kCtasPerSm);
   if (a.tc && (e = launch_decode_prefix(maps, a, false, ctx, st)) != cudaSuccess) return e;
-  decode_scores_kernel<T, D><<<grid, kThreads, cum, st>>>(a);
+  decode_scores_kernel<T, D><<<grid, kThreads, smem_scores, st>>>(a);
   if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
   decode_values_kernel<T, D><<<grid, kThreads, smem_values, st>>>(a);
   const int64_t join = static_cast<int64_t>(a.B) * a.Hq +
@@ -615,42 +710,51 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
 
 }  // namespace
 
-// The split of the keys.  Own items of 256 keys, or of 128 where that would leave SMs without an
-// item.  Shared keys of more than kTcRows rows per key head go to the tensor cores, in whole
-// tiles of 128, split so that one wave of CTAs takes them; otherwise in as many items as give
-// every SM three, of at least 128 keys.
+// The split of the keys.  Shared keys of more than kTcRows rows per key head go to the tensor
+// cores, in whole tiles of 128, split so that one wave of CTAs takes them.  Everything else is
+// cut into runs of equal length, at least min_run blocks: two where all runs could not be longer
+// anyway (latency), eight otherwise, which bounds the partial results of a long stream.
 constexpr int64_t kTcRows = 32;
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
   a->G = a->Hq / a->Hkv;
+  a->block = decode_block_keys(bf16, a->D);
   const int64_t shared_rows = static_cast<int64_t>(a->B) * a->G;
-  const int64_t own_blocks = (a->G + kRows - 1) / kRows;
-  a->chunk = static_cast<int64_t>(a->B) * a->Hkv * own_blocks * ((a->C + 255) / 256) < 2 * kSms ? 128 : 256;
-  const int own = (a->C + a->chunk - 1) / a->chunk;
-  a->own_width = own * a->chunk;
-  a->pchunk = a->pchunks = a->pre_width = 0;
+  a->own_rowblocks = (a->G + kRows - 1) / kRows;
+  a->shared_rowblocks = static_cast<int>((shared_rows + kRows - 1) / kRows);
+  const int own = (a->C + a->block - 1) / a->block;
+  a->own_width = own * a->block;
   a->tc = bf16 && a->P > 0 && shared_rows > kTcRows;
-  if (a->P > 0) {
-    const int64_t per = a->Hkv * (a->tc ? (shared_rows + 255) / 256 : (shared_rows + kRows - 1) / kRows);
-    const int64_t tiles = (a->P + 127) / 128;
-    int64_t n = a->tc ? kSms / per : (3 * kSms + per - 1) / per;
+  a->pblocks = a->tc ? 0 : (a->P + a->block - 1) / a->block;
+  a->pre_width = a->pblocks * a->block;
+  const int64_t total = static_cast<int64_t>(a->B) * own * a->Hkv * a->own_rowblocks +
+                        static_cast<int64_t>(a->pblocks) * a->Hkv * a->shared_rowblocks;
+  const int64_t even = total / kRuns;
+  a->min_run = static_cast<int>(even < 2 ? 2 : even > 8 ? 8 : even);
+  a->pchunk = a->pslots = 0;
+  if (a->tc) {
+    const int64_t per = a->Hkv * ((shared_rows + 255) / 256), tiles = (a->P + 127) / 128;
+    int64_t n = kSms / per;
     n = n < 1 ? 1 : n > tiles ? tiles : n;
     a->pchunk = static_cast<int>((tiles + n - 1) / n * 128);
-    a->pchunks = (a->P + a->pchunk - 1) / a->pchunk;
-    a->pre_width = a->tc ? 0 : a->pchunks * a->pchunk;
+    a->pslots = (a->P + a->pchunk - 1) / a->pchunk;
+  } else if (a->P > 0) {
+    a->pslots = (a->pblocks + a->min_run - 1) / a->min_run + 1;
   }
-  a->slots = a->pchunks + own;
+  // a stream of n blocks meets at most ceil(n / run) + 1 runs
+  a->slots = a->pslots + (own + a->min_run - 1) / a->min_run + 1;
   size_t at = 0;
   auto piece = [&](int64_t floats) {
-    float* p = reinterpret_cast<float*>(base + at);
+    char* p = base + at;
     at += (static_cast<size_t>(floats) * 4 + 255) & ~static_cast<size_t>(255);
     return p;
   };
-  a->s_own = piece(rows * a->own_width);
-  a->s_pre = piece(rows * a->pre_width);
-  a->row_max = piece(rows * a->slots);
-  a->part_sum = piece(rows * a->slots);
-  a->part_o = piece(rows * a->slots * a->D);
+  a->s_own = reinterpret_cast<float*>(piece(rows * a->own_width));
+  a->s_pre = reinterpret_cast<float*>(piece(rows * a->pre_width));
+  a->row_max = reinterpret_cast<float*>(piece(rows * a->slots));
+  a->part_sum = reinterpret_cast<float*>(piece(rows * a->slots));
+  a->part_o = reinterpret_cast<float*>(piece(rows * a->slots * a->D));
+  a->cum = reinterpret_cast<int*>(piece(a->B + 1));
   return at;
 }
 

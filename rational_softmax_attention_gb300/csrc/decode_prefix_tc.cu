@@ -18,7 +18,7 @@
 // rows are G at a time in memory) into the 128-byte-swizzled operand layout.
 //
 // Bound: HBM for K and V while rows are few, the products from about 256 rows per key head on.
-#include "kernels.cuh"
+#include "decode_split.cuh"
 #include "phi.cuh"
 
 namespace raattn {
@@ -80,6 +80,20 @@ __device__ __forceinline__ void store_p_half(const uint32_t (&pk)[32], uint8_t* 
   for (int c = 0; c < 8; ++c)
     *reinterpret_cast<uint4*>(row + ((c ^ (row_local & 7)) << 4)) =
         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+}
+
+// The maximum of a row over all its parts, read by one thread.
+__device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row) {
+  const int b = row / a.Hq;
+  int shared, own;
+  decode_row_slots(row, a.cum[b], a.cum[b + 1], decode_split(a, a.cum[a.B]), a, shared, own);
+  const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < shared; ++i) m = fmaxf(m, p[i]);
+#pragma unroll 4
+  for (int i = 0; i < own; ++i) m = fmaxf(m, p[a.pslots + i]);
+  return m;
 }
 
 template <int D, bool VALUES>
@@ -311,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (ok && row_ok) a.row_max[static_cast<int64_t>(row) * a.slots + split] = m;
     } else {
-      const float m = row_ok ? decode_row_max(a, row) : 0.0f;
+      const float m = row_ok ? row_maximum(a, row) : 0.0f;
       const float c2 = a.scale * (1.0f / 32.0f);
       uint8_t* prow = sP + g * C::P_BYTES + row_local * 128;
       float total = 0.0f;
@@ -390,7 +404,7 @@ cudaError_t go(const PrefixMaps& maps, const DecodeArgs& a, const LaunchCtx& ctx
                                              Cfg<D, VALUES>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int pairs = (a.B * a.G + NGROUP * BM - 1) / (NGROUP * BM);
-  kernel<<<a.Hkv * pairs * a.pchunks, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st>>>(maps, a, ctx);
+  kernel<<<a.Hkv * pairs * a.pslots, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st>>>(maps, a, ctx);
   return cudaGetLastError();
 }
 

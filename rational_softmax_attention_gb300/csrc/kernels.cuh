@@ -181,27 +181,27 @@ struct DecodeArgs {
   float* weight;                // [B, Hkv, C] or null
   void* o;                      // [B, Hq, D]
   float *s_own, *s_pre;         // unscaled scores: B Hq rows of own_width and pre_width
-  float *row_max, *part_sum;    // [B Hq][slots]: per item (unscaled); slots = shared items, then own ones
+  float *row_max, *part_sum;    // [B Hq][slots]: per part (maxima unscaled); shared parts, then own ones
   float* part_o;                // [B Hq][slots][D]
+  int* cum;                     // [B + 1] own blocks per stream of the sequences before b
   int B, Hq, Hkv, G, D, C, P;
   int tc;                       // the shared keys go to the tensor cores (decode_prefix_tc.cu)
-  int chunk, own_width;         // keys of an own item; padded length of a row of s_own
-  int pchunk, pchunks, pre_width;
-  int slots;
+  int block;                    // keys of a block
+  int own_rowblocks, shared_rowblocks;   // blocks of 16 rows of a key head: its G, the batch's B G
+  int own_width, pre_width;     // padded length of a row of s_own and s_pre
+  int pblocks;                  // blocks of the shared keys (none with tc)
+  int min_run;                  // blocks of a run at least
+  int pchunk;                   // tc: shared keys of a CTA
+  int pslots, slots;            // slots of the shared keys, and all
   float scale;
 };
-// The cache entries a sequence holds, and the maximum (unscaled) of a row over its shared and own
-// items, read by one thread.
+// The cache entries a sequence holds.
 __device__ __forceinline__ int decode_own_length(const DecodeArgs& a, int b) { return min(max(a.length[b], 0), a.C); }
-__device__ __forceinline__ float decode_row_max(const DecodeArgs& a, int row) {
-  const int n = a.pchunks + (decode_own_length(a, row / a.Hq) + a.chunk - 1) / a.chunk;
-  const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
-  float m = -__builtin_huge_valf();
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) m = fmaxf(m, p[i]);
-  return m;
+// Keys of a block (decode.cu): sixteen, one product's depth, in bf16; about 4 KB of a head's keys in fp32.
+__host__ __device__ constexpr int decode_block_keys(bool bf16, int D) {
+  return bf16 ? 16 : D == 128 ? 8 : D == 64 ? 16 : 32;
 }
-// Fills the split (tc, chunk .. slots) from the sizes; returns the workspace bytes and sets the
+// Fills the split (G, tc .. slots) from the sizes; returns the workspace bytes and sets the
 // workspace pointers from `base`.
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base);
 // Tensor maps of the prefix [Hkv, P, D] (the tensor-core form only).
