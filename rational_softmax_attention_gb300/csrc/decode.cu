@@ -18,14 +18,18 @@
 //
 // The unit of work is a block of keys (kKeys) of one stream: a key head's own keys of one
 // sequence, or its shared keys, for a block of up to 16 query rows that read them.  All blocks of
-// all streams, in order, are cut into equal runs, one per warp of a grid that fills every SM
-// once, so a ragged batch loads all SMs alike however its lengths lie; a stream's part in a run is
-// one partial result.  Every CTA counts the blocks from the lengths by itself: no host copy of
-// them is needed, and a cache much larger than what it holds costs nothing.
+// all streams, in order, are cut into equal runs over a grid that fills every SM once, so a ragged
+// batch loads all SMs alike however its lengths lie; a stream's part in a run is one partial
+// result.  Every CTA counts the blocks from the lengths by itself: no host copy of them is
+// needed, and a cache much larger than what it holds costs nothing.
 //
-// Each warp works alone, with no barrier beyond its own lanes: it streams its blocks through a
-// small ring in shared memory with asynchronous copies (which also zero the keys past a stream's
-// end, so that nothing in a cache's unused slots can reach a sum).  bf16: m16n8k16 products, query
+// A run belongs to a team of warps: one warp where streams are many, which then needs no barrier
+// beyond its lanes; the CTA's four where they are few, so that a long stream has a quarter of the
+// partial results (the team's warps take a part's blocks in turn and add theirs at its end).
+// B32 H8 C1024 with 1: 31 us in both kernels, with 4: 45; B2 H24/1 C65537 with 1: 25, with 4: 22.
+// Each warp streams its blocks through a small ring of its own in shared memory with asynchronous
+// copies (which also zero the keys past a stream's end, so that nothing in a cache's unused slots
+// can reach a sum).  bf16: m16n8k16 products, query
 // rows as M; the chunks of a row are permuted in shared memory so that the 16-byte fragment reads
 // below meet no bank conflict.  fp32: FFMA.
 //
@@ -36,7 +40,7 @@ namespace raattn {
 namespace {
 
 constexpr int kThreads = kDecodeThreads, kWarps = kThreads / 32, kCtasPerSm = kDecodeCtasPerSm;
-constexpr int kRuns = kDecodeRuns, kRows = kDecodeRows;
+constexpr int kRows = kDecodeRows;
 using Split = DecodeSplit;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -145,6 +149,18 @@ __device__ __forceinline__ Part get_part(int64_t u, int64_t end, const int* cum,
   return p;
 }
 
+// Teams of TW warps.  Blocks of a part that this warp takes: every TW-th.
+template <int TW>
+__device__ __forceinline__ int warp_of_team() { return static_cast<int>(threadIdx.x >> 5) % TW; }
+template <int TW>
+__device__ __forceinline__ int blocks_of_warp(const Part& p) { return (p.count - warp_of_team<TW>() + TW - 1) / TW; }
+template <int TW>
+__device__ __forceinline__ void team_sync() {
+  static_assert(TW == 1 || TW == kWarps, "a warp or the CTA");
+  if (TW == 1) __syncwarp();
+  else __syncthreads();
+}
+
 // Row r of a part as an index into [B, H_q].
 __device__ __forceinline__ int row_of(const Part& p, int r, const DecodeArgs& a) {
   const int x = p.row0 + r;
@@ -218,16 +234,19 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // t + 4, .. of its row: words 0, 1 of chunk 4 c + t are the B operand of product 2 c, words 2, 3 of
 // product 2 c + 1, and the query's chunks give the A operand in the same order (any order of the
 // D products of a score is the score).
-template <int D>
-__device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, uint32_t ring, __nv_bfloat16*) {
+template <int D, int TW>
+__device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, uint32_t ring, float* best_s,
+                                            __nv_bfloat16*) {
   using C = Cfg<__nv_bfloat16, D>;
   constexpr int NV = D / 32;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int mine = blocks_of_warp<TW>(p), first = (p.first + warp_of_team<TW>()) * C::kKeys;
+  constexpr int kStep = TW * C::kKeys;
   const char* keys = stream_of<__nv_bfloat16, D>(p, a.k, a.pk, a);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < p.count)
-      fetch_block<C::kKeys, C::kChunks, K16>(ring + i * C::kStageK, keys, (p.first + i) * C::kKeys, p.keys, lane);
+    if (i < mine)
+      fetch_block<C::kKeys, C::kChunks, K16>(ring + i * C::kStageK, keys, first + i * kStep, p.keys, lane);
     copy_commit();
   }
   uint4 q0[NV], q1[NV];
@@ -242,13 +261,13 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
   float* s1 = score_row(p, r1, a);
   const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
   float m0 = -kInf, m1 = -kInf;
-  for (int i = 0; i < p.count; ++i) {
+  for (int i = 0; i < mine; ++i) {
     copy_wait<C::kStages - 2>();
     __syncwarp();   // block i has landed for all lanes, and all have read block i - 1
     const int ahead = i + C::kStages - 1;
-    if (ahead < p.count)
-      fetch_block<C::kKeys, C::kChunks, K16>(ring + ahead % C::kStages * C::kStageK, keys,
-                                             (p.first + ahead) * C::kKeys, p.keys, lane);
+    if (ahead < mine)
+      fetch_block<C::kKeys, C::kChunks, K16>(ring + ahead % C::kStages * C::kStageK, keys, first + ahead * kStep,
+                                             p.keys, lane);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageK;
 #pragma unroll
@@ -260,7 +279,7 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
         mma_bf16(s, q0[c].x, q1[c].x, q0[c].y, q1[c].y, x.x, x.y);
         mma_bf16(s, q0[c].z, q1[c].z, q0[c].w, q1[c].w, x.z, x.w);
       }
-      const int key = (p.first + i) * C::kKeys + nb * 8 + 2 * t;
+      const int key = first + i * kStep + nb * 8 + 2 * t;
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[e] = key + (e & 1) < p.keys ? s[e] : -kInf;
       m0 = fmaxf(m0, fmaxf(s[0], s[1]));
@@ -274,33 +293,41 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
     m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
-  if (t == 0 && w0) a.row_max[static_cast<int64_t>(r0) * a.slots + p.slot] = m0;
-  if (t == 0 && w1) a.row_max[static_cast<int64_t>(r1) * a.slots + p.slot] = m1;
+  if (t == 0) {
+    best_s[(threadIdx.x >> 5) * kRows + g] = m0;
+    best_s[(threadIdx.x >> 5) * kRows + g + 8] = m1;
+  }
 }
 
 // fp32: 32 / kKeys lanes per key.
-template <int D>
-__device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, uint32_t ring, float*) {
+template <int D, int TW>
+__device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, uint32_t ring, float* best_s, float*) {
   using C = Cfg<float, D>;
   constexpr int PARTS = 32 / C::kKeys;
   const int lane = threadIdx.x & 31, kk = lane / PARTS, part = lane % PARTS;
+  const int mine = blocks_of_warp<TW>(p), first = (p.first + warp_of_team<TW>()) * C::kKeys;
+  constexpr int kStep = TW * C::kKeys;
   const char* keys = stream_of<float, D>(p, a.k, a.pk, a);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < p.count)
-      fetch_block<C::kKeys, C::kChunks, F32>(ring + i * C::kStageK, keys, (p.first + i) * C::kKeys, p.keys, lane);
+    if (i < mine)
+      fetch_block<C::kKeys, C::kChunks, F32>(ring + i * C::kStageK, keys, first + i * kStep, p.keys, lane);
     copy_commit();
   }
   float best[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) best[r] = -kInf;
-  for (int i = 0; i < p.count; ++i) {
+  // the rows' queries, which every block reads, into L1
+  for (int x = lane; x < p.rows * C::kChunks; x += 32)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(a.q) +
+                                                  (static_cast<int64_t>(row_of(p, x / C::kChunks, a)) * C::kChunks + x % C::kChunks) * 16));
+  for (int i = 0; i < mine; ++i) {
     copy_wait<C::kStages - 2>();
     __syncwarp();
     const int ahead = i + C::kStages - 1;
-    if (ahead < p.count)
-      fetch_block<C::kKeys, C::kChunks, F32>(ring + ahead % C::kStages * C::kStageK, keys,
-                                             (p.first + ahead) * C::kKeys, p.keys, lane);
+    if (ahead < mine)
+      fetch_block<C::kKeys, C::kChunks, F32>(ring + ahead % C::kStages * C::kStageK, keys, first + ahead * kStep,
+                                             p.keys, lane);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageK;
     float4 kx[C::kChunks / PARTS];
@@ -309,25 +336,28 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
       const uint4 u = lds128(stage + place<F32, C::kChunks>(kk, c * PARTS + part) * 16);
       kx[c] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
     }
-    const int key = (p.first + i) * C::kKeys + kk;
+    const int key = first + i * kStep + kk;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (r < p.rows) {
-        const int row = row_of(p, r, a);
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + static_cast<int64_t>(row) * D);
-        float s = 0.0f, s2 = 0.0f;
+    for (int r0 = 0; r0 < kRows; r0 += 4) {   // four rows at a time: independent chains
+      if (r0 < p.rows) {
 #pragma unroll
-        for (int c = 0; c < C::kChunks / PARTS; ++c) {
-          const float4 y = __ldg(q + c * PARTS + part);
-          s = fmaf(y.x, kx[c].x, fmaf(y.y, kx[c].y, s));
-          s2 = fmaf(y.z, kx[c].z, fmaf(y.w, kx[c].w, s2));
+        for (int r = r0; r < r0 + 4; ++r) {
+          const int row = row_of(p, min(r, p.rows - 1), a);
+          const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + static_cast<int64_t>(row) * D);
+          float s = 0.0f, s2 = 0.0f;
+#pragma unroll
+          for (int c = 0; c < C::kChunks / PARTS; ++c) {
+            const float4 y = __ldg(q + c * PARTS + part);
+            s = fmaf(y.x, kx[c].x, fmaf(y.y, kx[c].y, s));
+            s2 = fmaf(y.z, kx[c].z, fmaf(y.w, kx[c].w, s2));
+          }
+          s += s2;
+#pragma unroll
+          for (int o = 1; o < PARTS; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          s = key < p.keys ? s : -kInf;
+          best[r] = fmaxf(best[r], s);
+          if (part == 0 && r < p.rows) score_row(p, row, a)[key] = s;
         }
-        s += s2;
-#pragma unroll
-        for (int o = 1; o < PARTS; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s = key < p.keys ? s : -kInf;
-        best[r] = fmaxf(best[r], s);
-        if (part == 0) score_row(p, row, a)[key] = s;
       }
     }
   }
@@ -337,56 +367,71 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
       float v = best[r];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-      if (lane == 0) a.row_max[static_cast<int64_t>(row_of(p, r, a)) * a.slots + p.slot] = v;
+      if (lane == 0) best_s[(threadIdx.x >> 5) * kRows + r] = v;
     }
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int TW>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(const DecodeArgs a) {
   extern __shared__ uint4 dyn[];
-  int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * Cfg<T, D>::kStages * Cfg<T, D>::kStageK);
-  const uint32_t ring = smem_u32(dyn) + (threadIdx.x >> 5) * Cfg<T, D>::kStages * Cfg<T, D>::kStageK;
+  constexpr int kRing = Cfg<T, D>::kStages * Cfg<T, D>::kStageK;
+  int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
+  __shared__ float best[kWarps * kRows];
+  const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   const Split s = make_split(cum, a);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
   }
   // runs go to the CTAs in turn, so that few runs spread over the SMs
-  const int64_t run = (threadIdx.x >> 5) * static_cast<int64_t>(gridDim.x) + blockIdx.x;
-  const int64_t end = min((run + 1) * s.per, s.total);
+  const int64_t run = team * static_cast<int64_t>(gridDim.x) + blockIdx.x, end = min((run + 1) * s.per, s.total);
   for (int64_t u = run * s.per; u < end;) {
     const Part p = get_part(u, end, cum, s, a);
-    part_scores<D>(p, a, ring, static_cast<T*>(nullptr));
+    part_scores<D, TW>(p, a, smem_u32(dyn) + warp * kRing, best, static_cast<T*>(nullptr));
     u += p.count;
-    __syncwarp();   // the ring is free
+    team_sync<TW>();
+    if (tt < p.rows) {
+      float m = best[team * TW * kRows + tt];
+#pragma unroll
+      for (int w = 1; w < TW; ++w) m = fmaxf(m, best[(team * TW + w) * kRows + tt]);
+      a.row_max[static_cast<int64_t>(row_of(p, tt, a)) * a.slots + p.slot] = m;
+    }
+    team_sync<TW>();   // the maxima are read, and the rings are free
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------------------------
-// A row's values v[] over its slots, folded by f over four lanes (lane % 4).
-template <typename F>
+// A row's values v[] over its slots, folded by f over N neighbouring lanes, of which this is lane t.
+template <int N, typename F>
 __device__ __forceinline__ float fold_slots(const float* v, int shared, int own, int pslots, int t, float x, F f) {
-  for (int i = t; i < shared; i += 4) x = f(x, v[i]);
-  for (int i = t; i < own; i += 4) x = f(x, v[pslots + i]);
-  x = f(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return f(x, __shfl_xor_sync(0xffffffffu, x, 2));
+#pragma unroll 4
+  for (int i = t; i < shared; i += N) x = f(x, v[i]);
+#pragma unroll 4
+  for (int i = t; i < own; i += N) x = f(x, v[pslots + i]);
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
-__device__ __forceinline__ float row_maximum(int row, const int* cum, const Split& s, const DecodeArgs& a, int t) {
-  const int b = row / a.Hq;
+// The maxima of a part's rows, each by 2 TW of the team's threads.
+template <int TW>
+__device__ __forceinline__ void part_maxima(float* rowm, const Part& p, const int* cum, const Split& s,
+                                            const DecodeArgs& a) {
+  const int tt = threadIdx.x % (32 * TW), r = tt / (2 * TW), row = row_of(p, min(r, p.rows - 1), a), b = row / a.Hq;
   int shared, own;
   decode_row_slots(row, cum[b], cum[b + 1], s, a, shared, own);
-  return fold_slots(a.row_max + static_cast<int64_t>(row) * a.slots, shared, own, a.pslots, t, -kInf,
-                    [](float x, float y) { return fmaxf(x, y); });
+  const float m = fold_slots<2 * TW>(a.row_max + static_cast<int64_t>(row) * a.slots, shared, own, a.pslots,
+                                     tt % (2 * TW), -kInf, [](float x, float y) { return fmaxf(x, y); });
+  if (tt % (2 * TW) == 0) rowm[r] = m;
 }
 
 // A block of values and its scores into a stage.
-template <typename T, int D, Layout LAY>
+template <typename T, int D, int TW, Layout LAY>
 __device__ __forceinline__ void fetch_values(uint32_t stage, const char* vals, const Part& p, int i, const DecodeArgs& a,
                                              int lane) {
   using C = Cfg<T, D>;
-  const int first = (p.first + i) * C::kKeys;
+  const int first = (p.first + i * TW + warp_of_team<TW>()) * C::kKeys;
   fetch_block<C::kKeys, C::kChunks, LAY>(stage, vals, first, p.keys, lane);
   constexpr int PIECES = C::kKeys / 4;   // 16-byte pieces of a row of scores
 #pragma unroll
@@ -401,33 +446,35 @@ __device__ __forceinline__ void fetch_values(uint32_t stage, const char* vals, c
 // bf16.  Lane (g, t) reads, of keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of sixteen, the dimensions
 // 8 g .. 8 g + 7 of every 64: words of two keys, interleaved, are the B operand of the product
 // whose column g stands for dimension 8 g + j.  phi of the scores at the same keys is the A operand.
-template <int D>
+template <int D, int TW>
 __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
-                                            uint32_t ring, const char* ring_ptr, __nv_bfloat16*) {
+                                            uint32_t ring, char* ring_ptr, float* rowm, float* sums, __nv_bfloat16*) {
   using C = Cfg<__nv_bfloat16, D>;
   constexpr int NC = D / 64;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int mine = blocks_of_warp<TW>(p);
   const char* vals = stream_of<__nv_bfloat16, D>(p, a.v, a.pv, a);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < p.count) fetch_values<__nv_bfloat16, D, V16>(ring + i * C::kStageV, vals, p, i, a, lane);
+    if (i < mine) fetch_values<__nv_bfloat16, D, TW, V16>(ring + i * C::kStageV, vals, p, i, a, lane);
     copy_commit();
   }
-  const bool w0 = g < p.rows, w1 = g + 8 < p.rows, upper = p.rows > 8;
-  const int r0 = row_of(p, min(g, p.rows - 1), a), r1 = row_of(p, min(g + 8, p.rows - 1), a);
-  const float m0 = row_maximum(r0, cum, s, a, t), m1 = upper ? row_maximum(r1, cum, s, a, t) : 0.0f;
+  part_maxima<TW>(rowm, p, cum, s, a);
+  team_sync<TW>();
+  const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
+  const float m0 = rowm[g], m1 = rowm[g + 8];
   float acc[NC][8][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[c][j][0] = acc[c][j][1] = acc[c][j][2] = acc[c][j][3] = 0.0f;
   float t0 = 0.0f, t1 = 0.0f;
-  for (int i = 0; i < p.count; ++i) {
+  for (int i = 0; i < mine; ++i) {
     copy_wait<C::kStages - 2>();
     __syncwarp();
     const int ahead = i + C::kStages - 1;
-    if (ahead < p.count)
-      fetch_values<__nv_bfloat16, D, V16>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
+    if (ahead < mine)
+      fetch_values<__nv_bfloat16, D, TW, V16>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageV;
     const float* sc = reinterpret_cast<const float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
@@ -474,10 +521,14 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
     t0 += __shfl_xor_sync(0xffffffffu, t0, o);
     t1 += __shfl_xor_sync(0xffffffffu, t1, o);
   }
-  const int64_t at0 = static_cast<int64_t>(r0) * a.slots + p.slot, at1 = static_cast<int64_t>(r1) * a.slots + p.slot;
-  if (t == 0 && w0) a.part_sum[at0] = t0;
-  if (t == 0 && w1) a.part_sum[at1] = t1;
-  // accumulator columns 2 t, 2 t + 1 stand for dimensions 16 t + j and 16 t + 8 + j
+  if (t == 0) {
+    sums[(threadIdx.x >> 5) * kRows + g] = t0;
+    sums[(threadIdx.x >> 5) * kRows + g + 8] = t1;
+  }
+  // Into this warp's ring (its blocks have been read).  Accumulator columns 2 t, 2 t + 1 stand for
+  // dimensions 16 t + j and 16 t + 8 + j.
+  __syncwarp();
+  float* out = reinterpret_cast<float*>(ring_ptr);
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -485,41 +536,43 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (e < 2 ? w0 : w1)
-          *reinterpret_cast<float4*>(a.part_o + (e < 2 ? at0 : at1) * D + c * 64 + t * 16 + (e & 1) * 8 + j) =
+          *reinterpret_cast<float4*>(out + (g + (e >> 1) * 8) * D + c * 64 + t * 16 + (e & 1) * 8 + j) =
               make_float4(acc[c][j][e], acc[c][j + 1][e], acc[c][j + 2][e], acc[c][j + 3][e]);
 }
 
 // fp32: D / 4 lanes across the dimensions, the other lanes over the keys; phi replaces the scores in
 // shared memory.
-template <int D>
+template <int D, int TW>
 __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
-                                            uint32_t ring, const char* ring_ptr, float*) {
+                                            uint32_t ring, char* ring_ptr, float* rowm, float* sums, float*) {
   using C = Cfg<float, D>;
   constexpr int L = D / 4, KS = 32 / L;
   const int lane = threadIdx.x & 31, gl = lane % L, ks = lane / L;
+  const int mine = blocks_of_warp<TW>(p);
   const char* vals = stream_of<float, D>(p, a.v, a.pv, a);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < p.count) fetch_values<float, D, F32>(ring + i * C::kStageV, vals, p, i, a, lane);
+    if (i < mine) fetch_values<float, D, TW, F32>(ring + i * C::kStageV, vals, p, i, a, lane);
     copy_commit();
   }
   // four lanes per row for phi: lane (g, t) takes rows g and g + 8, keys t, t + 4, ..
   const int g = lane >> 2, t = lane & 3;
   const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
-  const float m0 = row_maximum(row_of(p, min(g, p.rows - 1), a), cum, s, a, t);
-  const float m1 = row_maximum(row_of(p, min(g + 8, p.rows - 1), a), cum, s, a, t);
+  part_maxima<TW>(rowm, p, cum, s, a);
+  team_sync<TW>();
+  const float m0 = rowm[g], m1 = rowm[g + 8];
   float acc[kRows][4];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.0f;
   float t0 = 0.0f, t1 = 0.0f;
-  for (int i = 0; i < p.count; ++i) {
+  for (int i = 0; i < mine; ++i) {
     copy_wait<C::kStages - 2>();
     __syncwarp();
     const int ahead = i + C::kStages - 1;
-    if (ahead < p.count) fetch_values<float, D, F32>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
+    if (ahead < mine) fetch_values<float, D, TW, F32>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageV;
-    float* sc = reinterpret_cast<float*>(const_cast<char*>(ring_ptr) + i % C::kStages * C::kStageV + C::kBlockBytes);
+    float* sc = reinterpret_cast<float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
 #pragma unroll
     for (int k = 0; k < C::kKeys; k += 4) {
       if (w0) {
@@ -540,14 +593,18 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
       const float4 v = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
                                    __uint_as_float(u.w));
 #pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < p.rows) {
-          const float f = sc[r * C::kScoreStride + kk];
-          acc[r][0] = fmaf(f, v.x, acc[r][0]);
-          acc[r][1] = fmaf(f, v.y, acc[r][1]);
-          acc[r][2] = fmaf(f, v.z, acc[r][2]);
-          acc[r][3] = fmaf(f, v.w, acc[r][3]);
+      for (int r0 = 0; r0 < kRows; r0 += 4) {
+        if (r0 < p.rows) {
+#pragma unroll
+          for (int r = r0; r < r0 + 4; ++r) {   // rows past the last add what is never written out
+            const float f = sc[r * C::kScoreStride + kk];
+            acc[r][0] = fmaf(f, v.x, acc[r][0]);
+            acc[r][1] = fmaf(f, v.y, acc[r][1]);
+            acc[r][2] = fmaf(f, v.z, acc[r][2]);
+            acc[r][3] = fmaf(f, v.w, acc[r][3]);
+          }
         }
+      }
     }
   }
 #pragma unroll
@@ -555,8 +612,11 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
     t0 += __shfl_xor_sync(0xffffffffu, t0, o);
     t1 += __shfl_xor_sync(0xffffffffu, t1, o);
   }
-  if (t == 0 && w0) a.part_sum[static_cast<int64_t>(row_of(p, g, a)) * a.slots + p.slot] = t0;
-  if (t == 0 && w1) a.part_sum[static_cast<int64_t>(row_of(p, g + 8, a)) * a.slots + p.slot] = t1;
+  if (t == 0) {
+    sums[(threadIdx.x >> 5) * kRows + g] = t0;
+    sums[(threadIdx.x >> 5) * kRows + g + 8] = t1;
+  }
+  __syncwarp();
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (r < p.rows) {
@@ -565,26 +625,48 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) acc[r][e] += __shfl_xor_sync(0xffffffffu, acc[r][e], o);
       if (ks == 0)
-        reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, r, a)) * a.slots + p.slot) * D)[gl] =
-            make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+        reinterpret_cast<float4*>(ring_ptr)[r * L + gl] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
     }
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int TW>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(const DecodeArgs a) {
   extern __shared__ uint4 dyn[];
   constexpr int kRing = Cfg<T, D>::kStages * Cfg<T, D>::kStageV;
+  static_assert(kRing >= kRows * D * 4, "a warp's partial sums fit its ring");
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
-  const char* ring_ptr = reinterpret_cast<const char*>(dyn) + (threadIdx.x >> 5) * kRing;
+  __shared__ float rowm_s[kWarps / TW * kRows], sums[kWarps * kRows];
+  const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
+  char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
+  const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
   const Split s = make_split(cum, a);
-  const int64_t run = (threadIdx.x >> 5) * static_cast<int64_t>(gridDim.x) + blockIdx.x;
-  const int64_t end = min((run + 1) * s.per, s.total);
+  const int64_t run = team * static_cast<int64_t>(gridDim.x) + blockIdx.x, end = min((run + 1) * s.per, s.total);
   for (int64_t u = run * s.per; u < end;) {
     const Part p = get_part(u, end, cum, s, a);
-    part_values<D>(p, a, s, cum, smem_u32(ring_ptr), ring_ptr, static_cast<T*>(nullptr));
+    part_values<D, TW>(p, a, s, cum, smem_u32(ring), ring, rowm_s + team * kRows, sums, static_cast<T*>(nullptr));
     u += p.count;
-    __syncwarp();
+    team_sync<TW>();
+    if (tt < p.rows) {
+      float f = sums[team * TW * kRows + tt];
+#pragma unroll
+      for (int w = 1; w < TW; ++w) f += sums[(team * TW + w) * kRows + tt];
+      a.part_sum[static_cast<int64_t>(row_of(p, tt, a)) * a.slots + p.slot] = f;
+    }
+    for (int e = tt; e < p.rows * (D / 4); e += 32 * TW) {
+      const int r = e / (D / 4), c = e % (D / 4);
+      float4 f = reinterpret_cast<const float4*>(rings)[e];
+#pragma unroll
+      for (int w = 1; w < TW; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(rings + w * kRing + e * 16);
+        f.x += x.x;
+        f.y += x.y;
+        f.z += x.z;
+        f.w += x.w;
+      }
+      reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, r, a)) * a.slots + p.slot) * D)[c] = f;
+    }
+    team_sync<TW>();
   }
 }
 
@@ -657,10 +739,10 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     int shared, own;
     decode_row_slots(row, a.cum[b], a.cum[b + 1], sp, a, shared, own);
     const int64_t at = static_cast<int64_t>(row) * a.slots;
-    const float m = fold_slots(a.row_max + at, shared, own, a.pslots, lane & 3, -kInf,
-                               [](float u, float v) { return fmaxf(u, v); });
-    const float s = fold_slots(a.part_sum + at, shared, own, a.pslots, lane & 3, 0.0f,
-                               [](float u, float v) { return u + v; });
+    const float m = fold_slots<4>(a.row_max + at, shared, own, a.pslots, lane & 3, -kInf,
+                                  [](float u, float v) { return fmaxf(u, v); });
+    const float s = fold_slots<4>(a.part_sum + at, shared, own, a.pslots, lane & 3, 0.0f,
+                                  [](float u, float v) { return u + v; });
     if ((lane & 3) == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / s);
   }
   __syncthreads();
@@ -682,38 +764,44 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     if (first + i * kThreads < last) w[first + i * kThreads] += sum[i];
 }
 
-template <typename T, int D>
+template <typename T, int D, int TW>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
   using C = Cfg<T, D>;
   const int cum = (a.B + 1) * 4;
   const int smem_scores = kWarps * C::kStages * C::kStageK + cum;
   const int smem_values = kWarps * C::kStages * C::kStageV + cum;
-  cudaError_t e = cudaFuncSetAttribute(decode_scores_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(decode_scores_kernel<T, D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem_scores);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_values_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_values);
+    e = cudaFuncSetAttribute(decode_values_kernel<T, D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_values);
   if (e != cudaSuccess) return e;
-  // CTAs for the runs that there can be (each has one run per warp)
-  const int64_t most = (a.tc ? 0 : static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks) +
+  // CTAs for the runs that there can be
+  const int64_t most = static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks +
                        static_cast<int64_t>(a.B) * (a.own_width / a.block) * a.Hkv * a.own_rowblocks;
   const int64_t runs = (most + a.min_run - 1) / a.min_run;
-  const int grid = static_cast<int>(runs < kSms * kCtasPerSm ? runs : kSms * kCtasPerSm);
+  const int grid = static_cast<int>(runs < kDecodeCtas ? runs : kDecodeCtas);
   if (a.tc && (e = launch_decode_prefix(maps, a, false, ctx, st)) != cudaSuccess) return e;
-  decode_scores_kernel<T, D><<<grid, kThreads, smem_scores, st>>>(a);
+  decode_scores_kernel<T, D, TW><<<grid, kThreads, smem_scores, st>>>(a);
   if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
-  decode_values_kernel<T, D><<<grid, kThreads, smem_values, st>>>(a);
+  decode_values_kernel<T, D, TW><<<grid, kThreads, smem_values, st>>>(a);
   const int64_t join = static_cast<int64_t>(a.B) * a.Hq +
                        (a.weight ? static_cast<int64_t>(a.B) * a.Hkv * ((a.C + kWeightKeys - 1) / kWeightKeys) : 0);
   decode_join_kernel<T, D><<<static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st>>>(a);
   return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
+  return a.runs == kDecodeCtas ? go<T, D, kWarps>(a, maps, ctx, st) : go<T, D, 1>(a, maps, ctx, st);
 }
 
 }  // namespace
 
 // The split of the keys.  Shared keys of more than kTcRows rows per key head go to the tensor
 // cores, in whole tiles of 128, split so that one wave of CTAs takes them.  Everything else is
-// cut into runs of equal length, at least min_run blocks: two where all runs could not be longer
-// anyway (latency), eight otherwise, which bounds the partial results of a long stream.
+// cut into runs of equal length: one per warp with 64 streams or more (a stream then has at most
+// about 30 partial results), one per CTA with fewer.  A run has at least min_run blocks: two per warp
+// (in flight together) where runs could not be longer anyway, up to eight, which bounds the partial
+// results of a long stream.
 constexpr int64_t kTcRows = 32;
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
@@ -729,8 +817,12 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   a->pre_width = a->pblocks * a->block;
   const int64_t total = static_cast<int64_t>(a->B) * own * a->Hkv * a->own_rowblocks +
                         static_cast<int64_t>(a->pblocks) * a->Hkv * a->shared_rowblocks;
-  const int64_t even = total / kRuns;
-  a->min_run = static_cast<int>(even < 2 ? 2 : even > 8 ? 8 : even);
+  const int64_t streams = static_cast<int64_t>(a->B) * a->Hkv * a->own_rowblocks +
+                          (a->pblocks ? static_cast<int64_t>(a->Hkv) * a->shared_rowblocks : 0);
+  const int team = streams >= 64 ? 1 : kWarps;
+  a->runs = kDecodeCtas * kWarps / team;
+  const int64_t even = total / a->runs;
+  a->min_run = static_cast<int>(even < 2 * team ? 2 * team : even > 8 * team ? 8 * team : even);
   a->pchunk = a->pslots = 0;
   if (a->tc) {
     const int64_t per = a->Hkv * ((shared_rows + 255) / 256), tiles = (a->P + 127) / 128;

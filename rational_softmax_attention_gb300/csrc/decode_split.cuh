@@ -6,7 +6,7 @@
 namespace raattn {
 
 constexpr int kDecodeThreads = 128, kDecodeCtasPerSm = 3;
-constexpr int kDecodeRuns = kSms * kDecodeCtasPerSm * kDecodeThreads / 32;   // one per warp of a full grid
+constexpr int kDecodeCtas = kSms * kDecodeCtasPerSm;   // a grid that fills every SM
 constexpr int kDecodeRows = 16;                                               // query rows of a stream
 
 struct DecodeSplit {
@@ -20,7 +20,7 @@ __device__ __forceinline__ DecodeSplit decode_split(const DecodeArgs& a, int own
   DecodeSplit s;
   s.own0 = a.tc ? 0 : static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks;
   s.total = s.own0 + static_cast<int64_t>(own) * a.Hkv * a.own_rowblocks;
-  const int64_t even = (s.total + kDecodeRuns - 1) / kDecodeRuns;
+  const int64_t even = (s.total + a.runs - 1) / a.runs;
   s.per = static_cast<int>(even > a.min_run ? even : a.min_run);
   return s;
 }
