@@ -61,7 +61,6 @@ ra_status_t norm_rope_shape(NormRopeShape* a, const void* qkv, int64_t batch_str
   a->D = D;
   a->norm = norm;
   a->eps = eps;
-  a->tile = 1;
   return RA_OK;
 }
 
@@ -111,7 +110,7 @@ ra_status_t ra_qk_norm_rope_fwd(const void* qkv, int64_t batch_stride, int64_t t
 }
 
 size_t ra_qk_norm_rope_bwd_workspace_size(int D) {
-  return head_dim_ok(D) ? static_cast<size_t>(norm_rope_bwd_ctas()) * 4 * D * sizeof(float) : 0;
+  return head_dim_ok(D) ? static_cast<size_t>(norm_rope_bwd_ctas()) * 2 * D * sizeof(float) : 0;
 }
 
 ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t token_stride, const void* q_weight,

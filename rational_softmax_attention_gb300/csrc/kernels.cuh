@@ -156,7 +156,7 @@ struct NormRopeShape {
   int B, N, Hq, Hkv, D;
   int norm;                     // ra_norm_t
   float eps;
-  int tile;                     // tokens of a CTA's tile (set by the launcher)
+  int ctas[3], tiles[3];        // set by the launcher: CTAs for query, key and value rows; tokens of their tiles
 };
 struct NormRopeFwd {
   void *q, *k, *v;              // q [B, Hq, N, D]; k, v [B, Hkv, capacity, D]
@@ -168,7 +168,7 @@ struct NormRopeBwd {
   const void *dq, *dk, *dv;     // [B, Hq or Hkv, N, D]
   void* dqkv;                   // [B, N, (Hq + 2 Hkv) D] dense
   float* dparams;               // [4][D]: q weight, q bias, k weight, k bias
-  float* partial;               // [norm_rope_bwd_ctas][4][D]
+  float* partial;               // [norm_rope_bwd_ctas][2][D]
 };
 int norm_rope_bwd_ctas();
 cudaError_t launch_norm_rope_fwd(NormRopeShape a, const NormRopeFwd& io, bool bf16, cudaStream_t st);

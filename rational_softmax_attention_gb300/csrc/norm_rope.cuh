@@ -13,16 +13,16 @@
 // xhat and r are formed again from the projection, whose row the backward would have to read
 // for xhat anyway, so the forward saves nothing else.
 //
-// Bound: HBM, with the issue slots close behind: a row lies across D * size / 16 lanes, one 16-byte
-// vector each, so every access is a whole vector and the row sums are a few shuffles.  A CTA takes
-// a tile of tokens; a lane group stays with one token and walks its heads, so what depends on the
-// token alone is formed once and not per row: the norm's weight w and the rotation fold into
-// two factors and an addend,
+// Bound: HBM, with the issue slots close behind.  A lane holds two 16-byte vectors of a row (a row
+// lies across D * size / 32 lanes), chosen so that in the half-split form it holds both members of
+// its pairs: the rotation needs no exchange between lanes, and the row sums are a few shuffles.  A
+// CTA works on one kind of row (queries, keys or values; the CTAs are shared out by their bytes)
+// and takes a tile of tokens at a time; a lane group stays with one token and walks its heads, so what
+// depends on the token alone is formed once and not per row.  In the forward the norm's weight w and
+// the rotation fold into two factors and an addend,
 //   y_j = r (x_j A_j + x_partner B_j) + C_j,  A = w cos, B = +-w_partner sin, C = the rotated bias,
-// and the arithmetic runs as packed pairs of floats.  The half-split form's partners are fetched
-// from the other lanes as the raw 16-byte vector, four words and not eight floats.  Each thread copies
-// the next rows' vectors asynchronously into shared-memory slots of its own, which costs no
-// registers and needs no barrier.
+// and all arithmetic runs as packed pairs of floats.  Each thread copies the next rows' vectors
+// asynchronously into shared-memory slots of its own, which costs no registers and no barrier.
 #pragma once
 
 #include "kernels.cuh"
@@ -105,134 +105,171 @@ __device__ __forceinline__ void init_turns(Tables& tb, const NormRopeShape& a) {
   __syncthreads();
 }
 
-__device__ __forceinline__ void fill_table(Tables& tb, int buf, const NormRopeShape& a, int64_t tok0) {
-  const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
-  for (int i = threadIdx.x; i < a.tile * a.pairs; i += kThreads) {
-    const int tl = i / a.pairs, p = i - tl * a.pairs;
-    const int64_t tok = tok0 + tl;
+// The cosines and sines of a tile's tokens.  Threads are laid out with the pairs (a power of two
+// of them) fastest; token numbers fit 32 bits, where a division is cheap.
+__device__ __forceinline__ void fill_table(Tables& tb, int buf, const NormRopeShape& a, int tok0, int tile) {
+  const int lg = 32 - __clz(a.pairs - 1), p = threadIdx.x & ((1 << lg) - 1);   // pairs = 1: lg = 0
+  if (p >= a.pairs) return;
+  const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
+  const int* pos = a.pos + axis * a.pos_axis_stride;
+  const float2 turns = tb.turns[p];
+  const int tokens = a.B * a.N;
+  for (int tl = threadIdx.x >> lg; tl < tile; tl += kThreads >> lg) {
+    const int tok = tok0 + tl;
     if (tok < tokens) {
-      const int b = static_cast<int>(tok / a.N), n = static_cast<int>(tok - static_cast<int64_t>(b) * a.N);
-      const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
-      const int pos = a.pos[axis * a.pos_axis_stride + b * a.pos_batch_stride + n];
+      const int b = tok / a.N, n = tok - b * a.N;
       float s, c;
-      sincospif(2.0f * turn_fraction(pos, tb.turns[p]), &s, &c);
+      sincospif(2.0f * turn_fraction(pos[b * a.pos_batch_stride + n], turns), &s, &c);
       tb.cs[buf][tl][p] = c;
       tb.sn[buf][tl][p] = s;
     }
   }
 }
 
-// The lane's part of a token's rotation, out = x cs + partner sn; a pair (j, j + 1) of its elements
-// is turned or not as a whole (pairs are even numbers of elements).
-template <int P>
-struct Turn {
-  float2 cs[P], sn[P];   // 1 and 0 where not turned
+// Which vectors of a row a lane holds, and how they are turned.
+struct LaneMap {
+  int v0, v1;       // vectors of E elements
+  int pair;         // half-split: first of the lane's E pairs (v0 holds their first members)
+  bool turned;      // half-split: whether they are turned
+  int n0, n1;       // interleaved: turned pairs of v0 and of v1
 };
-
-// What does not depend on the token: where a lane's partners are.
-struct Partner {
-  int from;         // lane of the warp that holds them (half-split), or this lane
-  uint32_t keep;    // half-split: all ones, or 0 where the lane's elements are not turned
-  int count;        // interleaved: how many of the lane's elements are turned
-};
-template <int E>
-__device__ __forceinline__ Partner find_partner(const NormRopeShape& a, int gl, int lane) {
-  Partner p;
-  const int e0 = gl * E;
-  const bool first = e0 < a.pairs, second = !first && e0 < 2 * a.pairs;   // pairs is a multiple of 8 then
-  p.from = a.interleaved ? lane : first ? lane + a.pairs / E : second ? lane - a.pairs / E : lane;
-  p.keep = first || second ? ~0u : 0u;
-  p.count = min(max(2 * a.pairs - e0, 0), E);
-  return p;
+template <int E, int L>
+__device__ __forceinline__ LaneMap lane_map(const NormRopeShape& a, int gl) {
+  LaneMap m;
+  const int half = a.pairs / E;   // half-split: pairs is a multiple of 8, so whole vectors
+  if (a.interleaved || gl >= half) {
+    // interleaved, or a lane of the part that is not turned: that part's vectors, two by two
+    m.v0 = a.interleaved ? gl : 2 * gl;
+    m.v1 = a.interleaved ? gl + L : 2 * gl + 1;
+    m.turned = false;
+    m.pair = 0;
+  } else {
+    m.v0 = gl;
+    m.v1 = gl + half;
+    m.turned = true;
+    m.pair = gl * E;
+  }
+  m.n0 = min(max(a.pairs - m.v0 * (E / 2), 0), E / 2);
+  m.n1 = min(max(a.pairs - m.v1 * (E / 2), 0), E / 2);
+  return m;
 }
 
+// A token's cosines and sines of a lane's pairs: half-split E pairs, v0 the first members; interleaved
+// E / 2 pairs of v0, then of v1.  1 and 0 where not turned (whole: everywhere turned).
 template <int E>
-__device__ __forceinline__ void load_turn(Turn<E / 2>& t, const Tables& tb, int buf, int tl, int gl,
-                                          const Partner& pt, const NormRopeShape& a) {
-  const int e0 = gl * E;
-  if (a.interleaved) {
+__device__ __forceinline__ void load_turn(float (&cs)[E], float (&sn)[E], const Tables& tb, int buf, int tl,
+                                          const LaneMap& m, const NormRopeShape& a, bool whole) {
+  const int p0 = a.interleaved ? m.v0 * (E / 2) : m.pair, p1 = a.interleaved ? m.v1 * (E / 2) : m.pair + E / 2;
+  const float* c = tb.cs[buf][tl];
+  const float* s = tb.sn[buf][tl];
 #pragma unroll
-    for (int j = 0; j < E / 2; ++j) {
-      const bool in = 2 * j < pt.count;
-      const float c = in ? tb.cs[buf][tl][e0 / 2 + j] : 1.0f, s = in ? tb.sn[buf][tl][e0 / 2 + j] : 0.0f;
-      t.cs[j] = f2(c);
-      t.sn[j] = make_float2(-s, s);
-    }
-  } else {
-    const bool first = e0 < a.pairs;
-    const int p = pt.keep ? (first ? e0 : e0 - a.pairs) : 0;
+  for (int j = 0; j < E / 2; j += 2) {
+    const float2 x = *reinterpret_cast<const float2*>(c + p0 + j), y = *reinterpret_cast<const float2*>(c + p1 + j);
+    const float2 u = *reinterpret_cast<const float2*>(s + p0 + j), v = *reinterpret_cast<const float2*>(s + p1 + j);
+    cs[j] = x.x;
+    cs[j + 1] = x.y;
+    cs[E / 2 + j] = y.x;
+    cs[E / 2 + j + 1] = y.y;
+    sn[j] = u.x;
+    sn[j + 1] = u.y;
+    sn[E / 2 + j] = v.x;
+    sn[E / 2 + j + 1] = v.y;
+  }
+  if (!whole) {
 #pragma unroll
-    for (int j = 0; j < E / 2; ++j) {
-      const float2 c = *reinterpret_cast<const float2*>(&tb.cs[buf][tl][p + 2 * j]);
-      const float2 s = *reinterpret_cast<const float2*>(&tb.sn[buf][tl][p + 2 * j]);
-      t.cs[j] = pt.keep ? c : f2(1.0f);
-      t.sn[j] = !pt.keep ? f2(0.0f) : first ? make_float2(-s.x, -s.y) : s;
+    for (int j = 0; j < E; ++j) {
+      const bool in = a.interleaved ? (j < E / 2 ? j < m.n0 : j - E / 2 < m.n1) : m.turned;
+      cs[j] = in ? cs[j] : 1.0f;
+      sn[j] = in ? sn[j] : 0.0f;
     }
   }
 }
 
-// The partners of a lane's vector (zeros where an element is not turned, so that nothing of it,
-// an infinity say, meets a factor 0).
-template <typename T>
-__device__ __forceinline__ void partners(const uint4& u, const float2 (&x)[Vec<T>::E / 2], float2 (&p)[Vec<T>::E / 2],
-                                         const Partner& pt, int interleaved) {
-  constexpr int E = Vec<T>::E;
-  if (interleaved) {
+// The rotation's factors on a row x0, x1: y0 = x0 a0 + p0 b0, y1 = x1 a1 + p1 b1 with the partners
+// p0, p1 of partners().
+template <int E>
+__device__ __forceinline__ void factors(const float (&cs)[E], const float (&sn)[E], int interleaved,
+                                        float2 (&a0)[E / 2], float2 (&b0)[E / 2], float2 (&a1)[E / 2],
+                                        float2 (&b1)[E / 2]) {
 #pragma unroll
-    for (int j = 0; j < E / 2; ++j) p[j] = 2 * j < pt.count ? swap(x[j]) : f2(0.0f);
-  } else {
-    uint4 w;
-    w.x = __shfl_sync(0xffffffffu, u.x, pt.from) & pt.keep;
-    w.y = __shfl_sync(0xffffffffu, u.y, pt.from) & pt.keep;
-    w.z = __shfl_sync(0xffffffffu, u.z, pt.from) & pt.keep;
-    w.w = __shfl_sync(0xffffffffu, u.w, pt.from) & pt.keep;
-    Vec<T>::get(w, p);
+  for (int k = 0; k < E / 2; ++k) {
+    if (interleaved) {
+      a0[k] = f2(cs[k]);
+      b0[k] = make_float2(-sn[k], sn[k]);
+      a1[k] = f2(cs[E / 2 + k]);
+      b1[k] = make_float2(-sn[E / 2 + k], sn[E / 2 + k]);
+    } else {
+      a0[k] = a1[k] = make_float2(cs[2 * k], cs[2 * k + 1]);
+      b1[k] = make_float2(sn[2 * k], sn[2 * k + 1]);
+      b0[k] = make_float2(-b1[k].x, -b1[k].y);
+    }
+  }
+}
+// The partners of x0 and x1: zero where a pair is not turned, so that nothing of it, an infinity
+// say, meets a factor 0.  whole: every pair of every lane is turned (no selection needed).
+template <int P>
+__device__ __forceinline__ void partners(const float2 (&x0)[P], const float2 (&x1)[P], float2 (&p0)[P],
+                                         float2 (&p1)[P], const LaneMap& m, int interleaved, bool whole) {
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    p0[k] = interleaved ? swap(x0[k]) : x1[k];
+    p1[k] = interleaved ? swap(x1[k]) : x0[k];
+  }
+  if (!whole) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if (!(interleaved ? k < m.n0 : m.turned)) p0[k] = f2(0.0f);
+      if (!(interleaved ? k < m.n1 : m.turned)) p1[k] = f2(0.0f);
+    }
   }
 }
 
 // Over a row's lanes.
 template <int P, int L>
-__device__ __forceinline__ float row_sum(const float2 (&x)[P]) {
-  float2 s = x[0];
+__device__ __forceinline__ float row_sum(const float2 (&x0)[P], const float2 (&x1)[P]) {
+  float2 s = __fadd2_rn(x0[0], x1[0]);
 #pragma unroll
-  for (int j = 1; j < P; ++j) s = __fadd2_rn(s, x[j]);
+  for (int j = 1; j < P; ++j) s = __fadd2_rn(s, __fadd2_rn(x0[j], x1[j]));
   return group_sum<L>(s.x + s.y);
 }
 template <int P, int L>
-__device__ __forceinline__ float row_dot(const float2 (&x)[P], const float2 (&y)[P]) {
-  float2 s = __fmul2_rn(x[0], y[0]);
+__device__ __forceinline__ float row_dot(const float2 (&x0)[P], const float2 (&x1)[P], const float2 (&y0)[P],
+                                         const float2 (&y1)[P]) {
+  float2 s = __fmul2_rn(x0[0], y0[0]), s2 = __fmul2_rn(x1[0], y1[0]);
 #pragma unroll
-  for (int j = 1; j < P; ++j) s = __ffma2_rn(x[j], y[j], s);
+  for (int j = 1; j < P; ++j) {
+    s = __ffma2_rn(x0[j], y0[j], s);
+    s2 = __ffma2_rn(x1[j], y1[j], s2);
+  }
+  s = __fadd2_rn(s, s2);
   return group_sum<L>(s.x + s.y);
 }
 // 1 / sqrt(mean square + eps); a row of zeros stays finite with eps = 0 too.
 __device__ __forceinline__ float inverse_rms(float mean_square, float eps) {
-  return rsqrtf(fmaxf(mean_square + eps, 1e-37f));
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(mean_square + eps, 1e-37f)));   // 2 ulp
+  return r;
 }
 
-// A tile's rows in the order in which a lane group walks them: its share of the token's query
-// heads, then of its key heads, then of its value heads, in batches of U heads of one kind.
-struct Walk {
-  int hs, hstep;    // heads hs, hs + hstep, ..
-  int q, k, all;    // batches of query heads; of query and key heads; of all
+// What a CTA works on.
+struct Work {
+  int kind;             // 0 queries, 1 keys, 2 values
+  int heads, head0;     // its heads, the first of them in a token of the projection
+  int tile;             // tokens of a tile
+  int first, step;      // tiles first, first + step, ..
 };
-template <int U>
-__device__ __forceinline__ Walk make_walk(const NormRopeShape& a, int g, int groups) {
-  Walk w;
-  w.hs = g / a.tile;
-  w.hstep = groups / a.tile;
-  const int per = U * w.hstep;
-  w.q = (a.Hq + per - 1) / per;
-  w.k = w.q + (a.Hkv + per - 1) / per;
-  w.all = w.k + (a.Hkv + per - 1) / per;
+__device__ __forceinline__ Work work_of(const NormRopeShape& a) {
+  Work w;
+  int x = blockIdx.x;
+  w.kind = x < a.ctas[0] ? 0 : x < a.ctas[0] + a.ctas[1] ? 1 : 2;
+  if (w.kind > 0) x -= a.ctas[0];
+  if (w.kind > 1) x -= a.ctas[1];
+  w.heads = w.kind == 0 ? a.Hq : a.Hkv;
+  w.head0 = w.kind == 0 ? 0 : w.kind == 1 ? a.Hq : a.Hq + a.Hkv;
+  w.tile = a.tiles[w.kind];
+  w.first = x;
+  w.step = a.ctas[w.kind];
   return w;
-}
-// Kind of batch i (0 query, 1 key, 2 value), its first head for this group, and the kind's heads.
-template <int U>
-__device__ __forceinline__ void batch_of(const Walk& w, int i, const NormRopeShape& a, int& kind, int& h, int& heads) {
-  kind = i < w.q ? 0 : i < w.k ? 1 : 2;
-  h = w.hs + (i - (kind == 0 ? 0 : kind == 1 ? w.q : w.k)) * U * w.hstep;
-  heads = kind == 0 ? a.Hq : a.Hkv;
 }
 
 // A thread's asynchronous 16-byte copies into its own slots (zeros when not `in`).
@@ -246,15 +283,23 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Tokens of a tile: what a token's rotation costs is shared by the heads that one lane group walks,
-// so as many tokens as lane groups are best, short of leaving SMs without tiles or the last round
-// of tiles half empty: up to half of the groups, and at least six tiles per SM.
-inline int tile_for(const NormRopeShape& a, int es) {
-  const int groups = kThreads / (a.D * es / 16);
-  const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
-  int t = 1;
-  while (t < kMaxTile && 4 * t <= groups && tokens / (2 * t) >= 6 * kSms) t *= 2;
-  return t;
+// Shares `most` CTAs among the kinds by their cost per head, and sets the tiles' tokens: as many as
+// leave no lane group without a head; then more, since what a token costs once is shared by the
+// heads that one lane group walks, while each CTA still gets four tiles or more.
+inline void plan_work(NormRopeShape* a, int es, int most, const int (&cost)[3]) {
+  const int groups = kThreads / (a->D * es / 32);
+  const int64_t tokens = static_cast<int64_t>(a->B) * a->N;
+  const int heads[3] = {a->Hq, a->Hkv, a->Hkv};
+  const int64_t all = static_cast<int64_t>(cost[0]) * heads[0] + static_cast<int64_t>(cost[1] + cost[2]) * heads[1];
+  for (int k = 0; k < 3; ++k) {
+    const int64_t share = static_cast<int64_t>(most) * cost[k] * heads[k] / all;
+    const int64_t ctas = share < 1 ? 1 : share;
+    int t = 1;
+    while (2 * t <= groups && t < kMaxTile && (groups / t > heads[k] || tokens / (2 * t) >= 4 * ctas)) t *= 2;
+    const int64_t tiles = (tokens + t - 1) / t;
+    a->tiles[k] = t;
+    a->ctas[k] = static_cast<int>(tiles < ctas ? tiles : ctas);
+  }
 }
 
 }  // namespace norm_rope

@@ -55,7 +55,7 @@ def test_norm_rope_own_arguments(lib):
     assert _norm_rope(lib, start=FAKE, cap=1 << 31 - 1, B=4, N=1) == ARG
     assert _norm_rope(lib, bwd=True, ws=None) == ARG
     assert lib.ra_qk_norm_rope_bwd_workspace_size(48) == 0
-    assert lib.ra_qk_norm_rope_bwd_workspace_size(64) % (4 * 64 * 4) == 0
+    assert lib.ra_qk_norm_rope_bwd_workspace_size(64) % (2 * 64 * 4) == 0
 
 
 def _decode(lib, q=FAKE, length=FAKE, pk=None, pv=None, o=FAKE, weight=None, ws=FAKE, B=2, Hq=4, Hkv=2, C=16, P=0,
