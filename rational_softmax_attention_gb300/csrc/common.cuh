@@ -195,6 +195,32 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* map, uin
 }
 
 // ----------------------------------------------------------------------------
+// Dependent launches: a kernel launched with launch_dependent() may start while the kernel
+// before it on the stream still runs, as soon as all of that one's CTAs have called
+// release_dependents() or ended.  Only after await_previous() has the previous kernel ended
+// and may its results be read; a kernel that needs none still calls it before it ends, so that
+// its own end means the end of all before it.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void release_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                             A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// ----------------------------------------------------------------------------
 // tcgen05: tensor memory, MMA, loads
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {

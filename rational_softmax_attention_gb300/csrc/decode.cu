@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
+  release_dependents();
   const Split s = make_split(cum, a);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
     }
     team_sync<TW>();   // the maxima are read, and the rings are free
   }
+  await_previous();   // the tensor cores' part, if any: whoever awaits this kernel awaits that too
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -407,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
 template <int N, typename F>
 __device__ __forceinline__ float fold_slots(const float* v, int shared, int own, int pslots, int t, float x, F f) {
 #pragma unroll 4
-  for (int i = t; i < shared; i += N) x = f(x, v[i]);
+  for (int i = t; i < shared; i += N) x = f(x, __ldcg(v + i));
 #pragma unroll 4
-  for (int i = t; i < own; i += N) x = f(x, v[pslots + i]);
+  for (int i = t; i < own; i += N) x = f(x, __ldcg(v + pslots + i));
 #pragma unroll
   for (int o = 1; o < N; o <<= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
@@ -640,7 +642,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(con
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
+  release_dependents();
   const Split s = make_split(cum, a);
+  // The scores have been written: by the kernel before, or, with the tensor cores, by the one before
+  // that, which all of the kernel before had awaited when this one could start.
+  if (!a.tc) await_previous();
   const int64_t run = team * static_cast<int64_t>(gridDim.x) + blockIdx.x, end = min((run + 1) * s.per, s.total);
   for (int64_t u = run * s.per; u < end;) {
     const Part p = get_part(u, end, cum, s, a);
@@ -668,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(con
     }
     team_sync<TW>();
   }
+  if (a.tc) await_previous();   // whoever awaits this kernel awaits the tensor cores' part too
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -679,6 +686,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+  await_previous();
   const Split sp = decode_split(a, a.cum[a.B]);   // the counts that the scores kernel left
   if (blockIdx.x < rows) {   // one output row
     constexpr int L = D / 4, KS = kThreads / L;
@@ -781,13 +789,18 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   const int64_t runs = (most + a.min_run - 1) / a.min_run;
   const int grid = static_cast<int>(runs < kDecodeCtas ? runs : kDecodeCtas);
   if (a.tc && (e = launch_decode_prefix(maps, a, false, ctx, st)) != cudaSuccess) return e;
-  decode_scores_kernel<T, D, TW><<<grid, kThreads, smem_scores, st>>>(a);
+  if (a.tc) {
+    e = launch_dependent(decode_scores_kernel<T, D, TW>, grid, kThreads, smem_scores, st, a);
+    if (e != cudaSuccess) return e;
+  } else {
+    decode_scores_kernel<T, D, TW><<<grid, kThreads, smem_scores, st>>>(a);
+  }
   if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
-  decode_values_kernel<T, D, TW><<<grid, kThreads, smem_values, st>>>(a);
+  e = launch_dependent(decode_values_kernel<T, D, TW>, grid, kThreads, smem_values, st, a);
+  if (e != cudaSuccess) return e;
   const int64_t join = static_cast<int64_t>(a.B) * a.Hq +
                        (a.weight ? static_cast<int64_t>(a.B) * a.Hkv * ((a.C + kWeightKeys - 1) / kWeightKeys) : 0);
-  decode_join_kernel<T, D><<<static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(decode_join_kernel<T, D>, static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st, a);
 }
 template <typename T, int D>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {

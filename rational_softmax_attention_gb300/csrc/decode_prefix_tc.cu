@@ -90,9 +90,9 @@ __device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row) {
   const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
   float m = -INFINITY;
 #pragma unroll 8
-  for (int i = 0; i < shared; ++i) m = fmaxf(m, p[i]);
+  for (int i = 0; i < shared; ++i) m = fmaxf(m, __ldcg(p + i));
 #pragma unroll 4
-  for (int i = 0; i < own; ++i) m = fmaxf(m, p[a.pslots + i]);
+  for (int i = 0; i < own; ++i) m = fmaxf(m, __ldcg(p + a.pslots + i));
   return m;
 }
 
@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  if constexpr (VALUES) await_previous();   // all maxima
+  release_dependents();                     // the sequences' own values need no more than that either
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -404,7 +406,9 @@ cudaError_t go(const PrefixMaps& maps, const DecodeArgs& a, const LaunchCtx& ctx
                                              Cfg<D, VALUES>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int pairs = (a.B * a.G + NGROUP * BM - 1) / (NGROUP * BM);
-  kernel<<<a.Hkv * pairs * a.pslots, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st>>>(maps, a, ctx);
+  const unsigned grid = static_cast<unsigned>(a.Hkv) * pairs * a.pslots;
+  if constexpr (VALUES) return launch_dependent(kernel, grid, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st, maps, a, ctx);
+  kernel<<<grid, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st>>>(maps, a, ctx);
   return cudaGetLastError();
 }
 

@@ -5,9 +5,13 @@
 // weights the lowest slots).  The kept entries' keys, values and weights are written, in their
 // order, to the first m slots of another cache.
 //
-//   select   one CTA per (sequence, head): the threshold by a radix selection over the weights'
-//            order-preserving bits, then the kept slots in order by prefix sums;
-//   gather   the kept entries, 16 bytes per lane: HBM-bound.
+//   select   a cluster of CTAs per (sequence, head), each with a slice of the entries: the threshold
+//            by a radix selection over the weights' order-preserving bits (11, 11 and 10 at a
+//            time; the CTAs' counts are added through distributed shared memory), then the kept
+//            slots in order by prefix sums.  Counts are integers, so nothing depends on the order
+//            of the atomics.  A CTA's first 8192 weights stay in registers between the passes.
+//   gather   the kept entries, 16 bytes per lane.
+// Bound: select by latency (four passes and their barriers), gather by HBM.
 #include "kernels.cuh"
 
 namespace raattn {
@@ -49,78 +53,159 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total
   return inc - v + (warp ? warp_sums[warp - 1] : 0);
 }
 
+constexpr int kPer = 4;                        // consecutive entries of a thread in a chunk
+constexpr int kChunk = kSelThreads * kPer;
+constexpr int kHeld = 2;                       // chunks held in registers
+
+template <int S>   // CTAs of a cluster
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[kBins];
+  __shared__ int2 hist[kBins / 2];
   __shared__ int warp_sums[32];
-  __shared__ uint32_t found;
-  __shared__ int left;
-  const int bk = blockIdx.x, b = bk / a.Hkv, kv = bk - b * a.Hkv;
+  __shared__ int found, left;
+  __shared__ int2 counts;   // entries of this CTA's slice above the threshold, and equal to it
+  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int bk = blockIdx.x / S, b = bk / a.Hkv, kv = bk - b * a.Hkv;
+  release_dependents();
   const int n = min(max(a.length[b], 0), a.C), m = min(n, a.keep), last = min(a.recent, n);
   const int cand = n - last, need = m - last;
   const float* w = a.weight + static_cast<int64_t>(bk) * a.C;
   int* index = a.index + static_cast<int64_t>(bk) * a.keep;
-  if (kv == 0 && threadIdx.x == 0) a.length_out[b] = m;
-  for (int i = m + threadIdx.x; i < a.keep; i += kSelThreads) index[i] = -1;
-  if (need == cand) {   // everything stays
-    for (int i = threadIdx.x; i < m; i += kSelThreads) index[i] = i;
-    return;
+  if (rank == 0 && kv == 0 && threadIdx.x == 0) a.length_out[b] = m;
+  for (int i = m + rank * kSelThreads + threadIdx.x; i < a.keep; i += S * kSelThreads) index[i] = -1;
+  for (int i = rank * kSelThreads + threadIdx.x; i < last; i += S * kSelThreads) index[need + i] = cand + i;
+  if (need == cand || need == 0) {   // all others stay, or none
+    for (int i = rank * kSelThreads + threadIdx.x; i < need; i += S * kSelThreads) index[i] = i;
+    return;   // uniform over the cluster
   }
-  // The threshold: the need-th largest, 11 + 11 + 10 bits at a time.  `rank` counts what is still
-  // wanted among the entries that share the bits found so far.
+  // this CTA's slice, in whole chunks
+  const int chunks = (cand + kChunk - 1) / kChunk, per = (chunks + S - 1) / S;
+  const int q0 = min(rank * per, chunks), q1 = min(q0 + per, chunks);
+  auto load = [&](int q, uint32_t (&u)[kPer]) {   // 0, below every weight's bits, past the last
+    const int i = q * kChunk + threadIdx.x * kPer;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) u[j] = i + j < cand ? order_bits(w[i + j]) : 0u;
+  };
+  uint32_t held[kHeld][kPer];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (q0 + h < q1) load(q0 + h, held[h]);
+  // f(entry bits of a chunk) for every chunk of the slice
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (q0 + h < q1) f(q0 + h, held[h]);
+    for (int q = q0 + kHeld; q < q1; ++q) {
+      uint32_t u[kPer];
+      load(q, u);
+      f(q, u);
+    }
+  };
+  // The threshold: the need-th largest.  `rest` counts what is still wanted among the entries that
+  // share the bits found so far.
   uint32_t prefix = 0;
-  int rank = need;
-  int done = 0;   // bits found
-  if (need > 0) {
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
-      for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = threadIdx.x; i < cand; i += kSelThreads) {
-        const uint32_t u = order_bits(w[i]);
-        if (done == 0 || u >> (32 - done) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1u)], 1);
+  int rest = need, done = 0;   // done: bits found
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
+    hist[threadIdx.x] = make_int2(0, 0);
+    __syncthreads();
+    each([&](int, const uint32_t (&u)[kPer]) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (u[j] && (done == 0 || u[j] >> (32 - done) == prefix))
+          atomicAdd(&reinterpret_cast<int*>(hist)[(u[j] >> shift) & ((1u << bits) - 1u)], 1);
+    });
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    // bins from the top: thread t owns the t-th pair of bins counted from the highest
+    const int pair = kBins / 2 - 1 - static_cast<int>(threadIdx.x);
+    int2 c = make_int2(0, 0);
+    if (S > 1) {
+      const uint32_t at = smem_u32(&hist[pair]);
+#pragma unroll
+      for (int r = 0; r < S; ++r) {
+        int x, y;
+        asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(mapa_shared(at, r)) : "memory");
+        c.x += x;
+        c.y += y;
       }
-      __syncthreads();
-      // bins from the top: thread t owns the t-th pair of bins counted from the highest
-      const int hi = kBins - 1 - 2 * static_cast<int>(threadIdx.x), c1 = hist[hi], c0 = hist[hi - 1];
-      int total;
-      const int before = block_exclusive(c1 + c0, warp_sums, &total);
-      if (before < rank && rank <= before + c1 + c0) {
-        const bool upper = rank <= before + c1;
-        found = static_cast<uint32_t>(upper ? hi : hi - 1);
-        left = rank - before - (upper ? 0 : c1);
-      }
-      __syncthreads();
-      prefix = prefix << bits | found;
-      rank = left;
-      done += bits;
-      __syncthreads();
+    } else {
+      c = hist[pair];
+    }
+    int total;
+    const int before = block_exclusive(c.x + c.y, warp_sums, &total);
+    if (before < rest && rest <= before + c.x + c.y) {
+      const bool upper = rest <= before + c.y;
+      found = 2 * pair + (upper ? 1 : 0);
+      left = rest - before - (upper ? 0 : c.y);
+    }
+    if (S > 1) cluster_sync();   // the counts have been read, too
+    else __syncthreads();
+    prefix = prefix << bits | static_cast<uint32_t>(found);
+    rest = left;
+    done += bits;
+  }
+  // The kept slots in order: entries above the threshold and the first `rest` equal to it.  Both
+  // counts of a chunk (at most 4096) go through one prefix sum.
+  int above = 0, equal = 0;   // of the entries before this chunk
+  if (S > 1) {
+    int mine = 0;
+    each([&](int, const uint32_t (&u)[kPer]) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) mine += u[j] > prefix ? 1 : 0;
+    });
+    int ties = 0;
+    each([&](int, const uint32_t (&u)[kPer]) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) ties += u[j] == prefix ? 1 : 0;
+    });
+    int total;
+    block_exclusive(mine, warp_sums, &total);
+    const int gt = total;
+    __syncthreads();
+    block_exclusive(ties, warp_sums, &total);
+    if (threadIdx.x == 0) counts = make_int2(gt, total);
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      int x, y;
+      asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                   : "=r"(x), "=r"(y)
+                   : "r"(mapa_shared(smem_u32(&counts), r))
+                   : "memory");
+      above += x;
+      equal += y;
     }
   }
-  // The kept slots in order: entries above the threshold and the first `rank` equal to it.
-  int kept = 0, equal = 0;
-  for (int i0 = 0; i0 < cand; i0 += kSelThreads) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t u = i < cand && need > 0 ? order_bits(w[i]) : 0u;
-    const bool in = i < cand && need > 0;
-    const int eq = in && u == prefix, gt = in && u > prefix;
-    int teq, tall;
-    const int eq_before = equal + block_exclusive(eq, warp_sums, &teq);
-    const int take = gt || (eq && eq_before < rank);
-    const int at = kept + block_exclusive(take, warp_sums, &tall);
-    if (take) index[at] = i;
-    kept += tall;
-    equal += teq;
-  }
-  for (int i = threadIdx.x; i < last; i += kSelThreads) index[need + i] = cand + i;
+  each([&](int q, const uint32_t (&u)[kPer]) {
+    int gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      gt += u[j] > prefix ? 1 : 0;
+      eq += u[j] == prefix ? 1 : 0;
+    }
+    int total;
+    const int x = block_exclusive(gt << 16 | eq, warp_sums, &total);
+    int a0 = above + (x >> 16), e0 = equal + (x & 0xffff);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const bool hi = u[j] > prefix, tie = u[j] == prefix;
+      if (hi || (tie && e0 < rest)) index[a0 + min(e0, rest)] = q * kChunk + threadIdx.x * kPer + j;
+      a0 += hi ? 1 : 0;
+      e0 += tie ? 1 : 0;
+    }
+    above += total >> 16;
+    equal += total & 0xffff;
+  });
+  if (S > 1) cluster_sync();   // nobody leaves while its counts may be read
 }
 
 constexpr int kGatherThreads = 256;
 
-// Lane groups of one entry's vectors; an entry's K and V vectors are read together.
+// Threads over the kept entries' vectors; an entry's K and V vectors are read together.
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a) {
   const int vecs = a.row_bytes / 16;
   const int64_t per_head = static_cast<int64_t>(a.keep) * vecs;
   const int64_t total = static_cast<int64_t>(a.B) * a.Hkv * per_head;
+  await_previous();
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGatherThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kGatherThreads) {
     const int64_t bk = i / per_head, r = i - bk * per_head;
@@ -135,14 +220,36 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
   }
 }
 
+template <int S>
+cudaError_t select(const EvictArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.Hkv * S);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = S > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<S>, a);
+}
+
 }  // namespace
 
+// CTAs of a row's cluster: as many as the SMs hold at once (two of 1024 threads each), while each
+// still gets a chunk of 4096 entries.  32 rows of 32768: 46 us with one, B32 H8 of 4352: 12 us.
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
-  evict_select_kernel<<<a.B * a.Hkv, kSelThreads, 0, st>>>(a);
-  const int64_t total = static_cast<int64_t>(a.B) * a.Hkv * a.keep * (a.row_bytes / 16);
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv, chunks = (a.C + kChunk - 1) / kChunk;
+  int s = 1;
+  while (s < 8 && rows * 2 * s <= 2 * kSms && 2 * s <= chunks) s *= 2;
+  const cudaError_t e = s == 8 ? select<8>(a, st) : s == 4 ? select<4>(a, st) : s == 2 ? select<2>(a, st) : select<1>(a, st);
+  if (e != cudaSuccess) return e;
+  const int64_t total = rows * a.keep * (a.row_bytes / 16);
   const int64_t blocks = (total + kGatherThreads - 1) / kGatherThreads;
-  evict_gather_kernel<<<static_cast<int>(blocks < 16 * kSms ? blocks : 16 * kSms), kGatherThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(evict_gather_kernel, static_cast<unsigned>(blocks < 16 * kSms ? blocks : 16 * kSms),
+                          kGatherThreads, 0, st, a);
 }
 
 }  // namespace raattn

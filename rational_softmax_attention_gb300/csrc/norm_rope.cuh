@@ -16,9 +16,9 @@
 // Bound: HBM, with the issue slots close behind.  A lane holds two 16-byte vectors of a row (a row
 // lies across D * size / 32 lanes), chosen so that in the half-split form it holds both members of
 // its pairs: the rotation needs no exchange between lanes, and the row sums are a few shuffles.  A
-// CTA works on one kind of row (queries, keys or values; the CTAs are shared out by their bytes)
-// and takes a tile of tokens at a time; a lane group stays with one token and walks its heads, so what
-// depends on the token alone is formed once and not per row.  In the forward the norm's weight w and
+// CTA takes a tile of tokens at a time; a lane group stays with one token and walks its heads, so what
+// depends on the token alone is formed once and not per row.  (In the backward a CTA works on one
+// kind of row, queries, keys or values, so that a lane holds one kind's sums.)  In the forward the norm's weight w and
 // the rotation fold into two factors and an addend,
 //   y_j = r (x_j A_j + x_partner B_j) + C_j,  A = w cos, B = +-w_partner sin, C = the rotated bias,
 // and all arithmetic runs as packed pairs of floats.  Each thread copies the next rows' vectors
@@ -283,9 +283,10 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Shares `most` CTAs among the kinds by their cost per head, and sets the tiles' tokens: as many as
-// leave no lane group without a head; then more, since what a token costs once is shared by the
-// heads that one lane group walks, while each CTA still gets four tiles or more.
+// Shares `most` CTAs among the kinds by their cost per head, and sets the tiles' tokens: a tile for
+// every CTA first; then as many tokens as leave no lane group without a head, and more, since what
+// a token costs once is shared by the heads that one lane group walks, while each CTA still gets
+// four tiles.
 inline void plan_work(NormRopeShape* a, int es, int most, const int (&cost)[3]) {
   const int groups = kThreads / (a->D * es / 32);
   const int64_t tokens = static_cast<int64_t>(a->B) * a->N;
@@ -295,7 +296,7 @@ inline void plan_work(NormRopeShape* a, int es, int most, const int (&cost)[3]) 
     const int64_t share = static_cast<int64_t>(most) * cost[k] * heads[k] / all;
     const int64_t ctas = share < 1 ? 1 : share;
     int t = 1;
-    while (2 * t <= groups && t < kMaxTile && (groups / t > heads[k] || tokens / (2 * t) >= 4 * ctas)) t *= 2;
+    while (2 * t <= groups && t < kMaxTile && tokens / (2 * t) >= (groups / t > heads[k] ? ctas : 4 * ctas)) t *= 2;
     const int64_t tiles = (tokens + t - 1) / t;
     a->tiles[k] = t;
     a->ctas[k] = static_cast<int>(tiles < ctas ? tiles : ctas);

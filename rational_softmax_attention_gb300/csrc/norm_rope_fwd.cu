@@ -13,65 +13,66 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_fwd_kernel(const NormRo
   constexpr int E = Vec<T>::E, P = E / 2, L = D / E / 2, NG = kThreads / L;
   __shared__ Tables tb;
   __shared__ uint4 ring[kAhead][2][kThreads];
-  const Work wk = work_of(a);
+  const int tile_tokens = a.tiles[0];
   const int g = threadIdx.x / L, gl = threadIdx.x % L;
-  const int tl = g % wk.tile, hs = g / wk.tile, hstep = NG / wk.tile;
-  const int rows = (wk.heads + hstep - 1) / hstep;   // of every lane group; some may be no head
+  const int tl = g % tile_tokens, hs = g / tile_tokens, hstep = NG / tile_tokens;
+  // rows of every lane group, query and key or value heads; some may be no head
+  const int q_rows = (a.Hq + hstep - 1) / hstep, kv_rows = (a.Hkv + hstep - 1) / hstep;
   const LaneMap lm = lane_map<E, L>(a, gl);
   const int tokens = a.B * a.N;   // fits, and so does a tile past the last
-  const int tiles = (tokens - 1) / wk.tile + 1;
+  const int tiles = (tokens - 1) / tile_tokens + 1;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const bool turns = a.pairs > 0 && wk.kind < 2, whole = 2 * a.pairs == D;
+  const bool turns = a.pairs > 0, whole = 2 * a.pairs == D;
   if (turns) init_turns(tb, a);
   int buf = 0;
-  for (int tile = wk.first; tile < tiles; tile += wk.step, buf ^= 1) {
-    const int tok = tile * wk.tile + tl;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    const int tok = tile * tile_tokens + tl;
     const bool there = tok < tokens;
     const int b = there ? tok / a.N : 0, n = there ? tok - b * a.N : 0;
-    const T* src = static_cast<const T*>(a.qkv) + b * a.batch_stride + n * a.token_stride + (wk.head0 + hs) * D;
-    int ahead = 0;
+    const T* row = static_cast<const T*>(a.qkv) + b * a.batch_stride + n * a.token_stride + hs * D;
+    // the rows in order: query heads, key heads, value heads
+    const T* src = row;
+    int f_kind = 0, f_row = 0, fetched = 0, used = 0;
     auto fetch = [&]() {
-      if (ahead < rows) {   // nothing past the tile's rows: every copy is waited for before its slot is used again
-        const bool in = there && hs + ahead * hstep < wk.heads;
-        uint4* slot = &ring[ahead % kAhead][0][threadIdx.x];
+      if (f_kind < 3) {   // nothing past the tile's rows: every copy is waited for before its slot is used again
+        const bool in = there && hs + f_row * hstep < (f_kind ? a.Hkv : a.Hq);
+        uint4* slot = &ring[fetched % kAhead][0][threadIdx.x];
         copy_own(slot, in ? src + lm.v0 * E : a.qkv, in);
         copy_own(slot + kThreads, in ? src + lm.v1 * E : a.qkv, in);
+        src += hstep * D;
+        if (++f_row == (f_kind ? kv_rows : q_rows)) {
+          f_row = 0;
+          src = row + (++f_kind == 1 ? a.Hq : a.Hq + a.Hkv) * D;
+        }
       }
       copy_commit();
-      ++ahead;
-      src += hstep * D;
+      ++fetched;
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch();
-    // where this token's rows go; keys and values to a slot of the cache, if it is one
-    bool writes = there;
-    int64_t out_row, out_step;
-    if (wk.kind == 0) {
-      out_row = static_cast<int64_t>(b) * a.Hq * a.N + n;
-      out_step = a.N;
-    } else {
-      int64_t slot = n;
-      if (io.start) {
-        slot += io.start[b];
-        if (slot < 0 || slot >= io.capacity || (io.count && n >= io.count[b])) writes = false;
-      }
-      out_row = static_cast<int64_t>(b) * a.Hkv * io.capacity + slot;
-      out_step = io.capacity;
+    // keys and values go to a slot of the cache, if it is one
+    bool kv_writes = there;
+    int64_t slot = n;
+    if (io.start) {
+      slot += io.start[b];
+      if (slot < 0 || slot >= io.capacity || (io.count && n >= io.count[b])) kv_writes = false;
     }
-    T* out = static_cast<T*>(wk.kind == 0 ? io.q : wk.kind == 1 ? io.k : io.v) + (out_row + hs * out_step) * D;
-    out_step *= static_cast<int64_t>(hstep) * D;
-    float2 A0[P], B0[P], C0[P], A1[P], B1[P], C1[P];
-    if (wk.kind < 2) {
-      if (turns) {   // under the first rows' copies
-        fill_table(tb, buf, a, tile * wk.tile, wk.tile);
-        __syncthreads();
+    const int64_t kv_at = (static_cast<int64_t>(b) * a.Hkv + hs) * io.capacity + slot;
+    if (turns) {   // under the first rows' copies
+      fill_table(tb, buf, a, tile * tile_tokens, tile_tokens);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+      float2 A0[P], B0[P], C0[P], A1[P], B1[P], C1[P];
+      if (turns) {
         float cs[E], sn[E];
         load_turn<E>(cs, sn, tb, buf, tl, lm, a, whole);
         factors<E>(cs, sn, a.interleaved, A0, B0, A1, B1);
       }
       if (NORM != RA_NORM_NONE) {
-        const uint4* w = reinterpret_cast<const uint4*>(wk.kind ? a.kw : a.qw);
-        const uint4* bias = NORM == RA_NORM_LAYER ? reinterpret_cast<const uint4*>(wk.kind ? a.kb : a.qb) : nullptr;
+        const uint4* w = reinterpret_cast<const uint4*>(kind ? a.kw : a.qw);
+        const uint4* bias = NORM == RA_NORM_LAYER ? reinterpret_cast<const uint4*>(kind ? a.kb : a.qb) : nullptr;
         float2 w0[P], w1[P], wp0[P], wp1[P];
         if (NORM == RA_NORM_LAYER) {   // C: the bias, turned by the factors alone
           Vec<T>::get(bias ? bias[lm.v0] : zero, C0);
@@ -98,15 +99,17 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_fwd_kernel(const NormRo
           }
         }
       }
-    }
+      const int heads = kind ? a.Hkv : a.Hq, rows = kind ? kv_rows : q_rows;
+      const bool writes = kind ? kv_writes : there;
+      T* out = static_cast<T*>(kind ? io.k : io.q) +
+               (kind ? kv_at : (static_cast<int64_t>(b) * a.Hq + hs) * a.N + n) * D;
+      const int64_t out_step = static_cast<int64_t>(hstep) * (kind ? io.capacity : a.N) * D;
 #pragma unroll 1
-    for (int i = 0; i < rows; ++i) {
-      copy_wait<kAhead - 1>();
-      uint4 u0 = ring[i % kAhead][0][threadIdx.x], u1 = ring[i % kAhead][1][threadIdx.x];
-      if (wk.kind < 2) {
+      for (int i = 0; i < rows; ++i, ++used) {
+        copy_wait<kAhead - 1>();
         float2 x0[P], x1[P], p0[P], p1[P];
-        Vec<T>::get(u0, x0);
-        Vec<T>::get(u1, x1);
+        Vec<T>::get(ring[used % kAhead][0][threadIdx.x], x0);
+        Vec<T>::get(ring[used % kAhead][1][threadIdx.x], x1);
         if (NORM == RA_NORM_LAYER) {
           const float2 m = f2(-row_sum<P, L>(x0, x1) * (1.0f / D));
 #pragma unroll
@@ -141,22 +144,32 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_fwd_kernel(const NormRo
             x1[k] = __fmul2_rn(x1[k], r);
           }
         }
-        u0 = Vec<T>::put(x0);
-        u1 = Vec<T>::put(x1);
+        if (writes && hs + i * hstep < heads) {
+          reinterpret_cast<uint4*>(out)[lm.v0] = Vec<T>::put(x0);
+          reinterpret_cast<uint4*>(out)[lm.v1] = Vec<T>::put(x1);
+        }
+        out += out_step;
+        fetch();   // into the slot just read: after the stores, which needed what it held
       }
-      if (writes && hs + i * hstep < wk.heads) {
-        reinterpret_cast<uint4*>(out)[lm.v0] = u0;
-        reinterpret_cast<uint4*>(out)[lm.v1] = u1;
+    }
+    T* out = static_cast<T*>(io.v) + kv_at * D;
+    const int64_t out_step = static_cast<int64_t>(hstep) * io.capacity * D;
+#pragma unroll 1
+    for (int i = 0; i < kv_rows; ++i, ++used) {
+      copy_wait<kAhead - 1>();
+      if (kv_writes && hs + i * hstep < a.Hkv) {
+        reinterpret_cast<uint4*>(out)[lm.v0] = ring[used % kAhead][0][threadIdx.x];
+        reinterpret_cast<uint4*>(out)[lm.v1] = ring[used % kAhead][1][threadIdx.x];
       }
       out += out_step;
-      fetch();   // into the slot just read: after the stores, which needed what it held
+      fetch();
     }
   }
 }
 
 template <typename T, int D>
 void go(const NormRopeShape& a, const NormRopeFwd& io, cudaStream_t st) {
-  const int grid = a.ctas[0] + a.ctas[1] + a.ctas[2];
+  const int grid = a.ctas[0];
   if (a.norm == RA_NORM_NONE) norm_rope_fwd_kernel<T, D, RA_NORM_NONE><<<grid, kThreads, 0, st>>>(a, io);
   else if (a.norm == RA_NORM_RMS) norm_rope_fwd_kernel<T, D, RA_NORM_RMS><<<grid, kThreads, 0, st>>>(a, io);
   else norm_rope_fwd_kernel<T, D, RA_NORM_LAYER><<<grid, kThreads, 0, st>>>(a, io);
@@ -165,7 +178,15 @@ void go(const NormRopeShape& a, const NormRopeFwd& io, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_norm_rope_fwd(NormRopeShape a, const NormRopeFwd& io, bool bf16, cudaStream_t st) {
-  plan_work(&a, bf16 ? 2 : 4, 2 * kSms, {1, 1, 1});
+  // Tokens of a tile: enough tiles for every SM first; then as many tokens as leave no lane group
+  // without a head, and more, since what a token costs once is shared by the heads that one lane
+  // group walks, while every CTA still gets eight tiles.
+  const int groups = kThreads / (a.D * (bf16 ? 2 : 4) / 32), tokens = a.B * a.N, most = 2 * kSms;
+  int t = 1;
+  while (2 * t <= groups && t < kMaxTile && tokens / (2 * t) >= (groups / t > a.Hq ? kSms : 8 * most)) t *= 2;
+  const int tiles = (tokens - 1) / t + 1;
+  a.tiles[0] = t;
+  a.ctas[0] = tiles < most ? tiles : most;
   if (bf16) {
     if (a.D == 16) go<__nv_bfloat16, 16>(a, io, st);
     if (a.D == 32) go<__nv_bfloat16, 32>(a, io, st);

@@ -11,24 +11,42 @@ kernels behind include/raattn.h, on torch's current stream of the tensors' devic
 """
 from __future__ import annotations
 
-import contextlib
+import ctypes
+import functools
 
 import torch
 
-from . import _check, _dtype_code, _ptr, _require_cuda, _stream, lib
+from . import _check, _dtype_code, lib
 
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
-_SAME = contextlib.nullcontext()
 
 
-def _on(device):
-    """Makes `device` current for a call whose tensors live there."""
-    return _SAME if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+# These calls are short on the GPU (single tokens), so their marshalling is kept lean: addresses are
+# passed as plain integers, and what follows from sizes and options alone is worked out once.
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, device, *args):
+    """Calls a libraattn entry point on torch's current stream of `device`, which becomes the current one."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if code:
+        _check(name, code)
 
 
 def _check_tensor(name, t, shape, dtype, device):
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_cuda(name, t):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor (there is no CPU path)")
 
 
 def ra_rope_frequencies(sections, theta=10000.0, per_axis=False, device="cuda"):
@@ -43,79 +61,94 @@ def ra_rope_frequencies(sections, theta=10000.0, per_axis=False, device="cuda"):
     return torch.cat([float(theta) ** (-torch.arange(n, dtype=torch.float64) / n) for n in parts]).to(device)
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_rope_sizes(width, num_heads, num_kv_heads, sections):
+    """(Hq, Hkv, D, pairs, axes, host array of the sections) of a projection `width` wide."""
+    Hq, Hkv = int(num_heads), int(num_heads if num_kv_heads is None else num_kv_heads)
+    if Hq < 1 or Hkv < 1 or width < 1 or width % (Hq + 2 * Hkv):
+        raise ValueError("qkv must be [B, N, (num_heads + 2 num_kv_heads) * head_dim]")
+    D = width // (Hq + 2 * Hkv)
+    if not sections:
+        return Hq, Hkv, D, 0, 0, None
+    secs = [int(s) for s in sections]
+    if min(secs) < 1 or 2 * sum(secs) > D:
+        raise ValueError("sections must be positive pair counts with 2 * sum(sections) <= head_dim")
+    return Hq, Hkv, D, sum(secs), len(secs), (ctypes.c_int32 * len(secs))(*secs)
+
+
 def _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies, sections, positions, interleaved):
-    """Checks the arguments that the forward, the append and the backward share; returns the C
-    call's leading arguments, what has to stay alive until it returns, and (B, N, Hq, Hkv, D)."""
+    """Checks the arguments that the forward, the append and the backward share; returns the C call's
+    leading arguments, the tensors that have to stay alive until it returns, and (B, N, Hq, Hkv, D, dtype code)."""
     if qkv.dim() != 3 or not qkv.is_cuda:
         raise ValueError("qkv must be a CUDA tensor [B, N, (num_heads + 2 num_kv_heads) * head_dim]")
     dtype, device = qkv.dtype, qkv.device
-    _dtype_code(dtype)
-    Hq, Hkv = int(num_heads), int(num_heads if num_kv_heads is None else num_kv_heads)
-    B, N, W = qkv.shape
-    if Hq < 1 or Hkv < 1 or W % (Hq + 2 * Hkv) or B < 1 or N < 1 or W < 1:
-        raise ValueError("qkv must be [B, N, (num_heads + 2 num_kv_heads) * head_dim], with at least one token")
-    D = W // (Hq + 2 * Hkv)
-    vec = 16 // qkv.element_size()
-    if qkv.stride(2) != 1 or qkv.stride(0) % vec or qkv.stride(1) % vec or qkv.data_ptr() % 16:
+    code = _dtype_code(dtype)
+    B, N, width = qkv.shape
+    Hq, Hkv, D, pairs, axes, secs = _norm_rope_sizes(width, num_heads, num_kv_heads,
+                                                     None if sections is None else tuple(sections))
+    if B < 1 or N < 1:
+        raise ValueError("qkv must hold at least one token")
+    mask = 7 if code else 3
+    row, tok, one = qkv.stride()
+    if one != 1 or row & mask or tok & mask or qkv.data_ptr() & 15:
         qkv = qkv.contiguous()
-    if norm not in _NORMS:
+        row, tok, one = qkv.stride()
+    kind = _NORMS.get(norm)
+    if kind is None:
         raise ValueError("norm must be 'none', 'layer' or 'rms'")
     qw, qb, kw, kb = params
-    if norm == "none" and any(p is not None for p in params):
-        raise ValueError("norm='none' takes no weights and no biases")
-    if norm != "none" and (qw is None or kw is None):
-        raise ValueError("q_weight and k_weight are required with a norm")
-    if norm == "rms" and (qb is not None or kb is not None):
-        raise ValueError("norm='rms' takes no biases")
-    for name, p in zip(("q_weight", "q_bias", "k_weight", "k_bias"), params):
-        if p is not None:
-            _check_tensor(name, p, (D,), dtype, device)
-    keep = [qkv, frequencies]
-    axes, pos, pos_axis, pos_batch, secs = 0, None, 0, 0, None
-    if sections is not None and len(sections):
-        secs = tuple(int(s) for s in sections)
-        axes, pairs = len(secs), sum(secs)
-        if min(secs) < 1 or 2 * pairs > D:
-            raise ValueError("sections must be positive pair counts with 2 * sum(sections) <= head_dim")
+    if kind == 0:
+        if not (qw is None and qb is None and kw is None and kb is None):
+            raise ValueError("norm='none' takes no weights and no biases")
+    else:
+        if qw is None or kw is None:
+            raise ValueError("q_weight and k_weight are required with a norm")
+        _check_tensor("q_weight", qw, (D,), dtype, device)
+        _check_tensor("k_weight", kw, (D,), dtype, device)
+        if qb is not None or kb is not None:
+            if kind == 2:
+                raise ValueError("norm='rms' takes no biases")
+            if qb is not None:
+                _check_tensor("q_bias", qb, (D,), dtype, device)
+            if kb is not None:
+                _check_tensor("k_bias", kb, (D,), dtype, device)
+    pos, pos_axis, pos_batch = None, 0, 0
+    if axes:
         if frequencies is None or positions is None:
             raise ValueError("sections need frequencies and positions")
         _check_tensor("frequencies", frequencies, (pairs,), torch.float64, device)
         pos = positions
-        if pos.dtype not in (torch.int32, torch.int64) or pos.device != device or not 1 <= pos.dim() <= 3:
-            raise ValueError("positions must be an int32 or int64 tensor [N], [B, N] or [axes, B, N] on qkv's device")
-        pos = pos.to(torch.int32)
-        pos = pos.view((1,) * (3 - pos.dim()) + tuple(pos.shape))
-        if pos.shape[0] not in (1, axes) or pos.shape[1] not in (1, B) or pos.shape[2] != N:
-            raise ValueError("positions must broadcast to [axes, B, N]")
-        if pos.stride(2) != 1 and N > 1:
+        if pos.dtype is not torch.int32:
+            if pos.dtype is not torch.int64:
+                raise ValueError("positions must be an int32 or int64 tensor")
+            pos = pos.to(torch.int32)
+        d = pos.dim()
+        shape = pos.shape
+        if (pos.device != device or not 1 <= d <= 3 or shape[-1] != N or (d > 1 and shape[-2] not in (1, B))
+                or (d > 2 and shape[0] not in (1, axes))):
+            raise ValueError("positions must be [N], [B, N] or [axes, B, N] on qkv's device, or broadcast to it")
+        if pos.stride(-1) != 1 and N > 1:
             pos = pos.contiguous()
-        pos_axis = pos.stride(0) if pos.shape[0] > 1 else 0
-        pos_batch = pos.stride(1) if pos.shape[1] > 1 else 0
-        keep.append(pos)
-        secs = _int_array(secs)
-        keep.append(secs)
+        if d > 1 and shape[-2] > 1:
+            pos_batch = pos.stride(-2)
+        if d > 2 and shape[0] > 1:
+            pos_axis = pos.stride(0)
     elif frequencies is not None or positions is not None:
         raise ValueError("frequencies and positions need sections")
-    lead = (_ptr(qkv), qkv.stride(0), qkv.stride(1), _ptr(qw), _ptr(qb), _ptr(kw), _ptr(kb), _NORMS[norm], float(eps),
-            _ptr(frequencies) if axes else None, _ptr(pos), pos_axis, pos_batch, secs, axes, 1 if interleaved else 0)
-    return lead, keep, (B, N, Hq, Hkv, D)
-
-
-def _int_array(values):
-    import ctypes
-    return (ctypes.c_int32 * len(values))(*values)
+    lead = (qkv.data_ptr(), row, tok, _addr(qw), _addr(qb), _addr(kw), _addr(kb), kind, eps,
+            frequencies.data_ptr() if axes else None, pos.data_ptr() if axes else None, pos_axis, pos_batch, secs,
+            axes, 1 if interleaved else 0)
+    return lead, (qkv, pos), (B, N, Hq, Hkv, D, code)
 
 
 def _norm_rope_forward(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies, sections, positions, interleaved):
-    lead, keep, (B, N, Hq, Hkv, D) = _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies,
-                                                     sections, positions, interleaved)
-    q = torch.empty((B, Hq, N, D), dtype=qkv.dtype, device=qkv.device)
-    k = torch.empty((B, Hkv, N, D), dtype=qkv.dtype, device=qkv.device)
-    v = torch.empty((B, Hkv, N, D), dtype=qkv.dtype, device=qkv.device)
-    with _on(qkv.device):
-        _check("ra_qk_norm_rope_fwd", lib().ra_qk_norm_rope_fwd(
-            *lead, _ptr(q), _ptr(k), _ptr(v), None, None, 0, B, N, Hq, Hkv, D, _dtype_code(qkv.dtype),
-            _stream(qkv.device)))
+    lead, keep, (B, N, Hq, Hkv, D, code) = _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps,
+                                                           frequencies, sections, positions, interleaved)
+    q = qkv.new_empty((B, Hq, N, D))
+    k = qkv.new_empty((B, Hkv, N, D))
+    v = qkv.new_empty((B, Hkv, N, D))
+    _call("ra_qk_norm_rope_fwd", qkv.device, *lead, q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None, 0, B, N, Hq,
+          Hkv, D, code)
     return q, k, v
 
 
@@ -140,6 +173,10 @@ class _RaQkNormRopeFn(torch.autograd.Function):
         return (dqkv, *dparams, None, None, None)
 
 
+def _asks(t):
+    return t is not None and t.requires_grad
+
+
 def ra_qk_norm_rope(qkv, num_heads, num_kv_heads=None, *, norm="layer", q_weight=None, q_bias=None, k_weight=None,
                     k_bias=None, eps=1e-5, frequencies=None, sections=None, positions=None, interleaved=False):
     """q [B, num_heads, N, D], k and v [B, num_kv_heads, N, D], ready for ra_attention, from the packed
@@ -150,8 +187,8 @@ def ra_qk_norm_rope(qkv, num_heads, num_kv_heads=None, *, norm="layer", q_weight
     float64 [sum(sections)], see ra_rope_frequencies; positions: integer [N], [B, N] or
     [axes, B, N].  Pair i is dimensions (i, i + R) of the first 2 R, or (2 i, 2 i + 1) when
     interleaved.  Differentiable in qkv, weights and biases."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (qkv, q_weight, q_bias, k_weight, k_bias)):
+    if torch.is_grad_enabled() and (qkv.requires_grad or _asks(q_weight) or _asks(k_weight) or _asks(q_bias)
+                                    or _asks(k_bias)):
         return _RaQkNormRopeFn.apply(qkv, q_weight, q_bias, k_weight, k_bias, frequencies, positions,
                                      (num_heads, num_kv_heads, norm, eps, sections, interleaved))
     return _norm_rope_forward(qkv, num_heads, num_kv_heads, norm, (q_weight, q_bias, k_weight, k_bias), eps,
@@ -164,20 +201,19 @@ def ra_qk_norm_rope_backward(qkv, dq, dk, dv, num_heads, num_kv_heads=None, *, n
     """Gradients of sum(dq q) + sum(dk k) + sum(dv v): (dqkv, dq_weight, dq_bias, dk_weight, dk_bias),
     the parameters' as float32 [D] (None where there is no such parameter)."""
     params = (q_weight, q_bias, k_weight, k_bias)
-    lead, keep, (B, N, Hq, Hkv, D) = _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies,
-                                                     sections, positions, interleaved)
-    for name, t, h in (("dq", dq, Hq), ("dk", dk, Hkv), ("dv", dv, Hkv)):
-        _check_tensor(name, t, (B, h, N, D), qkv.dtype, qkv.device)
-    L = lib()
-    dqkv = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
+    lead, keep, (B, N, Hq, Hkv, D, code) = _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps,
+                                                           frequencies, sections, positions, interleaved)
+    device = qkv.device
+    _check_tensor("dq", dq, (B, Hq, N, D), qkv.dtype, device)
+    _check_tensor("dk", dk, (B, Hkv, N, D), qkv.dtype, device)
+    _check_tensor("dv", dv, (B, Hkv, N, D), qkv.dtype, device)
+    dqkv = qkv.new_empty(qkv.shape)
     dparams = ws = None
     if norm != "none":
-        dparams = torch.empty((4, D), dtype=torch.float32, device=qkv.device)
-        ws = torch.empty(max(L.ra_qk_norm_rope_bwd_workspace_size(D), 16), dtype=torch.uint8, device=qkv.device)
-    with _on(qkv.device):
-        _check("ra_qk_norm_rope_bwd", L.ra_qk_norm_rope_bwd(
-            *lead, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dqkv), _ptr(dparams), _ptr(ws), B, N, Hq, Hkv, D,
-            _dtype_code(qkv.dtype), _stream(qkv.device)))
+        dparams = torch.empty((4, D), dtype=torch.float32, device=device)
+        ws = torch.empty(lib().ra_qk_norm_rope_bwd_workspace_size(D) or 16, dtype=torch.uint8, device=device)
+    _call("ra_qk_norm_rope_bwd", device, *lead, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dqkv.data_ptr(),
+          _addr(dparams), _addr(ws), B, N, Hq, Hkv, D, code)
     return (dqkv, *(None if p is None else dparams[i] for i, p in enumerate(params)))
 
 
@@ -191,22 +227,20 @@ def ra_cache_append(qkv, k, v, length, num_heads, num_kv_heads=None, *, count=No
     count[b] on, and slots outside the cache, are not written.  length (int32 [B]) is read, not
     advanced.  No autograd."""
     params = (q_weight, q_bias, k_weight, k_bias)
-    lead, keep, (B, N, Hq, Hkv, D) = _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies,
-                                                     sections, positions, interleaved)
-    device = qkv.device
+    lead, keep, (B, N, Hq, Hkv, D, code) = _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps,
+                                                           frequencies, sections, positions, interleaved)
+    dtype, device = qkv.dtype, qkv.device
     if k.dim() != 4 or k.shape[2] < 1:
         raise ValueError("the cache must be [B, num_kv_heads, C, head_dim] with C >= 1")
-    C = k.shape[2]
-    _check_tensor("k", k, (B, Hkv, C, D), qkv.dtype, device)
-    _check_tensor("v", v, (B, Hkv, C, D), qkv.dtype, device)
+    shape = (B, Hkv, k.shape[2], D)
+    _check_tensor("k", k, shape, dtype, device)
+    _check_tensor("v", v, shape, dtype, device)
     _check_tensor("length", length, (B,), torch.int32, device)
     if count is not None:
         _check_tensor("count", count, (B,), torch.int32, device)
-    q = torch.empty((B, Hq, N, D), dtype=qkv.dtype, device=device)
-    with _on(device):
-        _check("ra_qk_norm_rope_fwd", lib().ra_qk_norm_rope_fwd(
-            *lead, _ptr(q), _ptr(k), _ptr(v), _ptr(length), _ptr(count), C, B, N, Hq, Hkv, D,
-            _dtype_code(qkv.dtype), _stream(device)))
+    q = qkv.new_empty((B, Hq, N, D))
+    _call("ra_qk_norm_rope_fwd", device, *lead, q.data_ptr(), k.data_ptr(), v.data_ptr(), length.data_ptr(),
+          _addr(count), shape[2], B, N, Hq, Hkv, D, code)
     return q
 
 
@@ -221,12 +255,14 @@ def ra_attention_decode(q, k, v, length, *, prefix_k=None, prefix_v=None, scale=
     16, 32, 64 or 128.  No autograd."""
     if q.dim() != 3 or k.dim() != 4:
         raise ValueError("q must be [B, H, D] and the cache [B, H_kv, C, D]")
-    _require_cuda(q)
+    _check_cuda("q", q)
     B, Hq, D = q.shape
     Hkv, C = k.shape[1], k.shape[2]
-    device, code = q.device, _dtype_code(q.dtype)
-    _check_tensor("k", k, (B, Hkv, C, D), q.dtype, device)
-    _check_tensor("v", v, (B, Hkv, C, D), q.dtype, device)
+    dtype, device = q.dtype, q.device
+    code = _dtype_code(dtype)
+    shape = (B, Hkv, C, D)
+    _check_tensor("k", k, shape, dtype, device)
+    _check_tensor("v", v, shape, dtype, device)
     _check_tensor("length", length, (B,), torch.int32, device)
     if B < 1 or Hkv < 1 or C < 1 or Hq < 1 or D < 1 or Hq % Hkv:
         raise ValueError("the number of query heads must be a multiple of the key heads', and no size 0")
@@ -235,21 +271,23 @@ def ra_attention_decode(q, k, v, length, *, prefix_k=None, prefix_v=None, scale=
         raise ValueError("prefix_k and prefix_v come together")
     if prefix_k is not None:
         P = prefix_k.shape[1] if prefix_k.dim() == 3 else -1
-        _check_tensor("prefix_k", prefix_k, (Hkv, P, D), q.dtype, device)
-        _check_tensor("prefix_v", prefix_v, (Hkv, P, D), q.dtype, device)
+        _check_tensor("prefix_k", prefix_k, (Hkv, P, D), dtype, device)
+        _check_tensor("prefix_v", prefix_v, (Hkv, P, D), dtype, device)
         if P == 0:
             prefix_k = prefix_v = None
     if weight is not None:
         _check_tensor("weight", weight, (B, Hkv, C), torch.float32, device)
-    L = lib()
-    o = torch.empty_like(q)
-    ws = torch.empty(max(L.ra_attention_decode_workspace_size(B, Hq, Hkv, C, P, D, code), 16), dtype=torch.uint8,
-                     device=device)
-    with _on(device):
-        _check("ra_attention_decode", L.ra_attention_decode(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(length), _ptr(prefix_k), _ptr(prefix_v), _ptr(o), _ptr(weight), _ptr(ws),
-            B, Hq, Hkv, C, P, D, float(scale or 0.0), code, _stream(device)))
+    o = q.new_empty((B, Hq, D))
+    nbytes = _decode_workspace(B, Hq, Hkv, C, P, D, code)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    _call("ra_attention_decode", device, q.data_ptr(), k.data_ptr(), v.data_ptr(), length.data_ptr(), _addr(prefix_k),
+          _addr(prefix_v), o.data_ptr(), _addr(weight), ws.data_ptr(), B, Hq, Hkv, C, P, D, scale or 0.0, code)
     return o
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_workspace(B, Hq, Hkv, C, P, D, code):
+    return max(lib().ra_attention_decode_workspace_size(B, Hq, Hkv, C, P, D, code), 16)
 
 
 def ra_cache_evict(k, v, weight, length, keep, *, recent=0, out=None):
@@ -263,7 +301,7 @@ def ra_cache_evict(k, v, weight, length, keep, *, recent=0, out=None):
     entries are made, zero behind the new length."""
     if k.dim() != 4:
         raise ValueError("the cache must be [B, H_kv, C, D]")
-    _require_cuda(k)
+    _check_cuda("k", k)
     B, Hkv, C, D = k.shape
     device, code = k.device, _dtype_code(k.dtype)
     keep, recent = int(keep), int(recent)
@@ -283,12 +321,10 @@ def ra_cache_evict(k, v, weight, length, keep, *, recent=0, out=None):
     _check_tensor("out[0]", ko, (B, Hkv, Co, D), k.dtype, device)
     _check_tensor("out[1]", vo, (B, Hkv, Co, D), k.dtype, device)
     _check_tensor("out[2]", wo, (B, Hkv, Co), torch.float32, device)
-    new_length = torch.empty_like(length)
-    index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=device)
-    with _on(device):
-        _check("ra_cache_evict", lib().ra_cache_evict(
-            _ptr(k), _ptr(v), _ptr(weight), _ptr(length), _ptr(ko), _ptr(vo), _ptr(wo), _ptr(new_length), _ptr(index),
-            B, Hkv, C, Co, D, keep, recent, code, _stream(device)))
+    new_length = length.new_empty((B,))
+    index = length.new_empty((B, Hkv, keep))
+    _call("ra_cache_evict", device, k.data_ptr(), v.data_ptr(), weight.data_ptr(), length.data_ptr(), ko.data_ptr(),
+          vo.data_ptr(), wo.data_ptr(), new_length.data_ptr(), index.data_ptr(), B, Hkv, C, Co, D, keep, recent, code)
     return ko, vo, wo, new_length, index
 
 
