@@ -426,8 +426,8 @@ ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t t
  * with bounded waits, whose giving up ra_device_status() reports.
  * Errors: RA_ERR_ARG for null or misaligned pointers, sizes < 1 (P < 0), H_Q no multiple of
  * H_KV, B H_Q, B H_KV C or H_KV P beyond int32, a bad enum or scale; RA_ERR_UNSUPPORTED for D outside
- * the sets above, B > 8192 or more than 1024 query heads per key head; RA_ERR_LAUNCH.  The size
- * query returns 0 for such sizes.
+ * the sets above, B > 8192, more than 1024 query heads per key head, or sizes whose blocks of 8 to 32
+ * keys by 16 query rows number more than 2^30; RA_ERR_LAUNCH.  The size query returns 0 for such sizes.
  */
 size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D, ra_dtype_t dtype);
 ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, const int32_t* length,

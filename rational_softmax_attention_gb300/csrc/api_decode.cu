@@ -168,7 +168,7 @@ ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, con
   a.weight = weight;
   a.o = o;
   a.scale = scale;
-  plan_decode(&a, dtype == RA_BF16, static_cast<char*>(workspace));
+  if (plan_decode(&a, dtype == RA_BF16, static_cast<char*>(workspace)) == 0) return RA_ERR_UNSUPPORTED;
   PrefixMaps maps;
   LaunchCtx ctx;
   if (a.tc && (launch_context(&ctx) != RA_OK || !tensor_map_bf16(&maps.k, prefix_k, H_KV, P, D) ||

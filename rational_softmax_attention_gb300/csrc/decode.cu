@@ -34,6 +34,8 @@
 // below meet no bank conflict.  fp32: FFMA.
 //
 // Bound: HBM, K and V once.
+#include <climits>
+
 #include "decode_split.cuh"
 
 namespace raattn {
@@ -74,12 +76,19 @@ __device__ __forceinline__ float phi_t(float d) {
 // ---------------------------------------------------------------------------------------------
 // the split
 // ---------------------------------------------------------------------------------------------
-// cum[b] = own blocks per stream of the sequences before b, for b <= B.  All threads.
+// The sequences' entries and own blocks: cum[b] = blocks per stream of the sequences before b, for
+// b <= B, and behind it their lengths.  All threads.
+template <int KEYS>
 __device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a) {
   __shared__ int sums[kWarps];
+  int* len = cum + a.B + 1;
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
   int mine = 0;
-  for (int i = 0; i < per && b0 + i < a.B; ++i) mine += (decode_own_length(a, b0 + i) + a.block - 1) / a.block;
+  for (int i = b0; i < b0 + per && i < a.B; ++i) {
+    const int n = decode_own_length(a, i);
+    len[i] = n;
+    mine += (n + KEYS - 1) / KEYS;
+  }
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -90,9 +99,9 @@ __device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a) {
   __syncthreads();
   for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) inc += sums[w];
   int run = inc - mine;
-  for (int i = 0; i < per && b0 + i < a.B; ++i) {
-    cum[b0 + i] = run;
-    run += (decode_own_length(a, b0 + i) + a.block - 1) / a.block;
+  for (int i = b0; i < b0 + per && i < a.B; ++i) {
+    cum[i] = run;
+    run += (len[i] + KEYS - 1) / KEYS;
   }
   if (b0 < a.B && b0 + per >= a.B) cum[a.B] = run;
   __syncthreads();
@@ -108,44 +117,41 @@ struct Part {
   int row0, rows;      // rows: within the head's G (own) or the batch's B G (shared)
 };
 
-__device__ __forceinline__ Part get_part(int64_t u, int64_t end, const int* cum, const Split& s, const DecodeArgs& a) {
+// The part that begins at block u of run `run`, which ends at `end`.
+__device__ __forceinline__ Part get_part(int u, int run, int end, const int* cum, const Split& s, const DecodeArgs& a) {
   Part p;
-  int64_t stream0;   // the stream's first block among all
-  int blocks;
+  int stream0, blocks, stream;   // the stream's first block among all; its blocks
   if (u < s.own0) {
-    const int64_t st = u / a.pblocks;
-    const int rb = static_cast<int>(st % a.shared_rowblocks);
-    stream0 = st * a.pblocks;
     blocks = a.pblocks;
-    p.kv = static_cast<int>(st / a.shared_rowblocks);
+    stream = u / blocks;
+    stream0 = stream * blocks;
+    p.kv = stream / a.shared_rowblocks;
     p.b = -1;
     p.keys = a.P;
-    p.row0 = rb * kRows;
+    p.row0 = (stream - p.kv * a.shared_rowblocks) * kRows;
     p.rows = min(a.B * a.G - p.row0, kRows);
     p.slot = 0;
   } else {
-    const int streams = a.Hkv * a.own_rowblocks;
-    const int64_t x = u - s.own0;
-    const int c = static_cast<int>(x / streams);
+    const int streams = a.Hkv * a.own_rowblocks, x = u - s.own0, c = x / streams;
     int lo = 0, hi = a.B - 1;   // the last b with cum[b] <= c: c lies in its blocks
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (cum[mid] <= c) lo = mid; else hi = mid - 1;
     }
     blocks = cum[lo + 1] - cum[lo];
-    const int64_t seq0 = static_cast<int64_t>(cum[lo]) * streams;
-    const int st = static_cast<int>((x - seq0) / blocks);
-    stream0 = s.own0 + seq0 + static_cast<int64_t>(st) * blocks;
-    p.kv = st / a.own_rowblocks;
+    const int seq0 = cum[lo] * streams;
+    stream = (x - seq0) / blocks;
+    stream0 = s.own0 + seq0 + stream * blocks;
+    p.kv = a.own_rowblocks == 1 ? stream : stream / a.own_rowblocks;
     p.b = lo;
-    p.keys = decode_own_length(a, lo);
-    p.row0 = st % a.own_rowblocks * kRows;
+    p.keys = cum[a.B + 1 + lo];
+    p.row0 = (stream - p.kv * a.own_rowblocks) * kRows;
     p.rows = min(a.G - p.row0, kRows);
     p.slot = a.pslots;
   }
-  p.first = static_cast<int>(u - stream0);
-  p.count = static_cast<int>(min(static_cast<int64_t>(blocks - p.first), end - u));
-  p.slot += static_cast<int>(u / s.per - stream0 / s.per);
+  p.first = u - stream0;
+  p.count = min(blocks - p.first, end - u);
+  p.slot += run - stream0 / s.per;
   return p;
 }
 
@@ -161,11 +167,12 @@ __device__ __forceinline__ void team_sync() {
   else __syncthreads();
 }
 
-// Row r of a part as an index into [B, H_q].
+// Row r of a part (its last one for those past it) as an index into [B, H_q].
 __device__ __forceinline__ int row_of(const Part& p, int r, const DecodeArgs& a) {
-  const int x = p.row0 + r;
+  const int x = p.row0 + min(r, p.rows - 1);
   if (p.b >= 0) return p.b * a.Hq + p.kv * a.G + x;
-  return x / a.G * a.Hq + p.kv * a.G + x % a.G;
+  const int b = x / a.G;
+  return b * a.Hq + p.kv * a.G + x - b * a.G;
 }
 __device__ __forceinline__ float* score_row(const Part& p, int row, const DecodeArgs& a) {
   return p.b >= 0 ? a.s_own + static_cast<int64_t>(row) * a.own_width
@@ -200,17 +207,27 @@ __device__ __forceinline__ int place(int r, int c) {
   return r * CHUNKS + (CHUNKS >= 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
 }
 
-// One block (keys first .. of a stream of `keys`) into a stage.
+// A lane's share of the copies of a block: chunk c of rows r, r + kRowsPerCopy, ..; rows and places
+// are constants from one copy to the next.
 template <int KEYS, int CHUNKS, Layout LAY>
-__device__ __forceinline__ void fetch_block(uint32_t stage, const char* stream, int first, int keys, int lane) {
-#pragma unroll
-  for (int i = 0; i < KEYS * CHUNKS / 32; ++i) {
-    const int x = i * 32 + lane, r = x / CHUNKS, c = x % CHUNKS, key = first + r;
-    const bool in = key < keys;
-    copy16(stage + place<LAY, CHUNKS>(r, c) * 16,
-           stream + (static_cast<int64_t>(in ? key : 0) * CHUNKS + c) * 16, in);
+struct Fetch {
+  static constexpr int kRowsPerCopy = 32 / CHUNKS, kCopies = KEYS / kRowsPerCopy;
+  const char* src;   // the lane's chunk of the stream's row `lane / CHUNKS`
+  int r, c;
+  __device__ __forceinline__ Fetch(const char* stream, int lane) : r(lane / CHUNKS), c(lane % CHUNKS) {
+    src = stream + lane * 16;
   }
-}
+  // the block of keys first .. of a stream of `keys`
+  __device__ __forceinline__ void operator()(uint32_t stage, int first, int keys) const {
+    const char* s = src + static_cast<int64_t>(first) * (CHUNKS * 16);
+    const int left = keys - first - r;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const bool in = i * kRowsPerCopy < left;
+      copy16(stage + place<LAY, CHUNKS>(r + i * kRowsPerCopy, c) * 16, in ? s + i * 512 : src - r * (CHUNKS * 16), in);
+    }
+  }
+};
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 u;
@@ -243,14 +260,14 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
   const int mine = blocks_of_warp<TW>(p), first = (p.first + warp_of_team<TW>()) * C::kKeys;
   constexpr int kStep = TW * C::kKeys;
   const char* keys = stream_of<__nv_bfloat16, D>(p, a.k, a.pk, a);
+  const Fetch<C::kKeys, C::kChunks, K16> fetch(keys, lane);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < mine)
-      fetch_block<C::kKeys, C::kChunks, K16>(ring + i * C::kStageK, keys, first + i * kStep, p.keys, lane);
+    if (i < mine) fetch(ring + i * C::kStageK, first + i * kStep, p.keys);
     copy_commit();
   }
   uint4 q0[NV], q1[NV];
-  const int r0 = row_of(p, min(g, p.rows - 1), a), r1 = row_of(p, min(g + 8, p.rows - 1), a);
+  const int r0 = row_of(p, g, a), r1 = row_of(p, g + 8, a);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
@@ -265,9 +282,7 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
     copy_wait<C::kStages - 2>();
     __syncwarp();   // block i has landed for all lanes, and all have read block i - 1
     const int ahead = i + C::kStages - 1;
-    if (ahead < mine)
-      fetch_block<C::kKeys, C::kChunks, K16>(ring + ahead % C::kStages * C::kStageK, keys, first + ahead * kStep,
-                                             p.keys, lane);
+    if (ahead < mine) fetch(ring + ahead % C::kStages * C::kStageK, first + ahead * kStep, p.keys);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageK;
 #pragma unroll
@@ -308,26 +323,29 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
   const int mine = blocks_of_warp<TW>(p), first = (p.first + warp_of_team<TW>()) * C::kKeys;
   constexpr int kStep = TW * C::kKeys;
   const char* keys = stream_of<float, D>(p, a.k, a.pk, a);
-#pragma unroll
+  const Fetch<C::kKeys, C::kChunks, F32> fetch(keys, lane);
+#pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < mine)
-      fetch_block<C::kKeys, C::kChunks, F32>(ring + i * C::kStageK, keys, first + i * kStep, p.keys, lane);
+    if (i < mine) fetch(ring + i * C::kStageK, first + i * kStep, p.keys);
     copy_commit();
   }
-  float best[kRows];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) best[r] = -kInf;
-  // the rows' queries, which every block reads, into L1
-  for (int x = lane; x < p.rows * C::kChunks; x += 32)
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(a.q) +
-                                                  (static_cast<int64_t>(row_of(p, x / C::kChunks, a)) * C::kChunks + x % C::kChunks) * 16));
+  // Rows four at a time (independent chains) in a loop that is not unrolled: a part is short, and
+  // fetching the code of all sixteen would cost more than running it.  best_s holds this warp's
+  // maxima.
+  float* best = best_s + (threadIdx.x >> 5) * kRows;
+  if (lane < kRows) best[lane] = -kInf;
+  const int row_lane = row_of(p, lane, a);   // of lane's row
+  const float* q0 = static_cast<const float*>(a.q) + part * 4;
+  for (int x = lane; x < p.rows * C::kChunks; x += 32)   // the queries, which every block reads, into L1
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const float*>(a.q) +
+                                                  static_cast<int64_t>(row_of(p, x / C::kChunks, a)) * D +
+                                                  x % C::kChunks * 4));
+  __syncwarp();
   for (int i = 0; i < mine; ++i) {
     copy_wait<C::kStages - 2>();
     __syncwarp();
     const int ahead = i + C::kStages - 1;
-    if (ahead < mine)
-      fetch_block<C::kKeys, C::kChunks, F32>(ring + ahead % C::kStages * C::kStageK, keys, first + ahead * kStep,
-                                             p.keys, lane);
+    if (ahead < mine) fetch(ring + ahead % C::kStages * C::kStageK, first + ahead * kStep, p.keys);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageK;
     float4 kx[C::kChunks / PARTS];
@@ -337,37 +355,33 @@ __device__ __forceinline__ void part_scores(const Part& p, const DecodeArgs& a, 
       kx[c] = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
     }
     const int key = first + i * kStep + kk;
+#pragma unroll 1
+    for (int r0 = 0; r0 < p.rows; r0 += 4) {
+      float s[4];
+      int row[4];
 #pragma unroll
-    for (int r0 = 0; r0 < kRows; r0 += 4) {   // four rows at a time: independent chains
-      if (r0 < p.rows) {
+      for (int j = 0; j < 4; ++j) {
+        row[j] = __shfl_sync(0xffffffffu, row_lane, r0 + j);
+        const float4* q = reinterpret_cast<const float4*>(q0 + static_cast<int64_t>(row[j]) * D);
+        float u = 0.0f, v = 0.0f;
 #pragma unroll
-        for (int r = r0; r < r0 + 4; ++r) {
-          const int row = row_of(p, min(r, p.rows - 1), a);
-          const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + static_cast<int64_t>(row) * D);
-          float s = 0.0f, s2 = 0.0f;
-#pragma unroll
-          for (int c = 0; c < C::kChunks / PARTS; ++c) {
-            const float4 y = __ldg(q + c * PARTS + part);
-            s = fmaf(y.x, kx[c].x, fmaf(y.y, kx[c].y, s));
-            s2 = fmaf(y.z, kx[c].z, fmaf(y.w, kx[c].w, s2));
-          }
-          s += s2;
-#pragma unroll
-          for (int o = 1; o < PARTS; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          s = key < p.keys ? s : -kInf;
-          best[r] = fmaxf(best[r], s);
-          if (part == 0 && r < p.rows) score_row(p, row, a)[key] = s;
+        for (int c = 0; c < C::kChunks / PARTS; ++c) {
+          const float4 y = __ldg(q + c * PARTS);
+          u = fmaf(y.x, kx[c].x, fmaf(y.y, kx[c].y, u));
+          v = fmaf(y.z, kx[c].z, fmaf(y.w, kx[c].w, v));
         }
+        s[j] = u + v;
       }
-    }
-  }
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r < p.rows) {
-      float v = best[r];
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-      if (lane == 0) best_s[(threadIdx.x >> 5) * kRows + r] = v;
+        for (int o = 1; o < PARTS; o <<= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+        s[j] = key < p.keys ? s[j] : -kInf;
+        if (part == 0 && r0 + j < p.rows) score_row(p, row[j], a)[key] = s[j];
+#pragma unroll
+        for (int o = 16; o >= PARTS; o >>= 1) s[j] = fmaxf(s[j], __shfl_xor_sync(0xffffffffu, s[j], o));
+      }
+      if (lane < 4) best[r0 + lane] = fmaxf(best[r0 + lane], lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3]);
     }
   }
 }
@@ -380,14 +394,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   __shared__ float best[kWarps * kRows];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   release_dependents();
-  const Split s = make_split(cum, a);
+  const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
   }
   // runs go to the CTAs in turn, so that few runs spread over the SMs
-  const int64_t run = team * static_cast<int64_t>(gridDim.x) + blockIdx.x, end = min((run + 1) * s.per, s.total);
-  for (int64_t u = run * s.per; u < end;) {
-    const Part p = get_part(u, end, cum, s, a);
+  const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
+  for (int u = run * s.per; u < end;) {
+    const Part p = get_part(u, run, end, cum, s, a);
     part_scores<D, TW>(p, a, smem_u32(dyn) + warp * kRing, best, static_cast<T*>(nullptr));
     u += p.count;
     team_sync<TW>();
@@ -420,30 +434,39 @@ __device__ __forceinline__ float fold_slots(const float* v, int shared, int own,
 template <int TW>
 __device__ __forceinline__ void part_maxima(float* rowm, const Part& p, const int* cum, const Split& s,
                                             const DecodeArgs& a) {
-  const int tt = threadIdx.x % (32 * TW), r = tt / (2 * TW), row = row_of(p, min(r, p.rows - 1), a), b = row / a.Hq;
+  const int tt = threadIdx.x % (32 * TW), r = tt / (2 * TW), row = row_of(p, r, a), b = row / a.Hq;
   int shared, own;
-  decode_row_slots(row, cum[b], cum[b + 1], s, a, shared, own);
+  decode_row_slots(b, p.kv, row - b * a.Hq - p.kv * a.G, cum[b], cum[b + 1], s, a, shared, own);
   const float m = fold_slots<2 * TW>(a.row_max + static_cast<int64_t>(row) * a.slots, shared, own, a.pslots,
                                      tt % (2 * TW), -kInf, [](float x, float y) { return fmaxf(x, y); });
   if (tt % (2 * TW) == 0) rowm[r] = m;
 }
 
-// A block of values and its scores into a stage.
+// Blocks of values and their scores into a stage.
 template <typename T, int D, int TW, Layout LAY>
-__device__ __forceinline__ void fetch_values(uint32_t stage, const char* vals, const Part& p, int i, const DecodeArgs& a,
-                                             int lane) {
+struct FetchValues {
   using C = Cfg<T, D>;
-  const int first = (p.first + i * TW + warp_of_team<TW>()) * C::kKeys;
-  fetch_block<C::kKeys, C::kChunks, LAY>(stage, vals, first, p.keys, lane);
-  constexpr int PIECES = C::kKeys / 4;   // 16-byte pieces of a row of scores
+  static constexpr int kPieces = C::kKeys / 4;                              // 16-byte pieces of a row of scores
+  static constexpr int kLoads = (kRows * kPieces + 31) / 32, kRowsPerLoad = 32 / kPieces;
+  Fetch<C::kKeys, C::kChunks, LAY> values;
+  const float* src[kLoads];
+  int r, keys, first;
+  uint32_t at;
+  __device__ __forceinline__ FetchValues(const char* vals, const Part& p, const DecodeArgs& a, int lane)
+      : values(vals, lane), r(lane / kPieces), keys(p.keys), first((p.first + warp_of_team<TW>()) * C::kKeys) {
+    const int c = lane % kPieces;
+    at = C::kBlockBytes + (r * C::kScoreStride + c * 4) * 4;
 #pragma unroll
-  for (int j = 0; j < (kRows * PIECES + 31) / 32; ++j) {
-    const int x = j * 32 + lane, r = x / PIECES, c = x % PIECES;
-    if (r < p.rows)
-      copy16(stage + C::kBlockBytes + (r * C::kScoreStride + c * 4) * 4,
-             score_row(p, row_of(p, r, a), a) + first + c * 4, true);
+    for (int j = 0; j < kLoads; ++j) src[j] = score_row(p, row_of(p, r + j * kRowsPerLoad, a), a) + c * 4;
   }
-}
+  __device__ __forceinline__ void operator()(uint32_t stage, int i, int rows) const {
+    const int k = first + i * (TW * C::kKeys);
+    values(stage, k, keys);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      if (r + j * kRowsPerLoad < rows) copy16(stage + at + j * kRowsPerLoad * C::kScoreStride * 4, src[j] + k, true);
+  }
+};
 
 // bf16.  Lane (g, t) reads, of keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of sixteen, the dimensions
 // 8 g .. 8 g + 7 of every 64: words of two keys, interleaved, are the B operand of the product
@@ -456,9 +479,10 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int mine = blocks_of_warp<TW>(p);
   const char* vals = stream_of<__nv_bfloat16, D>(p, a.v, a.pv, a);
+  const FetchValues<__nv_bfloat16, D, TW, V16> fetch(vals, p, a, lane);
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < mine) fetch_values<__nv_bfloat16, D, TW, V16>(ring + i * C::kStageV, vals, p, i, a, lane);
+    if (i < mine) fetch(ring + i * C::kStageV, i, p.rows);
     copy_commit();
   }
   part_maxima<TW>(rowm, p, cum, s, a);
@@ -475,8 +499,7 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
     copy_wait<C::kStages - 2>();
     __syncwarp();
     const int ahead = i + C::kStages - 1;
-    if (ahead < mine)
-      fetch_values<__nv_bfloat16, D, TW, V16>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
+    if (ahead < mine) fetch(ring + ahead % C::kStages * C::kStageV, ahead, p.rows);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageV;
     const float* sc = reinterpret_cast<const float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
@@ -552,9 +575,10 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
   const int lane = threadIdx.x & 31, gl = lane % L, ks = lane / L;
   const int mine = blocks_of_warp<TW>(p);
   const char* vals = stream_of<float, D>(p, a.v, a.pv, a);
-#pragma unroll
+  const FetchValues<float, D, TW, F32> fetch(vals, p, a, lane);
+#pragma unroll 1
   for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < mine) fetch_values<float, D, TW, F32>(ring + i * C::kStageV, vals, p, i, a, lane);
+    if (i < mine) fetch(ring + i * C::kStageV, i, p.rows);
     copy_commit();
   }
   // four lanes per row for phi: lane (g, t) takes rows g and g + 8, keys t, t + 4, ..
@@ -571,11 +595,11 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
     copy_wait<C::kStages - 2>();
     __syncwarp();
     const int ahead = i + C::kStages - 1;
-    if (ahead < mine) fetch_values<float, D, TW, F32>(ring + ahead % C::kStages * C::kStageV, vals, p, ahead, a, lane);
+    if (ahead < mine) fetch(ring + ahead % C::kStages * C::kStageV, ahead, p.rows);
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageV;
     float* sc = reinterpret_cast<float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
-#pragma unroll
+#pragma unroll 2
     for (int k = 0; k < C::kKeys; k += 4) {
       if (w0) {
         float& x = sc[g * C::kScoreStride + k + t];
@@ -643,13 +667,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(con
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
   release_dependents();
-  const Split s = make_split(cum, a);
+  const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
   // The scores have been written: by the kernel before, or, with the tensor cores, by the one before
   // that, which all of the kernel before had awaited when this one could start.
   if (!a.tc) await_previous();
-  const int64_t run = team * static_cast<int64_t>(gridDim.x) + blockIdx.x, end = min((run + 1) * s.per, s.total);
-  for (int64_t u = run * s.per; u < end;) {
-    const Part p = get_part(u, end, cum, s, a);
+  const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
+  for (int u = run * s.per; u < end;) {
+    const Part p = get_part(u, run, end, cum, s, a);
     part_values<D, TW>(p, a, s, cum, smem_u32(ring), ring, rowm_s + team * kRows, sums, static_cast<T*>(nullptr));
     u += p.count;
     team_sync<TW>();
@@ -692,9 +716,9 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     constexpr int L = D / 4, KS = kThreads / L;
     __shared__ float4 part[KS][L];
     __shared__ float sums[KS];
-    const int row = blockIdx.x, b = row / a.Hq;
+    const int row = blockIdx.x, b = row / a.Hq, kv = (row - b * a.Hq) / a.G;
     int shared, own;
-    decode_row_slots(row, a.cum[b], a.cum[b + 1], sp, a, shared, own);
+    decode_row_slots(b, kv, row - b * a.Hq - kv * a.G, a.cum[b], a.cum[b + 1], sp, a, shared, own);
     const int gl = threadIdx.x % L, ks = threadIdx.x / L;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float total = 0.0f;
@@ -745,7 +769,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
   for (int g = warp * 8 + (lane >> 2); g < (a.G + 7) / 8 * 8; g += kWarps * 8) {   // four lanes per row
     const int row = b * a.Hq + kv * a.G + min(g, a.G - 1);
     int shared, own;
-    decode_row_slots(row, a.cum[b], a.cum[b + 1], sp, a, shared, own);
+    decode_row_slots(b, kv, min(g, a.G - 1), a.cum[b], a.cum[b + 1], sp, a, shared, own);
     const int64_t at = static_cast<int64_t>(row) * a.slots;
     const float m = fold_slots<4>(a.row_max + at, shared, own, a.pslots, lane & 3, -kInf,
                                   [](float u, float v) { return fmaxf(u, v); });
@@ -775,7 +799,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
 template <typename T, int D, int TW>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
   using C = Cfg<T, D>;
-  const int cum = (a.B + 1) * 4;
+  const int cum = (2 * a.B + 1) * 4;
   const int smem_scores = kWarps * C::kStages * C::kStageK + cum;
   const int smem_values = kWarps * C::kStages * C::kStageV + cum;
   cudaError_t e = cudaFuncSetAttribute(decode_scores_kernel<T, D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -832,6 +856,7 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
                         static_cast<int64_t>(a->pblocks) * a->Hkv * a->shared_rowblocks;
   const int64_t streams = static_cast<int64_t>(a->B) * a->Hkv * a->own_rowblocks +
                           (a->pblocks ? static_cast<int64_t>(a->Hkv) * a->shared_rowblocks : 0);
+  if (total > INT_MAX / 2) return 0;
   const int team = streams >= 64 ? 1 : kWarps;
   a->runs = kDecodeCtas * kWarps / team;
   const int64_t even = total / a->runs;

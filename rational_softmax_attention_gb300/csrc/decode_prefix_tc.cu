@@ -83,10 +83,9 @@ __device__ __forceinline__ void store_p_half(const uint32_t (&pk)[32], uint8_t* 
 }
 
 // The maximum of a row over all its parts, read by one thread.
-__device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row) {
-  const int b = row / a.Hq;
+__device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row, int b, int kv, int g) {
   int shared, own;
-  decode_row_slots(row, a.cum[b], a.cum[b + 1], decode_split(a, a.cum[a.B]), a, shared, own);
+  decode_row_slots(b, kv, g, a.cum[b], a.cum[b + 1], decode_split(a, a.cum[a.B]), a, shared, own);
   const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
   float m = -INFINITY;
 #pragma unroll 8
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (ok && row_ok) a.row_max[static_cast<int64_t>(row) * a.slots + split] = m;
     } else {
-      const float m = row_ok ? row_maximum(a, row) : 0.0f;
+      const float m = row_ok ? row_maximum(a, row, x / a.G, kv, x % a.G) : 0.0f;
       const float c2 = a.scale * (1.0f / 32.0f);
       uint8_t* prow = sP + g * C::P_BYTES + row_local * 128;
       float total = 0.0f;

@@ -201,8 +201,8 @@ __device__ __forceinline__ int decode_own_length(const DecodeArgs& a, int b) { r
 __host__ __device__ constexpr int decode_block_keys(bool bf16, int D) {
   return bf16 ? 16 : D == 128 ? 8 : D == 64 ? 16 : 32;
 }
-// Fills the split (G, tc .. slots) from the sizes; returns the workspace bytes and sets the
-// workspace pointers from `base`.
+// Fills the split (G, tc .. slots) from the sizes; returns the workspace bytes (0: more blocks than
+// 32 bits count) and sets the workspace pointers from `base`.
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base);
 // Tensor maps of the prefix [Hkv, P, D] (the tensor-core form only).
 struct PrefixMaps {
