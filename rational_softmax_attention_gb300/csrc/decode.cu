@@ -53,7 +53,7 @@ struct Cfg {
   static constexpr int kChunks = D * static_cast<int>(sizeof(T)) / 16;   // of a key's or value's row
   static constexpr int kBlockBytes = kKeys * kChunks * 16;
   static constexpr int kStages = kBlockBytes >= 4096 ? 3 : 4;
-  static constexpr int kScoreStride = kKeys + 8;                         // floats of a row of scores in shared memory
+  static constexpr int kScoreStride = kKeys + 4;                         // floats of a row of scores in shared memory
   static constexpr int kStageK = kBlockBytes;
   static constexpr int kStageV = kBlockBytes + kRows * kScoreStride * 4;
 };
@@ -64,7 +64,9 @@ __device__ __forceinline__ float phi_fast(float d) {   // bf16 inputs: 1 ulp rec
   return q4 * q4;
 }
 __device__ __forceinline__ float phi_exact(float d) {   // fp32 inputs: IEEE division
-  const float q = d < 16.0f ? (16.0f - d) / (16.0f + d) : 0.0f;
+  const bool in = d < 16.0f;
+  d = in ? d : 0.0f;   // always a plain quotient: a division's special cases are slow
+  const float q = in ? (16.0f - d) / (16.0f + d) : 0.0f;
   const float q2 = q * q, q4 = q2 * q2;
   return q4 * q4;
 }
@@ -863,7 +865,7 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   a->min_run = static_cast<int>(even < 2 * team ? 2 * team : even > 8 * team ? 8 * team : even);
   a->pchunk = a->pslots = 0;
   if (a->tc) {
-    const int64_t per = a->Hkv * ((shared_rows + 255) / 256), tiles = (a->P + 127) / 128;
+    const int64_t per = a->Hkv * ((shared_rows + 127) / 128), tiles = (a->P + 127) / 128;
     int64_t n = kSms / per;
     n = n < 1 ? 1 : n > tiles ? tiles : n;
     a->pchunk = static_cast<int>((tiles + n - 1) / n * 128);
