@@ -395,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
-  release_dependents();
   const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
@@ -415,19 +414,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
     }
     team_sync<TW>();   // the maxima are read, and the rings are free
   }
+  // Only now: dependents that wait beside this kernel's CTAs cost more than their early start gives
+  // (B64 H8 of 2048 own keys: 132 us with the release at the start, 117 with it here).
+  release_dependents();
   await_previous();   // the tensor cores' part, if any: whoever awaits this kernel awaits that too
 }
 
 // ---------------------------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------------------------
-// A row's values v[] over its slots, folded by f over N neighbouring lanes, of which this is lane t.
+// A row's values v[] over its slots, folded by f over N neighbouring lanes, of which this is lane t;
+// x0 is neutral.  Eight loads at a time are in flight.
 template <int N, typename F>
-__device__ __forceinline__ float fold_slots(const float* v, int shared, int own, int pslots, int t, float x, F f) {
-#pragma unroll 4
-  for (int i = t; i < shared; i += N) x = f(x, __ldcg(v + i));
-#pragma unroll 4
-  for (int i = t; i < own; i += N) x = f(x, __ldcg(v + pslots + i));
+__device__ __forceinline__ float fold_slots(const float* v, int shared, int own, int pslots, int t, float x0, F f) {
+  float x = x0;
+  for (int i0 = t; i0 < shared + own; i0 += 8 * N) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * N;
+      y[j] = i < shared + own ? __ldcg(v + (i < shared ? i : pslots + i - shared)) : x0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x = f(x, y[j]);
+  }
 #pragma unroll
   for (int o = 1; o < N; o <<= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
@@ -659,7 +669,7 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
 }
 
 template <typename T, int D, int TW>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const DecodeArgs a) {
   extern __shared__ uint4 dyn[];
   constexpr int kRing = Cfg<T, D>::kStages * Cfg<T, D>::kStageV;
   static_assert(kRing >= kRows * D * 4, "a warp's partial sums fit its ring");
@@ -668,7 +678,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(con
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
-  release_dependents();
   const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
   // The scores have been written: by the kernel before, or, with the tensor cores, by the one before
   // that, which all of the kernel before had awaited when this one could start.
@@ -700,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_values_kernel(con
     }
     team_sync<TW>();
   }
+  release_dependents();
   if (a.tc) await_previous();   // whoever awaits this kernel awaits the tensor cores' part too
 }
 
@@ -724,18 +734,26 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     const int gl = threadIdx.x % L, ks = threadIdx.x / L;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float total = 0.0f;
-#pragma unroll 4
-    for (int i = ks; i < shared + own; i += KS) {
-      const int64_t at = static_cast<int64_t>(row) * a.slots + (i < shared ? i : a.pslots + i - shared);
-      const float f = a.part_sum[at];
-      const float4 x = reinterpret_cast<const float4*>(a.part_o + at * D)[gl];
-      if (f > 0.0f) {   // a part whose weights are all 0 may have written no output
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
-        total += f;
+    for (int i0 = ks; i0 < shared + own; i0 += 4 * KS) {   // four parts at a time in flight
+      float f[4];
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * KS;
+        const int64_t at = static_cast<int64_t>(row) * a.slots + (i < shared ? i : a.pslots + i - shared);
+        const bool in = i < shared + own;
+        f[j] = in ? __ldcg(a.part_sum + at) : 0.0f;
+        x[j] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + gl) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (f[j] > 0.0f) {   // a part whose weights are all 0 may have written no output
+          s.x += x[j].x;
+          s.y += x[j].y;
+          s.z += x[j].z;
+          s.w += x[j].w;
+          total += f[j];
+        }
     }
     part[ks][gl] = s;
     if (gl == 0) sums[ks] = total;
@@ -768,6 +786,16 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
   const int bk = static_cast<int>(x / splits), b = bk / a.Hkv, kv = bk - b * a.Hkv;
   const int first = split * kWeightKeys + threadIdx.x, last = decode_own_length(a, b);
   if (split * kWeightKeys >= last) return;
+  // the scores of the first row and the weights are on their way while the statistics are gathered
+  const float* sc = a.s_own + (static_cast<int64_t>(b) * a.Hq + kv * a.G) * a.own_width + first;
+  float* w = a.weight + static_cast<int64_t>(bk) * a.C + first;
+  float sum[8], next[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool in = first + i * kThreads < last;
+    next[i] = in ? __ldcg(sc + i * kThreads) : -kInf;
+    sum[i] = in ? w[i * kThreads] : 0.0f;
+  }
   for (int g = warp * 8 + (lane >> 2); g < (a.G + 7) / 8 * 8; g += kWarps * 8) {   // four lanes per row
     const int row = b * a.Hq + kv * a.G + min(g, a.G - 1);
     int shared, own;
@@ -780,22 +808,34 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     if ((lane & 3) == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / s);
   }
   __syncthreads();
-  const float* sc = a.s_own + (static_cast<int64_t>(b) * a.Hq + kv * a.G) * a.own_width;
-  float sum[8] = {};
-#pragma unroll 2
+  float add[8] = {};   // this call's weights first, then one addition to the running total
   for (int g = 0; g < a.G; ++g) {
     const float2 ms = stat[g];
+    float s[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int key = first + i * kThreads;
-      const float s = key < last ? sc[static_cast<int64_t>(g) * a.own_width + key] : -kInf;
-      sum[i] = fmaf(phi_t<T>((ms.x - s) * a.scale), ms.y, sum[i]);
+    for (int i = 0; i < 8; ++i) s[i] = next[i];
+    sc += a.own_width;
+    if (g + 1 < a.G) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) next[i] = first + i * kThreads < last ? __ldcg(sc + i * kThreads) : -kInf;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) add[i] = fmaf(phi_t<T>((ms.x - s[i]) * a.scale), ms.y, add[i]);
   }
-  float* w = a.weight + static_cast<int64_t>(bk) * a.C;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (first + i * kThreads < last) w[first + i * kThreads] += sum[i];
+    if (first + i * kThreads < last) w[i * kThreads] = sum[i] + add[i];
+}
+
+// The most shared memory of an SM's carve-out, also for kernels that would do with less: an SM changes
+// it only when it is empty, and the next kernel's CTAs, launched as dependents, come before that.
+template <typename... P>
+cudaError_t prepare(void (*kernel)(P...), int smem) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+  return e == cudaSuccess && smem > 0
+             ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
+             : e;
 }
 
 template <typename T, int D, int TW>
@@ -804,16 +844,15 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   const int cum = (2 * a.B + 1) * 4;
   const int smem_scores = kWarps * C::kStages * C::kStageK + cum;
   const int smem_values = kWarps * C::kStages * C::kStageV + cum;
-  cudaError_t e = cudaFuncSetAttribute(decode_scores_kernel<T, D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_scores);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_values_kernel<T, D, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_values);
+  cudaError_t e = prepare(decode_scores_kernel<T, D, TW>, smem_scores);
+  if (e == cudaSuccess) e = prepare(decode_values_kernel<T, D, TW>, smem_values);
+  if (e == cudaSuccess) e = prepare(decode_join_kernel<T, D>, 0);
   if (e != cudaSuccess) return e;
   // CTAs for the runs that there can be
   const int64_t most = static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks +
                        static_cast<int64_t>(a.B) * (a.own_width / a.block) * a.Hkv * a.own_rowblocks;
-  const int64_t runs = (most + a.min_run - 1) / a.min_run;
-  const int grid = static_cast<int>(runs < kDecodeCtas ? runs : kDecodeCtas);
+  const int64_t runs = (most + a.min_run - 1) / a.min_run, all = a.runs * TW / kWarps;
+  const int grid = static_cast<int>(runs < all ? runs : all);
   if (a.tc && (e = launch_decode_prefix(maps, a, false, ctx, st)) != cudaSuccess) return e;
   if (a.tc) {
     e = launch_dependent(decode_scores_kernel<T, D, TW>, grid, kThreads, smem_scores, st, a);
@@ -830,7 +869,7 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
 }
 template <typename T, int D>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
-  return a.runs == kDecodeCtas ? go<T, D, kWarps>(a, maps, ctx, st) : go<T, D, 1>(a, maps, ctx, st);
+  return a.team == kWarps ? go<T, D, kWarps>(a, maps, ctx, st) : go<T, D, 1>(a, maps, ctx, st);
 }
 
 }  // namespace
@@ -859,10 +898,10 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t streams = static_cast<int64_t>(a->B) * a->Hkv * a->own_rowblocks +
                           (a->pblocks ? static_cast<int64_t>(a->Hkv) * a->shared_rowblocks : 0);
   if (total > INT_MAX / 2) return 0;
-  const int team = streams >= 64 ? 1 : kWarps;
-  a->runs = kDecodeCtas * kWarps / team;
+  a->team = streams >= 64 ? 1 : kWarps;
+  a->runs = kDecodeCtas * kWarps / a->team;
   const int64_t even = total / a->runs;
-  a->min_run = static_cast<int>(even < 2 * team ? 2 * team : even > 8 * team ? 8 * team : even);
+  a->min_run = static_cast<int>(even < 2 * a->team ? 2 * a->team : even > 8 * a->team ? 8 * a->team : even);
   a->pchunk = a->pslots = 0;
   if (a->tc) {
     const int64_t per = a->Hkv * ((shared_rows + 127) / 128), tiles = (a->P + 127) / 128;

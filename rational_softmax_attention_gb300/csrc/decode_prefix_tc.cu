@@ -81,10 +81,16 @@ __device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row, int b
   decode_row_slots(b, kv, g, a.cum[b], a.cum[b + 1], decode_split(a, a.cum[a.B]), a, shared, own);
   const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
   float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < shared; ++i) m = fmaxf(m, __ldcg(p + i));
-#pragma unroll 4
-  for (int i = 0; i < own; ++i) m = fmaxf(m, __ldcg(p + a.pslots + i));
+  for (int i0 = 0; i0 < shared + own; i0 += 8) {   // eight loads at a time in flight
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j;
+      y[j] = i < shared + own ? __ldcg(p + (i < shared ? i : a.pslots + i - shared)) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, y[j]);
+  }
   return m;
 }
 
@@ -143,8 +149,7 @@ __global__ void __launch_bounds__(512, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  if constexpr (VALUES) await_previous();   // all maxima
-  release_dependents();                     // the sequences' own values need no more than that either
+  if constexpr (!VALUES) release_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -320,6 +325,10 @@ __global__ void __launch_bounds__(512, 1)
       asm volatile("bar.sync 1, 256;" ::: "memory");   // the softmax warps
       if (!upper && ok && row_ok) a.row_max[static_cast<int64_t>(row) * a.slots + split] = fmaxf(m, half[row_local]);
     } else {
+      // All maxima, which the sequences' own values, the next kernel, need no less; the first tiles are
+      // on their way, and the first scores formed, meanwhile.
+      await_previous();
+      release_dependents();
       const float m = row_ok ? row_maximum(a, row, b, kv, g) : 0.0f;
       const float c2 = a.scale * (1.0f / 32.0f);
       uint8_t* prow = sP + upper * BOX_BYTES + row_local * 128;
@@ -392,8 +401,10 @@ __global__ void __launch_bounds__(512, 1)
 template <int D, bool VALUES>
 cudaError_t go(const PrefixMaps& maps, const DecodeArgs& a, const LaunchCtx& ctx, cudaStream_t st) {
   auto kernel = decode_prefix_kernel<D, VALUES>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             Cfg<D, VALUES>::SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                       cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, VALUES>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(a.Hkv) * ((a.B * a.G + BM - 1) / BM) * a.pslots;
   if constexpr (VALUES) return launch_dependent(kernel, grid, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st, maps, a, ctx);

@@ -190,6 +190,7 @@ struct DecodeArgs {
   int own_rowblocks, shared_rowblocks;   // blocks of 16 rows of a key head: its G, the batch's B G
   int own_width, pre_width;     // padded length of a row of s_own and s_pre
   int pblocks;                  // blocks of the shared keys (none with tc)
+  int team;                     // warps that share a run: 1 or 4
   int runs, min_run;            // equal parts of all blocks, and blocks of one at least
   int pchunk;                   // tc: shared keys of a CTA
   int pslots, slots;            // slots of the shared keys, and all
