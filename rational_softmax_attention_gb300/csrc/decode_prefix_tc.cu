@@ -5,16 +5,18 @@
 // 128-row products, 128 keys per tile.  The rational map needs the row maximum before any phi
 // (see decode.cu), so it comes as two kernels around the maxima of the sequences' own keys:
 //   max     S = Q K^T per tile into TMEM, each row's maximum over the CTA's keys;
-//   values  S again, phi on the FMA pipe, P (bf16) to shared memory, O += P V in TMEM; partial
-//           sums and outputs (fp32) per CTA to the workspace.
+//   values  S again, phi on the FMA pipe, P (bf16) over S's own columns in TMEM, O += P V with A read
+//           from there; partial sums and outputs (fp32) per CTA to the workspace.
 // Forming S twice costs a third more products, but 128 rows of scores in fp32 would be twice the
 // bytes of the keys.
 //
 // A CTA takes 128 rows of one key head and a run of key tiles; the keys are split so that one wave of
 // CTAs, one per SM, covers heads x row tiles x splits.  Roles: warp 8 feeds a ring of K (and V) tiles
 // by TMA; a thread of warp 9 issues the products; warps 0-3 and 4-7 own the 128 rows, thread = row,
-// for the lower and the upper 64 keys of a tile.  A score buffer is handed back as soon as its half
-// is in registers, so the next product runs under phi.  Query rows are gathered by their own
+// for the lower and the upper 64 keys of a tile.  Two score buffers: S of the next tile is formed under
+// phi of this one, and the thread that issues the products needs one hand-off per tile, "P is
+// written", since products run in the order of their issue (P V of tile j, then S of tile j + 2 into
+// the same columns).  Query rows are gathered by their own
 // threads (a head's rows are G at a time in memory) into the 128-byte-swizzled operand layout.
 //
 // One row tile per CTA leaves registers and shared memory for a CTA of the kernels that stream the
@@ -29,24 +31,26 @@ namespace {
 constexpr int BM = 128, BN = 128;
 constexpr int SOFTMAX_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int THREADS = 32 * 10;
-constexpr uint32_t TMEM_COLS = 256;       // max: two score buffers; values: S, O
-constexpr uint32_t TMEM_O = 128;
+constexpr uint32_t TMEM_O = 256;          // score buffer b at column 128 b, O behind both
+constexpr int SPLIT_BATCH = 256;          // up to so many sequences' block counts are kept in shared memory
 constexpr int BOX_BYTES = 128 * 64 * 2;   // one TMA box: 128 rows x 64 values
 
 template <int D, bool VALUES>
 struct Cfg {
+  static constexpr uint32_t TMEM_COLS = VALUES ? 512 : 256;
   static constexpr int TILE_BYTES = BN * D * 2;
-  static constexpr int NSTAGE = D == 128 ? 3 : 6;
-  static constexpr int P_BYTES = VALUES ? BM * BN * 2 : 0;
+  static constexpr int NSTAGE = D == 128 ? (VALUES ? 4 : 3) : 6;
   static constexpr int OFF_RING = TILE_BYTES;   // behind Q
-  static constexpr int OFF_P = OFF_RING + NSTAGE * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_P + P_BYTES;
-  // q_full, ring_full[], ring_empty[], s_full[2], s_empty[2], p_full, p_empty, o_full, drain
-  static constexpr int NUM_BARS = 1 + 2 * NSTAGE + 8;
-  static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // tmem base, abort flag, votes
-  static constexpr int OFF_HALF = OFF_MISC + 16 + SOFTMAX_WARPS * 4;         // the upper halves' row results
-  static constexpr int SMEM_BYTES = OFF_HALF + BM * 4 + 1024;                // 1024: alignment
-  static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+  static constexpr int OFF_BAR = OFF_RING + NSTAGE * TILE_BYTES;
+  // q_full, ring_full[], ring_empty[], s_full[2], handed[2], o_full, drain
+  static constexpr int NUM_BARS = 1 + 2 * NSTAGE + 6;
+  static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // tmem base, abort flag, votes [2][8]
+  static constexpr int OFF_HALF = OFF_MISC + 16 + 2 * SOFTMAX_WARPS * 4;     // the upper halves' row results
+  static constexpr int OFF_CUM = OFF_HALF + BM * 4;
+  static constexpr int SMEM_BYTES = OFF_CUM + (VALUES ? (SPLIT_BATCH + 1) * 4 : 0);
+  // beside it, on one SM, a CTA of decode_values_kernel: 66,564 bytes with 64 sequences
+  static_assert(SMEM_BYTES + 1024 + 66564 <= 233472, "shared memory per SM");
+  static_assert(NSTAGE * TILE_BYTES >= SOFTMAX_WARPS * 4096, "the output leaves through the ring");
 };
 
 // phi of 64 columns of a row: d = m - s is exact 0 at the maximum; columns from `n` on are not keys.
@@ -75,17 +79,19 @@ __device__ __forceinline__ float phi_half(const uint32_t (&h)[2][32], uint32_t (
   return sum.x + sum.y;
 }
 
-// The maximum of a row over all its parts, read by one thread.
-__device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row, int b, int kv, int g) {
+// The maximum of every second part of a row from part `first` on; cum: own blocks per stream of
+// the sequences before each.
+__device__ __forceinline__ float half_maximum(const DecodeArgs& a, const int* cum, int row, int b, int kv, int g,
+                                              int first) {
   int shared, own;
-  decode_row_slots(b, kv, g, a.cum[b], a.cum[b + 1], decode_split(a, a.cum[a.B]), a, shared, own);
+  decode_row_slots(b, kv, g, cum[b], cum[b + 1], decode_split(a, cum[a.B]), a, shared, own);
   const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
   float m = -INFINITY;
-  for (int i0 = 0; i0 < shared + own; i0 += 8) {   // eight loads at a time in flight
+  for (int i0 = first; i0 < shared + own; i0 += 16) {   // eight loads at a time in flight
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j;
+      const int i = i0 + 2 * j;
       y[j] = i < shared + own ? __ldcg(p + (i < shared ? i : a.pslots + i - shared)) : -INFINITY;
     }
 #pragma unroll
@@ -93,6 +99,8 @@ __device__ __forceinline__ float row_maximum(const DecodeArgs& a, int row, int b
   }
   return m;
 }
+
+__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Bounded as for 512 threads, that is 128 registers each: the 320 leave 24,576 of an SM's, enough
 // for a CTA of the kernels that run beside this one.
@@ -102,22 +110,23 @@ __global__ void __launch_bounds__(512, 1)
   using C = Cfg<D, VALUES>;
   constexpr int NST = C::NSTAGE;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  if (smem_u32(smem_raw) & 1023u) {   // uniform over the CTA: nothing has started
+    if (threadIdx.x == 0) atomicOr(ctx.status, kStatusBadSmem);
+    return;
+  }
+  uint8_t* smem = smem_raw;
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + C::OFF_RING;
-  uint8_t* sP = smem + C::OFF_P;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* ring_full = q_full + 1;
   uint64_t* ring_empty = ring_full + NST;
-  uint64_t* s_full = ring_empty + NST;   // [2] score buffers (values: the first)
-  uint64_t* s_empty = s_full + 2;
-  uint64_t* p_full = s_empty + 2;
-  uint64_t* p_empty = p_full + 1;
-  uint64_t* o_full = p_empty + 1;
+  uint64_t* s_full = ring_empty + NST;   // [2] per score buffer: S is formed
+  uint64_t* handed = s_full + 2;         // [2] max: its scores are in registers; values: P is written over them
+  uint64_t* o_full = handed + 2;
   uint64_t* drain = o_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  volatile int* live = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // votes of the softmax warps
+  volatile int* live = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // [2][8] the softmax warps' votes
   float* half = reinterpret_cast<float*>(smem + C::OFF_HALF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -136,17 +145,15 @@ __global__ void __launch_bounds__(512, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_empty[b], SOFTMAX_WARPS);
+      mbar_init(&handed[b], SOFTMAX_WARPS);
     }
-    mbar_init(p_full, SOFTMAX_WARPS);
-    mbar_init(p_empty, 1);
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
   if (warp == MMA_WARP) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
   if constexpr (!VALUES) release_dependents();
@@ -181,11 +188,11 @@ __global__ void __launch_bounds__(512, 1)
         return true;
       };
       bool ok = true;
-      for (int j = 0; j < nt && ok; ++j) {   // values: K_0, then K_j and V_(j-1), then the last V
-        ok = issue(&maps.k, j);
-        if (VALUES && ok && j > 0) ok = issue(&maps.v, j - 1);
+      ok = issue(&maps.k, 0);   // values: K_0, then K_(j+1) and V_j
+      for (int j = 0; j < nt && ok; ++j) {
+        if (j + 1 < nt) ok = issue(&maps.k, j + 1);
+        if (VALUES && ok) ok = issue(&maps.v, j);
       }
-      if (VALUES && ok) issue(&maps.v, nt - 1);
       for (int i = 0; i < NST; ++i)
         if (issued[i]) drain_wait(&ring_full[i], last_par[i], ctx);
     }
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(512, 1)
       constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
       constexpr uint32_t HI = sdesc_hi_sw128(1024);
       const uint32_t ring = smem_u32(sRing);
-      const uint32_t qlo = sdesc_lo(smem_u32(sQ), 16), plo = sdesc_lo(smem_u32(sP), 16);
+      const uint32_t qlo = sdesc_lo(smem_u32(sQ), 16);
       uint32_t pos = 0;
       bool o_started = false;
       auto ring_wait = [&](uint32_t p, uint32_t& addr) -> bool {
@@ -205,55 +212,58 @@ __global__ void __launch_bounds__(512, 1)
         addr = ring + st * C::TILE_BYTES;
         return true;
       };
-      auto mma_s = [&](uint32_t kaddr, int b, uint32_t use) -> bool {   // S = Q K^T into score buffer b
-        if (!mbar_wait(&s_empty[b], (use & 1u) ^ 1u, abort_flag, ctx)) return false;
-        tc_fence_after();
-        const uint32_t klo = sdesc_lo(kaddr, 16), col = tmem + 128 * b;
+      auto mma_s = [&](int j) -> bool {   // S of tile j into its buffer, and its ring stage back
+        uint32_t kaddr;
+        const uint32_t p = pos++;
+        if (!ring_wait(p, kaddr)) return false;
+        const uint32_t klo = sdesc_lo(kaddr, 16), col = tmem + 128 * (j & 1);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4;
           tc_mma_f16(col, sdesc(qlo + off, HI), sdesc(klo + off, HI), idesc_qk, kk > 0 ? 1u : 0u);
         }
-        tc_commit(&s_full[b]);
+        tc_commit(&s_full[j & 1]);
+        tc_commit(&ring_empty[p % NST]);
         return true;
       };
-      auto mma_pv = [&](uint32_t c, uint32_t vaddr) -> bool {   // O += P V of the c-th tile, unless P is 0
-        if (!mbar_wait(p_full, c & 1u, abort_flag, ctx)) return false;
+      // scores of tile j taken (max), or P of it written (values)
+      auto handed_over = [&](int j) -> bool {
+        if (!mbar_wait(&handed[j & 1], (j >> 1) & 1, abort_flag, ctx)) return false;
         tc_fence_after();
+        return true;
+      };
+      auto mma_pv = [&](int j) -> bool {   // O += P V of tile j, unless P is 0
+        uint32_t vaddr;
+        const uint32_t p = pos++;
+        if (!ring_wait(p, vaddr) || !handed_over(j)) return false;
         int any = 0;
 #pragma unroll
-        for (int w = 0; w < SOFTMAX_WARPS; ++w) any |= live[w];
+        for (int w = 0; w < SOFTMAX_WARPS; ++w) any |= live[(j & 1) * SOFTMAX_WARPS + w];
         if (any) {
-          const uint32_t vlo = sdesc_lo(vaddr, BOX_BYTES), col = tmem + TMEM_O;
+          const uint32_t vlo = sdesc_lo(vaddr, BOX_BYTES), col = tmem + TMEM_O, pcol = tmem + 128 * (j & 1);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
-            const uint32_t aoff = ((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4;   // P: K-major
-            const uint32_t boff = (kk * 16 * 128) >> 4;                            // V: MN-major, 16 key rows
-            tc_mma_f16(col, sdesc(plo + aoff, HI), sdesc(vlo + boff, HI), idesc_pv, kk > 0 || o_started ? 1u : 0u);
+            const uint32_t acol = pcol + (kk >> 2) * 64 + (kk & 3) * 8;   // each half's P over its own scores
+            const uint32_t boff = (kk * 16 * 128) >> 4;                    // V: MN-major, 16 key rows
+            tc_mma_f16_ts(col, acol, sdesc(vlo + boff, HI), idesc_pv, kk > 0 || o_started ? 1u : 0u);
           }
           o_started = true;
         }
-        tc_commit(p_empty);
+        tc_commit(&ring_empty[p % NST]);
         return true;
       };
       bool ok = mbar_wait(q_full, 0, abort_flag, ctx);
       // test knob: nothing is committed to `drain` yet, so this wait can only time out
       if (ok && ctx.force_timeout) ok = mbar_wait(drain, 0, abort_flag, ctx);
       tc_fence_after();
-      uint32_t addr = 0;
+      ok = ok && mma_s(0);
       for (int j = 0; j < nt && ok; ++j) {
-        const uint32_t kpos = pos++;
-        ok = ring_wait(kpos, addr) && (VALUES ? mma_s(addr, 0, j) : mma_s(addr, j & 1, j >> 1));
-        if (ok) tc_commit(&ring_empty[kpos % NST]);
-        if (VALUES && ok && j > 0) {
-          const uint32_t vpos = pos++;
-          ok = ring_wait(vpos, addr) && mma_pv(j - 1, addr);
-          if (ok) tc_commit(&ring_empty[vpos % NST]);
+        if constexpr (VALUES) {   // S(j + 1) goes where P(j - 1) was, whose product has been issued
+          if (j + 1 < nt) ok = mma_s(j + 1);
+          ok = ok && mma_pv(j);
+        } else if (j + 1 < nt) {   // S(j + 1) goes where S(j - 1) was
+          ok = (j == 0 || handed_over(j - 1)) && mma_s(j + 1);
         }
-      }
-      if (VALUES && ok) {
-        ok = ring_wait(pos, addr) && mma_pv(nt - 1, addr);
-        if (ok) tc_commit(&ring_empty[pos % NST]);
       }
       if (ok) tc_commit(o_full);
       tc_commit(drain);
@@ -286,27 +296,30 @@ __global__ void __launch_bounds__(512, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16), scol = lanes + 64 * upper;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int tail = a.P - t0 * BN - 64 * upper;   // keys from this half's first on
     bool ok = true;
     uint32_t h[2][32];
-    // a tile's scores into registers, and the buffer back
-    auto take = [&](int buf, uint32_t par) -> bool {
-      if (!warp_wait(&s_full[buf], par)) return false;
+    // this half's scores of tile j into registers
+    auto take = [&](int j) -> bool {
+      if (!warp_wait(&s_full[j & 1], (j >> 1) & 1)) return false;
       tc_fence_after();
-      tmem_ld32(scol + 128 * buf, h[0]);
-      tmem_ld32(scol + 128 * buf + 32, h[1]);
+      tmem_ld32(lanes + 128 * (j & 1) + 64 * upper, h[0]);
+      tmem_ld32(lanes + 128 * (j & 1) + 64 * upper + 32, h[1]);
       tc_wait_ld();
+      return true;
+    };
+    auto hand = [&](int j) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_empty[buf]);
-      return true;
+      if (lane == 0) mbar_arrive(&handed[j & 1]);
     };
     if constexpr (!VALUES) {
       float m = -INFINITY;
-      for (int j = 0; j < nt && ok; ++j) {
-        ok = take(j & 1, (j >> 1) & 1);
+      for (int j = 0; j < nt; ++j) {
+        ok = take(j);
         if (!ok) break;
+        hand(j);
         float u0 = -INFINITY, u1 = -INFINITY;
         if (j * BN + 64 <= tail) {
 #pragma unroll
@@ -322,49 +335,66 @@ __global__ void __launch_bounds__(512, 1)
         m = fmaxf(m, fmaxf(u0, u1));
       }
       if (upper) half[row_local] = m;
-      asm volatile("bar.sync 1, 256;" ::: "memory");   // the softmax warps
+      softmax_barrier();
       if (!upper && ok && row_ok) a.row_max[static_cast<int64_t>(row) * a.slots + split] = fmaxf(m, half[row_local]);
     } else {
+      // While the maxima are still being formed: where this row's parts are, from the lengths.
+      int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
+      if (warp == 0 && a.B <= SPLIT_BATCH) {
+        int run = 0;
+        for (int i = 0; i < a.B; i += 32) {
+          int n = i + lane < a.B ? (decode_own_length(a, i + lane) + a.block - 1) / a.block : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += v;
+          }
+          if (i + lane < a.B) cum[i + lane + 1] = run + n;
+          run += __shfl_sync(0xffffffffu, n, 31);
+        }
+        if (lane == 0) cum[0] = 0;
+      }
       // All maxima, which the sequences' own values, the next kernel, need no less; the first tiles are
       // on their way, and the first scores formed, meanwhile.
       await_previous();
       release_dependents();
-      const float m = row_ok ? row_maximum(a, row, b, kv, g) : 0.0f;
+      softmax_barrier();
+      float m = row_ok ? half_maximum(a, a.B <= SPLIT_BATCH ? cum : a.cum, row, b, kv, g, upper) : 0.0f;
+      if (upper) half[row_local] = m;
+      softmax_barrier();
+      if (!upper) half[row_local] = m = fmaxf(m, half[row_local]);
+      softmax_barrier();
+      m = half[row_local];
       const float c2 = a.scale * (1.0f / 32.0f);
-      uint8_t* prow = sP + upper * BOX_BYTES + row_local * 128;
       float total = 0.0f;
-      for (int j = 0; j < nt && ok; ++j) {
-        ok = take(0, j & 1);
+      for (int j = 0; j < nt; ++j) {
+        ok = take(j);
         if (!ok) break;
         const int n = tail - j * BN;
         uint32_t pk[32];
         const float t = n < 64 ? phi_half<true>(h, pk, n, c2, m) : phi_half<false>(h, pk, n, c2, m);
-        ok = warp_wait(p_empty, (j & 1) ^ 1);   // the previous product has read the P tile
-        if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(prow + ((c ^ (row_local & 7)) << 4)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        fence_proxy_async_smem();
+        // P over this half's own scores, which only this thread read: two keys per column
+        const uint32_t pcol = lanes + 128 * (j & 1) + 64 * upper;
+        tmem_st16(pcol, reinterpret_cast<const uint32_t(&)[16]>(pk[0]));
+        tmem_st16(pcol + 16, reinterpret_cast<const uint32_t(&)[16]>(pk[16]));
+        tc_wait_st();
         total += t;
         const unsigned any = __any_sync(0xffffffffu, t > 0.0f);
-        if (lane == 0) live[warp] = any ? 1 : 0;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) live[(j & 1) * SOFTMAX_WARPS + warp] = any ? 1 : 0;
+        hand(j);
       }
       if (ok) ok = warp_wait(o_full, 0);
+      softmax_barrier();   // both halves have read the row's maximum
       if (upper) half[row_local] = total;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      total += upper ? 0.0f : half[row_local];
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (!upper) half[row_local] = total;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      softmax_barrier();
+      if (!upper) half[row_local] = total += half[row_local];
+      softmax_barrier();
       total = half[row_local];
       if (ok) {
         tc_fence_after();
-        // through the P tile (its last product has read it), 4 KB per warp, so that whole 128-byte
-        // row segments leave; the two halves take the output's columns in turn
-        uint8_t* stage = sP + warp * 4096;
+        // through the ring (every tile has been read), 4 KB per warp, so that whole 128-byte row
+        // segments leave; the two halves take the output's columns in turn
+        uint8_t* stage = sRing + warp * 4096;
         const int64_t out = row_ok && total > 0.0f ? (static_cast<int64_t>(row) * a.slots + split) * D : -1;
 #pragma unroll
         for (int c0 = 32 * upper; c0 < D; c0 += 64) {
@@ -394,7 +424,7 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == MMA_WARP) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
