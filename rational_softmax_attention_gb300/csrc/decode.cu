@@ -53,7 +53,8 @@ struct Cfg {
   static constexpr int kChunks = D * static_cast<int>(sizeof(T)) / 16;   // of a key's or value's row
   static constexpr int kBlockBytes = kKeys * kChunks * 16;
   static constexpr int kStages = kBlockBytes >= 4096 ? 3 : 4;
-  static constexpr int kScoreStride = kKeys + 4;                         // floats of a row of scores in shared memory
+  // floats of a row of scores in shared memory; bf16: no padding, the 16-byte pieces permuted (piece_of)
+  static constexpr int kScoreStride = BF ? kKeys : kKeys + 4;
   static constexpr int kStageK = kBlockBytes;
   static constexpr int kStageV = kBlockBytes + kRows * kScoreStride * 4;
 };
@@ -454,6 +455,11 @@ __device__ __forceinline__ void part_maxima(float* rowm, const Part& p, const in
   if (tt % (2 * TW) == 0) rowm[r] = m;
 }
 
+// Where piece c (four keys) of row r's scores stands: in bf16 so that the reads of sixteen lanes (four
+// rows, eight keys) meet no bank conflict.
+template <bool BF>
+__device__ __forceinline__ int piece_of(int r, int c) { return BF ? c ^ (r & 2) : c; }
+
 // Blocks of values and their scores into a stage.
 template <typename T, int D, int TW, Layout LAY>
 struct FetchValues {
@@ -467,7 +473,7 @@ struct FetchValues {
   __device__ __forceinline__ FetchValues(const char* vals, const Part& p, const DecodeArgs& a, int lane)
       : values(vals, lane), r(lane / kPieces), keys(p.keys), first((p.first + warp_of_team<TW>()) * C::kKeys) {
     const int c = lane % kPieces;
-    at = C::kBlockBytes + (r * C::kScoreStride + c * 4) * 4;
+    at = C::kBlockBytes + (r * C::kScoreStride + piece_of<C::BF>(r, c) * 4) * 4;   // rows kRowsPerLoad apart: alike
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) src[j] = score_row(p, row_of(p, r + j * kRowsPerLoad, a), a) + c * 4;
   }
@@ -517,19 +523,20 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
     const float* sc = reinterpret_cast<const float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     float live = 0.0f;
+    const int at = 2 * t, flip = (g & 2) << 2;   // piece_of: pieces 2 e + t / 2, flipped by two in rows 2, 3, 6, 7
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       // V is bf16, so phi goes into the product as bf16: 2^-8 relative at most per weight, like the
       // rounding of the output; the sums keep all 32 bits.  Scores past the last key are -inf.
       if (w0) {
-        const float2 x = *reinterpret_cast<const float2*>(sc + g * C::kScoreStride + e * 8 + 2 * t);
+        const float2 x = *reinterpret_cast<const float2*>(sc + g * C::kScoreStride + at + ((e * 8) ^ flip));
         const float f0 = phi_fast((m0 - x.x) * a.scale), f1 = phi_fast((m0 - x.y) * a.scale);
         t0 += f0 + f1;
         live += f0 + f1;
         w[2 * e] = pack_bf16x2(f0, f1);
       }
       if (w1) {
-        const float2 x = *reinterpret_cast<const float2*>(sc + (g + 8) * C::kScoreStride + e * 8 + 2 * t);
+        const float2 x = *reinterpret_cast<const float2*>(sc + (g + 8) * C::kScoreStride + at + ((e * 8) ^ flip));
         const float f0 = phi_fast((m1 - x.x) * a.scale), f1 = phi_fast((m1 - x.y) * a.scale);
         t1 += f0 + f1;
         live += f0 + f1;

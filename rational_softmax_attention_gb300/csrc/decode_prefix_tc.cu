@@ -32,7 +32,7 @@ constexpr int BM = 128, BN = 128;
 constexpr int SOFTMAX_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int THREADS = 32 * 10;
 constexpr uint32_t TMEM_O = 256;          // score buffer b at column 128 b, O behind both
-constexpr int SPLIT_BATCH = 256;          // up to so many sequences' block counts are kept in shared memory
+constexpr int SPLIT_BATCH = 512;          // up to so many sequences' block counts are kept in shared memory
 constexpr int BOX_BYTES = 128 * 64 * 2;   // one TMA box: 128 rows x 64 values
 
 template <int D, bool VALUES>
@@ -48,33 +48,29 @@ struct Cfg {
   static constexpr int OFF_HALF = OFF_MISC + 16 + 2 * SOFTMAX_WARPS * 4;     // the upper halves' row results
   static constexpr int OFF_CUM = OFF_HALF + BM * 4;
   static constexpr int SMEM_BYTES = OFF_CUM + (VALUES ? (SPLIT_BATCH + 1) * 4 : 0);
-  // beside it, on one SM, a CTA of decode_values_kernel: 66,564 bytes with 64 sequences
-  static_assert(SMEM_BYTES + 1024 + 66564 <= 233472, "shared memory per SM");
+  // beside it, on one SM, a CTA of decode_values_kernel of 63.5 KB
+  static_assert(SMEM_BYTES + 1024 + 65024 <= 233472, "shared memory per SM");
   static_assert(NSTAGE * TILE_BYTES >= SOFTMAX_WARPS * 4096, "the output leaves through the ring");
 };
 
-// phi of 64 columns of a row: d = m - s is exact 0 at the maximum; columns from `n` on are not keys.
+// phi of 32 columns of a row: d = m - s is exact 0 at the maximum; columns from `n` on are not keys.
 template <bool RAGGED>
-__device__ __forceinline__ float phi_half(const uint32_t (&h)[2][32], uint32_t (&pk)[32], int n, float c2, float m) {
+__device__ __forceinline__ float phi_chunk(const uint32_t (&h)[32], uint32_t (&pk)[16], int n, float c2, float m) {
   float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int c8 = 0; c8 < 8; ++c8) {
-    float x[8];
+  for (int c = 0; c < 32; c += 4) {
+    float x[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c8 * 8 + e;
-      x[e] = u2f(h[c >> 5][c & 31]) - m;
-      if (RAGGED && c >= n) x[e] = -INFINITY;
+    for (int e = 0; e < 4; ++e) {
+      x[e] = u2f(h[c + e]) - m;
+      if (RAGGED && c + e >= n) x[e] = -INFINITY;
     }
-    float2 p0, p1, p2, p3;
+    float2 p0, p1;
     phi_quad(x[0], x[1], x[2], x[3], c2, 0.5f, p0, p1);
-    phi_quad(x[4], x[5], x[6], x[7], c2, 0.5f, p2, p3);
-    sum = __fadd2_rn(sum, __fadd2_rn(__fadd2_rn(p0, p1), __fadd2_rn(p2, p3)));
+    sum = __fadd2_rn(sum, __fadd2_rn(p0, p1));
     // V is bf16, so P is: half a step, 2^-8 relative at most per weight; the sum keeps fp32
-    pk[4 * c8 + 0] = pack_bf16x2(p0.x, p0.y);
-    pk[4 * c8 + 1] = pack_bf16x2(p1.x, p1.y);
-    pk[4 * c8 + 2] = pack_bf16x2(p2.x, p2.y);
-    pk[4 * c8 + 3] = pack_bf16x2(p3.x, p3.y);
+    pk[c / 2] = pack_bf16x2(p0.x, p0.y);
+    pk[c / 2 + 1] = pack_bf16x2(p1.x, p1.y);
   }
   return sum.x + sum.y;
 }
@@ -102,10 +98,10 @@ __device__ __forceinline__ float half_maximum(const DecodeArgs& a, const int* cu
 
 __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Bounded as for 512 threads, that is 128 registers each: the 320 leave 24,576 of an SM's, enough
-// for a CTA of the kernels that run beside this one.
+// Bounded as for 640 threads, that is 96 registers each: the 320 leave 34,816 of an SM's, enough
+// for two CTAs of the kernels that run beside this one.
 template <int D, bool VALUES>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(640, 1)
     decode_prefix_kernel(const __grid_constant__ PrefixMaps maps, const DecodeArgs a, const LaunchCtx ctx) {
   using C = Cfg<D, VALUES>;
   constexpr int NST = C::NSTAGE;
@@ -299,14 +295,15 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int tail = a.P - t0 * BN - 64 * upper;   // keys from this half's first on
     bool ok = true;
-    uint32_t h[2][32];
-    // this half's scores of tile j into registers
-    auto take = [&](int j) -> bool {
+    uint32_t h[32];
+    // 32 columns of this half's scores of tile j into registers
+    auto take = [&](int j, int c) {
+      tmem_ld32(lanes + 128 * (j & 1) + 64 * upper + c, h);
+      tc_wait_ld();
+    };
+    auto formed = [&](int j) -> bool {
       if (!warp_wait(&s_full[j & 1], (j >> 1) & 1)) return false;
       tc_fence_after();
-      tmem_ld32(lanes + 128 * (j & 1) + 64 * upper, h[0]);
-      tmem_ld32(lanes + 128 * (j & 1) + 64 * upper + 32, h[1]);
-      tc_wait_ld();
       return true;
     };
     auto hand = [&](int j) {
@@ -317,20 +314,24 @@ __global__ void __launch_bounds__(512, 1)
     if constexpr (!VALUES) {
       float m = -INFINITY;
       for (int j = 0; j < nt; ++j) {
-        ok = take(j);
+        ok = formed(j);
         if (!ok) break;
-        hand(j);
         float u0 = -INFINITY, u1 = -INFINITY;
-        if (j * BN + 64 <= tail) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            u0 = max3f(u0, u2f(h[0][c]), u2f(h[0][c + 1]));
-            u1 = max3f(u1, u2f(h[1][c]), u2f(h[1][c + 1]));
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          take(j, c0);
+          if (c0) hand(j);
+          if (j * BN + c0 + 32 <= tail) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              u0 = max3f(u0, u2f(h[c]), u2f(h[c + 1]));
+              u1 = max3f(u1, u2f(h[c + 2]), u2f(h[c + 3]));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (j * BN + c0 + c < tail) u0 = fmaxf(u0, u2f(h[c]));
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (j * BN + c < tail) u0 = fmaxf(u0, u2f(h[c >> 5][c & 31]));
         }
         m = fmaxf(m, fmaxf(u0, u1));
       }
@@ -368,15 +369,18 @@ __global__ void __launch_bounds__(512, 1)
       const float c2 = a.scale * (1.0f / 32.0f);
       float total = 0.0f;
       for (int j = 0; j < nt; ++j) {
-        ok = take(j);
+        ok = formed(j);
         if (!ok) break;
-        const int n = tail - j * BN;
-        uint32_t pk[32];
-        const float t = n < 64 ? phi_half<true>(h, pk, n, c2, m) : phi_half<false>(h, pk, n, c2, m);
-        // P over this half's own scores, which only this thread read: two keys per column
-        const uint32_t pcol = lanes + 128 * (j & 1) + 64 * upper;
-        tmem_st16(pcol, reinterpret_cast<const uint32_t(&)[16]>(pk[0]));
-        tmem_st16(pcol + 16, reinterpret_cast<const uint32_t(&)[16]>(pk[16]));
+        float t = 0.0f;
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          take(j, c0);
+          const int n = tail - j * BN - c0;
+          uint32_t pk[16];
+          t += n < 32 ? phi_chunk<true>(h, pk, n, c2, m) : phi_chunk<false>(h, pk, n, c2, m);
+          // P over this half's own scores, which only this thread reads: two keys per column
+          tmem_st16(lanes + 128 * (j & 1) + 64 * upper + c0 / 2, pk);
+        }
         tc_wait_st();
         total += t;
         const unsigned any = __any_sync(0xffffffffu, t > 0.0f);

@@ -6,8 +6,9 @@
 // order, to the first m slots of another cache.
 //
 //   select   a cluster of CTAs per (sequence, head), each with a slice of the entries: the threshold
-//            by a radix selection over the weights' order-preserving bits (11, 11 and 10 at a
-//            time; the CTAs' counts are added through distributed shared memory), then the kept
+//            by a radix selection over the weights' order-preserving bits (eight at a time; the
+//            CTAs' counts are added through distributed shared memory, whose reads cost more than
+//            a fourth pass: with 2048 bins they took 3 us a pass), then the kept
 //            slots in order by prefix sums.  Counts are integers, so nothing depends on the order
 //            of the atomics.  A CTA's first 8192 weights stay in registers between the passes.
 //   gather   the kept entries, 16 bytes per lane.
@@ -18,7 +19,7 @@ namespace raattn {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 
 // Order-preserving bits of a weight: larger weights give larger bits; -0 and 0 are equal; NaN above all.
 __device__ __forceinline__ uint32_t order_bits(float w) {
@@ -26,6 +27,8 @@ __device__ __forceinline__ uint32_t order_bits(float w) {
   if (w != w) return 0xffffffffu;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+
+constexpr uint32_t kZeroBits = 0x80000000u;   // order_bits(0)
 
 // Exclusive prefix sum of v over the CTA; *total the sum.  All threads.
 __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
@@ -59,7 +62,7 @@ constexpr int kHeld = 2;                       // chunks held in registers
 
 template <int S>   // CTAs of a cluster
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int2 hist[kBins / 2];
+  __shared__ int hist[kBins];
   __shared__ int warp_sums[32];
   __shared__ int found, left;
   __shared__ int2 counts;   // entries of this CTA's slice above the threshold, and equal to it
@@ -104,45 +107,48 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   // share the bits found so far.
   uint32_t prefix = 0;
   int rest = need, done = 0;   // done: bits found
-  for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass < 2 ? 11 : 10, shift = 32 - done - bits;
-    hist[threadIdx.x] = make_int2(0, 0);
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (threadIdx.x < kBins) hist[threadIdx.x] = 0;
     __syncthreads();
     each([&](int, const uint32_t (&u)[kPer]) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (u[j] && (done == 0 || u[j] >> (32 - done) == prefix))
-          atomicAdd(&reinterpret_cast<int*>(hist)[(u[j] >> shift) & ((1u << bits) - 1u)], 1);
+      for (int j = 0; j < kPer; ++j) {
+        const bool in = u[j] && (done == 0 || u[j] >> (32 - done) == prefix);
+        // weights of exactly 0 (entries outside every query's support) are many: one addition for a warp's
+        const unsigned zeros = __ballot_sync(0xffffffffu, in && u[j] == kZeroBits);
+        if (zeros && (threadIdx.x & 31) == 0) atomicAdd(&hist[kZeroBits >> shift & 255u], __popc(zeros));
+        if (in && u[j] != kZeroBits) atomicAdd(&hist[u[j] >> shift & 255u], 1);
+      }
     });
     if (S > 1) cluster_sync();
     else __syncthreads();
-    // bins from the top: thread t owns the t-th pair of bins counted from the highest
-    const int pair = kBins / 2 - 1 - static_cast<int>(threadIdx.x);
-    int2 c = make_int2(0, 0);
-    if (S > 1) {
-      const uint32_t at = smem_u32(&hist[pair]);
+    // bins from the top, one thread each
+    const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+    int c = 0;
+    if (threadIdx.x < kBins) {
+      if (S > 1) {
+        const uint32_t at = smem_u32(&hist[bin]);
+        int x[S];
 #pragma unroll
-      for (int r = 0; r < S; ++r) {
-        int x, y;
-        asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(mapa_shared(at, r)) : "memory");
-        c.x += x;
-        c.y += y;
+        for (int r = 0; r < S; ++r)
+          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x[r]) : "r"(mapa_shared(at, r)) : "memory");
+#pragma unroll
+        for (int r = 0; r < S; ++r) c += x[r];
+      } else {
+        c = hist[bin];
       }
-    } else {
-      c = hist[pair];
     }
     int total;
-    const int before = block_exclusive(c.x + c.y, warp_sums, &total);
-    if (before < rest && rest <= before + c.x + c.y) {
-      const bool upper = rest <= before + c.y;
-      found = 2 * pair + (upper ? 1 : 0);
-      left = rest - before - (upper ? 0 : c.y);
+    const int before = block_exclusive(c, warp_sums, &total);
+    if (before < rest && rest <= before + c) {
+      found = bin;
+      left = rest - before;
     }
     if (S > 1) cluster_sync();   // the counts have been read, too
     else __syncthreads();
-    prefix = prefix << bits | static_cast<uint32_t>(found);
+    prefix = prefix << 8 | static_cast<uint32_t>(found);
     rest = left;
-    done += bits;
+    done += 8;
   }
   // The kept slots in order: entries above the threshold and the first `rest` equal to it.  Both
   // counts of a chunk (at most 4096) go through one prefix sum.
@@ -238,12 +244,13 @@ cudaError_t select(const EvictArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// CTAs of a row's cluster: as many as the SMs hold at once (two of 1024 threads each), while each
-// still gets a chunk of 4096 entries.  32 rows of 32768: 46 us with one, B32 H8 of 4352: 12 us.
+// CTAs of a row's cluster: as many as give every SM one at most, while each still gets a chunk of
+// 4096 entries.  (Two per SM do not all find room in clusters of eight: 32 rows of 32768 took 44 us
+// so, gather included, against 23 with clusters of four; with one CTA per row 42.)
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv, chunks = (a.C + kChunk - 1) / kChunk;
   int s = 1;
-  while (s < 8 && rows * 2 * s <= 2 * kSms && 2 * s <= chunks) s *= 2;
+  while (s < 8 && rows * 2 * s <= kSms && 2 * s <= chunks) s *= 2;
   const cudaError_t e = s == 8 ? select<8>(a, st) : s == 4 ? select<4>(a, st) : s == 2 ? select<2>(a, st) : select<1>(a, st);
   if (e != cudaSuccess) return e;
   const int64_t total = rows * a.keep * (a.row_bytes / 16);

@@ -156,7 +156,8 @@ struct NormRopeShape {
   int B, N, Hq, Hkv, D;
   int norm;                     // ra_norm_t
   float eps;
-  int ctas[3], tiles[3];        // set by the launcher: CTAs for query, key and value rows; tokens of their tiles
+  int ctas[3], tiles[3], stride;   // set by the launcher: CTAs for query, key and value rows; tokens of their
+                                   // tiles; the step of the CTAs' permutation
 };
 struct NormRopeFwd {
   void *q, *k, *v;              // q [B, Hq, N, D]; k, v [B, Hkv, capacity, D]

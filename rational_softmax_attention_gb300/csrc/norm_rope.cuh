@@ -106,7 +106,9 @@ __device__ __forceinline__ void init_turns(Tables& tb, const NormRopeShape& a) {
 }
 
 // The cosines and sines of a tile's tokens.  Threads are laid out with the pairs (a power of two
-// of them) fastest; token numbers fit 32 bits, where a division is cheap.
+// of them) fastest; token numbers fit 32 bits, where a division is cheap.  FAST (bf16): the
+// approximate sine and cosine, off by 2^-21 at most within half a turn, far below bf16's 2^-8.
+template <bool FAST>
 __device__ __forceinline__ void fill_table(Tables& tb, int buf, const NormRopeShape& a, int tok0, int tile) {
   const int lg = 32 - __clz(a.pairs - 1), p = threadIdx.x & ((1 << lg) - 1);   // pairs = 1: lg = 0
   if (p >= a.pairs) return;
@@ -119,7 +121,9 @@ __device__ __forceinline__ void fill_table(Tables& tb, int buf, const NormRopeSh
     if (tok < tokens) {
       const int b = tok / a.N, n = tok - b * a.N;
       float s, c;
-      sincospif(2.0f * turn_fraction(pos[b * a.pos_batch_stride + n], turns), &s, &c);
+      const float f = turn_fraction(pos[b * a.pos_batch_stride + n], turns);
+      if (FAST) __sincosf(6.28318531f * f, &s, &c);
+      else sincospif(2.0f * f, &s, &c);
       tb.cs[buf][tl][p] = c;
       tb.sn[buf][tl][p] = s;
     }
@@ -257,10 +261,13 @@ struct Work {
   int heads, head0;     // its heads, the first of them in a token of the projection
   int tile;             // tokens of a tile
   int first, step;      // tiles first, first + step, ..
+  int place;            // among all CTAs, those of a kind together
 };
 __device__ __forceinline__ Work work_of(const NormRopeShape& a) {
   Work w;
-  int x = blockIdx.x;
+  const int all = a.ctas[0] + a.ctas[1] + a.ctas[2];
+  int x = blockIdx.x * a.stride % all;   // a permutation: an SM's CTAs are seldom of one kind
+  w.place = x;
   w.kind = x < a.ctas[0] ? 0 : x < a.ctas[0] + a.ctas[1] ? 1 : 2;
   if (w.kind > 0) x -= a.ctas[0];
   if (w.kind > 1) x -= a.ctas[1];
@@ -283,17 +290,18 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Shares `most` CTAs among the kinds by their cost per head, and sets the tiles' tokens: a tile for
+// Shares `most` CTAs among the kinds by their cost per head and per token, and sets the tiles' tokens: a tile for
 // every CTA first; then as many tokens as leave no lane group without a head, and more, since what
 // a token costs once is shared by the heads that one lane group walks, while each CTA still gets
 // four tiles.
-inline void plan_work(NormRopeShape* a, int es, int most, const int (&cost)[3]) {
+inline void plan_work(NormRopeShape* a, int es, int most, const int (&head_cost)[3], const int (&token_cost)[3]) {
   const int groups = kThreads / (a->D * es / 32);
   const int64_t tokens = static_cast<int64_t>(a->B) * a->N;
   const int heads[3] = {a->Hq, a->Hkv, a->Hkv};
-  const int64_t all = static_cast<int64_t>(cost[0]) * heads[0] + static_cast<int64_t>(cost[1] + cost[2]) * heads[1];
+  int64_t cost[3], all = 0;
+  for (int k = 0; k < 3; ++k) all += cost[k] = static_cast<int64_t>(head_cost[k]) * heads[k] + token_cost[k];
   for (int k = 0; k < 3; ++k) {
-    const int64_t share = static_cast<int64_t>(most) * cost[k] * heads[k] / all;
+    const int64_t share = most * cost[k] / all;
     const int64_t ctas = share < 1 ? 1 : share;
     int t = 1;
     while (2 * t <= groups && t < kMaxTile && tokens / (2 * t) >= (groups / t > heads[k] ? ctas : 4 * ctas)) t *= 2;
@@ -301,6 +309,18 @@ inline void plan_work(NormRopeShape* a, int es, int most, const int (&cost)[3]) 
     a->tiles[k] = t;
     a->ctas[k] = static_cast<int>(tiles < ctas ? tiles : ctas);
   }
+  // a step of about three eighths of the grid that has no divisor in common with it
+  const int grid = a->ctas[0] + a->ctas[1] + a->ctas[2];
+  auto common = [](int x, int y) {
+    while (y) {
+      const int r = x % y;
+      x = y;
+      y = r;
+    }
+    return x;
+  };
+  a->stride = grid * 3 / 8 + 1;
+  while (common(a->stride, grid) != 1) ++a->stride;
 }
 
 }  // namespace norm_rope

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_fwd_kernel(const NormRo
     }
     const int64_t kv_at = (static_cast<int64_t>(b) * a.Hkv + hs) * io.capacity + slot;
     if (turns) {   // under the first rows' copies
-      fill_table(tb, buf, a, tile * tile_tokens, tile_tokens);
+      fill_table<sizeof(T) == 2>(tb, buf, a, tile * tile_tokens, tile_tokens);
       __syncthreads();
     }
 #pragma unroll 1

@@ -211,10 +211,18 @@ def ra_qk_norm_rope_backward(qkv, dq, dk, dv, num_heads, num_kv_heads=None, *, n
     dparams = ws = None
     if norm != "none":
         dparams = torch.empty((4, D), dtype=torch.float32, device=device)
-        ws = torch.empty(lib().ra_qk_norm_rope_bwd_workspace_size(D) or 16, dtype=torch.uint8, device=device)
+        ws = torch.empty(_norm_rope_workspace(D), dtype=torch.uint8, device=device)
     _call("ra_qk_norm_rope_bwd", device, *lead, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dqkv.data_ptr(),
           _addr(dparams), _addr(ws), B, N, Hq, Hkv, D, code)
-    return (dqkv, *(None if p is None else dparams[i] for i, p in enumerate(params)))
+    if dparams is None:
+        return dqkv, None, None, None, None
+    dqw, dqb, dkw, dkb = dparams.unbind(0)
+    return dqkv, dqw, None if q_bias is None else dqb, dkw, None if k_bias is None else dkb
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_rope_workspace(D):
+    return lib().ra_qk_norm_rope_bwd_workspace_size(D) or 16
 
 
 def ra_cache_append(qkv, k, v, length, num_heads, num_kv_heads=None, *, count=None, norm="layer", q_weight=None,

@@ -100,7 +100,7 @@ CASES = [  # B, Hq, Hkv, C, P, D, sigma, lengths
     (128, 2, 2, 9, 1024, 64, 1.0, [i % 10 for i in range(128)]),       # exactly one row tile
     (150, 4, 1, 5, 1000, 64, 3.0, [i % 6 for i in range(150)]),        # 600 rows
     (36, 8, 8, 700, 2900, 128, 3.0, [700 - i for i in range(36)]),
-    (600, 2, 1, 5, 300, 64, 1.0, [i % 6 for i in range(600)]),         # more than 256 sequences
+    (600, 2, 1, 5, 300, 64, 1.0, [i % 6 for i in range(600)]),         # more than 512 sequences
 ]
 
 
