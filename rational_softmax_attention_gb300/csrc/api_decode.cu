@@ -64,13 +64,11 @@ ra_status_t norm_rope_shape(NormRopeShape* a, const void* qkv, int64_t batch_str
   return RA_OK;
 }
 
-constexpr int kMaxBatch = 8192;   // a decode CTA keeps one count per sequence in shared memory
-
 ra_status_t decode_shape(DecodeArgs* a, int B, int Hq, int Hkv, int C, int P, int D) {
   if (B < 1 || Hq < 1 || Hkv < 1 || C < 1 || P < 0 || D < 1 || Hq % Hkv) return RA_ERR_ARG;
   if (!rows_ok(B, Hq, 1) || C > INT_MAX - 1024 || P > INT_MAX - 1024) return RA_ERR_ARG;
   if (!rows_ok(B, Hkv, C) || !rows_ok(Hkv, P, 1)) return RA_ERR_ARG;
-  if (!head_dim_ok(D) || B > kMaxBatch || Hq / Hkv > 1024) return RA_ERR_UNSUPPORTED;
+  if (!head_dim_ok(D) || B > kDecodeMaxBatch || Hq / Hkv > 1024) return RA_ERR_UNSUPPORTED;
   a->B = B;
   a->Hq = Hq;
   a->Hkv = Hkv;

@@ -3,6 +3,7 @@
 // tensor-core kernels use (mbarrier, TMA bulk tensor copies, tcgen05).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -218,6 +219,24 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// A kernel's attributes, set on its first launch on a device (they last as long as the device's
+// context, like the library's other per-device state): the most dynamic shared memory that any
+// launch of it asks for, and with `carveout` the largest shared-memory part of an SM's L1.
+template <auto KERNEL>
+cudaError_t set_up_kernel(int smem, bool carveout) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  if (smem > 0) e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && carveout)
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // ----------------------------------------------------------------------------

@@ -834,26 +834,19 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     if (first + i * kThreads < last) w[i * kThreads] = sum[i] + add[i];
 }
 
-// The most shared memory of an SM's carve-out, also for kernels that would do with less: an SM changes
-// it only when it is empty, and the next kernel's CTAs, launched as dependents, come before that.
-template <typename... P>
-cudaError_t prepare(void (*kernel)(P...), int smem) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                             cudaSharedmemCarveoutMaxShared);
-  return e == cudaSuccess && smem > 0
-             ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
-             : e;
-}
-
 template <typename T, int D, int TW>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
   using C = Cfg<T, D>;
   const int cum = (2 * a.B + 1) * 4;
   const int smem_scores = kWarps * C::kStages * C::kStageK + cum;
   const int smem_values = kWarps * C::kStages * C::kStageV + cum;
-  cudaError_t e = prepare(decode_scores_kernel<T, D, TW>, smem_scores);
-  if (e == cudaSuccess) e = prepare(decode_values_kernel<T, D, TW>, smem_values);
-  if (e == cudaSuccess) e = prepare(decode_join_kernel<T, D>, 0);
+  // The most shared memory of an SM's carve-out also for kernels that would do with less: an SM changes
+  // it only when it is empty, and the next kernel's CTAs, launched as dependents, come before that.
+  constexpr int kMostCum = (2 * kDecodeMaxBatch + 1) * 4;
+  cudaError_t e = set_up_kernel<decode_scores_kernel<T, D, TW>>(kWarps * C::kStages * C::kStageK + kMostCum, true);
+  if (e == cudaSuccess)
+    e = set_up_kernel<decode_values_kernel<T, D, TW>>(kWarps * C::kStages * C::kStageV + kMostCum, true);
+  if (e == cudaSuccess) e = set_up_kernel<decode_join_kernel<T, D>>(0, true);
   if (e != cudaSuccess) return e;
   // CTAs for the runs that there can be
   const int64_t most = static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks +

@@ -435,10 +435,7 @@ __global__ void __launch_bounds__(640, 1)
 template <int D, bool VALUES>
 cudaError_t go(const PrefixMaps& maps, const DecodeArgs& a, const LaunchCtx& ctx, cudaStream_t st) {
   auto kernel = decode_prefix_kernel<D, VALUES>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                       cudaSharedmemCarveoutMaxShared);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, VALUES>::SMEM_BYTES);
+  const cudaError_t e = set_up_kernel<decode_prefix_kernel<D, VALUES>>(Cfg<D, VALUES>::SMEM_BYTES, true);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(a.Hkv) * ((a.B * a.G + BM - 1) / BM) * a.pslots;
   if constexpr (VALUES) return launch_dependent(kernel, grid, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st, maps, a, ctx);

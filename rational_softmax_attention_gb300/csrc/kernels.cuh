@@ -176,6 +176,7 @@ cudaError_t launch_norm_rope_fwd(NormRopeShape a, const NormRopeFwd& io, bool bf
 cudaError_t launch_norm_rope_bwd(NormRopeShape a, const NormRopeBwd& io, bool bf16, cudaStream_t st);
 
 // One query token per sequence against its cache and a shared prefix (decode.cu).
+constexpr int kDecodeMaxBatch = 8192;   // a CTA keeps two counts per sequence in shared memory
 struct DecodeArgs {
   const void *q, *k, *v, *pk, *pv;   // [B, Hq, D], [B, Hkv, C, D] x2, [Hkv, P, D] x2
   const int32_t* length;        // [B], read as min(max(length, 0), C)

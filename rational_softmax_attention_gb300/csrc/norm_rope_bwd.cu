@@ -192,10 +192,9 @@ static_assert(kRingBytes >= kThreads * 16 * 4, "the lane groups' sums fit the ri
 
 template <typename T, int D, int NORM>
 cudaError_t go(const NormRopeShape& a, const NormRopeBwd& io, cudaStream_t st) {
-  auto kernel = norm_rope_bwd_kernel<T, D, NORM>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  cudaError_t e = set_up_kernel<norm_rope_bwd_kernel<T, D, NORM>>(kRingBytes, false);
   if (e != cudaSuccess) return e;
-  kernel<<<a.ctas[0] + a.ctas[1] + a.ctas[2], kThreads, kRingBytes, st>>>(a, io);
+  norm_rope_bwd_kernel<T, D, NORM><<<a.ctas[0] + a.ctas[1] + a.ctas[2], kThreads, kRingBytes, st>>>(a, io);
   if (NORM == RA_NORM_NONE) return cudaGetLastError();
   e = cudaGetLastError();
   return e != cudaSuccess ? e
