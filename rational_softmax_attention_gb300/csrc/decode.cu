@@ -723,29 +723,30 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
 // ---------------------------------------------------------------------------------------------
 // join
 // ---------------------------------------------------------------------------------------------
-constexpr int kWeightKeys = 8 * kThreads;   // keys of a weight CTA
+constexpr int kWeightKeys = 4 * kThreads;   // keys a weight CTA takes at a time, four consecutive ones per thread
+constexpr int kWeightRows = 8;              // rows whose scores a thread has in flight
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs a, int weight_keys) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+  const int row_ctas = (a.B * a.Hq + kWarps - 1) / kWarps;
   await_previous();
   const Split sp = decode_split(a, a.cum[a.B]);   // the counts that the scores kernel left
-  if (blockIdx.x < rows) {   // one output row
-    constexpr int L = D / 4, KS = kThreads / L;
-    __shared__ float4 part[KS][L];
-    __shared__ float sums[KS];
-    const int row = blockIdx.x, b = row / a.Hq, kv = (row - b * a.Hq) / a.G;
+  if (static_cast<int>(blockIdx.x) < row_ctas) {   // one output row per warp
+    constexpr int L = D / 4, KS = 32 / L;
+    const int row = blockIdx.x * kWarps + warp;
+    if (row >= a.B * a.Hq) return;
+    const int b = row / a.Hq, kv = (row - b * a.Hq) / a.G;
     int shared, own;
     decode_row_slots(b, kv, row - b * a.Hq - kv * a.G, a.cum[b], a.cum[b + 1], sp, a, shared, own);
-    const int gl = threadIdx.x % L, ks = threadIdx.x / L;
+    const int gl = lane % L, ks = lane / L;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float total = 0.0f;
-    for (int i0 = ks; i0 < shared + own; i0 += 4 * KS) {   // four parts at a time in flight
-      float f[4];
-      float4 x[4];
+    for (int i0 = ks; i0 < shared + own; i0 += 8 * KS) {   // eight parts at a time in flight
+      float f[8];
+      float4 x[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const int i = i0 + j * KS;
         const int64_t at = static_cast<int64_t>(row) * a.slots + (i < shared ? i : a.pslots + i - shared);
         const bool in = i < shared + own;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
         x[j] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D) + gl) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j)
         if (f[j] > 0.0f) {   // a part whose weights are all 0 may have written no output
           s.x += x[j].x;
           s.y += x[j].y;
@@ -762,19 +763,15 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
           total += f[j];
         }
     }
-    part[ks][gl] = s;
-    if (gl == 0) sums[ks] = total;
-    __syncthreads();
-    if (ks == 0) {
 #pragma unroll
-      for (int i = 1; i < KS; ++i) {
-        const float4 x = part[i][gl];
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
-        total += sums[i];
-      }
+    for (int o = L; o < 32; o <<= 1) {
+      s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+      s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+      s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+      s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (ks == 0) {
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // no key at all: zeros
       T* o = static_cast<T*>(a.o) + static_cast<int64_t>(row) * D + gl * 4;
       if constexpr (sizeof(T) == 2) {
@@ -785,53 +782,82 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
     }
     return;
   }
-  // weights of kWeightKeys keys of one (sequence, key head)
+  // the weights of weight_keys keys of one (sequence, key head)
   extern __shared__ float2 stat[];   // [G] maximum, 1 / sum
-  const int splits = (a.C + kWeightKeys - 1) / kWeightKeys;
-  const int64_t x = blockIdx.x - rows;
-  const int split = static_cast<int>(x % splits);
-  const int bk = static_cast<int>(x / splits), b = bk / a.Hkv, kv = bk - b * a.Hkv;
-  const int first = split * kWeightKeys + threadIdx.x, last = decode_own_length(a, b);
-  if (split * kWeightKeys >= last) return;
-  // the scores of the first row and the weights are on their way while the statistics are gathered
-  const float* sc = a.s_own + (static_cast<int64_t>(b) * a.Hq + kv * a.G) * a.own_width + first;
-  float* w = a.weight + static_cast<int64_t>(bk) * a.C + first;
-  float sum[8], next[8];
+  const int splits = (a.C + weight_keys - 1) / weight_keys;
+  const int item = blockIdx.x - row_ctas, bk = item / splits, b = bk / a.Hkv, kv = bk - b * a.Hkv;
+  const int split0 = (item - bk * splits) * weight_keys, last = min(split0 + weight_keys, decode_own_length(a, b));
+  if (split0 >= last) return;
+  int first = split0 + threadIdx.x * 4;
+  // the scores of the first rows and the weights are on their way while the statistics are gathered
+  const float* sc = a.s_own + (static_cast<int64_t>(b) * a.Hq + kv * a.G) * a.own_width;
+  float* w = a.weight + static_cast<int64_t>(bk) * a.C;
+  float4 s[kWeightRows];
+  auto load = [&](int g0) {   // a row of scores is padded to whole blocks
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool in = first + i * kThreads < last;
-    next[i] = in ? __ldcg(sc + i * kThreads) : -kInf;
-    sum[i] = in ? w[i * kThreads] : 0.0f;
-  }
+    for (int j = 0; j < kWeightRows; ++j)
+      if (first < last && g0 + j < a.G)
+        s[j] = __ldcg(reinterpret_cast<const float4*>(sc + static_cast<int64_t>(g0 + j) * a.own_width + first));
+  };
+  float old[4];
+  auto load_old = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) old[i] = first + i < last ? w[first + i] : 0.0f;
+  };
+  load(0);
+  load_old();
   for (int g = warp * 8 + (lane >> 2); g < (a.G + 7) / 8 * 8; g += kWarps * 8) {   // four lanes per row
-    const int row = b * a.Hq + kv * a.G + min(g, a.G - 1);
+    const int gg = min(g, a.G - 1);
     int shared, own;
-    decode_row_slots(b, kv, min(g, a.G - 1), a.cum[b], a.cum[b + 1], sp, a, shared, own);
-    const int64_t at = static_cast<int64_t>(row) * a.slots;
-    const float m = fold_slots<4>(a.row_max + at, shared, own, a.pslots, lane & 3, -kInf,
-                                  [](float u, float v) { return fmaxf(u, v); });
-    const float s = fold_slots<4>(a.part_sum + at, shared, own, a.pslots, lane & 3, 0.0f,
-                                  [](float u, float v) { return u + v; });
-    if ((lane & 3) == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / s);
-  }
-  __syncthreads();
-  float add[8] = {};   // this call's weights first, then one addition to the running total
-  for (int g = 0; g < a.G; ++g) {
-    const float2 ms = stat[g];
-    float s[8];
+    decode_row_slots(b, kv, gg, a.cum[b], a.cum[b + 1], sp, a, shared, own);
+    const int64_t at = (static_cast<int64_t>(b) * a.Hq + kv * a.G + gg) * a.slots;
+    float m = -kInf, total = 0.0f;
+    for (int i0 = lane & 3; i0 < shared + own; i0 += 16) {
+      float y[4], z[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = next[i];
-    sc += a.own_width;
-    if (g + 1 < a.G) {
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 4 * j;
+        const bool in = i < shared + own;
+        const int64_t slot = at + (i < shared ? i : a.pslots + i - shared);
+        y[j] = in ? __ldcg(a.row_max + slot) : -kInf;
+        z[j] = in ? __ldcg(a.part_sum + slot) : 0.0f;
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) next[i] = first + i * kThreads < last ? __ldcg(sc + i * kThreads) : -kInf;
+      for (int j = 0; j < 4; ++j) {
+        m = fmaxf(m, y[j]);
+        total += z[j];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) add[i] = fmaf(phi_t<T>((ms.x - s[i]) * a.scale), ms.y, add[i]);
+    for (int o = 1; o < 4; o <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if ((lane & 3) == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / total);
   }
+  __syncthreads();
+  while (first < last) {
+    float add[4] = {};   // this call's weights first, then one addition to the running total
+    for (int g0 = 0; g0 < a.G; g0 += kWeightRows) {
+      if (g0) load(g0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (first + i * kThreads < last) w[i * kThreads] = sum[i] + add[i];
+      for (int j = 0; j < kWeightRows; ++j) {
+        if (g0 + j < a.G) {
+          const float2 ms = stat[g0 + j];
+          add[0] = fmaf(phi_t<T>((ms.x - s[j].x) * a.scale), ms.y, add[0]);
+          add[1] = fmaf(phi_t<T>((ms.x - s[j].y) * a.scale), ms.y, add[1]);
+          add[2] = fmaf(phi_t<T>((ms.x - s[j].z) * a.scale), ms.y, add[2]);
+          add[3] = fmaf(phi_t<T>((ms.x - s[j].w) * a.scale), ms.y, add[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (first + i < last) w[first + i] = old[i] + add[i];
+    first += kWeightKeys;
+    load(0);
+    load_old();
+  }
 }
 
 template <typename T, int D, int TW>
@@ -863,9 +889,17 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
   e = launch_dependent(decode_values_kernel<T, D, TW>, grid, kThreads, smem_values, st, a);
   if (e != cudaSuccess) return e;
-  const int64_t join = static_cast<int64_t>(a.B) * a.Hq +
-                       (a.weight ? static_cast<int64_t>(a.B) * a.Hkv * ((a.C + kWeightKeys - 1) / kWeightKeys) : 0);
-  return launch_dependent(decode_join_kernel<T, D>, static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st, a);
+  // Few CTAs: a weight CTA takes as many keys, up to 4096, as leave about six per SM (starting the
+  // 6144 CTAs of one row or 512 keys each took most of 15 us at B64 H32/8 C4096).
+  int64_t join = (static_cast<int64_t>(a.B) * a.Hq + kWarps - 1) / kWarps;
+  int weight_keys = kWeightKeys;
+  if (a.weight) {
+    const int64_t streams = static_cast<int64_t>(a.B) * a.Hkv;
+    while (weight_keys < 8 * kWeightKeys && streams * ((a.C + weight_keys - 1) / weight_keys) > 6 * kSms) weight_keys *= 2;
+    join += streams * ((a.C + weight_keys - 1) / weight_keys);
+  }
+  return launch_dependent(decode_join_kernel<T, D>, static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st, a,
+                          weight_keys);
 }
 template <typename T, int D>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
