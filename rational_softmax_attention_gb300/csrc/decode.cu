@@ -418,7 +418,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   // Only now: dependents that wait beside this kernel's CTAs cost more than their early start gives
   // (B64 H8 of 2048 own keys: 132 us with the release at the start, 117 with it here).
   release_dependents();
-  await_previous();   // the tensor cores' part, if any: whoever awaits this kernel awaits that too
+  // The tensor cores' part, if any: whoever awaits this kernel awaits that too.  One CTA sees to it; the
+  // others make room for the next ones.
+  if (blockIdx.x == gridDim.x - 1) await_previous();
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -717,7 +719,8 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
     team_sync<TW>();
   }
   release_dependents();
-  if (a.tc) await_previous();   // whoever awaits this kernel awaits the tensor cores' part too
+  // Whoever awaits this kernel awaits the tensor cores' part too: see the scores kernel.
+  if (a.tc && blockIdx.x == gridDim.x - 1) await_previous();
 }
 
 // ---------------------------------------------------------------------------------------------
