@@ -914,9 +914,10 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
 // The split of the keys.  Shared keys of more than kTcRows rows per key head go to the tensor
 // cores, in whole tiles of 128, split so that one wave of CTAs takes them.  Everything else is
 // cut into runs of equal length: one per warp with 64 streams or more (a stream then has at most
-// about 30 partial results), one per CTA with fewer.  A run has at least min_run blocks: two per warp
-// (in flight together) where runs could not be longer anyway, up to eight, which bounds the partial
-// results of a long stream.
+// about 30 partial results), one per CTA with fewer.  A run has at least min_run blocks: one per warp
+// (with two, fp32 B5 H12/4 C1003 P777 took 32.7 us instead of 27.0, bf16 B1 H16 C512 11.9 instead of
+// 11.2), more, up to eight, where all blocks give each run as many, which bounds the partial results of a
+// long stream.
 constexpr int64_t kTcRows = 32;
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
@@ -938,7 +939,7 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   a->team = streams >= 64 ? 1 : kWarps;
   a->runs = kDecodeCtas * kWarps / a->team;
   const int64_t even = total / a->runs;
-  a->min_run = static_cast<int>(even < 2 * a->team ? 2 * a->team : even > 8 * a->team ? 8 * a->team : even);
+  a->min_run = static_cast<int>(even < a->team ? a->team : even > 8 * a->team ? 8 * a->team : even);
   a->pchunk = a->pslots = 0;
   if (a->tc) {
     const int64_t per = a->Hkv * ((shared_rows + 127) / 128), tiles = (a->P + 127) / 128;
