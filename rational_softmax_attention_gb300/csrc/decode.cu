@@ -491,8 +491,10 @@ struct FetchValues {
 // bf16.  Lane (g, t) reads, of keys 2 t, 2 t + 1, 2 t + 8 and 2 t + 9 of sixteen, the dimensions
 // 8 g .. 8 g + 7 of every 64: words of two keys, interleaved, are the B operand of the product
 // whose column g stands for dimension 8 g + j.  phi of the scores at the same keys is the A operand.
-template <int D, int TW>
-__device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
+// TWO: the part has more than eight query rows, so the weights' second halves take a product of their
+// own; otherwise they stand in the upper eight rows of the same one.
+template <int D, int TW, bool TWO>
+__device__ __forceinline__ void bf16_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
                                             uint32_t ring, char* ring_ptr, float* rowm, float* sums, __nv_bfloat16*) {
   using C = Cfg<__nv_bfloat16, D>;
   constexpr int NC = D / 64;
@@ -507,7 +509,7 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
   }
   part_maxima<TW>(rowm, p, cum, s, a);
   team_sync<TW>();
-  const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
+  const bool w0 = g < p.rows, w1 = TWO && g + 8 < p.rows;
   const float m0 = rowm[g], m1 = rowm[g + 8];
   float acc[NC][8][4];
 #pragma unroll
@@ -523,29 +525,33 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
     copy_commit();
     const uint32_t stage = ring + i % C::kStages * C::kStageV;
     const float* sc = reinterpret_cast<const float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    uint32_t w[4] = {0u, 0u, 0u, 0u}, rest[4] = {0u, 0u, 0u, 0u};
     float live = 0.0f;
     const int at = 2 * t, flip = (g & 2) << 2;   // piece_of: pieces 2 e + t / 2, flipped by two in rows 2, 3, 6, 7
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      // V is bf16, so phi goes into the product as bf16: 2^-8 relative at most per weight, like the
-      // rounding of the output; the sums keep all 32 bits.  Scores past the last key are -inf.
+      // V is bf16, so phi goes into the product as two bf16: one alone would cost as much as the
+      // rounding of the output.  Scores past the last key are -inf.
       if (w0) {
         const float2 x = *reinterpret_cast<const float2*>(sc + g * C::kScoreStride + at + ((e * 8) ^ flip));
         const float f0 = phi_fast((m0 - x.x) * a.scale), f1 = phi_fast((m0 - x.y) * a.scale);
         t0 += f0 + f1;
         live += f0 + f1;
-        w[2 * e] = pack_bf16x2(f0, f1);
+        split_bf16x2(f0, f1, w[2 * e], rest[2 * e]);
       }
       if (w1) {
         const float2 x = *reinterpret_cast<const float2*>(sc + (g + 8) * C::kScoreStride + at + ((e * 8) ^ flip));
         const float f0 = phi_fast((m1 - x.x) * a.scale), f1 = phi_fast((m1 - x.y) * a.scale);
         t1 += f0 + f1;
         live += f0 + f1;
-        w[2 * e + 1] = pack_bf16x2(f0, f1);
+        split_bf16x2(f0, f1, w[2 * e + 1], rest[2 * e + 1]);
       }
     }
     if (!__any_sync(0xffffffffu, live > 0.0f)) continue;   // every weight is exactly 0
+    if constexpr (!TWO) {
+      w[1] = rest[0];
+      w[3] = rest[2];
+    }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       uint4 v[4];
@@ -557,8 +563,9 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-        mma_bf16(acc[c][j], w[0], w[1], w[2], w[3], __byte_perm(x0[j >> 1], x1[j >> 1], sel),
-                 __byte_perm(x2[j >> 1], x3[j >> 1], sel));
+        const uint32_t b0 = __byte_perm(x0[j >> 1], x1[j >> 1], sel), b1 = __byte_perm(x2[j >> 1], x3[j >> 1], sel);
+        mma_bf16(acc[c][j], w[0], w[1], w[2], w[3], b0, b1);
+        if constexpr (TWO) mma_bf16(acc[c][j], rest[0], rest[1], rest[2], rest[3], b0, b1);
       }
     }
   }
@@ -575,6 +582,15 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
   // dimensions 16 t + j and 16 t + 8 + j.
   __syncwarp();
   float* out = reinterpret_cast<float*>(ring_ptr);
+  if constexpr (!TWO) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[c][j][0] += acc[c][j][2];
+        acc[c][j][1] += acc[c][j][3];
+      }
+  }
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -584,6 +600,15 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
         if (e < 2 ? w0 : w1)
           *reinterpret_cast<float4*>(out + (g + (e >> 1) * 8) * D + c * 64 + t * 16 + (e & 1) * 8 + j) =
               make_float4(acc[c][j][e], acc[c][j + 1][e], acc[c][j + 2][e], acc[c][j + 3][e]);
+}
+
+template <int D, int TW>
+__device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, const Split& s, const int* cum,
+                                            uint32_t ring, char* ring_ptr, float* rowm, float* sums, __nv_bfloat16* t) {
+  if (p.rows > 8)
+    bf16_values<D, TW, true>(p, a, s, cum, ring, ring_ptr, rowm, sums, t);
+  else
+    bf16_values<D, TW, false>(p, a, s, cum, ring, ring_ptr, rowm, sums, t);
 }
 
 // fp32: D / 4 lanes across the dimensions, the other lanes over the keys; phi replaces the scores in

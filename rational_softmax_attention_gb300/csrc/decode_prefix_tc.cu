@@ -10,6 +10,11 @@
 // Forming S twice costs a third more products, but 128 rows of scores in fp32 would be twice the
 // bytes of the keys.
 //
+// V is bf16, so P is, rounded: 2^-8 relative at most per weight, like the output.  Up
+// to 128 rows a key head P goes in as two bf16 instead, itself and what that leaves: the loads bound
+// the kernel then, and the second product costs little (whole call, B32 H32/8 C1024 P8192: 46.5 us ->
+// 48.3).  With more rows the products bound it (prefix alone, P32768: B64 72.7 -> 86.6 us, B128 130 -> 158).
+//
 // A CTA takes 128 rows of one key head and a run of key tiles; the keys are split so that one wave of
 // CTAs, one per SM, covers heads x row tiles x splits.  Roles: warp 8 feeds a ring of K (and V) tiles
 // by TMA; a thread of warp 9 issues the products; warps 0-3 and 4-7 own the 128 rows, thread = row,
@@ -53,9 +58,11 @@ struct Cfg {
   static_assert(NSTAGE * TILE_BYTES >= SOFTMAX_WARPS * 4096, "the output leaves through the ring");
 };
 
-// phi of 32 columns of a row: d = m - s is exact 0 at the maximum; columns from `n` on are not keys.
-template <bool RAGGED>
-__device__ __forceinline__ float phi_chunk(const uint32_t (&h)[32], uint32_t (&pk)[16], int n, float c2, float m) {
+// phi of 32 columns of a row, as bf16 or (TWO) as two of them; d = m - s is exact 0 at the maximum; columns
+// from `n` on are not keys.
+template <bool RAGGED, bool TWO>
+__device__ __forceinline__ float phi_chunk(const uint32_t (&h)[32], uint32_t (&pk)[16], uint32_t (&lo)[16],
+                                           int n, float c2, float m) {
   float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int c = 0; c < 32; c += 4) {
@@ -68,9 +75,13 @@ __device__ __forceinline__ float phi_chunk(const uint32_t (&h)[32], uint32_t (&p
     float2 p0, p1;
     phi_quad(x[0], x[1], x[2], x[3], c2, 0.5f, p0, p1);
     sum = __fadd2_rn(sum, __fadd2_rn(p0, p1));
-    // V is bf16, so P is: half a step, 2^-8 relative at most per weight; the sum keeps fp32
-    pk[c / 2] = pack_bf16x2(p0.x, p0.y);
-    pk[c / 2 + 1] = pack_bf16x2(p1.x, p1.y);
+    if constexpr (TWO) {
+      split_bf16x2(p0.x, p0.y, pk[c / 2], lo[c / 2]);
+      split_bf16x2(p1.x, p1.y, pk[c / 2 + 1], lo[c / 2 + 1]);
+    } else {
+      pk[c / 2] = pack_bf16x2(p0.x, p0.y);
+      pk[c / 2 + 1] = pack_bf16x2(p1.x, p1.y);
+    }
   }
   return sum.x + sum.y;
 }
@@ -100,7 +111,7 @@ __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 25
 
 // Bounded as for 640 threads, that is 96 registers each: the 320 leave 34,816 of an SM's, enough
 // for two CTAs of the kernels that run beside this one.
-template <int D, bool VALUES>
+template <int D, bool VALUES, bool TWO>
 __global__ void __launch_bounds__(640, 1)
     decode_prefix_kernel(const __grid_constant__ PrefixMaps maps, const DecodeArgs a, const LaunchCtx ctx) {
   using C = Cfg<D, VALUES>;
@@ -239,9 +250,10 @@ __global__ void __launch_bounds__(640, 1)
           const uint32_t vlo = sdesc_lo(vaddr, BOX_BYTES), col = tmem + TMEM_O, pcol = tmem + 128 * (j & 1);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk) {
-            const uint32_t acol = pcol + (kk >> 2) * 64 + (kk & 3) * 8;   // each half's P over its own scores
+            const uint32_t acol = pcol + (kk >> 1) * 32 + (kk & 1) * 8;   // P over its own scores, 32 keys at a time
             const uint32_t boff = (kk * 16 * 128) >> 4;                    // V: MN-major, 16 key rows
             tc_mma_f16_ts(col, acol, sdesc(vlo + boff, HI), idesc_pv, kk > 0 || o_started ? 1u : 0u);
+            if constexpr (TWO) tc_mma_f16_ts(col, acol + 16, sdesc(vlo + boff, HI), idesc_pv, 1u);
           }
           o_started = true;
         }
@@ -376,10 +388,12 @@ __global__ void __launch_bounds__(640, 1)
         for (int c0 = 0; c0 < 64; c0 += 32) {
           take(j, c0);
           const int n = tail - j * BN - c0;
-          uint32_t pk[16];
-          t += n < 32 ? phi_chunk<true>(h, pk, n, c2, m) : phi_chunk<false>(h, pk, n, c2, m);
-          // P over this half's own scores, which only this thread reads: two keys per column
-          tmem_st16(lanes + 128 * (j & 1) + 64 * upper + c0 / 2, pk);
+          uint32_t pk[16], lo[16];
+          t += n < 32 ? phi_chunk<true, TWO>(h, pk, lo, n, c2, m) : phi_chunk<false, TWO>(h, pk, lo, n, c2, m);
+          // P over its own scores, which only this thread reads: two keys per column, 16 columns of
+          // P and 16 of what its rounding left
+          tmem_st16(lanes + 128 * (j & 1) + 64 * upper + c0, pk);
+          if constexpr (TWO) tmem_st16(lanes + 128 * (j & 1) + 64 * upper + c0 + 16, lo);
         }
         tc_wait_st();
         total += t;
@@ -432,10 +446,10 @@ __global__ void __launch_bounds__(640, 1)
   }
 }
 
-template <int D, bool VALUES>
+template <int D, bool VALUES, bool TWO = false>
 cudaError_t go(const PrefixMaps& maps, const DecodeArgs& a, const LaunchCtx& ctx, cudaStream_t st) {
-  auto kernel = decode_prefix_kernel<D, VALUES>;
-  const cudaError_t e = set_up_kernel<decode_prefix_kernel<D, VALUES>>(Cfg<D, VALUES>::SMEM_BYTES, true);
+  auto kernel = decode_prefix_kernel<D, VALUES, TWO>;
+  const cudaError_t e = set_up_kernel<decode_prefix_kernel<D, VALUES, TWO>>(Cfg<D, VALUES>::SMEM_BYTES, true);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(a.Hkv) * ((a.B * a.G + BM - 1) / BM) * a.pslots;
   if constexpr (VALUES) return launch_dependent(kernel, grid, THREADS, Cfg<D, VALUES>::SMEM_BYTES, st, maps, a, ctx);
@@ -447,8 +461,9 @@ cudaError_t go(const PrefixMaps& maps, const DecodeArgs& a, const LaunchCtx& ctx
 
 cudaError_t launch_decode_prefix(const PrefixMaps& maps, const DecodeArgs& a, bool values, const LaunchCtx& ctx,
                                  cudaStream_t st) {
-  if (a.D == 64) return values ? go<64, true>(maps, a, ctx, st) : go<64, false>(maps, a, ctx, st);
-  return values ? go<128, true>(maps, a, ctx, st) : go<128, false>(maps, a, ctx, st);
+  if (!values) return a.D == 64 ? go<64, false>(maps, a, ctx, st) : go<128, false>(maps, a, ctx, st);
+  if (a.B * a.G <= BM) return a.D == 64 ? go<64, true, true>(maps, a, ctx, st) : go<128, true, true>(maps, a, ctx, st);
+  return a.D == 64 ? go<64, true>(maps, a, ctx, st) : go<128, true>(maps, a, ctx, st);
 }
 
 }  // namespace raattn

@@ -112,6 +112,22 @@ def test_decode_matches_the_oracle(case, dtype):
                  *inputs(B, Hq, Hkv, C, P, D, dtype, seed=C + P, sigma=sigma)[3:])
 
 
+@pytest.mark.parametrize("case", [(4, 16, 16, 700, 0, 128), (16, 16, 4, 700, 0, 64), (4, 64, 4, 500, 300, 128),
+                                  (8, 48, 2, 300, 0, 64), (33, 4, 4, 40, 1500, 64), (32, 32, 8, 100, 1000, 128)], ids=str)
+def test_decode_bf16_errors_are_the_outputs_own_rounding(case):
+    """Up to 128 rows per shared key head the weights go into the products as two bf16 each (2^-15 lost), so what is
+    off is the rounding of the output: uniform within half a step of each element, whose mean square
+    follows from the exact outputs.  15% above its root leaves room for the sample (8192 elements or
+    more: 1.3% for one standard deviation) and the scores' fp32 sums; weights of one bf16 would add as
+    much again as the output's rounding, in all 41%."""
+    B, Hq, Hkv, C, P, D = case
+    q, k, v, pk, pv = inputs(B, Hq, Hkv, C, P, D, torch.bfloat16, seed=C + D)
+    o = check_decode(q, k, v, [C - b for b in range(B)], pk, pv)
+    O = S.attention_decode(f64(q), f64(k), f64(v), [C - b for b in range(B)], f64(pk), f64(pv))[0]
+    half = 2.0 ** (np.floor(np.log2(np.abs(O))) - 8)
+    assert np.sqrt(np.mean((f64(o) - O) ** 2)) <= 1.15 * np.sqrt(np.mean(half ** 2) / 3)
+
+
 @pytest.mark.parametrize("D", [16, 32])
 def test_decode_small_heads_fp32(D):
     q, k, v, pk, pv = inputs(3, 6, 3, 77, 50, D, torch.float32, seed=D)
