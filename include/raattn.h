@@ -421,13 +421,16 @@ ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t t
  *                 irrelevant.  Calls that may run at the same time need one each.
  *   scale         score scale; <= 0 means 1/sqrt(D).
  *   dtype         of q, k, v, prefix and o.  RA_BF16: D in {64, 128}; RA_F32: {16, 32, 64, 128}.
- * Scores, row maxima, sums and weights are fp32.  Results do not depend on scheduling.
+ * Scores, row maxima, sums and weights are fp32.  RA_BF16: weights enter the value products as two
+ * bf16 (2^-15 lost), a prefix's with more than 128 query rows per key head as one (2^-8).  Results do
+ * not depend on scheduling.
  * With a prefix and more than 32 query rows per key head (B H_Q / H_KV), bf16 calls use kernels
  * with bounded waits, whose giving up ra_device_status() reports.
  * Errors: RA_ERR_ARG for null or misaligned pointers, sizes < 1 (P < 0), H_Q no multiple of
- * H_KV, B H_Q, B H_KV C or H_KV P beyond int32, a bad enum or scale; RA_ERR_UNSUPPORTED for D outside
- * the sets above, B > 8192, more than 1024 query heads per key head, or sizes whose blocks of 8 to 32
- * keys by 16 query rows number more than 2^30; RA_ERR_LAUNCH.  The size query returns 0 for such sizes.
+ * H_KV, B H_Q, B H_KV C or H_KV P beyond int32, C or P beyond 2^31 - 16385, a bad enum or scale;
+ * RA_ERR_UNSUPPORTED for D outside the sets above, B > 8192, more than 1024 query heads per key head,
+ * or sizes whose blocks of 8 to 32 keys by 16 query rows number more than 2^30; RA_ERR_LAUNCH.  The
+ * size query returns 0 for such sizes.
  */
 size_t ra_attention_decode_workspace_size(int B, int H_Q, int H_KV, int C, int P, int D, ra_dtype_t dtype);
 ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, const int32_t* length,
@@ -447,7 +450,7 @@ ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, con
  *   index         [B, H_KV, keep] int32 (written): the kept slots, ascending, then -1.
  *   keep, recent  1 <= keep <= C_out, 0 <= recent <= keep.
  * Errors: RA_ERR_ARG for null, misaligned or equal in and out pointers and sizes outside the above,
- * B H_KV C or B H_KV C_out beyond int32; RA_ERR_UNSUPPORTED where D elements are no multiple of 16
+ * B H_KV C or B H_KV C_out beyond int32, C or C_out beyond 2^31 - 16385; RA_ERR_UNSUPPORTED where D elements are no multiple of 16
  * bytes; RA_ERR_LAUNCH.
  */
 ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, const int32_t* length, void* k_out,

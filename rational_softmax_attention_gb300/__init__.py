@@ -373,6 +373,8 @@ class RaAttention(torch.nn.Module):
         if cache.bound:
             raise ValueError("prefill needs an empty cache")
         B, N, _ = x.shape
+        if cache.k.shape[:2] != (B, self.num_heads) or cache.k.shape[3] != self.head_dim or cache.k.dtype != x.dtype:
+            raise ValueError("the cache must have the batch size, heads, head dimension and dtype of x in this module")
         cache.require_room(N)
         P = cache.prefix_length
         if P and x.dtype != torch.bfloat16:

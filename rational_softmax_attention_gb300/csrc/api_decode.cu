@@ -15,6 +15,9 @@ bool head_dim_ok(int D) { return D == 16 || D == 32 || D == 64 || D == 128; }
 // Sizes whose row counts fit 32 bits; elements are addressed in 64.
 bool rows_ok(int64_t a, int64_t b, int64_t c) { return a * b <= INT_MAX && a * b * c <= INT_MAX; }
 
+// Loops over a cache's slots step by up to 8192 in 32 bits.
+constexpr int kMostKeys = INT_MAX - 16384;
+
 ra_status_t norm_rope_shape(NormRopeShape* a, const void* qkv, int64_t batch_stride, int64_t token_stride,
                             const void* qw, const void* qb, const void* kw, const void* kb, ra_norm_t norm, float eps,
                             const double* freq, const int32_t* pos, int64_t pos_axis_stride, int64_t pos_batch_stride,
@@ -66,7 +69,7 @@ ra_status_t norm_rope_shape(NormRopeShape* a, const void* qkv, int64_t batch_str
 
 ra_status_t decode_shape(DecodeArgs* a, int B, int Hq, int Hkv, int C, int P, int D) {
   if (B < 1 || Hq < 1 || Hkv < 1 || C < 1 || P < 0 || D < 1 || Hq % Hkv) return RA_ERR_ARG;
-  if (!rows_ok(B, Hq, 1) || C > INT_MAX - 1024 || P > INT_MAX - 1024) return RA_ERR_ARG;
+  if (!rows_ok(B, Hq, 1) || C > kMostKeys || P > kMostKeys) return RA_ERR_ARG;
   if (!rows_ok(B, Hkv, C) || !rows_ok(Hkv, P, 1)) return RA_ERR_ARG;
   if (!head_dim_ok(D) || B > kDecodeMaxBatch || Hq / Hkv > 1024) return RA_ERR_UNSUPPORTED;
   a->B = B;
@@ -184,7 +187,8 @@ ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, co
     return RA_ERR_ARG;
   if (B < 1 || H_KV < 1 || C < 1 || C_out < 1 || D < 1 || keep < 1 || keep > C_out || recent < 0 || recent > keep)
     return RA_ERR_ARG;
-  if (!rows_ok(B, H_KV, C) || !rows_ok(B, H_KV, C_out) || D > (1 << 20)) return RA_ERR_ARG;
+  if (!rows_ok(B, H_KV, C) || !rows_ok(B, H_KV, C_out) || C > kMostKeys || C_out > kMostKeys || D > (1 << 20))
+    return RA_ERR_ARG;
   for (const void* p : {k, v, static_cast<const void*>(k_out), static_cast<const void*>(v_out)})
     if (!aligned(p, 16)) return RA_ERR_ARG;
   for (const void* p : {static_cast<const void*>(weight), static_cast<const void*>(length),

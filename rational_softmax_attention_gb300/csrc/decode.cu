@@ -65,7 +65,7 @@ __device__ __forceinline__ float phi_fast(float d) {   // bf16 inputs: 1 ulp rec
   return q4 * q4;
 }
 __device__ __forceinline__ float phi_exact(float d) {   // fp32 inputs: IEEE division
-  const bool in = d < 16.0f;
+  const bool in = !(d >= 16.0f);   // NaN stays NaN
   d = in ? d : 0.0f;   // always a plain quotient: a division's special cases are slow
   const float q = in ? (16.0f - d) / (16.0f + d) : 0.0f;
   const float q2 = q * q, q4 = q2 * q2;
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (f[j] > 0.0f) {   // a part whose weights are all 0 may have written no output
+        if (f[j] != 0.0f) {   // a part whose weights are all 0 may have written no output
           s.x += x[j].x;
           s.y += x[j].y;
           s.z += x[j].z;
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
       total += __shfl_xor_sync(0xffffffffu, total, o);
     }
     if (ks == 0) {
-      const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // no key at all: zeros
+      const float inv = total != 0.0f ? 1.0f / total : 0.0f;   // no key at all: zeros
       T* o = static_cast<T*>(a.o) + static_cast<int64_t>(row) * D + gl * 4;
       if constexpr (sizeof(T) == 2) {
         *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(s.x * inv, s.y * inv), pack_bf16x2(s.z * inv, s.w * inv));

@@ -15,6 +15,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check, _dtype_code, lib
 
@@ -152,6 +153,12 @@ def _norm_rope_forward(qkv, num_heads, num_kv_heads, norm, params, eps, frequenc
     return q, k, v
 
 
+def _dense(t):
+    """A gradient as the kernels read it, whatever view of another tensor autograd hands over."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 class _RaQkNormRopeFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, qkv, q_weight, q_bias, k_weight, k_bias, frequencies, positions, how):
@@ -162,13 +169,14 @@ class _RaQkNormRopeFn(torch.autograd.Function):
                                   sections, positions, interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk, dv):
         qkv, qw, qb, kw, kb, frequencies, positions = ctx.saved_tensors
         heads, kv_heads, norm, eps, sections, interleaved = ctx.how
         dqkv, *dparams = ra_qk_norm_rope_backward(
-            qkv, dq.contiguous(), dk.contiguous(), dv.contiguous(), heads, kv_heads, norm=norm, q_weight=qw,
-            q_bias=qb, k_weight=kw, k_bias=kb, eps=eps, frequencies=frequencies, sections=sections,
-            positions=positions, interleaved=interleaved)
+            qkv, _dense(dq), _dense(dk), _dense(dv), heads, kv_heads, norm=norm, q_weight=qw, q_bias=qb, k_weight=kw,
+            k_bias=kb, eps=eps, frequencies=frequencies, sections=sections, positions=positions,
+            interleaved=interleaved)
         dparams = [None if d is None else d.to(p.dtype) for d, p in zip(dparams, (qw, qb, kw, kb))]
         return (dqkv, *dparams, None, None, None)
 
@@ -186,7 +194,8 @@ def ra_qk_norm_rope(qkv, num_heads, num_kv_heads=None, *, norm="layer", q_weight
     of q and k.  sections: pairs of dimensions per position axis (None: no rotation); frequencies:
     float64 [sum(sections)], see ra_rope_frequencies; positions: integer [N], [B, N] or
     [axes, B, N].  Pair i is dimensions (i, i + R) of the first 2 R, or (2 i, 2 i + 1) when
-    interleaved.  Differentiable in qkv, weights and biases."""
+    interleaved.  Differentiable (once) in qkv, weights and biases; as with any torch operator, a backward
+    pass is captured into a CUDA graph only while no eager graph of the same leaves is alive."""
     if torch.is_grad_enabled() and (qkv.requires_grad or _asks(q_weight) or _asks(k_weight) or _asks(q_bias)
                                     or _asks(k_bias)):
         return _RaQkNormRopeFn.apply(qkv, q_weight, q_bias, k_weight, k_bias, frequencies, positions,
@@ -342,7 +351,13 @@ class RaCache:
 
     k, v [B, H_kv, C, D]; length int32 [B] (entries held) and position int32 [B] (position of the
     next token: evicted entries still count, and so does the prefix), both on the device; weight
-    float32 [B, H_kv, C] with track_weight, the attention each entry has received."""
+    float32 [B, H_kv, C] with track_weight, the attention each entry has received from attend (a
+    module's prefill adds none).
+
+    A captured graph of append and attend advances length and position when it is replayed, but not
+    `bound`, which is the host's: whoever replays it sees to it that there is room (tokens beyond the
+    capacity are not stored).  evict changes which tensors the cache uses, so graphs of it are
+    captured anew afterwards."""
 
     def __init__(self, batch, num_kv_heads, capacity, head_dim, *, prefix=None, track_weight=False, device="cuda",
                  dtype=torch.bfloat16):
@@ -375,7 +390,7 @@ class RaCache:
 
     def advance(self, tokens, count=None):
         """Counts `tokens` new entries (or count[b] of them, int32 [B])."""
-        step = tokens if count is None else count
+        step = tokens if count is None else count.clamp(0, tokens)
         self.length.add_(step)
         self.position.add_(step)
         self.bound += tokens

@@ -101,6 +101,8 @@ CASES = [  # B, Hq, Hkv, C, P, D, sigma, lengths
     (150, 4, 1, 5, 1000, 64, 3.0, [i % 6 for i in range(150)]),        # 600 rows
     (36, 8, 8, 700, 2900, 128, 3.0, [700 - i for i in range(36)]),
     (600, 2, 1, 5, 300, 64, 1.0, [i % 6 for i in range(600)]),         # more than 512 sequences
+    (1, 1024, 1, 70, 40, 64, 1.0, [69]),                   # as many query heads per key head as there may be
+    (8192, 1, 1, 3, 130, 64, 1.0, [i % 4 for i in range(8192)]),       # and as many sequences
 ]
 
 
@@ -203,6 +205,66 @@ def test_decode_repeats_streams_and_graphs_agree(dtype):
         torch.cuda.synchronize()
         for g, og, wg in graphs:
             assert torch.equal(og, ref[name][0]) and torch.equal(wg, ref[name][1])
+
+
+def test_decode_calls_on_two_streams():
+    """Calls that run at the same time, each in its own workspace, with and without the tensor cores' part."""
+    sets = [tuple(t.cuda() for t in inputs(48, 8, 4, 300, 900, 64, torch.bfloat16, seed=27)),
+            tuple(t.cuda() for t in inputs(70, 4, 2, 200, 1500, 128, torch.bfloat16, seed=28)),
+            tuple(t.cuda() for t in inputs(6, 4, 4, 900, 100, 64, torch.float32, seed=29))]
+    lengths = [torch.arange(q.shape[0], dtype=torch.int32, device="cuda") * 4 % k.shape[2] for q, k, *_ in sets]
+
+    def call(i):
+        q, k, v, pk, pv = sets[i]
+        return ra.ra_attention_decode(q, k, v, lengths[i], prefix_k=pk, prefix_v=pv)
+    want = [call(i) for i in range(3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append((i, call(i)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in got) and ra.device_status() == "RA_OK"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decode_nan_stays_in_its_rows(dtype):
+    q, k, v, _, _ = inputs(3, 4, 2, 200, 0, 64, dtype, seed=30)
+    n = torch.tensor([200, 150, 0], dtype=torch.int32, device="cuda")
+    want = ra.ra_attention_decode(q.cuda(), k.cuda(), v.cuda(), n)
+    q[0, 1] = float("nan")              # a query
+    k[1, 0, 17, 3] = float("nan")       # a key of two queries
+    got = ra.ra_attention_decode(q.cuda(), k.cuda(), v.cuda(), n)
+    bad = torch.zeros(3, 4, dtype=torch.bool)
+    bad[0, 1] = bad[1, 0] = bad[1, 1] = True
+    assert torch.isnan(got[bad.cuda()]).all() and torch.equal(got[~bad.cuda()], want[~bad.cuda()])
+
+
+def test_a_cache_beyond_32_bit_offsets():
+    """More than 2^31 elements before the second sequence, and 2^31 scores: append, decode and evict
+    find the entries at the far ends.  One key lies so far above the others that it decides alone."""
+    C, D, Hq = (1 << 24) + 64, 128, 64
+    k = torch.zeros(2, 1, C, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    qkv = torch.randn(2, 1, (Hq + 2) * D, device="cuda").bfloat16()
+    qkv[:, :, :Hq * D] = 2.0
+    qkv[:, :, Hq * D:Hq * D + D] = 2.0               # score 4 * 128 / sqrt(128) = 45 against 0
+    n = torch.tensor([C - 1, 39], dtype=torch.int32, device="cuda")
+    q = ra.ra_cache_append(qkv, k, v, n, Hq, 1, norm="none")
+    n += 1
+    new = qkv[:, 0, (Hq + 1) * D:]
+    assert torch.equal(v[0, 0, C - 1], new[0]) and torch.equal(v[1, 0, 39], new[1])
+    weight = torch.zeros(2, 1, C, device="cuda")
+    o = ra.ra_attention_decode(q[:, :, 0].contiguous(), k, v, n, weight=weight)
+    assert torch.equal(o, new.unsqueeze(1).expand_as(o))
+    assert weight[0, 0, C - 1] == Hq and weight[1, 0, 39] == Hq and weight.sum() == 2 * Hq
+    weight[0, 0, 7], weight[0, 0, C - 2], weight[1, 0, 5] = 3.0, 2.0, 1.0
+    k[1, 0, 5] = 0.5
+    ko, vo, wo, m, index = ra.ra_cache_evict(k, v, weight, n, 3, recent=1)
+    assert index.tolist() == [[[7, C - 2, C - 1]], [[0, 5, 39]]] and m.tolist() == [3, 3]
+    assert torch.equal(vo[:, 0, 2], new) and torch.equal(ko[1, 0, 1], k[1, 0, 5]) and wo[0, 0].tolist() == [3, 2, Hq]
 
 
 def test_decode_shared_keys_beyond_the_support():

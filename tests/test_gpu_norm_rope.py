@@ -221,6 +221,38 @@ def test_bit_identical_on_streams_and_in_a_graph():
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_autograd_takes_any_view_once_and_in_a_graph():
+    """Gradients that start at an odd address, a second derivative (refused), and a backward pass captured with its
+    forward (of a leaf without a live eager graph: torch ties a leaf's accumulation to the stream of
+    its first graph, and a capture cannot wait for another stream, whatever the operators)."""
+    B, N, Hq, Hkv, D = 2, 50, 2, 1, 64
+    qkv, params, how = make(B, N, Hq, Hkv, D, torch.bfloat16, "layer", True, (32,), False, 15)
+    params, how, x = cuda(params), cuda(how), qkv.cuda()
+    d = [torch.randn(B, h, N, D, device="cuda").bfloat16() for h in (Hq, Hkv, Hkv)]
+    want = ra.ra_qk_norm_rope_backward(x, *d, Hq, Hkv, **params, **how)[0]
+    odd = [torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view_as(t).copy_(t) for t in d]
+    y = x.clone().requires_grad_(True)
+    out = ra.ra_qk_norm_rope(y, Hq, Hkv, **params, **how)
+    assert torch.equal(torch.autograd.grad(out, y, odd, retain_graph=True)[0], want)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g, = torch.autograd.grad(out, y, [t.requires_grad_(True) for t in d], create_graph=True)
+        g.float().sum().backward()
+    d = [t.detach() for t in d]
+    y = x.clone().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(ra.ra_qk_norm_rope(y, Hq, Hkv, **params, **how), y, d)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got, = torch.autograd.grad(ra.ra_qk_norm_rope(y, Hq, Hkv, **params, **how), y, d)
+    got.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_refusals():
     x = torch.zeros(1, 2, 3 * 64, device="cuda")
     w, f = torch.ones(64, device="cuda"), ra.ra_rope_frequencies((32,))

@@ -92,7 +92,8 @@ def _evict(lib, k=FAKE, ko=OTHER[0], vo=OTHER[1], v=OTHER[2], w=OTHER[3], wo=OTH
 def test_evict_validation(lib):
     bad = [dict(k=None), dict(k=MISALIGNED), dict(ko=FAKE), dict(vo=OTHER[2]), dict(ko=OTHER[1]), dict(wo=OTHER[3]),
            dict(no=OTHER[5]), dict(index=None), dict(B=0), dict(H=0), dict(C=0), dict(Co=0), dict(D=0), dict(keep=0),
-           dict(keep=33), dict(recent=17), dict(recent=-1), dict(dt=9), dict(C=1 << 30), dict(Co=1 << 30)]
+           dict(keep=33), dict(recent=17), dict(recent=-1), dict(dt=9), dict(C=1 << 30), dict(Co=1 << 30),
+           dict(B=1, H=1, C=(1 << 31) - 1), dict(B=1, H=1, Co=(1 << 31) - 1)]
     for how in bad:
         assert _evict(lib, **how) == ARG, how
     assert _evict(lib, D=20) == UNSUPPORTED
@@ -152,3 +153,14 @@ def test_module_host_side_checks():
         m.decode(torch.zeros(1, 2, 64), m.new_cache(1, 4))
     with pytest.raises(ValueError, match="no room"):
         m.prefill(torch.zeros(1, 5, 64), m.new_cache(1, 4))
+    with pytest.raises(ValueError, match="batch size"):
+        m.prefill(torch.zeros(1, 3, 64), m.new_cache(2, 4))
+    with pytest.raises(ValueError, match="dtype"):
+        m.prefill(torch.zeros(1, 3, 64), ra.RaCache(1, 2, 4, 32, device="cpu"))
+
+
+def test_counts_beyond_the_call_are_not_counted():
+    """Tokens that an append does not write do not lengthen the cache."""
+    c = ra.RaCache(3, 1, 8, 64, device="cpu")
+    c.advance(2, torch.tensor([5, -1, 1], dtype=torch.int32))
+    assert c.length.tolist() == [2, 0, 1] and c.position.tolist() == [2, 0, 1] and c.bound == 2
