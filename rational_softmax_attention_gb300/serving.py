@@ -30,12 +30,14 @@ def _addr(t):
 
 def _call(name, device, *args):
     """Calls a libraattn entry point on torch's current stream of `device`, which becomes the current one."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn, index = getattr(lib(), name), device.index
+    # the stream's address without a torch.cuda.Stream around it, whose making takes 2 us
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        code = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            code = fn(*args, stream)
     if code:
         _check(name, code)
 
