@@ -28,9 +28,19 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    lib()                       # raises if the library has not been built
+    try:
+        from . import _calls    # its marshalling in C
+    except ImportError:
+        return getattr(lib(), name)
+    return getattr(_calls, name)
+
+
 def _call(name, device, *args):
     """Calls a libraattn entry point on torch's current stream of `device`, which becomes the current one."""
-    fn, index = getattr(lib(), name), device.index
+    fn, index = _entry(name), device.index
     # the stream's address without a torch.cuda.Stream around it, whose making takes 2 us
     stream = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
@@ -66,17 +76,18 @@ def ra_rope_frequencies(sections, theta=10000.0, per_axis=False, device="cuda"):
 
 @functools.lru_cache(maxsize=256)
 def _norm_rope_sizes(width, num_heads, num_kv_heads, sections):
-    """(Hq, Hkv, D, pairs, axes, host array of the sections) of a projection `width` wide."""
+    """(Hq, Hkv, D, pairs, axes, host array of the sections, its address) of a projection `width` wide."""
     Hq, Hkv = int(num_heads), int(num_heads if num_kv_heads is None else num_kv_heads)
     if Hq < 1 or Hkv < 1 or width < 1 or width % (Hq + 2 * Hkv):
         raise ValueError("qkv must be [B, N, (num_heads + 2 num_kv_heads) * head_dim]")
     D = width // (Hq + 2 * Hkv)
     if not sections:
-        return Hq, Hkv, D, 0, 0, None
+        return Hq, Hkv, D, 0, 0, None, None
     secs = [int(s) for s in sections]
     if min(secs) < 1 or 2 * sum(secs) > D:
         raise ValueError("sections must be positive pair counts with 2 * sum(sections) <= head_dim")
-    return Hq, Hkv, D, sum(secs), len(secs), (ctypes.c_int32 * len(secs))(*secs)
+    host = (ctypes.c_int32 * len(secs))(*secs)
+    return Hq, Hkv, D, sum(secs), len(secs), host, ctypes.addressof(host)
 
 
 def _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies, sections, positions, interleaved):
@@ -87,7 +98,7 @@ def _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies
     dtype, device = qkv.dtype, qkv.device
     code = _dtype_code(dtype)
     B, N, width = qkv.shape
-    Hq, Hkv, D, pairs, axes, secs = _norm_rope_sizes(width, num_heads, num_kv_heads,
+    Hq, Hkv, D, pairs, axes, host, secs = _norm_rope_sizes(width, num_heads, num_kv_heads,
                                                      None if sections is None else tuple(sections))
     if B < 1 or N < 1:
         raise ValueError("qkv must hold at least one token")
@@ -141,7 +152,7 @@ def _norm_rope_args(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies
     lead = (qkv.data_ptr(), row, tok, _addr(qw), _addr(qb), _addr(kw), _addr(kb), kind, eps,
             frequencies.data_ptr() if axes else None, pos.data_ptr() if axes else None, pos_axis, pos_batch, secs,
             axes, 1 if interleaved else 0)
-    return lead, (qkv, pos), (B, N, Hq, Hkv, D, code)
+    return lead, (qkv, pos, host), (B, N, Hq, Hkv, D, code)
 
 
 def _norm_rope_forward(qkv, num_heads, num_kv_heads, norm, params, eps, frequencies, sections, positions, interleaved):

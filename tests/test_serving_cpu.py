@@ -164,3 +164,24 @@ def test_counts_beyond_the_call_are_not_counted():
     c = ra.RaCache(3, 1, 8, 64, device="cpu")
     c.advance(2, torch.tensor([5, -1, 1], dtype=torch.int32))
     assert c.length.tolist() == [2, 0, 1] and c.position.tolist() == [2, 0, 1] and c.bound == 2
+
+
+def test_native_marshalling(lib):
+    """The C module takes the header's arguments, in its order and types, and refuses others."""
+    calls = pytest.importorskip("rational_softmax_attention_gb300._calls")
+    kinds = {"ra_qk_norm_rope_fwd": [None, 768, 192, *[None] * 4, 2, 1e-5, None, None, 0, 0, None, 0, 0, *[None] * 5, 0, 2,
+                                     4, 1, 1, 64, 0, None],
+             "ra_qk_norm_rope_bwd": [None, 768, 192, *[None] * 4, 2, 1e-5, None, None, 0, 0, None, 0, 0, *[None] * 6, 2, 4,
+                                     1, 1, 64, 0, None],
+             "ra_attention_decode": [*[None] * 9, 1, 1, 1, 16, 0, 64, 0.0, 0, None],
+             "ra_cache_evict": [*[None] * 9, 1, 1, 16, 16, 64, 8, 0, 0, None]}
+    for name, args in kinds.items():
+        fn = getattr(calls, name)
+        assert len(args) == len(getattr(lib, name).argtypes)
+        assert fn(*args) == ARG, name               # null pointers, as through ctypes
+        with pytest.raises(TypeError):
+            fn(*args[:-1])
+        with pytest.raises(TypeError):
+            fn("0", *args[1:])
+        with pytest.raises(OverflowError):
+            fn(*args[:-4], 1 << 31, *args[-3:])
