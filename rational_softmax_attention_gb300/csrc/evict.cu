@@ -9,17 +9,20 @@
 //            by a radix selection over the weights' order-preserving bits (eight at a time; the
 //            CTAs' counts are added through distributed shared memory, whose reads cost more than
 //            a fourth pass: with 2048 bins they took 3 us a pass), then the kept
-//            slots in order by prefix sums.  Counts are integers, so nothing depends on the order
+//            slots in order by prefix sums.  Each pass has counters of its own, so that one barrier of
+//            the cluster per pass is enough.  Counts are integers, so nothing depends on the order
 //            of the atomics.  A CTA's first 8192 weights stay in registers between the passes.
 //   gather   the kept entries, 16 bytes per lane.
-// Bound: select by latency (four passes and their barriers), gather by HBM.
+// Bound: select by latency (four passes and their barriers: 14 us for 32 rows of 32768), gather by HBM
+// (B32 H8 4352 -> 4096, D128 bf16: 849 MB in 133 us, 6.4 TB/s).  Both together, in a graph: B4 H8
+// 32768 -> 2048 21.5 us.
 #include "kernels.cuh"
 
 namespace raattn {
 namespace {
 
 constexpr int kSelThreads = 1024;
-constexpr int kBins = 256;
+constexpr int kBins = 256, kPasses = 4;
 
 // Order-preserving bits of a weight: larger weights give larger bits; -0 and 0 are equal; NaN above all.
 __device__ __forceinline__ uint32_t order_bits(float w) {
@@ -62,9 +65,9 @@ constexpr int kHeld = 2;                       // chunks held in registers
 
 template <int S>   // CTAs of a cluster
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[kBins];
+  __shared__ int hist[kPasses][kBins];   // a pass's own: one barrier of the cluster per pass
   __shared__ int warp_sums[32];
-  __shared__ int found, left;
+  __shared__ int found[kPasses], left;
   __shared__ int2 counts;   // entries of this CTA's slice above the threshold, and equal to it
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int bk = blockIdx.x / S, b = bk / a.Hkv, kv = bk - b * a.Hkv;
@@ -105,29 +108,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   };
   // The threshold: the need-th largest.  `rest` counts what is still wanted among the entries that
   // share the bits found so far.
+  static_assert(kPasses * kBins == kSelThreads, "a thread per bin");
+  hist[0][threadIdx.x] = 0;
+  if (threadIdx.x == 0) counts = make_int2(0, 0);
+  __syncthreads();
   uint32_t prefix = 0;
-  int rest = need, done = 0;   // done: bits found
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (threadIdx.x < kBins) hist[threadIdx.x] = 0;
-    __syncthreads();
+  int rest = need;
+#pragma unroll 1
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int shift = 24 - 8 * pass, done = 8 * pass;   // done: bits found
     each([&](int, const uint32_t (&u)[kPer]) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const bool in = u[j] && (done == 0 || u[j] >> (32 - done) == prefix);
         // weights of exactly 0 (entries outside every query's support) are many: one addition for a warp's
         const unsigned zeros = __ballot_sync(0xffffffffu, in && u[j] == kZeroBits);
-        if (zeros && (threadIdx.x & 31) == 0) atomicAdd(&hist[kZeroBits >> shift & 255u], __popc(zeros));
-        if (in && u[j] != kZeroBits) atomicAdd(&hist[u[j] >> shift & 255u], 1);
+        if (zeros && (threadIdx.x & 31) == 0) atomicAdd(&hist[pass][kZeroBits >> shift & 255u], __popc(zeros));
+        if (in && u[j] != kZeroBits) atomicAdd(&hist[pass][u[j] >> shift & 255u], 1);
       }
     });
     if (S > 1) cluster_sync();
     else __syncthreads();
     // bins from the top, one thread each
     const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
-    int c = 0;
+    int c = 0, sum = 0;
     if (threadIdx.x < kBins) {
       if (S > 1) {
-        const uint32_t at = smem_u32(&hist[bin]);
+        const uint32_t at = smem_u32(&hist[pass][bin]);
         int x[S];
 #pragma unroll
         for (int r = 0; r < S; ++r)
@@ -135,50 +142,50 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 #pragma unroll
         for (int r = 0; r < S; ++r) c += x[r];
       } else {
-        c = hist[bin];
+        c = hist[pass][bin];
+      }
+      sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if ((threadIdx.x & 31) >= o) sum += x;
+      }
+      if ((threadIdx.x & 31) == 31) warp_sums[threadIdx.x >> 5] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBins) {
+      int before = sum - c;
+      for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) before += warp_sums[w];
+      if (before < rest && rest <= before + c) {
+        found[pass] = bin;
+        left = rest - before;
       }
     }
-    int total;
-    const int before = block_exclusive(c, warp_sums, &total);
-    if (before < rest && rest <= before + c) {
-      found = bin;
-      left = rest - before;
-    }
-    if (S > 1) cluster_sync();   // the counts have been read, too
-    else __syncthreads();
-    prefix = prefix << 8 | static_cast<uint32_t>(found);
-    rest = left;
-    done += 8;
+    __syncthreads();
+    prefix = prefix << 8 | static_cast<uint32_t>(found[pass]);
+    rest = left;   // written again only behind the next pass's barriers
   }
   // The kept slots in order: entries above the threshold and the first `rest` equal to it.  Both
-  // counts of a chunk (at most 4096) go through one prefix sum.
+  // counts of a chunk (at most 4096) go through one prefix sum.  A slice's counts are in its bins: above
+  // the threshold lie those above the found bin of each pass.
   int above = 0, equal = 0;   // of the entries before this chunk
   if (S > 1) {
-    int mine = 0;
-    each([&](int, const uint32_t (&u)[kPer]) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) mine += u[j] > prefix ? 1 : 0;
-    });
-    int ties = 0;
-    each([&](int, const uint32_t (&u)[kPer]) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) ties += u[j] == prefix ? 1 : 0;
-    });
-    int total;
-    block_exclusive(mine, warp_sums, &total);
-    const int gt = total;
-    __syncthreads();
-    block_exclusive(ties, warp_sums, &total);
-    if (threadIdx.x == 0) counts = make_int2(gt, total);
+    const int pass = threadIdx.x / kBins, bin = threadIdx.x % kBins;
+    const int mine = __reduce_add_sync(0xffffffffu, bin > found[pass] ? hist[pass][bin] : 0);
+    if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&counts.x, mine);
+    if (threadIdx.x == 0) counts.y = hist[kPasses - 1][found[kPasses - 1]];
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      int x, y;
+    int x[S], y[S];
+#pragma unroll
+    for (int r = 0; r < S; ++r)
       asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
-                   : "=r"(x), "=r"(y)
+                   : "=r"(x[r]), "=r"(y[r])
                    : "r"(mapa_shared(smem_u32(&counts), r))
                    : "memory");
-      above += x;
-      equal += y;
+#pragma unroll
+    for (int r = 0; r < S; ++r) {
+      above += r < rank ? x[r] : 0;
+      equal += r < rank ? y[r] : 0;
     }
   }
   each([&](int q, const uint32_t (&u)[kPer]) {
@@ -246,7 +253,7 @@ cudaError_t select(const EvictArgs& a, cudaStream_t st) {
 
 // CTAs of a row's cluster: as many as give every SM one at most, while each still gets a chunk of
 // 4096 entries.  (Two per SM do not all find room in clusters of eight: 32 rows of 32768 took 44 us
-// so, gather included, against 23 with clusters of four; with one CTA per row 42.)
+// so, gather included, when clusters of four took 23; with one CTA per row 42.)
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv, chunks = (a.C + kChunk - 1) / kChunk;
   int s = 1;
