@@ -20,7 +20,8 @@
 // sequence, or its shared keys, for a block of up to 16 query rows that read them.  All blocks of
 // all streams, in order, are cut into equal runs over a grid that fills every SM once, so a ragged
 // batch loads all SMs alike however its lengths lie; a stream's part in a run is one partial
-// result.  Every CTA counts the blocks from the lengths by itself: no host copy of them is
+// result.  (Few streams are cut one by one, so that no CTA starts on a second one: fp32 B5 H12/4 C1003 P777
+// 27.3 us -> 19.4, bf16 B1 H16 C512 11.5 -> 10.1.)  Every CTA counts the blocks from the lengths by itself: no host copy of them is
 // needed, and a cache much larger than what it holds costs nothing.
 //
 // A run belongs to a team of warps: one warp where streams are many, which then needs no barrier
@@ -156,6 +157,76 @@ __device__ __forceinline__ Part get_part(int u, int run, int end, const int* cum
   p.count = min(blocks - p.first, end - u);
   p.slot += run - stream0 / s.per;
   return p;
+}
+
+// With a run per CTA: run `run` of the streams in order, each cut for itself; false where there is none.  All
+// lanes; few streams, so few sequences: two per lane.
+__device__ __forceinline__ bool get_run(int run, const int* cum, const Split& s, const DecodeArgs& a, Part& p) {
+  int blocks, i;   // the stream's blocks; the run's place in it
+  const int shared_runs = (a.pblocks + s.per - 1) / s.per, shared_streams = a.Hkv * a.shared_rowblocks;
+  if (run < shared_runs * shared_streams) {
+    const int stream = run / shared_runs;
+    i = run - stream * shared_runs;
+    blocks = a.pblocks;
+    p.kv = stream / a.shared_rowblocks;
+    p.b = -1;
+    p.keys = a.P;
+    p.row0 = (stream - p.kv * a.shared_rowblocks) * kRows;
+    p.rows = min(a.B * a.G - p.row0, kRows);
+    p.slot = i;
+  } else {
+    const int lane = threadIdx.x & 31, streams = a.Hkv * a.own_rowblocks;
+    int at = run - shared_runs * shared_streams;
+    int b = -1, n = 0, seq0 = 0;   // the sequence, its runs per stream and all before it
+    for (int b0 = 0; b0 < a.B && b < 0; b0 += 32) {
+      const int mine = b0 + lane < a.B ? (cum[b0 + lane + 1] - cum[b0 + lane] + s.per - 1) / s.per : 0;
+      int upto = mine * streams;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, seq0 + upto > at);
+      const int l = past ? __ffs(past) - 1 : 31;
+      n = __shfl_sync(0xffffffffu, mine, l);
+      if (past) {
+        b = b0 + l;
+        seq0 += __shfl_sync(0xffffffffu, upto, l) - n * streams;
+      } else {
+        seq0 += __shfl_sync(0xffffffffu, upto, 31);
+      }
+    }
+    if (b < 0) return false;
+    at -= seq0;
+    const int stream = at / n;
+    i = at - stream * n;
+    blocks = cum[b + 1] - cum[b];
+    p.kv = stream / a.own_rowblocks;
+    p.b = b;
+    p.keys = cum[a.B + 1 + b];
+    p.row0 = (stream - p.kv * a.own_rowblocks) * kRows;
+    p.rows = min(a.G - p.row0, kRows);
+    p.slot = a.pslots + i;
+  }
+  p.first = i * s.per;
+  p.count = min(blocks - p.first, s.per);
+  return true;
+}
+
+// f(part) for the parts of this team's run.
+template <int TW, typename F>
+__device__ __forceinline__ void each_part(int team, const int* cum, const Split& s, const DecodeArgs& a, F f) {
+  if constexpr (TW == 1) {   // runs go to the CTAs in turn, so that few runs spread over the SMs
+    const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
+    for (int u = run * s.per; u < end;) {
+      const Part p = get_part(u, run, end, cum, s, a);
+      f(p);
+      u += p.count;
+    }
+  } else {
+    Part p;
+    if (get_run(blockIdx.x, cum, s, a, p)) f(p);
+  }
 }
 
 // Teams of TW warps.  Blocks of a part that this warp takes: every TW-th.
@@ -400,12 +471,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
   }
-  // runs go to the CTAs in turn, so that few runs spread over the SMs
-  const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
-  for (int u = run * s.per; u < end;) {
-    const Part p = get_part(u, run, end, cum, s, a);
+  each_part<TW>(team, cum, s, a, [&](const Part& p) {
     part_scores<D, TW>(p, a, smem_u32(dyn) + warp * kRing, best, static_cast<T*>(nullptr));
-    u += p.count;
     team_sync<TW>();
     if (tt < p.rows) {
       float m = best[team * TW * kRows + tt];
@@ -414,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
       a.row_max[static_cast<int64_t>(row_of(p, tt, a)) * a.slots + p.slot] = m;
     }
     team_sync<TW>();   // the maxima are read, and the rings are free
-  }
+  });
   // Only now: dependents that wait beside this kernel's CTAs cost more than their early start gives
   // (B64 H8 of 2048 own keys: 132 us with the release at the start, 117 with it here).
   release_dependents();
@@ -716,11 +783,8 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
   // The scores have been written: by the kernel before, or, with the tensor cores, by the one before
   // that, which all of the kernel before had awaited when this one could start.
   if (!a.tc) await_previous();
-  const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
-  for (int u = run * s.per; u < end;) {
-    const Part p = get_part(u, run, end, cum, s, a);
+  each_part<TW>(team, cum, s, a, [&](const Part& p) {
     part_values<D, TW>(p, a, s, cum, smem_u32(ring), ring, rowm_s + team * kRows, sums, static_cast<T*>(nullptr));
-    u += p.count;
     team_sync<TW>();
     if (tt < p.rows) {
       float f = sums[team * TW * kRows + tt];
@@ -742,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
       reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, r, a)) * a.slots + p.slot) * D)[c] = f;
     }
     team_sync<TW>();
-  }
+  });
   release_dependents();
   // Whoever awaits this kernel awaits the tensor cores' part too: see the scores kernel.
   if (a.tc && blockIdx.x == gridDim.x - 1) await_previous();
@@ -903,10 +967,12 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   if (e == cudaSuccess) e = set_up_kernel<decode_join_kernel<T, D>>(0, true);
   if (e != cudaSuccess) return e;
   // CTAs for the runs that there can be
-  const int64_t most = static_cast<int64_t>(a.Hkv) * a.pblocks * a.shared_rowblocks +
-                       static_cast<int64_t>(a.B) * (a.own_width / a.block) * a.Hkv * a.own_rowblocks;
-  const int64_t runs = (most + a.min_run - 1) / a.min_run, all = a.runs * TW / kWarps;
-  const int grid = static_cast<int>(runs < all ? runs : all);
+  const int64_t shared_streams = static_cast<int64_t>(a.Hkv) * a.shared_rowblocks,
+                own_streams = static_cast<int64_t>(a.B) * a.Hkv * a.own_rowblocks, own = a.own_width / a.block;
+  auto runs_of = [&](int64_t blocks) { return (blocks + a.min_run - 1) / a.min_run; };
+  const int64_t ctas = TW == 1 ? runs_of(shared_streams * a.pblocks + own_streams * own)   // few runs: a CTA each
+                               : shared_streams * runs_of(a.pblocks) + own_streams * runs_of(own);
+  const int grid = static_cast<int>(ctas < kDecodeCtas ? ctas : kDecodeCtas);
   if (a.tc && (e = launch_decode_prefix(maps, a, false, ctx, st)) != cudaSuccess) return e;
   if (a.tc) {
     e = launch_dependent(decode_scores_kernel<T, D, TW>, grid, kThreads, smem_scores, st, a);
@@ -962,7 +1028,7 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
                           (a->pblocks ? static_cast<int64_t>(a->Hkv) * a->shared_rowblocks : 0);
   if (total > INT_MAX / 2) return 0;
   a->team = streams >= 64 ? 1 : kWarps;
-  a->runs = kDecodeCtas * kWarps / a->team;
+  a->runs = a->team == 1 ? kDecodeCtas * kWarps : kDecodeCtas - static_cast<int>(streams);
   const int64_t even = total / a->runs;
   a->min_run = static_cast<int>(even < a->team ? a->team : even > 8 * a->team ? 8 * a->team : even);
   a->pchunk = a->pslots = 0;

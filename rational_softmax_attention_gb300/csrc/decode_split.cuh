@@ -16,12 +16,15 @@ struct DecodeSplit {
   int per;     // blocks of a run
 };
 
-// own: blocks per stream of all sequences together (cum[B]).
+// own: blocks per stream of all sequences together (cum[B]).  With a run per warp the runs are equal parts of
+// all blocks.  With one per CTA each stream is cut for itself, into runs of `per` blocks that are
+// few enough for one grid: no more than total / per and one for each of the (few) streams.
 __device__ __forceinline__ DecodeSplit decode_split(const DecodeArgs& a, int own) {
   DecodeSplit s;
   s.own0 = a.Hkv * a.pblocks * a.shared_rowblocks;   // 0 with tc
   s.total = s.own0 + own * a.Hkv * a.own_rowblocks;
   s.per = max((s.total + a.runs - 1) / a.runs, a.min_run);
+  if (a.team > 1) s.per = (s.per + a.team - 1) / a.team * a.team;   // as many for each warp
   return s;
 }
 
@@ -32,9 +35,14 @@ __device__ __forceinline__ int decode_slots_of(int stream0, int blocks, int per)
 }
 __device__ __forceinline__ void decode_row_slots(int b, int kv, int g, int cum0, int cum1, const DecodeSplit& s,
                                                  const DecodeArgs& a, int& shared, int& own) {
+  const int n = cum1 - cum0;
+  if (a.team > 1) {
+    shared = a.tc ? a.pslots : (a.pblocks + s.per - 1) / s.per;
+    own = (n + s.per - 1) / s.per;
+    return;
+  }
   shared = a.tc ? a.pslots
                 : decode_slots_of((kv * a.shared_rowblocks + (b * a.G + g) / kDecodeRows) * a.pblocks, a.pblocks, s.per);
-  const int n = cum1 - cum0;
   own = decode_slots_of(s.own0 + cum0 * a.Hkv * a.own_rowblocks + (kv * a.own_rowblocks + g / kDecodeRows) * n, n,
                         s.per);
 }
