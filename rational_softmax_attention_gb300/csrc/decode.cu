@@ -467,6 +467,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
+  constexpr bool EARLY = TW > 1;
+  if (EARLY) release_dependents();
   const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
@@ -482,9 +484,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
     }
     team_sync<TW>();   // the maxima are read, and the rings are free
   });
-  // Only now: dependents that wait beside this kernel's CTAs cost more than their early start gives
-  // (B64 H8 of 2048 own keys: 132 us with the release at the start, 117 with it here).
-  release_dependents();
+  // Only now, with many streams: dependents that wait beside this kernel's CTAs cost more than their early start
+  // gives (B64 H8 of 2048 own keys: 132 us with the release at the start, 117 with it here).  Few
+  // streams are bound by latency: B2 H24/1 C65537 19.2 us with the release here, 17.6 at the start.
+  if (!EARLY) release_dependents();
   // The tensor cores' part, if any: whoever awaits this kernel awaits that too.  One CTA sees to it; the
   // others make room for the next ones.
   if (blockIdx.x == gridDim.x - 1) await_previous();
@@ -546,12 +549,33 @@ struct FetchValues {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) src[j] = score_row(p, row_of(p, r + j * kRowsPerLoad, a), a) + c * 4;
   }
-  __device__ __forceinline__ void operator()(uint32_t stage, int i, int rows) const {
+  __device__ __forceinline__ void block(uint32_t stage, int i) const { values(stage, first + i * (TW * C::kKeys), keys); }
+  __device__ __forceinline__ void scores(uint32_t stage, int i, int rows) const {
     const int k = first + i * (TW * C::kKeys);
-    values(stage, k, keys);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
       if (r + j * kRowsPerLoad < rows) copy16(stage + at + j * kRowsPerLoad * C::kScoreStride * 4, src[j] + k, true);
+  }
+  __device__ __forceinline__ void operator()(uint32_t stage, int i, int rows) const {
+    block(stage, i);
+    scores(stage, i, rows);
+  }
+  // The first blocks of a part; in a run per CTA, which has one part, their values do not wait for the scores.
+  __device__ __forceinline__ void start(uint32_t ring, int blocks, int rows, bool wait) const {
+    if (TW > 1) {
+#pragma unroll
+      for (int i = 0; i < C::kStages - 1; ++i)
+        if (i < blocks) block(ring + i * C::kStageV, i);
+    }
+    if (wait) await_previous();
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      if (i < blocks) {
+        if (TW == 1) block(ring + i * C::kStageV, i);
+        scores(ring + i * C::kStageV, i, rows);
+      }
+      copy_commit();   // with TW > 1 the first group has all values
+    }
   }
 };
 
@@ -569,11 +593,7 @@ __device__ __forceinline__ void bf16_values(const Part& p, const DecodeArgs& a, 
   const int mine = blocks_of_warp<TW>(p);
   const char* vals = stream_of<__nv_bfloat16, D>(p, a.v, a.pv, a);
   const FetchValues<__nv_bfloat16, D, TW, V16> fetch(vals, p, a, lane);
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < mine) fetch(ring + i * C::kStageV, i, p.rows);
-    copy_commit();
-  }
+  fetch.start(ring, mine, p.rows, !a.tc);
   part_maxima<TW>(rowm, p, cum, s, a);
   team_sync<TW>();
   const bool w0 = g < p.rows, w1 = TWO && g + 8 < p.rows;
@@ -689,11 +709,7 @@ __device__ __forceinline__ void part_values(const Part& p, const DecodeArgs& a, 
   const int mine = blocks_of_warp<TW>(p);
   const char* vals = stream_of<float, D>(p, a.v, a.pv, a);
   const FetchValues<float, D, TW, F32> fetch(vals, p, a, lane);
-#pragma unroll 1
-  for (int i = 0; i < C::kStages - 1; ++i) {
-    if (i < mine) fetch(ring + i * C::kStageV, i, p.rows);
-    copy_commit();
-  }
+  fetch.start(ring, mine, p.rows, !a.tc);
   // four lanes per row for phi: lane (g, t) takes rows g and g + 8, keys t, t + 4, ..
   const int g = lane >> 2, t = lane & 3;
   const bool w0 = g < p.rows, w1 = g + 8 < p.rows;
@@ -780,9 +796,8 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
   const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
-  // The scores have been written: by the kernel before, or, with the tensor cores, by the one before
-  // that, which all of the kernel before had awaited when this one could start.
-  if (!a.tc) await_previous();
+  // The scores are awaited behind the first values' copies, unless, with the tensor cores, the kernel before the
+  // previous one has written them, which all of the previous one had awaited when this one could start.
   each_part<TW>(team, cum, s, a, [&](const Part& p) {
     part_values<D, TW>(p, a, s, cum, smem_u32(ring), ring, rowm_s + team * kRows, sums, static_cast<T*>(nullptr));
     team_sync<TW>();
@@ -809,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
   });
   release_dependents();
   // Whoever awaits this kernel awaits the tensor cores' part too: see the scores kernel.
-  if (a.tc && blockIdx.x == gridDim.x - 1) await_previous();
+  if (blockIdx.x == gridDim.x - 1) await_previous();
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -819,27 +834,28 @@ constexpr int kWeightKeys = 4 * kThreads;   // keys a weight CTA takes at a time
 constexpr int kWeightRows = 8;              // rows whose scores a thread has in flight
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs a, int weight_keys) {
+__global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs a, int row_warps, int weight_keys) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row_ctas = (a.B * a.Hq + kWarps - 1) / kWarps;
+  const int row_ctas = (a.B * a.Hq * row_warps + kWarps - 1) / kWarps;
   await_previous();
   const Split sp = decode_split(a, a.cum[a.B]);   // the counts that the scores kernel left
-  if (static_cast<int>(blockIdx.x) < row_ctas) {   // one output row per warp
+  if (static_cast<int>(blockIdx.x) < row_ctas) {   // one output row per warp, or per CTA
     constexpr int L = D / 4, KS = 32 / L;
-    const int row = blockIdx.x * kWarps + warp;
+    const bool whole = row_warps > 1;
+    const int row = whole ? blockIdx.x : blockIdx.x * kWarps + warp;
     if (row >= a.B * a.Hq) return;
     const int b = row / a.Hq, kv = (row - b * a.Hq) / a.G;
     int shared, own;
     decode_row_slots(b, kv, row - b * a.Hq - kv * a.G, a.cum[b], a.cum[b + 1], sp, a, shared, own);
-    const int gl = lane % L, ks = lane / L;
+    const int gl = lane % L, ks = lane / L, step = KS * row_warps;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float total = 0.0f;
-    for (int i0 = ks; i0 < shared + own; i0 += 8 * KS) {   // eight parts at a time in flight
+    for (int i0 = whole ? warp * KS + ks : ks; i0 < shared + own; i0 += 8 * step) {   // eight parts at a time in flight
       float f[8];
       float4 x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * KS;
+        const int i = i0 + j * step;
         const int64_t at = static_cast<int64_t>(row) * a.slots + (i < shared ? i : a.pslots + i - shared);
         const bool in = i < shared + own;
         f[j] = in ? __ldcg(a.part_sum + at) : 0.0f;
@@ -862,6 +878,23 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
       s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
       s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
       total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (whole) {
+      __shared__ float4 sums[kWarps][L];
+      __shared__ float totals[kWarps];
+      if (ks == 0) sums[warp][gl] = s;
+      if (lane == 0) totals[warp] = total;
+      __syncthreads();
+      if (warp) return;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 x = sums[w][gl];
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+        total += totals[w];
+      }
     }
     if (ks == 0) {
       const float inv = total != 0.0f ? 1.0f / total : 0.0f;   // no key at all: zeros
@@ -898,17 +931,19 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
   };
   load(0);
   load_old();
-  for (int g = warp * 8 + (lane >> 2); g < (a.G + 7) / 8 * 8; g += kWarps * 8) {   // four lanes per row
-    const int gg = min(g, a.G - 1);
+  // lanes per row: four, each with four of its parts in flight; more where parts are many and rows few
+  const int lanes = a.slots <= 64 || a.G > 16 ? 4 : a.G > 8 ? 8 : a.G > 4 ? 16 : 32, t = threadIdx.x & (lanes - 1);
+  for (int g0 = 0; g0 < a.G; g0 += kThreads / lanes) {
+    const int g = g0 + threadIdx.x / lanes, gg = min(g, a.G - 1);
     int shared, own;
     decode_row_slots(b, kv, gg, a.cum[b], a.cum[b + 1], sp, a, shared, own);
     const int64_t at = (static_cast<int64_t>(b) * a.Hq + kv * a.G + gg) * a.slots;
     float m = -kInf, total = 0.0f;
-    for (int i0 = lane & 3; i0 < shared + own; i0 += 16) {
+    for (int i0 = t; i0 < shared + own; i0 += 4 * lanes) {
       float y[4], z[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 4 * j;
+        const int i = i0 + lanes * j;
         const bool in = i < shared + own;
         const int64_t slot = at + (i < shared ? i : a.pslots + i - shared);
         y[j] = in ? __ldcg(a.row_max + slot) : -kInf;
@@ -920,12 +955,11 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
         total += z[j];
       }
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
+    for (int o = 1; o < lanes; o <<= 1) {
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    if ((lane & 3) == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / total);
+    if (t == 0 && g < a.G) stat[g] = make_float2(m, 1.0f / total);
   }
   __syncthreads();
   while (first < last) {
@@ -985,7 +1019,10 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   if (e != cudaSuccess) return e;
   // Few CTAs: a weight CTA takes as many keys, up to 4096, as leave about six per SM (starting the
   // 6144 CTAs of one row or 512 keys each took most of 15 us at B64 H32/8 C4096).
-  int64_t join = (static_cast<int64_t>(a.B) * a.Hq + kWarps - 1) / kWarps;
+  // A CTA per row where rows are few and their partial results many.
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+  const int row_warps = rows <= 2 * kSms && a.slots > 8 * (128 / D) ? kWarps : 1;
+  int64_t join = (rows * row_warps + kWarps - 1) / kWarps;
   int weight_keys = kWeightKeys;
   if (a.weight) {
     const int64_t streams = static_cast<int64_t>(a.B) * a.Hkv;
@@ -993,7 +1030,7 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
     join += streams * ((a.C + weight_keys - 1) / weight_keys);
   }
   return launch_dependent(decode_join_kernel<T, D>, static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st, a,
-                          weight_keys);
+                          row_warps, weight_keys);
 }
 template <typename T, int D>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
