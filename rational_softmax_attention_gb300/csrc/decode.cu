@@ -21,20 +21,23 @@
 // all streams, in order, are cut into equal runs over a grid that fills every SM once, so a ragged
 // batch loads all SMs alike however its lengths lie; a stream's part in a run is one partial
 // result.  (Few streams are cut one by one, so that no CTA starts on a second one: fp32 B5 H12/4 C1003 P777
-// 27.3 us -> 19.4, bf16 B1 H16 C512 11.5 -> 10.1.)  Every CTA counts the blocks from the lengths by itself: no host copy of them is
-// needed, and a cache much larger than what it holds costs nothing.
+// 27.3 us -> 19.4, bf16 B1 H16 C512 11.5 -> 10.1.)  Every CTA counts the blocks from the lengths by
+// itself: no host copy of them is needed, and a cache much larger than what it holds costs nothing.
 //
 // A run belongs to a team of warps: one warp where streams are many, which then needs no barrier
 // beyond its lanes; the CTA's four where they are few, so that a long stream has a quarter of the
 // partial results (the team's warps take a part's blocks in turn and add theirs at its end).
-// B32 H8 C1024 with 1: 31 us in both kernels, with 4: 45; B2 H24/1 C65537 with 1: 25, with 4: 22.
+// bf16, whole call in a graph, with 1 / with 4: B2 H24/1 D64 C65537 76 / 24 us, B4 H8 D128 C8192 38.6 /
+// 34.3; with 128 streams B16 H8 C512 16.2 / 15.2, C2048 36.5 / 36.3; B12 H8 C4096 48.7 / 50.0, B32 H8 C1024 36.1 / 37.0.
 // Each warp streams its blocks through a small ring of its own in shared memory with asynchronous
 // copies (which also zero the keys past a stream's end, so that nothing in a cache's unused slots
 // can reach a sum).  bf16: m16n8k16 products, query
 // rows as M; the chunks of a row are permuted in shared memory so that the 16-byte fragment reads
 // below meet no bank conflict.  fp32: FFMA.
 //
-// Bound: HBM, K and V once.
+// Bound: HBM, K and V once, where there is much of them: B64 H32/8 D128 C8192 reads 2.1 GB in 391 us, 5.5
+// TB/s, B1 H32/8 C131072 0.54 GB in 112 us, 4.8 TB/s.  Latency below that: B1 H16 C512 takes 8.5 us in
+// a graph, three launches of a few dependent loads each.
 #include <climits>
 
 #include "decode_split.cuh"
@@ -1041,8 +1044,9 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
 
 // The split of the keys.  Shared keys of more than kTcRows rows per key head go to the tensor
 // cores, in whole tiles of 128, split so that one wave of CTAs takes them.  Everything else is
-// cut into runs of equal length: one per warp with 64 streams or more (a stream then has at most
-// about 30 partial results), one per CTA with fewer.  A run has at least min_run blocks: one per warp
+// cut into runs: equal ones, one per warp, with many streams (a stream then has at most about 30
+// partial results); one per CTA, each stream for itself, with fewer than 64, or up to 128 where a warp's
+// equal run would be short.  A run has at least min_run blocks: one per warp
 // (with two, fp32 B5 H12/4 C1003 P777 took 32.7 us instead of 27.0, bf16 B1 H16 C512 11.9 instead of
 // 11.2), more, up to eight, where all blocks give each run as many, which bounds the partial results of a
 // long stream.
@@ -1064,7 +1068,7 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t streams = static_cast<int64_t>(a->B) * a->Hkv * a->own_rowblocks +
                           (a->pblocks ? static_cast<int64_t>(a->Hkv) * a->shared_rowblocks : 0);
   if (total > INT_MAX / 2) return 0;
-  a->team = streams >= 64 ? 1 : kWarps;
+  a->team = streams < 64 || (streams <= 128 && total < 10 * kDecodeCtas * kWarps) ? kWarps : 1;
   a->runs = a->team == 1 ? kDecodeCtas * kWarps : kDecodeCtas - static_cast<int>(streams);
   const int64_t even = total / a->runs;
   a->min_run = static_cast<int>(even < a->team ? a->team : even > 8 * a->team ? 8 * a->team : even);

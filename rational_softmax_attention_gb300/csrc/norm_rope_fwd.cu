@@ -1,4 +1,6 @@
 // The forward of the per-head normalisation and rotation (the mathematics: norm_rope.cuh).
+// bf16 B4 N8192 H16 D128, layer norm with biases: 537 MB in 95 us, 5.7 TB/s; issue slots 55% busy.  Four rows
+// ahead per lane group: what is in flight then covers the latency at two CTAs per SM.
 #include "norm_rope.cuh"
 
 namespace raattn {
