@@ -268,6 +268,11 @@ __device__ __forceinline__ const char* stream_of(const Part& p, const void* own,
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {   // zeros when not in
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
+// The same without the choice, for keys and values: no later kernel reads them, so they are the first to leave
+// L2, where the scores had better stay (B64 H32/8 D128 C2048, whole call: 111.5 us -> 99.0).
+__device__ __forceinline__ void copy16_once(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -291,17 +296,25 @@ struct Fetch {
   static constexpr int kRowsPerCopy = 32 / CHUNKS, kCopies = KEYS / kRowsPerCopy;
   const char* src;   // the lane's chunk of the stream's row `lane / CHUNKS`
   int r, c;
+  uint64_t policy;
   __device__ __forceinline__ Fetch(const char* stream, int lane) : r(lane / CHUNKS), c(lane % CHUNKS) {
     src = stream + lane * 16;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
   }
   // the block of keys first .. of a stream of `keys`
   __device__ __forceinline__ void operator()(uint32_t stage, int first, int keys) const {
     const char* s = src + static_cast<int64_t>(first) * (CHUNKS * 16);
-    const int left = keys - first - r;
+    if (first + KEYS <= keys) {
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const bool in = i * kRowsPerCopy < left;
-      copy16(stage + place<LAY, CHUNKS>(r + i * kRowsPerCopy, c) * 16, in ? s + i * 512 : src - r * (CHUNKS * 16), in);
+      for (int i = 0; i < kCopies; ++i)
+        copy16_once(stage + place<LAY, CHUNKS>(r + i * kRowsPerCopy, c) * 16, s + i * 512, policy);
+    } else {
+      const int left = keys - first - r;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        const bool in = i * kRowsPerCopy < left;
+        copy16(stage + place<LAY, CHUNKS>(r + i * kRowsPerCopy, c) * 16, in ? s + i * 512 : src - r * (CHUNKS * 16), in);
+      }
     }
   }
 };
