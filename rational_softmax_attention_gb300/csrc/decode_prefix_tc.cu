@@ -21,8 +21,8 @@
 // for the lower and the upper 64 keys of a tile.  Two score buffers: S of the next tile is formed under
 // phi of this one, and the thread that issues the products needs one hand-off per tile, "P is
 // written", since products run in the order of their issue (P V of tile j, then S of tile j + 2 into
-// the same columns).  Query rows are gathered by their own
-// threads (a head's rows are G at a time in memory) into the 128-byte-swizzled operand layout.
+// the same columns).  Query rows are gathered by their own threads (a head's rows are G at a time in
+// memory) into tensor memory, from where the products read them: shared memory is all ring.
 //
 // One row tile per CTA leaves registers and shared memory for a CTA of the kernels that stream the
 // sequences' own keys (decode.cu), which are launched behind these as dependents and run beside
@@ -36,17 +36,16 @@ namespace {
 constexpr int BM = 128, BN = 128;
 constexpr int SOFTMAX_WARPS = 8, PRODUCER_WARP = 8, MMA_WARP = 9;
 constexpr int THREADS = 32 * 10;
-constexpr uint32_t TMEM_O = 256;          // score buffer b at column 128 b, O behind both
+// score buffer b at column 128 b, O behind both, then Q (bf16 pairs), in all that there is
+constexpr uint32_t TMEM_O = 256, TMEM_Q = 384, TMEM_COLS = 512;
 constexpr int SPLIT_BATCH = 512;          // up to so many sequences' block counts are kept in shared memory
 constexpr int BOX_BYTES = 128 * 64 * 2;   // one TMA box: 128 rows x 64 values
 
 template <int D, bool VALUES>
 struct Cfg {
-  static constexpr uint32_t TMEM_COLS = VALUES ? 512 : 256;
   static constexpr int TILE_BYTES = BN * D * 2;
-  static constexpr int NSTAGE = D == 128 ? (VALUES ? 4 : 3) : 6;
-  static constexpr int OFF_RING = TILE_BYTES;   // behind Q
-  static constexpr int OFF_BAR = OFF_RING + NSTAGE * TILE_BYTES;
+  static constexpr int NSTAGE = D == 128 ? 5 : 8;
+  static constexpr int OFF_BAR = NSTAGE * TILE_BYTES;
   // q_full, ring_full[], ring_empty[], s_full[2], handed[2], o_full, drain
   static constexpr int NUM_BARS = 1 + 2 * NSTAGE + 6;
   static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // tmem base, abort flag, votes [2][8]
@@ -122,8 +121,7 @@ __global__ void __launch_bounds__(640, 1)
     return;
   }
   uint8_t* smem = smem_raw;
-  uint8_t* sQ = smem;
-  uint8_t* sRing = smem + C::OFF_RING;
+  uint8_t* sRing = smem;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* ring_full = q_full + 1;
   uint64_t* ring_empty = ring_full + NST;
@@ -160,7 +158,7 @@ __global__ void __launch_bounds__(640, 1)
     fence_mbarrier_init();
   }
   if (warp == MMA_WARP) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   if constexpr (!VALUES) release_dependents();
@@ -215,7 +213,6 @@ __global__ void __launch_bounds__(640, 1)
       constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
       constexpr uint32_t HI = sdesc_hi_sw128(1024);
       const uint32_t ring = smem_u32(sRing);
-      const uint32_t qlo = sdesc_lo(smem_u32(sQ), 16);
       uint32_t pos = 0;
       bool o_started = false;
       auto ring_wait = [&](uint32_t p, uint32_t& addr) -> bool {
@@ -233,7 +230,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * BOX_BYTES + (kk & 3) * 32) >> 4;
-          tc_mma_f16(col, sdesc(qlo + off, HI), sdesc(klo + off, HI), idesc_qk, kk > 0 ? 1u : 0u);
+          tc_mma_f16_ts(col, tmem + TMEM_Q + kk * 8, sdesc(klo + off, HI), idesc_qk, kk > 0 ? 1u : 0u);
         }
         tc_commit(&s_full[j & 1]);
         tc_commit(&ring_empty[p % NST]);
@@ -294,23 +291,28 @@ __global__ void __launch_bounds__(640, 1)
       if (lane == 0) r = mbar_wait(bar, par, abort_flag, ctx) ? 1 : 0;
       return __shfl_sync(0xffffffffu, r, 0) != 0;
     };
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     {   // this row's half of Q
-      constexpr int V = D / 16;
       const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(row) * D) +
-                       upper * V;
-      uint4 v[V];
+                       upper * (D / 16);
 #pragma unroll
-      for (int c = 0; c < V; ++c) v[c] = row_ok ? q[c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = upper * V + i;
-        *reinterpret_cast<uint4*>(sQ + row_local * 128 + (c >> 3) * BOX_BYTES + (((c & 7) ^ (row_local & 7)) << 4)) = v[i];
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = row_ok ? q[c * 4 + i] : make_uint4(0, 0, 0, 0);
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+        tmem_st16(lanes + TMEM_Q + upper * (D / 4) + c * 16, w);
       }
-      fence_proxy_async_smem();
+      tc_wait_st();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int tail = a.P - t0 * BN - 64 * upper;   // keys from this half's first on
     bool ok = true;
     uint32_t h[32];
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(640, 1)
   if (warp == MMA_WARP) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
