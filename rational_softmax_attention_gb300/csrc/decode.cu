@@ -483,8 +483,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
-  constexpr bool EARLY = TW > 1;
-  if (EARLY) release_dependents();
+  release_dependents();   // the next kernel's first values are on their way while this one ends
   const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
@@ -500,10 +499,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
     }
     team_sync<TW>();   // the maxima are read, and the rings are free
   });
-  // Only now, with many streams: dependents that wait beside this kernel's CTAs cost more than their early start
-  // gives (B64 H8 of 2048 own keys: 132 us with the release at the start, 117 with it here).  Few
-  // streams are bound by latency: B2 H24/1 C65537 19.2 us with the release here, 17.6 at the start.
-  if (!EARLY) release_dependents();
   // The tensor cores' part, if any: whoever awaits this kernel awaits that too.  One CTA sees to it; the
   // others make room for the next ones.
   if (blockIdx.x == gridDim.x - 1) await_previous();
@@ -576,21 +571,17 @@ struct FetchValues {
     block(stage, i);
     scores(stage, i, rows);
   }
-  // The first blocks of a part; in a run per CTA, which has one part, their values do not wait for the scores.
+  // The first blocks of a part; their values do not wait for the scores (B32 H32/8 C1024 34.3 us -> 33.4, B2 H24/1
+  // C65537 19.2 -> 17.6, with the early start of the kernel).
   __device__ __forceinline__ void start(uint32_t ring, int blocks, int rows, bool wait) const {
-    if (TW > 1) {
 #pragma unroll
-      for (int i = 0; i < C::kStages - 1; ++i)
-        if (i < blocks) block(ring + i * C::kStageV, i);
-    }
+    for (int i = 0; i < C::kStages - 1; ++i)
+      if (i < blocks) block(ring + i * C::kStageV, i);
     if (wait) await_previous();
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
-      if (i < blocks) {
-        if (TW == 1) block(ring + i * C::kStageV, i);
-        scores(ring + i * C::kStageV, i, rows);
-      }
-      copy_commit();   // with TW > 1 the first group has all values
+      if (i < blocks) scores(ring + i * C::kStageV, i, rows);
+      copy_commit();   // the first group has all values
     }
   }
 };
