@@ -3,8 +3,8 @@
 Each translation unit under csrc/ is compiled in parallel to an object file in
 _build/, then linked into rational_softmax_attention_gb300/libraattn.so.  The
 CUDA runtime is linked statically, so the library needs only the driver at run
-time.  csrc/calls.c becomes _calls.so beside it, a Python module over the serving
-calls; without Python's headers it is left out, and ctypes makes those calls too.  `python -m rational_softmax_attention_gb300.build` runs it by hand.
+time.  csrc/calls.cpp becomes _calls.so beside it, the Python module that binds the
+serving calls; it is compiled against the installed torch and loaded into it.  `python -m rational_softmax_attention_gb300.build` runs it by hand.
 """
 from __future__ import annotations
 
@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libraattn.so")
 CALLS_PATH = os.path.join(PKG_DIR, "_calls.so")
-CALLS_SRC = os.path.join(CSRC, "calls.c")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v", "-I", os.path.join(ROOT, "include")]
@@ -60,18 +60,23 @@ def _stale(srcs):
 
 
 def _build_calls(force):
-    headers = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(headers, "Python.h")):
-        return
     deps = [CALLS_SRC, LIB_PATH, os.path.join(ROOT, "include", "raattn.h")]
     if not force and os.path.exists(CALLS_PATH) and os.path.getmtime(CALLS_PATH) >= max(map(os.path.getmtime, deps)):
         return
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     tmp = CALLS_PATH + ".tmp"
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I", headers, "-I", os.path.join(ROOT, "include"),
-           CALLS_SRC, "-o", tmp, "-L", PKG_DIR, "-l:libraattn.so", "-Wl,-rpath,$ORIGIN"]
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           *(x for d in include for x in ("-isystem", d)), CALLS_SRC, "-o", tmp, "-L", PKG_DIR, "-l:libraattn.so",
+           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"gcc failed on {CALLS_SRC}:\n{res.stderr[-4000:]}")
+        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{res.stderr[-4000:]}")
     os.replace(tmp, CALLS_PATH)
 
 

@@ -166,22 +166,11 @@ def test_counts_beyond_the_call_are_not_counted():
     assert c.length.tolist() == [2, 0, 1] and c.position.tolist() == [2, 0, 1] and c.bound == 2
 
 
-def test_native_marshalling(lib):
-    """The C module takes the header's arguments, in its order and types, and refuses others."""
+def test_native_binding_refuses_what_is_no_tensor_or_size(lib):
+    x, k = torch.zeros(2, 4, 192), torch.zeros(2, 1, 8, 64)
+    for bad in ((None, k, k, k), ([1.0], k, k, k), (x, "k", k, k)):
+        with pytest.raises(TypeError, match="tensor"):
+            ra.ra_attention_decode(*bad)
     calls = pytest.importorskip("rational_softmax_attention_gb300._calls")
-    kinds = {"ra_qk_norm_rope_fwd": [None, 768, 192, *[None] * 4, 2, 1e-5, None, None, 0, 0, None, 0, 0, *[None] * 5, 0, 2,
-                                     4, 1, 1, 64, 0, None],
-             "ra_qk_norm_rope_bwd": [None, 768, 192, *[None] * 4, 2, 1e-5, None, None, 0, 0, None, 0, 0, *[None] * 6, 2, 4,
-                                     1, 1, 64, 0, None],
-             "ra_attention_decode": [*[None] * 9, 1, 1, 1, 16, 0, 64, 0.0, 0, None],
-             "ra_cache_evict": [*[None] * 9, 1, 1, 16, 16, 64, 8, 0, 0, None]}
-    for name, args in kinds.items():
-        fn = getattr(calls, name)
-        assert len(args) == len(getattr(lib, name).argtypes)
-        assert fn(*args) == ARG, name               # null pointers, as through ctypes
-        with pytest.raises(TypeError):
-            fn(*args[:-1])
-        with pytest.raises(TypeError):
-            fn("0", *args[1:])
-        with pytest.raises(OverflowError):
-            fn(*args[:-4], 1 << 31, *args[-3:])
+    with pytest.raises(TypeError, match="arguments"):
+        calls.attention_decode(x)
