@@ -422,10 +422,11 @@ ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t t
  *   scale         score scale; <= 0 means 1/sqrt(D).
  *   dtype         of q, k, v, prefix and o.  RA_BF16: D in {64, 128}; RA_F32: {16, 32, 64, 128}.
  * Scores, row maxima, sums and weights are fp32.  RA_BF16: weights enter the value products as two
- * bf16 (2^-15 lost), a prefix's with more than 128 query rows per key head as one (2^-8).  Results do
- * not depend on scheduling.
- * With a prefix and more than 32 query rows per key head (B H_Q / H_KV), bf16 calls use kernels
- * with bounded waits, whose giving up ra_device_status() reports.
+ * bf16 (2^-15 lost), or, in the kernels named below with more than 128 query rows per key head, as one
+ * (2^-8).  Results do not depend on scheduling.
+ * bf16 calls with more than 32 query rows per key head (B H_Q / H_KV) and a prefix of more than 3648
+ * blocks, 16 keys by 16 of the rows, over all key heads use kernels with bounded waits, whose giving up
+ * ra_device_status() reports.
  * Errors: RA_ERR_ARG for null or misaligned pointers, sizes < 1 (P < 0), H_Q no multiple of
  * H_KV, B H_Q, B H_KV C or H_KV P beyond int32, C or P beyond 2^31 - 16385, a bad enum or scale;
  * RA_ERR_UNSUPPORTED for D outside the sets above, B > 8192, more than 1024 query heads per key head,

@@ -86,16 +86,19 @@ __device__ __forceinline__ float phi_t(float d) {
 // The sequences' entries and own blocks: cum[b] = blocks per stream of the sequences before b, for
 // b <= B, and behind it their lengths.  All threads.
 template <int KEYS>
-__device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a) {
-  __shared__ int sums[kWarps];
+__device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a, int* most_blocks) {
+  __shared__ int sums[kWarps], longest[kWarps];
   int* len = cum + a.B + 1;
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-  int mine = 0;
+  int mine = 0, most = 0;
   for (int i = b0; i < b0 + per && i < a.B; ++i) {
-    const int n = decode_own_length(a, i);
+    const int n = decode_own_length(a, i), blocks = (n + KEYS - 1) / KEYS;
     len[i] = n;
-    mine += (n + KEYS - 1) / KEYS;
+    mine += blocks;
+    most = max(most, blocks);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((threadIdx.x & 31) == 0) longest[threadIdx.x >> 5] = most;
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -112,7 +115,10 @@ __device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a) {
   }
   if (b0 < a.B && b0 + per >= a.B) cum[a.B] = run;
   __syncthreads();
-  return decode_split(a, cum[a.B]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) most = max(most, longest[w]);
+  *most_blocks = most;
+  return decode_split(a, cum[a.B], most);
 }
 
 // A stream's part in a run.
@@ -216,19 +222,28 @@ __device__ __forceinline__ bool get_run(int run, const int* cum, const Split& s,
   return true;
 }
 
+// A short prefix counts for more blocks than it has, see plan_decode: those that it has of them.
+__device__ __forceinline__ void clip(Part& p, const DecodeArgs& a) {
+  if (p.b < 0) p.count = max(min(p.count, (a.P + a.block - 1) / a.block - p.first), 0);
+}
+
 // f(part) for the parts of this team's run.
 template <int TW, typename F>
 __device__ __forceinline__ void each_part(int team, const int* cum, const Split& s, const DecodeArgs& a, F f) {
   if constexpr (TW == 1) {   // runs go to the CTAs in turn, so that few runs spread over the SMs
     const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
     for (int u = run * s.per; u < end;) {
-      const Part p = get_part(u, run, end, cum, s, a);
-      f(p);
+      Part p = get_part(u, run, end, cum, s, a);
       u += p.count;
+      clip(p, a);
+      f(p);
     }
   } else {
     Part p;
-    if (get_run(blockIdx.x, cum, s, a, p)) f(p);
+    if (get_run(blockIdx.x, cum, s, a, p)) {
+      clip(p, a);
+      f(p);
+    }
   }
 }
 
@@ -484,9 +499,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
   __shared__ float best[kWarps * kRows];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   release_dependents();   // the next kernel's first values are on their way while this one ends
-  const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
+  int longest;
+  const Split s = make_split<Cfg<T, D>::kKeys>(cum, a, &longest);
   if (blockIdx.x == 0) {   // for the kernels that look up a row's slots
     for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
+    if (threadIdx.x == 0) a.cum[a.B + 1] = longest;
   }
   each_part<TW>(team, cum, s, a, [&](const Part& p) {
     part_scores<D, TW>(p, a, smem_u32(dyn) + warp * kRing, best, static_cast<T*>(nullptr));
@@ -802,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, 4) decode_values_kernel(const Decode
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
-  const Split s = make_split<Cfg<T, D>::kKeys>(cum, a);
+  int longest;
+  const Split s = make_split<Cfg<T, D>::kKeys>(cum, a, &longest);
   // The scores are awaited behind the first values' copies, unless, with the tensor cores, the kernel before the
   // previous one has written them, which all of the previous one had awaited when this one could start.
   each_part<TW>(team, cum, s, a, [&](const Part& p) {
@@ -845,7 +863,7 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_ctas = (a.B * a.Hq * row_warps + kWarps - 1) / kWarps;
   await_previous();
-  const Split sp = decode_split(a, a.cum[a.B]);   // the counts that the scores kernel left
+  const Split sp = decode_split(a, a.cum[a.B], a.cum[a.B + 1]);   // the counts that the scores kernel left
   if (static_cast<int>(blockIdx.x) < row_ctas) {   // one output row per warp, or per CTA
     constexpr int L = D / 4, KS = 32 / L;
     const bool whole = row_warps > 1;
@@ -1010,7 +1028,7 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   // CTAs for the runs that there can be
   const int64_t shared_streams = static_cast<int64_t>(a.Hkv) * a.shared_rowblocks,
                 own_streams = static_cast<int64_t>(a.B) * a.Hkv * a.own_rowblocks, own = a.own_width / a.block;
-  auto runs_of = [&](int64_t blocks) { return (blocks + a.min_run - 1) / a.min_run; };
+  auto runs_of = [&](int64_t blocks) { return (blocks + TW - 1) / TW; };
   const int64_t ctas = TW == 1 ? runs_of(shared_streams * a.pblocks + own_streams * own)   // few runs: a CTA each
                                : shared_streams * runs_of(a.pblocks) + own_streams * runs_of(own);
   const int grid = static_cast<int>(ctas < kDecodeCtas ? ctas : kDecodeCtas);
@@ -1046,15 +1064,19 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
 
 }  // namespace
 
-// The split of the keys.  Shared keys of more than kTcRows rows per key head go to the tensor
-// cores, in whole tiles of 128, split so that one wave of CTAs takes them.  Everything else is
-// cut into runs: equal ones, one per warp, with many streams (a stream then has at most about 30
-// partial results); one per CTA, each stream for itself, with fewer than 64, or up to 128 where a warp's
-// equal run would be short.  A run has at least min_run blocks: one per warp
-// (with two, fp32 B5 H12/4 C1003 P777 took 32.7 us instead of 27.0, bf16 B1 H16 C512 11.9 instead of
-// 11.2), more, up to eight, where all blocks give each run as many, which bounds the partial results of a
-// long stream.
+// The split of the keys.  Shared keys of more than kTcRows rows per key head, and of more than two blocks (16
+// keys by 16 rows) for every warp of the grid, go to the tensor cores, in whole tiles of 128, split so
+// that one wave of CTAs takes them.  That costs two more launches, which few blocks do not pay back:
+// bf16 D128 with them / without, B64 H32/8 P128 31.3 us / 24.8, P1024 35.0 / 38.0, B32 H32/8 P128 24.8 / 18.5,
+// P2048 32.6 / 31.5, B128 H32/8 P256 31.5 / 28.1, P512 34.0 / 37.4.  Everything else is cut into runs:
+// equal ones, one per warp, with many streams; one per CTA, each stream for itself, with fewer than 64, or
+// up to 128 where a warp's equal run would be short.  `full`, the blocks of a run when the cache is
+// full, one to eight per warp, bounds the partial results that a stream has places for; with shorter
+// sequences runs are shorter (B64 H32/8 C4096 of 10 keys each: 39.9 us -> 11.8), but not beside the tensor
+// cores' part, which fewer warps disturb less (B32 H32/8 C1024 P2048: 39.2 us with the shortest, 36.0).  A short prefix counts for kShortPrefix blocks: what starting on its few
+// keys costs (with P1, eight parts of one block to a warp took 62 us, B64 H32/8).
 constexpr int64_t kTcRows = 32;
+constexpr int kShortPrefix = 8;
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
   a->G = a->Hq / a->Hkv;
@@ -1064,18 +1086,19 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   a->shared_rowblocks = static_cast<int>((shared_rows + kRows - 1) / kRows);
   const int own = (a->C + a->block - 1) / a->block;
   a->own_width = own * a->block;
-  a->tc = bf16 && a->P > 0 && shared_rows > kTcRows;
-  a->pblocks = a->tc ? 0 : (a->P + a->block - 1) / a->block;
+  const int64_t shared = (a->P + a->block - 1) / a->block, shared_streams = static_cast<int64_t>(a->Hkv) * a->shared_rowblocks;
+  a->tc = bf16 && shared_rows > kTcRows && shared * shared_streams > 2 * kDecodeCtas * kWarps;
+  a->pblocks = a->tc || !a->P ? 0 : static_cast<int>(shared < kShortPrefix ? kShortPrefix : shared);
   a->pre_width = a->pblocks * a->block;
   const int64_t total = static_cast<int64_t>(a->B) * own * a->Hkv * a->own_rowblocks +
                         static_cast<int64_t>(a->pblocks) * a->Hkv * a->shared_rowblocks;
   const int64_t streams = static_cast<int64_t>(a->B) * a->Hkv * a->own_rowblocks +
-                          (a->pblocks ? static_cast<int64_t>(a->Hkv) * a->shared_rowblocks : 0);
+                          (a->pblocks ? shared_streams : 0);
   if (total > INT_MAX / 2) return 0;
   a->team = streams < 64 || (streams <= 128 && total < 10 * kDecodeCtas * kWarps) ? kWarps : 1;
   a->runs = a->team == 1 ? kDecodeCtas * kWarps : kDecodeCtas - static_cast<int>(streams);
   const int64_t even = total / a->runs;
-  a->min_run = static_cast<int>(even < a->team ? a->team : even > 8 * a->team ? 8 * a->team : even);
+  const int64_t full = even < a->team ? a->team : even > 8 * a->team ? 8 * a->team : even;
   a->pchunk = a->pslots = 0;
   if (a->tc) {
     const int64_t per = a->Hkv * ((shared_rows + 127) / 128), tiles = (a->P + 127) / 128;
@@ -1084,10 +1107,11 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
     a->pchunk = static_cast<int>((tiles + n - 1) / n * 128);
     a->pslots = (a->P + a->pchunk - 1) / a->pchunk;
   } else if (a->P > 0) {
-    a->pslots = (a->pblocks + a->min_run - 1) / a->min_run + 1;
+    a->pslots = static_cast<int>((a->pblocks + full - 1) / full + 1);
   }
   // a stream of n blocks meets at most ceil(n / run) + 1 runs
-  a->slots = a->pslots + (own + a->min_run - 1) / a->min_run + 1;
+  a->slots = a->pslots + static_cast<int>((own + full - 1) / full + 1);
+  a->least = a->tc ? static_cast<int>(full) : 1;
   size_t at = 0;
   auto piece = [&](int64_t floats) {
     char* p = base + at;
@@ -1099,7 +1123,7 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   a->row_max = reinterpret_cast<float*>(piece(rows * a->slots));
   a->part_sum = reinterpret_cast<float*>(piece(rows * a->slots));
   a->part_o = reinterpret_cast<float*>(piece(rows * a->slots * a->D));
-  a->cum = reinterpret_cast<int*>(piece(a->B + 1));
+  a->cum = reinterpret_cast<int*>(piece(a->B + 2));
   return at;
 }
 

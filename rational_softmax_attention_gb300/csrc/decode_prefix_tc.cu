@@ -51,7 +51,7 @@ struct Cfg {
   static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;   // tmem base, abort flag, votes [2][8]
   static constexpr int OFF_HALF = OFF_MISC + 16 + 2 * SOFTMAX_WARPS * 4;     // the upper halves' row results
   static constexpr int OFF_CUM = OFF_HALF + BM * 4;
-  static constexpr int SMEM_BYTES = OFF_CUM + (VALUES ? (SPLIT_BATCH + 1) * 4 : 0);
+  static constexpr int SMEM_BYTES = OFF_CUM + (VALUES ? (SPLIT_BATCH + 2) * 4 : 0);
   // beside it, on one SM, a CTA of decode_values_kernel of 63.5 KB
   static_assert(SMEM_BYTES + 1024 + 65024 <= 233472, "shared memory per SM");
   static_assert(NSTAGE * TILE_BYTES >= SOFTMAX_WARPS * 4096, "the output leaves through the ring");
@@ -90,7 +90,7 @@ __device__ __forceinline__ float phi_chunk(const uint32_t (&h)[32], uint32_t (&p
 __device__ __forceinline__ float half_maximum(const DecodeArgs& a, const int* cum, int row, int b, int kv, int g,
                                               int first) {
   int shared, own;
-  decode_row_slots(b, kv, g, cum[b], cum[b + 1], decode_split(a, cum[a.B]), a, shared, own);
+  decode_row_slots(b, kv, g, cum[b], cum[b + 1], decode_split(a, cum[a.B], cum[a.B + 1]), a, shared, own);
   const float* p = a.row_max + static_cast<int64_t>(row) * a.slots;
   float m = -INFINITY;
   for (int i0 = first; i0 < shared + own; i0 += 16) {   // eight loads at a time in flight
@@ -362,9 +362,10 @@ __global__ void __launch_bounds__(640, 1)
       // While the maxima are still being formed: where this row's parts are, from the lengths.
       int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
       if (warp == 0 && a.B <= SPLIT_BATCH) {
-        int run = 0;
+        int run = 0, longest = 0;
         for (int i = 0; i < a.B; i += 32) {
           int n = i + lane < a.B ? (decode_own_length(a, i + lane) + a.block - 1) / a.block : 0;
+          longest = max(longest, n);
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, n, o);
@@ -373,7 +374,11 @@ __global__ void __launch_bounds__(640, 1)
           if (i + lane < a.B) cum[i + lane + 1] = run + n;
           run += __shfl_sync(0xffffffffu, n, 31);
         }
-        if (lane == 0) cum[0] = 0;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) {
+          cum[0] = 0;
+          cum[a.B + 1] = longest;
+        }
       }
       // All maxima, which the sequences' own values, the next kernel, need no less; the first tiles are
       // on their way, and the first scores formed, meanwhile.

@@ -16,14 +16,18 @@ struct DecodeSplit {
   int per;     // blocks of a run
 };
 
-// own: blocks per stream of all sequences together (cum[B]).  With a run per warp the runs are equal parts of
+// own: blocks per stream of all sequences together (cum[B]); longest: the most of one.  A run is as short as the
+// grid allows, and long enough for the streams' partial results to find their places.  With a run per warp the runs are equal parts of
 // all blocks.  With one per CTA each stream is cut for itself, into runs of `per` blocks that are
 // few enough for one grid: no more than total / per and one for each of the (few) streams.
-__device__ __forceinline__ DecodeSplit decode_split(const DecodeArgs& a, int own) {
+__device__ __forceinline__ DecodeSplit decode_split(const DecodeArgs& a, int own, int longest) {
   DecodeSplit s;
   s.own0 = a.Hkv * a.pblocks * a.shared_rowblocks;   // 0 with tc
   s.total = s.own0 + own * a.Hkv * a.own_rowblocks;
-  s.per = max((s.total + a.runs - 1) / a.runs, a.min_run);
+  s.per = max((s.total + a.runs - 1) / a.runs, a.least);
+  const int own_places = a.slots - a.pslots - 1;   // a stream of n blocks meets at most ceil(n / per) + 1 runs
+  s.per = max(s.per, (longest + own_places - 1) / own_places);
+  if (a.pblocks) s.per = max(s.per, (a.pblocks + a.pslots - 2) / (a.pslots - 1));
   if (a.team > 1) s.per = (s.per + a.team - 1) / a.team * a.team;   // as many for each warp
   return s;
 }

@@ -193,7 +193,7 @@ struct DecodeArgs {
   int own_width, pre_width;     // padded length of a row of s_own and s_pre
   int pblocks;                  // blocks of the shared keys (none with tc)
   int team;                     // warps that share a run: 1 or 4
-  int runs, min_run;            // equal parts of all blocks, and blocks of one at least
+  int runs, least;              // parts of all blocks, and blocks of one at least
   int pchunk;                   // tc: shared keys of a CTA
   int pslots, slots;            // slots of the shared keys, and all
   float scale;

@@ -93,7 +93,7 @@ CASES = [  # B, Hq, Hkv, C, P, D, sigma, lengths
     (40, 4, 2, 48, 600, 64, 1.0, list(range(40))),         # rows of many sequences against the prefix
     (1, 5, 5, 4999, 0, 64, 3.0, [4990]),
     (2, 2, 1, 16, 2, 128, 1.0, [-3, 99]),                  # lengths outside the cache
-    # the shared keys on the tensor cores (bf16, more than 32 rows per key head)
+    # many rows per shared key
     (33, 1, 1, 3, 1, 64, 1.0, [i % 4 for i in range(33)]),
     (70, 8, 2, 20, 129, 128, 1.0, [i % 21 for i in range(70)]),        # 280 rows: a second row pair of 24
     (100, 3, 1, 40, 2500, 128, 2.0, [i % 41 for i in range(100)]),     # three heads per key head, 300 rows
@@ -103,6 +103,17 @@ CASES = [  # B, Hq, Hkv, C, P, D, sigma, lengths
     (600, 2, 1, 5, 300, 64, 1.0, [i % 6 for i in range(600)]),         # more than 512 sequences
     (1, 1024, 1, 70, 40, 64, 1.0, [69]),                   # as many query heads per key head as there may be
     (8192, 1, 1, 3, 130, 64, 1.0, [i % 4 for i in range(8192)]),       # and as many sequences
+    # the shared keys on the tensor cores (bf16, more than 3648 blocks of 16 rows by 16 keys)
+    (33, 1, 1, 3, 20001, 64, 1.0, [i % 4 for i in range(33)]),
+    (70, 8, 2, 20, 1700, 128, 1.0, [i % 21 for i in range(70)]),
+    (100, 3, 1, 40, 3333, 128, 2.0, [i % 41 for i in range(100)]),
+    (128, 2, 2, 9, 3712, 64, 1.0, [i % 10 for i in range(128)]),       # exactly one row tile
+    (150, 4, 1, 5, 1600, 64, 3.0, [i % 6 for i in range(150)]),
+    (600, 2, 1, 5, 800, 64, 1.0, [i % 6 for i in range(600)]),
+    # short sequences in a large cache, one or more of them long
+    (64, 8, 4, 6000, 0, 64, 1.0, [1 + i % 7 for i in range(64)]),
+    (64, 8, 4, 3000, 5, 128, 1.0, [3000 if i == 9 else i % 5 for i in range(64)]),
+    (3, 4, 2, 9000, 0, 64, 1.0, [2, 9000, 17]),
 ]
 
 
@@ -209,8 +220,8 @@ def test_decode_repeats_streams_and_graphs_agree(dtype):
 
 def test_decode_calls_on_two_streams():
     """Calls that run at the same time, each in its own workspace, with and without the tensor cores' part."""
-    sets = [tuple(t.cuda() for t in inputs(48, 8, 4, 300, 900, 64, torch.bfloat16, seed=27)),
-            tuple(t.cuda() for t in inputs(70, 4, 2, 200, 1500, 128, torch.bfloat16, seed=28)),
+    sets = [tuple(t.cuda() for t in inputs(48, 8, 4, 300, 2600, 64, torch.bfloat16, seed=27)),
+            tuple(t.cuda() for t in inputs(70, 4, 2, 200, 3400, 128, torch.bfloat16, seed=28)),
             tuple(t.cuda() for t in inputs(6, 4, 4, 900, 100, 64, torch.float32, seed=29))]
     lengths = [torch.arange(q.shape[0], dtype=torch.int32, device="cuda") * 4 % k.shape[2] for q, k, *_ in sets]
 
@@ -269,7 +280,7 @@ def test_a_cache_beyond_32_bit_offsets():
 
 def test_decode_shared_keys_beyond_the_support():
     """Row tiles whose every shared weight is 0 (a far larger own score), mixed with others."""
-    q, k, v, pk, pv = inputs(64, 4, 2, 6, 700, 128, torch.bfloat16, seed=25)
+    q, k, v, pk, pv = inputs(64, 4, 2, 6, 4000, 128, torch.bfloat16, seed=25)
     k[:32, :, 2] = q[:32, ::2] * 8                # own scores of about 90 for half of the heads
     check_decode(q, k, v, [6] * 32 + [0] * 32, pk, pv)
     k[:, :, 2] = (q[:, ::2] + q[:, 1::2]) * 8     # and for all rows of all sequences
@@ -278,7 +289,7 @@ def test_decode_shared_keys_beyond_the_support():
 
 
 def test_decode_wait_timeout_is_reported_and_the_context_survives():
-    q, k, v, pk, pv = inputs(40, 4, 2, 16, 300, 64, torch.bfloat16, seed=26)
+    q, k, v, pk, pv = inputs(40, 4, 2, 16, 6000, 64, torch.bfloat16, seed=26)
     args = [t.cuda() for t in (q, k, v)] + [torch.full((40,), 16, dtype=torch.int32, device="cuda")]
     how = dict(prefix_k=pk.cuda(), prefix_v=pv.cuda())
     assert ra.device_status() == "RA_OK"
