@@ -451,8 +451,8 @@ ra_status_t ra_attention_decode(const void* q, const void* k, const void* v, con
  *   index         [B, H_KV, keep] int32 (written): the kept slots, ascending, then -1.
  *   keep, recent  1 <= keep <= C_out, 0 <= recent <= keep.
  * Errors: RA_ERR_ARG for null, misaligned or equal in and out pointers and sizes outside the above,
- * B H_KV C or B H_KV C_out beyond int32, C or C_out beyond 2^31 - 16385; RA_ERR_UNSUPPORTED where D elements are no multiple of 16
- * bytes; RA_ERR_LAUNCH.
+ * B H_KV C or B H_KV C_out beyond int32, C or C_out beyond 2^31 - 16385; RA_ERR_UNSUPPORTED where D
+ * elements are no multiple of 16 bytes; RA_ERR_LAUNCH.
  */
 ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, const int32_t* length, void* k_out,
                            void* v_out, float* weight_out, int32_t* length_out, int32_t* index, int B, int H_KV,

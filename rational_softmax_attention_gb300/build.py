@@ -4,7 +4,8 @@ Each translation unit under csrc/ is compiled in parallel to an object file in
 _build/, then linked into rational_softmax_attention_gb300/libraattn.so.  The
 CUDA runtime is linked statically, so the library needs only the driver at run
 time.  csrc/calls.cpp becomes _calls.so beside it, the Python module that binds the
-serving calls; it is compiled against the installed torch and loaded into it.  `python -m rational_softmax_attention_gb300.build` runs it by hand.
+serving calls; it is compiled against the installed torch and loaded into it.
+`python -m rational_softmax_attention_gb300.build` runs it by hand.
 """
 from __future__ import annotations
 

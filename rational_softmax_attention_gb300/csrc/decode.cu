@@ -35,9 +35,9 @@
 // rows as M; the chunks of a row are permuted in shared memory so that the 16-byte fragment reads
 // below meet no bank conflict.  fp32: FFMA.
 //
-// Bound: HBM, K and V once, where there is much of them: B64 H32/8 D128 C8192 reads 2.1 GB in 391 us, 5.5
-// TB/s, B1 H32/8 C131072 0.54 GB in 112 us, 4.8 TB/s.  Latency below that: B1 H16 C512 takes 8.5 us in
-// a graph, three launches of a few dependent loads each.
+// Bound: HBM, K and V once, where there is much of them: B1 H32/8 D128 C131072 reads 537 MB in 92 us, 5.8
+// TB/s; B64 H32/8, 2000 keys each, 524 MB in 92 us.  Latency below that: B1 H16 C512 takes 8.6 us in a
+// graph, three launches of a few dependent loads each.
 #include <climits>
 
 #include "decode_split.cuh"
@@ -1073,8 +1073,9 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
 // up to 128 where a warp's equal run would be short.  `full`, the blocks of a run when the cache is
 // full, one to eight per warp, bounds the partial results that a stream has places for; with shorter
 // sequences runs are shorter (B64 H32/8 C4096 of 10 keys each: 39.9 us -> 11.8), but not beside the tensor
-// cores' part, which fewer warps disturb less (B32 H32/8 C1024 P2048: 39.2 us with the shortest, 36.0).  A short prefix counts for kShortPrefix blocks: what starting on its few
-// keys costs (with P1, eight parts of one block to a warp took 62 us, B64 H32/8).
+// cores' part, which fewer warps disturb less (B32 H32/8 C1024 P2048: 39.2 us with the shortest, 36.0).
+// A short prefix counts for kShortPrefix blocks: what starting on its few keys costs (with P1, eight
+// parts of one block to a warp took 62 us, B64 H32/8).
 constexpr int64_t kTcRows = 32;
 constexpr int kShortPrefix = 8;
 size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {

@@ -16,10 +16,11 @@ struct DecodeSplit {
   int per;     // blocks of a run
 };
 
-// own: blocks per stream of all sequences together (cum[B]); longest: the most of one.  A run is as short as the
-// grid allows, and long enough for the streams' partial results to find their places.  With a run per warp the runs are equal parts of
-// all blocks.  With one per CTA each stream is cut for itself, into runs of `per` blocks that are
-// few enough for one grid: no more than total / per and one for each of the (few) streams.
+// own: blocks per stream of all sequences together (cum[B]); longest: the most of one.  A run is as short
+// as the grid allows, and long enough for the streams' partial results to find their places.  With a
+// run per warp the runs are equal parts of all blocks.  With one per CTA each stream is cut for itself,
+// into runs of `per` blocks that are few enough for one grid: no more than total / per and one for each
+// of the (few) streams.
 __device__ __forceinline__ DecodeSplit decode_split(const DecodeArgs& a, int own, int longest) {
   DecodeSplit s;
   s.own0 = a.Hkv * a.pblocks * a.shared_rowblocks;   // 0 with tc
