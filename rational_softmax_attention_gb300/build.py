@@ -70,7 +70,7 @@ def _build_calls(force):
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = CALLS_PATH + ".tmp"
+    tmp = f"{CALLS_PATH[:-3]}.{os.getpid()}.so"     # builds may run at the same time
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
            *(x for d in include for x in ("-isystem", d)), CALLS_SRC, "-o", tmp, "-L", PKG_DIR, "-l:libraattn.so",
@@ -95,7 +95,7 @@ def _build_lib(force, verbose):
     os.makedirs(BUILD_DIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(_compile, srcs))
-    tmp = LIB_PATH + ".tmp"
+    tmp = f"{LIB_PATH}.{os.getpid()}.tmp"
     cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
