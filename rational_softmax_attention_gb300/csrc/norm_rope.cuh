@@ -31,7 +31,7 @@ namespace raattn {
 namespace norm_rope {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 16;   // tokens of a CTA's tile
+constexpr int kMaxTile = 32;   // tokens of a CTA's tile
 constexpr int kMaxPairs = 64;
 
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
@@ -290,10 +290,27 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Shares `most` CTAs among the kinds by their cost per head and per token, and sets the tiles' tokens: a tile for
-// every CTA first; then as many tokens as leave no lane group without a head, and more, since what
-// a token costs once is shared by the heads that one lane group walks, while each CTA still gets
-// four tiles.
+// The tokens of a tile for which the CTA with most tiles is done first: a tile takes its rows per lane group and
+// `start` more (the token's factors, the refilled ring).  rows(step): rows of a lane group that takes
+// every step-th head.  Forward, bf16 B4 N8192: 16 tokens, 7 tiles and 18 rows each for the longest CTA, 86 us
+// with H16/8 D128, against 94 with 8 tokens and 92 with 32; with H8/1, 32 tokens 39 us against 46 with 16.
+template <typename F>
+int best_tile(int64_t tokens, int groups, int64_t ctas, int start, F rows) {
+  int best = 1;
+  int64_t least = 0;
+  for (int t = 1; t <= groups && t <= kMaxTile; t *= 2) {
+    const int64_t tiles = (tokens + t - 1) / t;
+    if (t > 1 && 4 * tiles < 3 * ctas) break;   // loads in flight on every SM count for more
+    const int64_t time = (tiles + ctas - 1) / ctas * (rows(groups / t) + start);
+    if (t == 1 || 33 * time < 32 * least) {   // near ties to the smaller
+      least = time;
+      best = t;
+    }
+  }
+  return best;
+}
+
+// Shares `most` CTAs among the kinds by their cost per head and per token, and sets the tiles' tokens.
 inline void plan_work(NormRopeShape* a, int es, int most, const int (&head_cost)[3], const int (&token_cost)[3]) {
   const int groups = kThreads / (a->D * es / 32);
   const int64_t tokens = static_cast<int64_t>(a->B) * a->N;
@@ -303,8 +320,7 @@ inline void plan_work(NormRopeShape* a, int es, int most, const int (&head_cost)
   for (int k = 0; k < 3; ++k) {
     const int64_t share = most * cost[k] / all;
     const int64_t ctas = share < 1 ? 1 : share;
-    int t = 1;
-    while (2 * t <= groups && t < kMaxTile && tokens / (2 * t) >= (groups / t > heads[k] ? ctas : 4 * ctas)) t *= 2;
+    const int t = best_tile(tokens, groups, ctas, 1, [&](int step) { return (heads[k] + step - 1) / step; });
     const int64_t tiles = (tokens + t - 1) / t;
     a->tiles[k] = t;
     a->ctas[k] = static_cast<int>(tiles < ctas ? tiles : ctas);

@@ -1,5 +1,5 @@
 // The gradient of the per-head normalisation and rotation (the mathematics: norm_rope.cuh).
-// bf16 B4 N8192 H16 D128, layer norm with biases: 1.07 GB in 199 us, 5.4 TB/s; issue slots 52% busy.
+// bf16 B4 N8192 H16 D128, layer norm with biases: 1.07 GB in 203 us, 5.3 TB/s; issue slots 52% busy.
 #include "norm_rope.cuh"
 
 namespace raattn {
