@@ -129,6 +129,29 @@ def _require_cuda(*ts):
             raise ValueError("libraattn takes contiguous CUDA tensors (there is no CPU path)")
 
 
+def _require_attention(q, k, v, mask):
+    """The kernels take B, H and the dtype from q alone and read k, v and the mask by them."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3] or v.shape != k.shape:
+        raise ValueError("q must be [B, H, N_Q, D] and k and v both [B, H, N_K, D], with as many heads as q, not "
+                         f"{list(q.shape)}, {list(k.shape)} and {list(v.shape)}")
+    _require_like(q.dtype, q.device, k=k, v=v)
+    if mask is None:
+        return
+    mask_q, mask_k, MB, MH = mask
+    (B, H, n_q, _), n_k, words = q.shape, k.shape[2], lib().ra_attention_mask_words
+    if MB not in (1, B) or MH not in (1, H) or mask_q.shape != (MB * MH, n_q, words(n_k)) \
+            or mask_k.shape != (MB * MH, n_k, words(n_q)):
+        raise ValueError("mask must come from pack_attn_mask for these sizes")
+    _require_like(torch.int32, q.device, mask_q=mask_q, mask_k=mask_k)
+    _require_cuda(mask_q, mask_k)
+
+
+def _require_like(dtype, device, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != dtype or t.device != device:
+            raise ValueError(f"{name} must be {dtype} on {device}, not {t.dtype} on {t.device}")
+
+
 def ra_softmax(x):
     """ra_softmax along the last dimension of a float32 or bfloat16 CUDA tensor (same dtype out)."""
     _require_cuda(x)
@@ -194,6 +217,7 @@ def ra_attention_forward(q, k, v, *, scale=None, causal=False, out_dtype=None, w
     with_stats; counts is an int64 CUDA tensor [pairs visited, pairs skipped]
     when tile_counts, else None.
     """
+    _require_attention(q, k, v, mask)
     _require_cuda(q, k, v)
     B, H, NQ, D = q.shape
     NK = k.shape[2]
@@ -228,12 +252,25 @@ def ra_attention_backward(q, k, v, o, dout, row_m, row_s, row_arg, *, scale=None
                           grad_dtype=torch.float32, workspace=None, mask=None):
     """Gradients (dq, dk, dv) of sum(dout * O) for the forward that produced o and the row
     statistics; mask as given to that forward."""
-    _require_cuda(q, k, v, o, dout, row_m, row_s, row_arg)
+    _require_attention(q, k, v, mask)
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must be shaped like q")
+    if any(t.shape != q.shape[:3] for t in (row_m, row_s, row_arg)):
+        raise ValueError("row_m, row_s and row_arg must be [B, H, N_Q], as the forward gives them")
+    _require_like(q.dtype, q.device, dout=dout)
+    _require_like(o.dtype, q.device, o=o)
+    _require_like(torch.float32, q.device, row_m=row_m, row_s=row_s)
+    _require_like(torch.int32, q.device, row_arg=row_arg)
     B, H, NQ, D = q.shape
     NK = k.shape[2]
     L = lib()
+    nbytes = L.ra_attention_bwd_workspace_size(B, H, NQ, NK, D)
+    if workspace is not None:
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes")
+        _require_like(workspace.dtype, q.device, workspace=workspace)
+    _require_cuda(q, k, v, o, dout, row_m, row_s, row_arg, workspace)
     if workspace is None:
-        nbytes = L.ra_attention_bwd_workspace_size(B, H, NQ, NK, D)
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
     dq = torch.empty((B, H, NQ, D), dtype=grad_dtype, device=q.device)
     dk = torch.empty((B, H, NK, D), dtype=grad_dtype, device=q.device)
@@ -274,7 +311,8 @@ class _RaAttentionFn(torch.autograd.Function):
 
 
 def ra_attention(q, k, v, attn_mask=None, is_causal=False, scale=None):
-    """Rational-softmax attention, a drop-in for scaled_dot_product_attention (no dropout).
+    """Rational-softmax attention, a drop-in for scaled_dot_product_attention (no dropout): q [B, H, N_Q, D],
+    k and v [B, H, N_K, D] of one dtype, with as many key heads as query heads.
 
     attn_mask: optional boolean mask broadcastable to [B, H, N_Q, N_K], True where the query
     may attend to the key (bf16 inputs only); combined with is_causal."""

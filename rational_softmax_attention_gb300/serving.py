@@ -77,8 +77,9 @@ def _asks(t):
 
 def ra_qk_norm_rope(qkv, num_heads, num_kv_heads=None, *, norm="layer", q_weight=None, q_bias=None, k_weight=None,
                     k_bias=None, eps=1e-5, frequencies=None, sections=None, positions=None, interleaved=False):
-    """q [B, num_heads, N, D], k and v [B, num_kv_heads, N, D], ready for ra_attention, from the packed
-    projection qkv [B, N, (num_heads + 2 num_kv_heads) * D] (query heads, key heads, value heads).
+    """q [B, num_heads, N, D], k and v [B, num_kv_heads, N, D] from the packed projection
+    qkv [B, N, (num_heads + 2 num_kv_heads) * D] (query heads, key heads, value heads).  They are what
+    ra_attention takes where num_kv_heads is num_heads; it takes no fewer key heads than query heads.
 
     norm: 'layer' (weights, optional biases), 'rms' (weights) or 'none', over each head's D elements
     of q and k.  sections: pairs of dimensions per position axis (None: no rotation); frequencies:
