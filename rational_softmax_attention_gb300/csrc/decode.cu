@@ -1038,6 +1038,7 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
     if (e != cudaSuccess) return e;
   } else {
     decode_scores_kernel<T, D, TW><<<grid, kThreads, smem_scores, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;   // the next kernels read what this one leaves
   }
   if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
   e = launch_dependent(decode_values_kernel<T, D, TW>, grid, kThreads, smem_values, st, a);
