@@ -372,8 +372,8 @@ typedef enum { RA_NORM_NONE = 0, RA_NORM_LAYER = 1, RA_NORM_RMS = 2 } ra_norm_t;
  *                 nothing else of the cache is touched, and start is not changed.
  *   dtype         RA_F32 or RA_BF16; arithmetic in fp32, each output rounded once.  v is copied.
  * Outputs must not overlap inputs.  Errors: RA_ERR_ARG for null or misaligned pointers, sizes
- * < 1, B N (H_Q + 2 H_KV) or B H_KV capacity beyond int32, weights that do not go with `norm`, a
- * bad enum, eps or section; RA_ERR_UNSUPPORTED for D outside {16, 32, 64, 128}, more than
+ * < 1, B N (H_Q + 2 H_KV) or B H_KV capacity beyond int32, a token of more than 2^31 - 32769
+ * elements, weights that do not go with `norm`, a bad enum, eps or section; RA_ERR_UNSUPPORTED for D outside {16, 32, 64, 128}, more than
  * four axes, or an R that is no multiple of 8 when not interleaved; RA_ERR_LAUNCH.
  */
 ra_status_t ra_qk_norm_rope_fwd(const void* qkv, int64_t batch_stride, int64_t token_stride, const void* q_weight,

@@ -18,6 +18,9 @@ bool rows_ok(int64_t a, int64_t b, int64_t c) { return a * b <= INT_MAX && a * b
 // Loops over a cache's slots step by up to 8192 in 32 bits.
 constexpr int kMostKeys = INT_MAX - 16384;
 
+// Offsets within a token are formed in 32 bits, up to 256 heads of 128 past its last one.
+constexpr int kMostTokenElements = INT_MAX - 256 * 128;
+
 ra_status_t norm_rope_shape(NormRopeShape* a, const void* qkv, int64_t batch_stride, int64_t token_stride,
                             const void* qw, const void* qb, const void* kw, const void* kb, ra_norm_t norm, float eps,
                             const double* freq, const int32_t* pos, int64_t pos_axis_stride, int64_t pos_batch_stride,
@@ -26,6 +29,7 @@ ra_status_t norm_rope_shape(NormRopeShape* a, const void* qkv, int64_t batch_str
   if (!qkv || !aligned(qkv, 16) || !dtype_ok(dtype)) return RA_ERR_ARG;
   if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || D < 1 || axes < 0 || (axes > 0 && !sections)) return RA_ERR_ARG;
   if (Hq > INT_MAX / 4 || Hkv > INT_MAX / 4 || !rows_ok(B, N, Hq + 2 * Hkv)) return RA_ERR_ARG;
+  if (static_cast<int64_t>(Hq + 2 * Hkv) * D > kMostTokenElements) return RA_ERR_ARG;
   if (norm != RA_NORM_NONE && norm != RA_NORM_LAYER && norm != RA_NORM_RMS) return RA_ERR_ARG;
   if (norm == RA_NORM_NONE ? (qw || qb || kw || kb) : (!qw || !kw)) return RA_ERR_ARG;
   if (norm == RA_NORM_RMS && (qb || kb)) return RA_ERR_ARG;

@@ -174,3 +174,11 @@ def test_native_binding_refuses_what_is_no_tensor_or_size(lib):
     calls = pytest.importorskip("rational_softmax_attention_gb300._calls")
     with pytest.raises(TypeError, match="arguments"):
         calls.attention_decode(x)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_norm_rope_refuses_a_token_beyond_32_bit_offsets(lib, bwd):
+    """The kernels form offsets within a token, head * D up to 256 heads past the last, in 32 bits."""
+    for Hq, Hkv, D in ((1 << 24, 1, 128), (1, 1 << 23, 128), (1 << 25, 1, 64), (((1 << 31) - 1) // 128 - 2, 1, 128)):
+        assert (Hq + 2 * Hkv + 256) * D >= 1 << 31
+        assert _norm_rope(lib, bwd, B=1, N=1, Hq=Hq, Hkv=Hkv, D=D, ts=0, bs=0) == ARG, (Hq, Hkv, D)
