@@ -248,10 +248,12 @@ __device__ __forceinline__ float row_dot(const float2 (&x0)[P], const float2 (&x
   s = __fadd2_rn(s, s2);
   return group_sum<L>(s.x + s.y);
 }
-// 1 / sqrt(mean square + eps); a row of zeros stays finite with eps = 0 too.
+// 1 / sqrt(mean square + eps); a row of zeros stays finite with eps = 0 too, and a NaN in the row (which a
+// maximum would drop) makes all of it NaN.
 __device__ __forceinline__ float inverse_rms(float mean_square, float eps) {
+  const float s = mean_square + eps;
   float r;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(mean_square + eps, 1e-37f)));   // 2 ulp
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s < 1e-37f ? 1e-37f : s));   // 2 ulp
   return r;
 }
 

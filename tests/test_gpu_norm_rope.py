@@ -253,6 +253,48 @@ def test_autograd_takes_any_view_once_and_in_a_graph():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("norm", ["layer", "rms"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_that_is_not_finite(value, norm, dtype):
+    """A NaN makes its whole row NaN, and an infinity what the definition gives for it (NaN where it stands and in its
+    partner; zeros, or with a mean NaN, elsewhere); the other rows do not change a bit.  The weights' gradients
+    are NaN in every column that the definition gives as NaN, and the others' rows of dqkv stay."""
+    B, N, Hq, Hkv, D = 2, 37, 3, 2, 64
+    qkv, params, how = make(B, N, Hq, Hkv, D, dtype, norm, False, (24,), False, 16)
+    d = [torch.randn(B, h, N, D, generator=torch.Generator().manual_seed(6)).to(dtype).cuda() for h in (Hq, Hkv, Hkv)]
+
+    def both():
+        args = cuda(params), cuda(how)
+        return ra.ra_qk_norm_rope(qkv.cuda(), Hq, Hkv, **args[0], **args[1]), \
+            ra.ra_qk_norm_rope_backward(qkv.cuda(), *d, Hq, Hkv, **args[0], **args[1])
+    clean, clean_b = both()
+    rows = qkv.view(B, N, Hq + 2 * Hkv, D)
+    rows[1, 5, 2, 11] = value              # query head 2 of a token
+    rows[0, 36, Hq, 63] = value            # key head 0 of another, in a dimension that is not turned
+    got, got_b = both()
+    oh = oracle_how(params, how)
+    with np.errstate(all="ignore"):
+        want = S.qk_norm_rope(f64(qkv), Hq, Hkv, **oh)
+        DX, DP = S.qk_norm_rope_bwd(f64(qkv), *(f64(t) for t in d), Hq, Hkv, **oh)
+    for g, c, w, at in ((got[0], clean[0], want[0], (1, 2, 5)), (got[1], clean[1], want[1], (0, 0, 36))):
+        row = f64(g)[at]
+        assert np.array_equal(np.isnan(row), np.isnan(w[at])) and np.isnan(row).any()
+        assert np.array_equal(row[~np.isnan(row)], np.zeros(np.count_nonzero(~np.isnan(row))))
+        if value != value:
+            assert np.isnan(row).all()
+        g[at] = c[at]
+        assert torch.equal(g, c)
+    assert torch.equal(got[2], clean[2])
+    dx, c = (t.view(B, N, -1, D).clone() for t in (got_b[0], clean_b[0]))
+    for at in ((1, 5, 2), (0, 36, Hq)):
+        assert np.array_equal(np.isnan(f64(dx)[at]), np.isnan(DX.reshape(B, N, -1, D)[at]))
+        dx[at] = c[at]
+    assert torch.equal(dx, c)
+    for i in (0, 2):                       # the weights; without biases there are no others
+        assert np.array_equal(np.isnan(f64(got_b[1 + i])), np.isnan(DP[i])) and np.isnan(DP[i]).any()
+
+
 def test_refusals():
     x = torch.zeros(1, 2, 3 * 64, device="cuda")
     w, f = torch.ones(64, device="cuda"), ra.ra_rope_frequencies((32,))
