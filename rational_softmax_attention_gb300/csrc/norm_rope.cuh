@@ -118,15 +118,15 @@ __device__ __forceinline__ void fill_table(Tables& tb, int buf, const NormRopeSh
   const int tokens = a.B * a.N;
   for (int tl = threadIdx.x >> lg; tl < tile; tl += kThreads >> lg) {
     const int tok = tok0 + tl;
+    float s = 0.0f, c = 1.0f;   // a token past the last: what its rows of zeros meet has to be finite
     if (tok < tokens) {
       const int b = tok / a.N, n = tok - b * a.N;
-      float s, c;
       const float f = turn_fraction(pos[b * a.pos_batch_stride + n], turns);
       if (FAST) __sincosf(6.28318531f * f, &s, &c);
       else sincospif(2.0f * f, &s, &c);
-      tb.cs[buf][tl][p] = c;
-      tb.sn[buf][tl][p] = s;
     }
+    tb.cs[buf][tl][p] = c;
+    tb.sn[buf][tl][p] = s;
   }
 }
 

@@ -295,6 +295,31 @@ def test_a_row_that_is_not_finite(value, norm, dtype):
         assert np.array_equal(np.isnan(f64(got_b[1 + i])), np.isnan(DP[i])) and np.isnan(DP[i]).any()
 
 
+def _fill_shared_memory_with_nan():
+    """Leaves NaN in the SMs' shared memory: a decode whose keys are all NaN stages them there on every SM."""
+    q = torch.full((64, 8, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    k = torch.full((64, 8, 600, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ra.ra_attention_decode(q, k, k, torch.full((64,), 600, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,N", [(torch.bfloat16, 333), (torch.bfloat16, 1217), (torch.float32, 333)])
+def test_parameter_gradients_of_a_ragged_last_tile(dtype, N):
+    """The last tile of tokens has places without a token (one head of 128: tiles of 4 and more), whose sines and
+    cosines nobody forms: whatever shared memory held before, they add nothing to the weights' gradients."""
+    qkv, params, how = make(1, N, 1, 1, 128, dtype, "rms", False, (64,), False, 17)
+    params, how, x = cuda(params), cuda(how), qkv.cuda()
+    d = [torch.randn(1, 1, N, 128, device="cuda").to(dtype) for _ in range(3)]
+    oh = oracle_how({n: None if t is None else t.cpu() for n, t in params.items()},
+                    dict(how, positions=how["positions"].cpu()))
+    _, DP = S.qk_norm_rope_bwd(f64(qkv), *(f64(t) for t in d), 1, 1, **oh)
+    for _ in range(3):
+        _fill_shared_memory_with_nan()
+        got = ra.ra_qk_norm_rope_backward(x, *d, 1, 1, **params, **how)
+        for i in (0, 2):
+            size = N * 1.5 * d[i // 2].abs().float().mean().item() * 2.0
+            assert np.abs(f64(got[1 + i]) - DP[i]).max() <= (16 + np.log2(N)) * 4 * U32 * size
+
+
 def test_refusals():
     x = torch.zeros(1, 2, 3 * 64, device="cuda")
     w, f = torch.ones(64, device="cuda"), ra.ra_rope_frequencies((32,))
