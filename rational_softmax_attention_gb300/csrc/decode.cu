@@ -637,7 +637,7 @@ __device__ __forceinline__ void bf16_values(const Part& p, const DecodeArgs& a, 
     const uint32_t stage = ring + i % C::kStages * C::kStageV;
     const float* sc = reinterpret_cast<const float*>(ring_ptr + i % C::kStages * C::kStageV + C::kBlockBytes);
     uint32_t w[4] = {0u, 0u, 0u, 0u}, rest[4] = {0u, 0u, 0u, 0u};
-    float live = 0.0f;
+    bool live = false;   // some weight that is not 0 (a NaN is not)
     const int at = 2 * t, flip = (g & 2) << 2;   // piece_of: pieces 2 e + t / 2, flipped by two in rows 2, 3, 6, 7
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -647,18 +647,18 @@ __device__ __forceinline__ void bf16_values(const Part& p, const DecodeArgs& a, 
         const float2 x = *reinterpret_cast<const float2*>(sc + g * C::kScoreStride + at + ((e * 8) ^ flip));
         const float f0 = phi_fast((m0 - x.x) * a.scale), f1 = phi_fast((m0 - x.y) * a.scale);
         t0 += f0 + f1;
-        live += f0 + f1;
+        live |= f0 + f1 != 0.0f;
         split_bf16x2(f0, f1, w[2 * e], rest[2 * e]);
       }
       if (w1) {
         const float2 x = *reinterpret_cast<const float2*>(sc + (g + 8) * C::kScoreStride + at + ((e * 8) ^ flip));
         const float f0 = phi_fast((m1 - x.x) * a.scale), f1 = phi_fast((m1 - x.y) * a.scale);
         t1 += f0 + f1;
-        live += f0 + f1;
+        live |= f0 + f1 != 0.0f;
         split_bf16x2(f0, f1, w[2 * e + 1], rest[2 * e + 1]);
       }
     }
-    if (!__any_sync(0xffffffffu, live > 0.0f)) continue;   // every weight is exactly 0
+    if (!__any_sync(0xffffffffu, live)) continue;   // every weight is exactly 0
     if constexpr (!TWO) {
       w[1] = rest[0];
       w[3] = rest[2];

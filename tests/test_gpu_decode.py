@@ -253,6 +253,25 @@ def test_decode_nan_stays_in_its_rows(dtype):
     assert torch.isnan(got[bad.cuda()]).all() and torch.equal(got[~bad.cuda()], want[~bad.cuda()])
 
 
+@pytest.mark.parametrize("bad,good", [(0, 8), (8, 0), (3, 11)])
+def test_decode_nan_in_one_head_does_not_drop_anothers_values(bad, good):
+    """Two heads that the same lanes hold, one NaN; the other alone has weight in a block of keys."""
+    H, C, D = 16, 100, 64
+    q, k = torch.zeros(1, H, D), torch.zeros(1, 1, C, D)
+    q[:, :, 0] = 32.0
+    q[0, good, 0], q[0, good, 1] = 0.0, 32.0
+    k[0, 0, 3, 0] = k[0, 0, 85, 1] = 8.0        # scores of 32 against 0: key 3 for all heads, key 85 for `good`
+    q[0, bad] = float("nan")
+    v = torch.randn(1, 1, C, D, generator=torch.Generator().manual_seed(31)).bfloat16()
+    o = ra.ra_attention_decode(q.bfloat16().cuda(), k.bfloat16().cuda(), v.cuda(),
+                               torch.full((1,), C, dtype=torch.int32, device="cuda")).cpu()
+    want = v[0, :, 3].expand(H, D).clone()
+    want[good] = v[0, 0, 85]
+    assert torch.isnan(o[0, bad]).all()
+    keep = [h for h in range(H) if h != bad]
+    assert torch.equal(o[0, keep], want[keep])
+
+
 def test_a_cache_beyond_32_bit_offsets():
     """More than 2^31 elements before the second sequence, and 2^31 scores: append, decode and evict
     find the entries at the far ends.  One key lies so far above the others that it decides alone."""
