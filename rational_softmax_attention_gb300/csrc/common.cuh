@@ -451,11 +451,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // A pair of weights as two bf16 each, which lose 2^-15 of it at most: its upper 16 bits, and what those
-// leave, rounded.
+// leave, rounded.  The last bit is set for that (2^-23 at most): a positive weight leaves something above 0, and
+// an infinite value times the second half is an infinity too, not NaN.  A weight of 0 is 0 twice.
 __device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
   hi = __byte_perm(a, b, 0x7632);
-  lo = pack_bf16x2(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+  lo = pack_bf16x2(__uint_as_float(a | 1u) - __uint_as_float(a & 0xffff0000u),
+                   __uint_as_float(b | 1u) - __uint_as_float(b & 0xffff0000u));
 }
 
 // Two floats to fp16x2 (lo in the low half), round to nearest, saturating at +-65504.

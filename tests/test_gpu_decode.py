@@ -272,6 +272,31 @@ def test_decode_nan_in_one_head_does_not_drop_anothers_values(bad, good):
     assert torch.equal(o[0, keep], want[keep])
 
 
+# own keys of up to 8 rows and of more, a short prefix, the tensor cores with one row tile and with several
+@pytest.mark.parametrize("case", [(2, 4, 2, 50, 0, 64), (2, 16, 1, 50, 0, 128), (3, 4, 2, 20, 40, 64),
+                                  (40, 2, 1, 20, 21000, 64), (70, 8, 2, 20, 1700, 128)], ids=str)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decode_infinite_values(case, dtype):
+    """Every key has weight, those of the maxima exactly 1: an infinite value of any key makes its dimension
+    infinite in every row that reads it, with its sign, and nothing else changes."""
+    B, Hq, Hkv, C, P, D = case
+    q, k, v, pk, pv = inputs(B, Hq, Hkv, C, P, D, dtype, seed=33, sigma=0.5)
+    n = torch.full((B,), C, dtype=torch.int32, device="cuda")
+
+    def call():
+        how = {} if pk is None else dict(prefix_k=pk.cuda(), prefix_v=pv.cuda())
+        return ra.ra_attention_decode(q.cuda(), k.cuda(), v.cuda(), n, **how)
+    want = call()
+    best = (k[0, 0].double() @ q[0, 0].double()).argmax()          # of the first row, among its own keys
+    v[:, :, best, 5], v[:, :, 7, 6] = float("inf"), float("-inf")
+    want[..., 5], want[..., 6] = float("inf"), float("-inf")
+    if P:
+        rest = (pk[0].double() @ q[0, 0].double()).argmax()
+        pv[:, rest, 9] = float("inf")
+        want[..., 9] = float("inf")
+    assert torch.equal(call(), want)
+
+
 def test_a_cache_beyond_32_bit_offsets():
     """More than 2^31 elements before the second sequence, and 2^31 scores: append, decode and evict
     find the entries at the far ends.  One key lies so far above the others that it decides alone."""
