@@ -108,6 +108,13 @@ PyObject* tuple(std::initializer_list<Tensor> ts) {
 // ---- norm and rotation --------------------------------------------------------------------------
 constexpr int kLead = 13;   // arguments that the forward, the append and the backward share
 
+// The kernels read a tensor's values alone, so a tangent that it carries would be lost without a word.
+void refuse_tangents(PyObject* const* a, std::initializer_list<int> which) {
+  for (const int i : which)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i])._fw_grad(0).defined())
+      throw Refusal{PyExc_NotImplementedError, "forward-mode derivatives of ra_qk_norm_rope are not supported"};
+}
+
 struct NormRope {
   Tensor qkv, positions;
   const Tensor *qw, *qb, *kw, *kb, *frequencies;
@@ -237,6 +244,7 @@ struct NormRope {
 };
 
 PyObject* norm_rope(PyObject* const* a) {
+  refuse_tangents(a, {0, 4, 5, 6, 7});   // qkv, the weights and biases
   const NormRope s(a);
   const Tensor q = make({s.B, s.Hq, s.N, s.D}, s.dtype, s.device), k = make({s.B, s.Hkv, s.N, s.D}, s.dtype, s.device),
                v = make({s.B, s.Hkv, s.N, s.D}, s.dtype, s.device);
@@ -246,6 +254,7 @@ PyObject* norm_rope(PyObject* const* a) {
 
 // .., dq, dk, dv
 PyObject* norm_rope_backward(PyObject* const* a) {
+  refuse_tangents(a, {0, 4, 5, 6, 7, kLead, kLead + 1, kLead + 2});
   const NormRope s(a);
   const Tensor &dq = tensor(a[kLead], "dq"), &dk = tensor(a[kLead + 1], "dk"), &dv = tensor(a[kLead + 2], "dv");
   check("dq", dq, {s.B, s.Hq, s.N, s.D}, s.dtype, s.device);

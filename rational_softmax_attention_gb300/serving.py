@@ -85,7 +85,7 @@ def ra_qk_norm_rope(qkv, num_heads, num_kv_heads=None, *, norm="layer", q_weight
     of q and k.  sections: pairs of dimensions per position axis (None: no rotation); frequencies:
     float64 [sum(sections)], see ra_rope_frequencies; positions: integer [N], [B, N] or
     [axes, B, N].  Pair i is dimensions (i, i + R) of the first 2 R, or (2 i, 2 i + 1) when
-    interleaved.  Differentiable (once) in qkv, weights and biases; as with any torch operator, a backward
+    interleaved.  Differentiable (once, in reverse mode) in qkv, weights and biases; as with any torch operator, a backward
     pass is captured into a CUDA graph only while no eager graph of the same leaves is alive."""
     if torch.is_grad_enabled() and (qkv.requires_grad or _asks(q_weight) or _asks(k_weight) or _asks(q_bias)
                                     or _asks(k_bias)):

@@ -320,6 +320,14 @@ def test_parameter_gradients_of_a_ragged_last_tile(dtype, N):
             assert np.abs(f64(got[1 + i]) - DP[i]).max() <= (16 + np.log2(N)) * 4 * U32 * size
 
 
+def test_a_tangent_is_refused_with_and_without_an_input_that_asks_for_a_gradient():
+    from torch.autograd import forward_ad
+    x, w = torch.randn(1, 2, 3 * 64, device="cuda"), torch.ones(64, device="cuda")
+    for weight in (w, w.clone().requires_grad_(True)):
+        with forward_ad.dual_level(), pytest.raises(NotImplementedError):   # the second: torch's own refusal
+            ra.ra_qk_norm_rope(forward_ad.make_dual(x, torch.ones_like(x)), 1, 1, norm="rms", q_weight=weight, k_weight=w)
+
+
 def test_refusals():
     x = torch.zeros(1, 2, 3 * 64, device="cuda")
     w, f = torch.ones(64, device="cuda"), ra.ra_rope_frequencies((32,))

@@ -182,3 +182,22 @@ def test_norm_rope_refuses_a_token_beyond_32_bit_offsets(lib, bwd):
     for Hq, Hkv, D in ((1 << 24, 1, 128), (1, 1 << 23, 128), (1 << 25, 1, 64), (((1 << 31) - 1) // 128 - 2, 1, 128)):
         assert (Hq + 2 * Hkv + 256) * D >= 1 << 31
         assert _norm_rope(lib, bwd, B=1, N=1, Hq=Hq, Hkv=Hkv, D=D, ts=0, bs=0) == ARG, (Hq, Hkv, D)
+
+
+@pytest.mark.parametrize("which", ["qkv", "q_weight", "k_bias", "dk"])
+def test_forward_mode_derivatives_are_refused(lib, which):
+    """A tensor with a tangent has requires_grad False; its tangent would be dropped silently.  The refusal comes
+    before the one of CPU tensors."""
+    from torch.autograd import forward_ad
+    x, w, d = torch.zeros(2, 4, 192), torch.ones(64), torch.zeros(2, 1, 4, 64)
+    with forward_ad.dual_level():
+        t = {"qkv": x, "q_weight": w, "k_bias": w, "dk": d}
+        t[which] = forward_ad.make_dual(t[which], torch.ones_like(t[which]))
+        how = dict(q_weight=t["q_weight"], k_weight=w, q_bias=w, k_bias=t["k_bias"])
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            if which == "dk":
+                ra.ra_qk_norm_rope_backward(t["qkv"], d, t["dk"], d, 1, 1, **how)
+            else:
+                ra.ra_qk_norm_rope(t["qkv"], 1, 1, **how)
+    with pytest.raises(ValueError, match="CUDA"):
+        ra.ra_qk_norm_rope(x, 1, 1, **dict(how, q_weight=w, k_bias=w))
