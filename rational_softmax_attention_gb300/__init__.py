@@ -371,7 +371,8 @@ class RaAttention(torch.nn.Module):
         if self.rope_sections:
             device = self.proj.weight.device
             if device not in self._frequencies:
-                self._frequencies[device] = ra_rope_frequencies(self.rope_sections, self.rope_theta, device=device)
+                with torch.inference_mode(False):   # a later training step saves them for its backward
+                    self._frequencies[device] = ra_rope_frequencies(self.rope_sections, self.rope_theta, device=device)
             how.update(frequencies=self._frequencies[device], sections=self.rope_sections, positions=positions,
                        interleaved=self.rope_interleaved)
         return how

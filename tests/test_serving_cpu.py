@@ -201,3 +201,12 @@ def test_forward_mode_derivatives_are_refused(lib, which):
                 ra.ra_qk_norm_rope(t["qkv"], 1, 1, **how)
     with pytest.raises(ValueError, match="CUDA"):
         ra.ra_qk_norm_rope(x, 1, 1, **dict(how, q_weight=w, k_bias=w))
+
+
+def test_a_module_first_called_in_inference_mode_can_be_trained():
+    """Its frequencies are made on the first call and saved for the backward of later ones, which torch allows
+    only of tensors made outside inference mode."""
+    m = ra.RaAttention(64, num_heads=2, rope_sections=(16,))
+    with torch.inference_mode():
+        how = m._how(torch.arange(3, dtype=torch.int32))
+    assert not how["frequencies"].is_inference() and m._how(None)["frequencies"] is how["frequencies"]
