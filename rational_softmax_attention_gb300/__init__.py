@@ -357,6 +357,12 @@ class RaAttention(torch.nn.Module):
         self.rope_sections = tuple(int(s) for s in rope_sections) if rope_sections else None
         if self.rope_sections and (min(self.rope_sections) < 1 or 2 * sum(self.rope_sections) > self.head_dim):
             raise ValueError("rope_sections must be positive pair counts with 2 * sum(rope_sections) <= dim / num_heads")
+        if self.rope_sections and not rope_interleaved and sum(self.rope_sections) % 8:
+            raise ValueError("rope_sections must sum to a multiple of 8 pairs unless rope_interleaved")
+        if self.rope_sections and self.head_dim not in (16, 32, 64, 128):
+            raise ValueError("rope_sections need a head dimension (dim / num_heads) of 16, 32, 64 or 128")
+        if self.rope_sections and len(self.rope_sections) > 4:
+            raise ValueError("rope_sections are at most four, one per position axis")
         self.rope_theta = float(rope_theta)
         self.rope_interleaved = bool(rope_interleaved)
         # float64 whatever the module's dtype becomes, so not a buffer; made on a device's first call

@@ -210,3 +210,14 @@ def test_a_module_first_called_in_inference_mode_can_be_trained():
     with torch.inference_mode():
         how = m._how(torch.arange(3, dtype=torch.int32))
     assert not how["frequencies"].is_inference() and m._how(None)["frequencies"] is how["frequencies"]
+
+
+def test_module_refuses_rotations_that_no_call_takes():
+    """What the kernels do not take is refused when the module is made, not at its first forward."""
+    for dim, heads, how in ((64, 2, dict(rope_sections=(4,))), (64, 2, dict(rope_sections=(8, 3))),
+                            (96, 2, dict(rope_sections=(8,))), (512, 2, dict(rope_sections=(64,))),
+                            (64, 2, dict(rope_sections=(2, 2, 2, 1, 1)))):
+        with pytest.raises(ValueError, match="rope_sections"):
+            ra.RaAttention(dim, num_heads=heads, **how)
+    ra.RaAttention(64, num_heads=2, rope_sections=(3, 2), rope_interleaved=True)
+    ra.RaAttention(64, num_heads=2, rope_sections=(3, 5))
