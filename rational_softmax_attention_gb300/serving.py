@@ -189,15 +189,26 @@ class RaCache:
         step = tokens if count is None else count.clamp(0, tokens)
         self.length.add_(step)
         self.position.add_(step)
-        self.bound += tokens
+        self.bound = min(self.bound + tokens, self.capacity)   # require_room has seen to it that there is room
 
-    def require_room(self, tokens):
-        if self.bound + tokens > self.capacity:
+    def require_room(self, tokens, count=None):
+        """Raises unless every sequence has room for `tokens` more entries, or count[b] of them.  `bound` counts a
+        padded batch's padding too: where it leaves no room, the lengths are read back, which waits for the
+        device (not while a graph is captured)."""
+        if self.bound + tokens <= self.capacity:
+            return
+        room = False
+        if not (self.length.is_cuda and torch.cuda.is_current_stream_capturing()):
+            held = self.length.clamp(0, self.capacity)
+            after = held + (tokens if count is None else count.clamp(0, tokens))
+            self.bound, most = (int(n.max()) for n in (held, after))
+            room = most <= self.capacity
+        if not room:
             raise ValueError(f"the cache holds up to {self.bound} of {self.capacity} entries: no room for {tokens} more")
 
     def append(self, qkv, num_heads, *, count=None, **how):
         """ra_cache_append at this cache's lengths, which advance; returns q."""
-        self.require_room(qkv.shape[1])
+        self.require_room(qkv.shape[1], count)
         q = ra_cache_append(qkv, self.k, self.v, self.length, num_heads, self.k.shape[1], count=count, **how)
         self.advance(qkv.shape[1], count)
         return q

@@ -535,6 +535,23 @@ def test_ragged_prompts_and_eviction_in_a_generation():
     assert again[0].shape == cache.k.shape and cache.length.tolist() == [16, 16]
 
 
+def test_ragged_appends_until_the_cache_is_full():
+    """Padded appends go on while every sequence has room, whatever the padding adds up to; their entries stand
+    one after the other."""
+    cache = ra.RaCache(2, 1, 16, 64, dtype=torch.float32)
+    want = [[], []]
+    for i, count in enumerate(([4, 1], [0, 3], [4, 4], [4, 0], [4, 4], [0, 4])):
+        qkv = torch.randn(2, 4, 3 * 64, device="cuda")
+        cache.append(qkv, 1, count=torch.tensor(count, dtype=torch.int32, device="cuda"), norm="none")
+        for b in range(2):
+            want[b].append(qkv[b, :count[b], 64:128])
+    assert cache.length.tolist() == [16, 16]
+    for b in range(2):
+        assert torch.equal(cache.k[b, 0], torch.cat(want[b]))
+    with pytest.raises(ValueError, match="no room"):
+        cache.append(qkv, 1, count=torch.tensor([1, 0], dtype=torch.int32, device="cuda"), norm="none")
+
+
 def test_decode_step_in_a_graph():
     """The module's single-token step captured once and replayed: lengths and positions advance on the device."""
     m = module(rope_sections=(64,))

@@ -221,3 +221,20 @@ def test_module_refuses_rotations_that_no_call_takes():
             ra.RaAttention(dim, num_heads=heads, **how)
     ra.RaAttention(64, num_heads=2, rope_sections=(3, 2), rope_interleaved=True)
     ra.RaAttention(64, num_heads=2, rope_sections=(3, 5))
+
+
+def test_padding_does_not_fill_a_cache():
+    """A ragged batch's padded tokens are not entries: what counts is whether each sequence has room."""
+    c = ra.RaCache(2, 1, 8, 64, device="cpu")
+    for _ in range(3):                       # 4 padded tokens a time, 2 and 1 of them real
+        n = torch.tensor([2, 1], dtype=torch.int32)
+        c.require_room(4, n)
+        c.advance(4, n)
+    assert c.length.tolist() == [6, 3] and c.bound <= 8
+    c.require_room(2)
+    assert c.bound == 6
+    c.require_room(4, torch.tensor([2, 4], dtype=torch.int32))
+    for tokens, n in ((3, None), (4, [3, 0]), (9, [0, 6])):
+        with pytest.raises(ValueError, match="no room"):
+            c.require_room(tokens, None if n is None else torch.tensor(n, dtype=torch.int32))
+    assert c.bound == 6
