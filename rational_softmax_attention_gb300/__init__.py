@@ -368,12 +368,15 @@ class RaAttention(torch.nn.Module):
         # float64 whatever the module's dtype becomes, so not a buffer; made on a device's first call
         self._frequencies = {}
 
-    def _how(self, positions):
-        """ra_qk_norm_rope's keyword arguments for this module."""
+    def _how(self, positions, dtype=None):
+        """ra_qk_norm_rope's keyword arguments for this module and a projection of this dtype."""
         how = {"norm": "none"}
         if self.q_norm is not None:
-            how = {"norm": "layer", "q_weight": self.q_norm.weight, "q_bias": self.q_norm.bias,
-                   "k_weight": self.k_norm.weight, "k_bias": self.k_norm.bias, "eps": self.q_norm.eps}
+            how = {"q_weight": self.q_norm.weight, "q_bias": self.q_norm.bias, "k_weight": self.k_norm.weight,
+                   "k_bias": self.k_norm.bias}
+            # under autocast the projection has another type than the parameters; the kernels take one
+            how = {n: t if dtype is None else t.to(dtype) for n, t in how.items()}
+            how.update(norm="layer", eps=self.q_norm.eps)
         if self.rope_sections:
             device = self.proj.weight.device
             if device not in self._frequencies:
@@ -393,20 +396,21 @@ class RaAttention(torch.nn.Module):
         if self.rope_sections:
             if positions is None:
                 positions = torch.arange(N, device=x.device, dtype=torch.int32)
-            q, k, v = ra_qk_norm_rope(self.qkv(x), self.num_heads, **self._how(positions))
+            qkv = self.qkv(x)
+            q, k, v = ra_qk_norm_rope(qkv, self.num_heads, **self._how(positions, qkv.dtype))
             return self._merge(ra_attention(q, k, v, is_causal=self.causal))
         if positions is not None:
             raise ValueError("positions need rope_sections")
         q, k, v = self.qkv(x).reshape(B, N, 3, self.num_heads, self.head_dim).permute(2, 0, 3, 1, 4).unbind(0)
         if self.q_norm is not None:
-            q, k = self.q_norm(q), self.k_norm(k)
+            q, k = self.q_norm(q).to(v.dtype), self.k_norm(k).to(v.dtype)   # autocast's norms return fp32
         o = ra_attention(q, k, v, is_causal=self.causal)
         return self.proj(o.transpose(1, 2).reshape(B, N, C))
 
-    def new_cache(self, batch, capacity, *, prefix=None, track_weight=False):
-        """An empty RaCache for this module."""
+    def new_cache(self, batch, capacity, *, prefix=None, track_weight=False, dtype=None):
+        """An empty RaCache for this module, of its dtype or (under autocast, the projection's) the one given."""
         return RaCache(batch, self.num_heads, capacity, self.head_dim, prefix=prefix, track_weight=track_weight,
-                       device=self.proj.weight.device, dtype=self.proj.weight.dtype)
+                       device=self.proj.weight.device, dtype=dtype or self.proj.weight.dtype)
 
     @torch.no_grad()
     def prefill(self, x, cache, positions=None, count=None):
@@ -418,15 +422,18 @@ class RaAttention(torch.nn.Module):
         if cache.bound:
             raise ValueError("prefill needs an empty cache")
         B, N, _ = x.shape
-        if cache.k.shape[:2] != (B, self.num_heads) or cache.k.shape[3] != self.head_dim or cache.k.dtype != x.dtype:
-            raise ValueError("the cache must have the batch size, heads, head dimension and dtype of x in this module")
+        if cache.k.shape[:2] != (B, self.num_heads) or cache.k.shape[3] != self.head_dim:
+            raise ValueError("the cache must have the batch size, heads and head dimension of x in this module")
         cache.require_room(N)
+        qkv = self.qkv(x)
+        if cache.k.dtype != qkv.dtype:
+            raise ValueError(f"the cache must have the projection's dtype, {qkv.dtype}")
         P = cache.prefix_length
-        if P and x.dtype != torch.bfloat16:
+        if P and qkv.dtype != torch.bfloat16:
             raise NotImplementedError("prefill behind a prefix takes bf16 modules only")
         if self.rope_sections and positions is None:
             positions = torch.arange(P, P + N, device=x.device, dtype=torch.int32)
-        q, k, v = ra_qk_norm_rope(self.qkv(x), self.num_heads, **self._how(positions))
+        q, k, v = ra_qk_norm_rope(qkv, self.num_heads, **self._how(positions, qkv.dtype))
         cache.k[:, :, :N].copy_(k)
         cache.v[:, :, :N].copy_(v)
         cache.advance(N, count)
@@ -447,7 +454,8 @@ class RaAttention(torch.nn.Module):
             raise ValueError("decode takes one token per sequence: x [B, 1, dim]")
         if self.rope_sections and positions is None:
             positions = cache.position.view(1, -1, 1)
-        q = cache.append(self.qkv(x), self.num_heads, **self._how(positions))
+        qkv = self.qkv(x)
+        q = cache.append(qkv, self.num_heads, **self._how(positions, qkv.dtype))
         return self._merge(cache.attend(q[:, :, 0]).unsqueeze(2))
 
 

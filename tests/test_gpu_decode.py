@@ -579,6 +579,30 @@ def test_decode_step_in_a_graph():
     assert torch.equal(eager.weight, captured.weight) and captured.length.tolist() == [20, 20]
 
 
+@pytest.mark.parametrize("how", [dict(rope_sections=(64,)), {}], ids=str)
+def test_module_under_autocast(how):
+    """fp32 parameters under bf16 autocast: the forward, its gradients, a prompt and single tokens are those of the bf16
+    module (parameters that bf16 holds: the same products, and norms of the same rows, whose results may
+    differ by a rounding, as in the runs above)."""
+    m = module(dtype=torch.bfloat16, **how)
+    wide = module(dtype=torch.float32, **how)
+    wide.load_state_dict({n: t.float() for n, t in m.state_dict().items()})
+    x = torch.randn(2, 24, 256, device="cuda").bfloat16()
+    want, got = m(x), None
+    want.float().sum().backward()
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        got = wide(x.float())
+        assert got.dtype == torch.bfloat16 and (got.float() - want.float()).abs().max() <= 6e-2
+        cache = wide.new_cache(2, 24, dtype=torch.bfloat16)
+        y = [wide.prefill(x[:, :20].float(), cache)] + [wide.decode(x[:, i:i + 1].float(), cache) for i in range(20, 24)]
+        assert (torch.cat(y, 1).float() - want.float()).abs().max() <= 6e-2
+        with pytest.raises(ValueError, match="dtype"):
+            wide.prefill(x.float(), wide.new_cache(2, 24))
+    got.float().sum().backward()
+    for (n, a), (_, b) in zip(m.named_parameters(), wide.named_parameters()):
+        assert b.grad.dtype == torch.float32 and torch.isfinite(b.grad).all(), n
+
+
 def test_module_gradients_with_rotation():
     """fp32 gradients of a rotated, normalised module against differences of its own forward in 64-bit sums."""
     m = module(dim=64, heads=2, dtype=torch.float32, rope_sections=(8, 8))
