@@ -116,6 +116,16 @@ def test_forward_and_backward_match_the_oracle(case, dtype):
         assert err <= (16 + np.log2(rows)) * 4 * U32 * size, (name, err)
 
 
+# Long batches, whose CTAs take three tiles of tokens and more, so that both halves of the table of cosines and sines
+# are written again, and whose last tile is ragged: forward tiles of 32 (bf16, one head), 16 and 8 tokens.
+@pytest.mark.parametrize("case,dtype", [((1, 30011, 1, 1, 128, "layer", True, (64,), False), torch.bfloat16),
+                                        ((1, 9999, 5, 5, 32, "rms", False, (9, 5), True), torch.bfloat16),
+                                        ((1, 5003, 4, 2, 128, "layer", True, (32, 16), False), torch.float32),
+                                        ((3, 9001, 8, 1, 64, "none", False, (16,), False), torch.bfloat16)], ids=str)
+def test_many_tiles_of_tokens_match_the_oracle(case, dtype):
+    test_forward_and_backward_match_the_oracle(case, dtype)
+
+
 @pytest.mark.parametrize("start", [(1 << 24) + 1, (1 << 31) - 6000, -(1 << 31)])
 def test_far_positions_keep_their_angles(start):
     """Angles of positions that fp32 cannot hold, against 64 bits; positions shared by axes and batch."""
