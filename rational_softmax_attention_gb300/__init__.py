@@ -131,7 +131,8 @@ def _require_cuda(*ts):
 
 def _require_attention(q, k, v, mask):
     """The kernels take B, H and the dtype from q alone and read k, v and the mask by them."""
-    if q.dim() != 4 or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3] or v.shape != k.shape:
+    s, t = q.shape, k.shape
+    if len(s) != 4 or len(t) != 4 or t[0] != s[0] or t[1] != s[1] or t[3] != s[3] or v.shape != t:
         raise ValueError("q must be [B, H, N_Q, D] and k and v both [B, H, N_K, D], with as many heads as q, not "
                          f"{list(q.shape)}, {list(k.shape)} and {list(v.shape)}")
     _require_like(q.dtype, q.device, k=k, v=v)
