@@ -364,7 +364,7 @@ typedef enum { RA_NORM_NONE = 0, RA_NORM_LAYER = 1, RA_NORM_RMS = 2 } ra_norm_t;
  *   frequencies   [R] doubles in device memory, radians per position.
  *   positions     int32: token n of sequence b has position
  *                 positions[axis * pos_axis_stride + b * pos_batch_stride + n] on an axis (a
- *                 stride of 0 shares them).  Any int32; angles keep fp32 accuracy at all of them.
+ *                 stride of 0 shares them).  Any int32: angles are as exact at far positions as at near ones.
  *   q             [B, H_Q, N, D] (written).
  *   k, v          start NULL (then count NULL, capacity 0): [B, H_KV, N, D] (written).
  *                 Otherwise a cache [B, H_KV, capacity, D]: token n of sequence b goes to slot

@@ -78,52 +78,60 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// position * turns as a fraction of a turn in about [-0.5, 0.5]: the position is split into two
-// parts that fp32 holds exactly, each product into its rounded value (whose whole turns leave
-// exactly) and its rounding error, so far positions lose nothing.
-__device__ __forceinline__ float turn_fraction(int pos, float2 turns) {
-  const float lo = static_cast<float>(pos & 0xfff), hi = static_cast<float>(pos & ~0xfff);
-  const float a = lo * turns.x, b = hi * turns.x;
-  const float c = hi * turns.y;
-  float f = (a - rintf(a)) + (b - rintf(b));
-  f += (c - rintf(c)) + fmaf(lo, turns.y, fmaf(lo, turns.x, -a) + (fmaf(hi, turns.x, -b) + fmaf(hi, turns.y, -c)));
-  return f - rintf(f);
-}
-
 struct Tables {
-  float2 turns[kMaxPairs];              // frequency / (2 pi) as the sum of two floats
+  unsigned long long turns[kMaxPairs];  // frequency / (2 pi) without its whole turns, in units of 2^-64
   float cs[2][kMaxTile][kMaxPairs];     // double-buffered by tile: one barrier per tile
   float sn[2][kMaxTile][kMaxPairs];
 };
 
+// frequency / (2 pi) to about 2^-64 turns: 1 / (2 pi) as the sum of two doubles, the first product with its
+// rounding error.
 __device__ __forceinline__ void init_turns(Tables& tb, const NormRopeShape& a) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
   for (int p = threadIdx.x; p < a.pairs; p += kThreads) {
-    const double t = a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
-    const float hi = static_cast<float>(t);
-    tb.turns[p] = make_float2(hi, static_cast<float>(t - static_cast<double>(hi)));
+    const double f = a.freq[p], t = f * kHi, rest = fma(f, kHi, -t) + f * kLo;
+    tb.turns[p] = static_cast<unsigned long long>(__double2ll_rn((t - rint(t)) * 0x1p64)) +
+                  static_cast<unsigned long long>(__double2ll_rn(rest * 0x1p64));
   }
   __syncthreads();
 }
 
+// The cosine and sine of position * turns.  The product wraps at a whole turn, so every position's angle is within
+// its 2^-64 of turns times the position, 2^-33 at most.  FAST (bf16): the approximate functions, off by 2^-21 at most
+// within half a turn, far below bf16's 2^-8.  Else the angle from the nearest quarter turn, which fp32 holds
+// to 2^-28 turns.
+template <bool FAST>
+__device__ __forceinline__ void turn(unsigned long long turns, int pos, float& c, float& s) {
+  const unsigned long long x = turns * static_cast<unsigned long long>(static_cast<long long>(pos));
+  if (FAST) {
+    __sincosf(static_cast<float>(static_cast<int>(x >> 32)) * 1.46291808e-9f, &s, &c);   // 2 pi / 2^32
+  } else {
+    const unsigned q = static_cast<unsigned>((x + (1ull << 61)) >> 62);
+    float c0, s0;
+    sincospif(static_cast<float>(static_cast<long long>(x - (static_cast<unsigned long long>(q) << 62))) * 0x1p-63f, &s0, &c0);
+    c = q & 1 ? s0 : c0;
+    s = q & 1 ? c0 : s0;
+    if (q == 1 || q == 2) c = -c;
+    if (q & 2) s = -s;
+  }
+}
+
 // The cosines and sines of a tile's tokens.  Threads are laid out with the pairs (a power of two
-// of them) fastest; token numbers fit 32 bits, where a division is cheap.  FAST (bf16): the
-// approximate sine and cosine, off by 2^-21 at most within half a turn, far below bf16's 2^-8.
+// of them) fastest; token numbers fit 32 bits, where a division is cheap.
 template <bool FAST>
 __device__ __forceinline__ void fill_table(Tables& tb, int buf, const NormRopeShape& a, int tok0, int tile) {
   const int lg = 32 - __clz(a.pairs - 1), p = threadIdx.x & ((1 << lg) - 1);   // pairs = 1: lg = 0
   if (p >= a.pairs) return;
   const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
   const int* pos = a.pos + axis * a.pos_axis_stride;
-  const float2 turns = tb.turns[p];
+  const unsigned long long turns = tb.turns[p];
   const int tokens = a.B * a.N;
   for (int tl = threadIdx.x >> lg; tl < tile; tl += kThreads >> lg) {
     const int tok = tok0 + tl;
     float s = 0.0f, c = 1.0f;   // a token past the last: what its rows of zeros meet has to be finite
     if (tok < tokens) {
       const int b = tok / a.N, n = tok - b * a.N;
-      const float f = turn_fraction(pos[b * a.pos_batch_stride + n], turns);
-      if (FAST) __sincosf(6.28318531f * f, &s, &c);
-      else sincospif(2.0f * f, &s, &c);
+      turn<FAST>(turns, pos[b * a.pos_batch_stride + n], c, s);
     }
     tb.cs[buf][tl][p] = c;
     tb.sn[buf][tl][p] = s;

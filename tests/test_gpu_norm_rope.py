@@ -139,6 +139,23 @@ def test_far_positions_keep_their_angles(start):
         assert np.all(np.abs(f64(got) - want) <= bound)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("start", [0, 1 << 20, (1 << 24) + 1, (1 << 31) - 6000, -(1 << 31)])
+def test_every_position_keeps_the_accuracy_of_a_near_one(start, inter):
+    """The same bound at all int32 positions.  An angle within an eighth of a turn of a quarter: rounded once, pi / 4 *
+    2^-24; cosine and sine within 2 ulp, 2 * 2^-24; two products and a sum, 2 * 2^-24: 5 * 2^-24 of |x0| + |x1|, which is
+    10 of the row's largest.  The oracle's own angle is a rounded product, 2^-53 of it."""
+    qkv, params, how = make(2, 300, 2, 1, 64, torch.float32, "none", False, (24, 8), inter, 19, start)
+    how["frequencies"][24] = 1.0
+    how["frequencies"][25] = -7.5              # more than a turn per position, and backwards
+    q, k, _ = ra.ra_qk_norm_rope(qkv.cuda(), 2, 1, **cuda(params), **cuda(how))
+    Q, K, _ = S.qk_norm_rope(f64(qkv), 2, 1, **oracle_how(params, how))
+    angle = 7.5 * (abs(start) + 5000)
+    for got, want in ((q, Q), (k, K)):
+        most = np.abs(want).max(-1, keepdims=True) * np.sqrt(2)
+        assert np.all(np.abs(f64(got) - want) <= (10 * U32 + 2.0 ** -53 * angle) * most)
+
+
 def test_strided_projection_and_position_forms():
     """qkv as a slice of a wider row, misaligned slices, [N] and [B, N] and int64 positions: the same results."""
     B, N, Hq, Hkv, D = 2, 21, 3, 1, 64
