@@ -10,7 +10,8 @@ using namespace norm_rope;
 constexpr int kAhead = 4;   // rows of a lane group, gradient and projection, in flight: 64 KB per CTA
 
 // Each lane keeps its elements' sums of the weight's and the bias's gradient over all rows that it
-// meets; a CTA adds its lane groups' sums in a fixed order and writes them to its own place of the
+// meets; a CTA adds its lane groups' sums in a fixed order (in short chains: one after the other, the 128 groups of
+// D16 in fp32 had twice the plain form's error) and writes them to its own place of the
 // workspace, and norm_rope_param_kernel adds the CTAs', so results do not depend on the order in
 // which CTAs run.
 template <typename T, int D, int NORM>
@@ -157,10 +158,23 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
       *reinterpret_cast<float2*>(&part[g * D + lm.v1 * E + 2 * k]) = s ? db1[k] : dw1[k];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < D; e += kThreads) {
-      float f = 0.0f;
-      for (int i = 0; i < NG; ++i) f += part[i * D + e];
-      io.partial[(static_cast<int64_t>(wk.place) * 2 + s) * D + e] = f;
+    // SLICES threads per column, each adding every SLICES-th lane group, then theirs by halves
+    constexpr int SLICES = kThreads / D;
+    float f = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NG / SLICES; ++i) f += part[threadIdx.x + i * kThreads];
+    __syncthreads();
+    part[threadIdx.x] = f;
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float v[SLICES];
+#pragma unroll
+      for (int i = 0; i < SLICES; ++i) v[i] = part[i * D + threadIdx.x];
+#pragma unroll
+      for (int o = SLICES / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) v[i] += v[i + o];
+      io.partial[(static_cast<int64_t>(wk.place) * 2 + s) * D + threadIdx.x] = v[0];
     }
   }
 }

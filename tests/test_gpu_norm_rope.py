@@ -347,6 +347,25 @@ def test_parameter_gradients_of_a_ragged_last_tile(dtype, N):
             assert np.abs(f64(got[1 + i]) - DP[i]).max() <= (16 + np.log2(N)) * 4 * U32 * size
 
 
+def test_parameter_gradients_are_added_in_short_chains():
+    """The biases' gradients, sums of exact terms of unit variance over 80000 rows.  Rounding a sum S is off by 0.42 *
+    2^-24 |S| in the mean square (uniform within half a step, over mantissas); so adding k equal parts of a
+    sum one after the other costs 0.42 * 2^-24 sqrt(k / 2) of it, and by halves 0.42 * 2^-24 sqrt(log2 k).  A lane
+    adds about 5.4 rows, a CTA 8 sums one after the other and 16 by halves, the whole 2 and 64 by halves:
+    0.42 * sqrt(2.7 + 4 + 4 + 1 + 6) = 1.8 of 2^-24; with the CTA's 128 one after the other it would be 3.6.  256
+    samples: 4.4% for one standard deviation; a third more is allowed."""
+    N, H, D, total = 20000, 4, 16, []
+    w = torch.ones(D, device="cuda")
+    for seed in range(8):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        qkv = torch.randn(1, N, 3 * H * D, device="cuda", generator=g)
+        d = [torch.randn(1, H, N, D, device="cuda", generator=g) for _ in range(3)]
+        got = ra.ra_qk_norm_rope_backward(qkv, *d, H, H, norm="layer", q_weight=w, q_bias=w, k_weight=w, k_bias=w)
+        total += [got[2].double() - d[0].double().sum((0, 1, 2)), got[4].double() - d[1].double().sum((0, 1, 2))]
+    rms = torch.cat(total).square().mean().sqrt().item() / (N * H) ** 0.5
+    assert rms <= 1.8 * 1.33 * U32, rms / U32
+
+
 def test_a_tangent_is_refused_with_and_without_an_input_that_asks_for_a_gradient():
     from torch.autograd import forward_ad
     x, w = torch.randn(1, 2, 3 * 64, device="cuda"), torch.ones(64, device="cuda")
