@@ -423,7 +423,9 @@ ra_status_t ra_qk_norm_rope_bwd(const void* qkv, int64_t batch_stride, int64_t t
  *   dtype         of q, k, v, prefix and o.  RA_BF16: D in {64, 128}; RA_F32: {16, 32, 64, 128}.
  * Scores, row maxima, sums and weights are fp32.  RA_BF16: weights enter the value products as two
  * bf16 (2^-15 lost), or, in the kernels named below with more than 128 query rows per key head, as one
- * (2^-8).  Results do not depend on scheduling.
+ * (2^-8): so the last bits of a sequence's output depend on how many sequences the call has.  A value
+ * that is infinite makes its dimension infinite where its weight is positive; where the weight is 0 it
+ * may give NaN (0 times infinity) or be left out with its block.  Results do not depend on scheduling.
  * bf16 calls with more than 32 query rows per key head (B H_Q / H_KV) and a prefix of more than 3648
  * blocks, 16 keys by 16 of the rows, over all key heads use kernels with bounded waits, whose giving up
  * ra_device_status() reports.

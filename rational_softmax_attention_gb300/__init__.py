@@ -392,7 +392,8 @@ class RaAttention(torch.nn.Module):
         return self.proj(o.transpose(1, 2).reshape(B, N, self.num_heads * self.head_dim))
 
     def forward(self, x, positions=None):
-        """positions (with rope_sections): integer [N], [B, N] or [axes, B, N]; 0 .. N - 1 when not given."""
+        """positions (with rope_sections): integers that int32 holds, [N], [B, N] or [axes, B, N]; 0 .. N - 1 when not
+        given."""
         B, N, C = x.shape
         if self.rope_sections:
             if positions is None:

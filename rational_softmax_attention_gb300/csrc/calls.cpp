@@ -1,7 +1,7 @@
 // The binding of the position and serving calls, as a Python module (_calls).  A single token's kernels
 // run for a few microseconds; checking tensors, making outputs and converting 20 to 30 arguments in
 // Python took longer, so these calls do it here (calls one after the other: append B64 H32/8 17.7 us ->
-// 6.3, norm and rotation B2 N128 H12 21.1 -> 8.5, its gradient 38.7 -> 16, decode B1 H16 C512 21.9 -> 10.6).  serving.py
+// 6.3, norm and rotation B2 N128 H12 21.1 -> 8.5, its gradient 38.7 -> 16 to 20, decode B1 H16 C512 21.9 -> 10.6).  serving.py
 // holds the public functions and their documentation, and this file their checks: the same
 // refusals (ValueError, TypeError, RaError), then the C ABI call on torch's current stream of the
 // tensors' device, with the interpreter free.  Host code only; it holds no state.

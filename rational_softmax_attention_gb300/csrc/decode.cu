@@ -9,10 +9,10 @@
 // phi(d + c) is no multiple of phi(d), so a running maximum cannot rescale what was summed
 // before it, as an exponential's can: the maximum comes first.  Three launches, each with its
 // work split over the keys:
-//   scores   the keys are read once; unscaled scores go to the workspace in fp32 (4 bytes per
+//   scores   the keys are read once per 16 query rows; unscaled scores go to the workspace in fp32 (4 bytes per
 //            query head against the key's 2 D), with each part's maximum;
-//   values   phi from the scores and the final maximum; the values are read once; partial sums
-//            (fp32) per part.  Sums need no rescaling: all parts share one maximum;
+//   values   phi from the scores and the final maximum; the values are read, likewise;
+//            partial sums (fp32) per part.  Sums need no rescaling: all parts share one maximum;
 //   join     adds an output row's partial sums in a fixed order, and the weights.
 // The shared keys of many rows go to the tensor cores instead (decode_prefix_tc.cu).
 //
@@ -35,9 +35,11 @@
 // rows as M; the chunks of a row are permuted in shared memory so that the 16-byte fragment reads
 // below meet no bank conflict.  fp32: FFMA.
 //
-// Bound: HBM, K and V once, where there is much of them: B1 H32/8 D128 C131072 reads 537 MB in 92 us, 5.8
-// TB/s; B64 H32/8, 2000 keys each, 524 MB in 92 us.  Latency below that: B1 H16 C512 takes 8.6 us in a
-// graph, three launches of a few dependent loads each.
+// Bound: HBM, K and V once (the row blocks of more than 16 query rows share them through L2), where there is
+// much of them: B1 H32/8 D128 C131072 reads 537 MB in 92 us, 5.8
+// TB/s; B64 H32/8, 2000 keys each, 524 MB in 92 us.  Latency below that: B1 H16 C512 takes 9.0 us in a
+// graph, three launches of a few dependent loads each.  fp32 rows against a long prefix: the query loads, one of
+// 16 bytes for four FMAs, and the keys anew for every 16 rows (B32 H8 D64 C64 P16384: 128 us, 8 TFLOP/s).
 #include <climits>
 
 #include "decode_split.cuh"
@@ -284,7 +286,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 // The same without the choice, for keys and values: no later kernel reads them, so they are the first to leave
-// L2, where the scores had better stay (B64 H32/8 D128 C2048, whole call: 111.5 us -> 99.0).
+// L2, where the scores had better stay (B64 H32/8 D128 C2048, whole call: 111.5 us -> 99.0).  So too where several
+// row blocks read them, close to one another in time: with the ordinary policy B8 H32/1 D128 C32768 takes 50.8 us
+// instead of 44.8, B1 H24/1 D128 C524288 94.5 instead of 88.4, fp32 B32 H8 D64 P16384 130.5 instead of 128.5.
 __device__ __forceinline__ void copy16_once(uint32_t dst, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }

@@ -11,9 +11,12 @@
 // bytes of the keys.
 //
 // V is bf16, so P is, rounded: 2^-8 relative at most per weight, like the output.  Up
-// to 128 rows a key head P goes in as two bf16 instead, itself and what that leaves: the loads bound
-// the kernel then, and the second product costs little (whole call, B32 H32/8 C1024 P8192: 46.5 us ->
-// 48.3).  With more rows the products bound it (prefix alone, P32768: B64 72.7 -> 86.6 us, B128 130 -> 158).
+// to 128 rows a key head P goes in as two bf16 instead, itself and what that leaves, for little (whole call,
+// B32 H32/8 C1024 P8192: 46.5 us -> 48.3).  With more rows it costs more: prefix alone, P32768, B64 72.7 -> 86.6 us, B128
+// 130 -> 158; whole call, full caches, B64 H32/8 C4096 P32768 242 -> 251, B40 H32/8 C1024 P8192 57.8 -> 62.0, B128 H16/4 D64
+// C512 P16384 52.3 -> 59.2.  So the error there is 0.0023 of the output instead of 0.0017, its own rounding.  The
+// tensor pipe is 29 to 32% busy then: what the second product lengthens is the chain of a tile, load, S, phi,
+// hand-off and P V.
 //
 // A CTA takes 128 rows of one key head and a run of key tiles; the keys are split so that one wave of
 // CTAs, one per SM, covers heads x row tiles x splits.  Roles: warp 8 feeds a ring of K (and V) tiles
@@ -26,7 +29,7 @@
 //
 // One row tile per CTA leaves registers and shared memory for a CTA of the kernels that stream the
 // sequences' own keys (decode.cu), which are launched behind these as dependents and run beside
-// them: this part is bound by the tile loads into an SM and by the products, that one by HBM.
+// them: this part is bound by the tile loads into an SM and the chain of its steps, that one by HBM.
 #include "decode_split.cuh"
 #include "phi.cuh"
 

@@ -13,7 +13,8 @@
 //            the cluster per pass is enough.  Counts are integers, so nothing depends on the order
 //            of the atomics.  A CTA's first 8192 weights stay in registers between the passes.
 //   gather   the kept entries, 16 bytes per lane.
-// Bound: select by latency (four passes and their barriers: 14 us for 32 rows of 32768), gather by HBM
+// Bound: select by latency (four passes, each of atomics that meet in few bins where weights have few exponents, and a
+// barrier; the two were not timed apart: 14 us for 32 rows of 32768), gather by HBM
 // (B32 H8 4352 -> 4096, D128 bf16: 849 MB in 133 us, 6.4 TB/s).  Both together, in a graph: B4 H8
 // 32768 -> 2048 21.5 us.
 #include "kernels.cuh"

@@ -83,8 +83,8 @@ def ra_qk_norm_rope(qkv, num_heads, num_kv_heads=None, *, norm="layer", q_weight
 
     norm: 'layer' (weights, optional biases), 'rms' (weights) or 'none', over each head's D elements
     of q and k.  sections: pairs of dimensions per position axis (None: no rotation); frequencies:
-    float64 [sum(sections)], see ra_rope_frequencies; positions: integer [N], [B, N] or
-    [axes, B, N].  Pair i is dimensions (i, i + R) of the first 2 R, or (2 i, 2 i + 1) when
+    float64 [sum(sections)], see ra_rope_frequencies; positions: int32, or int64 of values that
+    int32 holds (converted, one more kernel; greater ones wrap), [N], [B, N] or [axes, B, N].  Pair i is dimensions (i, i + R) of the first 2 R, or (2 i, 2 i + 1) when
     interleaved.  Differentiable (once, in reverse mode) in qkv, weights and biases; as with any torch operator, a backward
     pass is captured into a CUDA graph only while no eager graph of the same leaves is alive."""
     if torch.is_grad_enabled() and (qkv.requires_grad or _asks(q_weight) or _asks(k_weight) or _asks(q_bias)
@@ -150,8 +150,9 @@ class RaCache:
     float32 [B, H_kv, C] with track_weight, the attention each entry has received from attend (a
     module's prefill adds none).
 
-    A captured graph of append and attend advances length and position when it is replayed, but not
-    `bound`, which is the host's: whoever replays it sees to it that there is room (tokens beyond the
+    `bound` is the host's count of the entries of the longest sequence, or more (padding included until
+    require_room reads the lengths back).  A captured graph of append and attend advances length and position when it is replayed, but not
+    `bound`: whoever replays it sees to it that there is room (tokens beyond the
     capacity are not stored).  evict changes which tensors the cache uses, so graphs of it are
     captured anew afterwards."""
 
@@ -219,7 +220,8 @@ class RaCache:
                                    scale=scale, weight=self.weight)
 
     def evict(self, keep, *, recent=0, spare=None):
-        """Cuts every sequence down to `keep` entries (ra_cache_evict); needs track_weight.  The cache moves
+        """Cuts every sequence down to `keep` entries (ra_cache_evict); needs track_weight.  Weights come from
+        attend: straight after a prefill all are 0, and the oldest entries are kept beside the last `recent`.  The cache moves
         to `spare`, a (k, v) pair of the same shape (made when not given), and the pair it held
         before is returned: one spare pair serves all layers in turn."""
         if self.weight is None:
