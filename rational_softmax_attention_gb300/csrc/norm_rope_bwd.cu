@@ -1,6 +1,6 @@
 // The gradient of the per-head normalisation and rotation (the mathematics: norm_rope.cuh).
 // bf16 B4 N8192 H16 D128, layer norm with biases: 1.07 GB in 201 us, 5.3 TB/s; issue slots 52% busy.  fp32 B4 N8192
-// H16/8: 1.48 GB in 249 us, 5.9 TB/s.  Small ones (fp32 B3 N1001 H6/2 D64: 12.4 us) are two launches, the second of
+// H16/8: 1.48 GB in 249 us, 5.9 TB/s.  Small ones (fp32 B3 N1001 H6/2 D64: 12.7 us) are two launches, the second of
 // which starts when the first has ended.
 #include "norm_rope.cuh"
 
