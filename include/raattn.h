@@ -460,6 +460,109 @@ ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, co
                            void* v_out, float* weight_out, int32_t* length_out, int32_t* index, int B, int H_KV,
                            int C, int C_out, int D, int keep, int recent, ra_dtype_t dtype, void* stream);
 
+/*
+ * A cache whose keys and values lie in pages, held in 4 bits.
+ *
+ * Pool.  `pages` pages, page_stride bytes apart (a multiple of 16), each [H_KV][2 (keys, values)] parts without
+ * gaps; a part holds `page` (16, 32, 64, 128 or 256) tokens in page * row bytes, row = D / 2 + D / 16, D = 64 or
+ * 128.  A token's row of D elements is cut into G = D / 64 groups of 64 dimensions; a group is held as
+ *   lo   the largest bfloat16 number that is not above its minimum (never -0),
+ *   s    the least bfloat16 number with 15 s >= maximum - lo,
+ *   u    64 codes 0 .. 15, the integers nearest to (x - lo) / s, ties to even,
+ * and stands for lo + s u: at most s / 2 from x.  A group with a NaN, an infinity or a maximum - lo beyond fp32
+ * is held as lo = NaN, s = 0; where s would be below 2^-100 it is 0.
+ * Bytes of a part: codes [page][D / 2], then bfloat16 [page][2 G]: s of each group, lo of each group.  Dimension
+ * 64 g + 8 w + n of a token is nibble n (the lowest bits first) of its little-endian 32-bit word w G + g; with
+ * D = 128 a token whose slot in the page has bit 1 set holds bytes 32 .. 63 of its codes first.
+ *
+ * Table.  [B, M] int32 in device memory: slot t of sequence b lies in page table[b][t / page], at t % page.  A
+ * number outside [0, pages) is no page: what would be written there is dropped, what is read there is zeros
+ * (keys and values of zeros).  uses [pages] int32: in how many places of the table a page stands; 0: it is free.
+ * The calls keep them so (ra_page_fork, ra_page_reserve, ra_page_compact); nothing else looks at the uses.
+ *
+ * All pointers to int32 are 4-byte aligned, pools, keys, values, outputs and workspaces 16-byte; a workspace's
+ * contents on entry are irrelevant, and calls that may run at the same time need one each.  Results do not depend on
+ * scheduling.  Common errors: RA_ERR_ARG for null or misaligned pointers, sizes < 1, strides that are no
+ * multiple of 16 bytes or make pages overlap, B M, B H_KV N 2 G or B H_Q beyond int32, M page beyond 2^31 - 16385, a bad
+ * enum; RA_ERR_UNSUPPORTED for another D or page; RA_ERR_LAUNCH.
+ *
+ * ra_page_write -- N tokens of each sequence into its pages.
+ *   k, v          [B, H_KV, N, D] of dtype; strides (of batch, head, token) in elements, multiples of 16 bytes.
+ *   start, count  [B] int32 or NULL: token n goes to slot start[b] + n (NULL: n), for n < count[b] (NULL: all)
+ *                 and slots in [0, M page).  Nothing else of the pool changes.  No two tokens of a call may share a slot.
+ *   k_held, v_held  NULL, or [B, H_KV, N, D] of dtype (written): what k and v are held as, rounded once to dtype,
+ *                 for every token, stored or not.
+ */
+ra_status_t ra_page_write(const void* k, const void* v, const int64_t* k_strides, const int64_t* v_strides, void* pool,
+                          int64_t page_stride, const int32_t* table, const int32_t* start, const int32_t* count,
+                          void* k_held, void* v_held, int B, int N, int H_KV, int D, int pages, int page, int M,
+                          ra_dtype_t dtype, void* stream);
+
+/*
+ * ra_page_read -- what slots start[b] + n (start NULL: n), n < N, hold: k, v [B, H_KV, N, D] of dtype (written),
+ * rounded once.  Slots that are negative, at or past length[b] (NULL: no limit) or without a page give zeros.
+ */
+ra_status_t ra_page_read(const void* pool, int64_t page_stride, const int32_t* table, const int32_t* start,
+                         const int32_t* length, void* k, void* v, int B, int N, int H_KV, int D, int pages, int page,
+                         int M, ra_dtype_t dtype, void* stream);
+
+/*
+ * ra_attention_decode_paged -- ra_attention of one query token per sequence over the first length[b] slots
+ * (read as min(max(length, 0), M page)) of its pages, with the keys and values that they hold.
+ *   q, o          [B, H_Q, D] of dtype (o written).  H_Q is a multiple of H_KV; query head h reads key head
+ *                 h / (H_Q / H_KV).  A sequence without any key gives zeros.
+ *   workspace     ra_attention_decode_paged_workspace_size() bytes.
+ *   scale         score scale; <= 0 means 1/sqrt(D).
+ * Scores, maxima and sums are fp32.  RA_BF16: queries enter the products as fp16 times a power of two (exact down to
+ * 2^-28 of the row's largest), weights times scales as fp16 times a power of two, 2^-11 lost of each at most; RA_F32: as two fp16
+ * (2^-22).  A query, scale or minimum that is not finite makes the output of its heads not finite; so may
+ * scales or queries beyond 2^117.
+ * Errors: the common ones, H_Q no multiple of H_KV, a scale that is not finite (RA_ERR_ARG); B > 8192, more than 1024 query
+ * heads per key head, or sizes whose blocks of 32 keys by 16 query rows number more than 2^30
+ * (RA_ERR_UNSUPPORTED).  The size query returns 0 for such sizes.
+ */
+size_t ra_attention_decode_paged_workspace_size(int B, int H_Q, int H_KV, int M, int page, int D);
+ra_status_t ra_attention_decode_paged(const void* q, const void* pool, int64_t page_stride, const int32_t* table,
+                                      const int32_t* length, void* o, void* workspace, int B, int H_Q, int H_KV, int D,
+                                      int pages, int page, int M, float scale, ra_dtype_t dtype, void* stream);
+
+/*
+ * ra_page_fork -- the table's rows replaced: row b and length[b] become what row parent[b] and its length were
+ * before the call (beams reordered, sequences forked); parent[b] outside [0, B): an empty row, -1 throughout, and length
+ * 0 (a sequence freed).  uses follow.  In place; B <= 8192 (else RA_ERR_UNSUPPORTED).
+ */
+ra_status_t ra_page_fork(int32_t* table, int32_t* length, int32_t* uses, const int32_t* parent, int B, int M, int pages,
+                         void* stream);
+
+/*
+ * ra_page_reserve -- room for the next tokens.  For every sequence, n = min(max(count[b], 0), tokens) (count NULL:
+ * tokens): of the pages that slots length[b] .. length[b] + n - 1 touch, those that are missing or have more than one
+ * use are replaced by free ones, the lowest free page first, in the order of the sequences and of their slots.  The
+ * uses are those before the call, so all sharers of a page that ask leave it.  Where tokens below length[b] lie in
+ * a page that is replaced its content is copied (page_bytes, 2 H_KV part bytes).
+ *   granted       [B] int32 (written): how many of the n tokens have room: fewer where pages run out (then
+ *                 the remaining ones stay as they were) or at the end of the table's row.
+ *   workspace     ra_page_reserve_workspace_size() bytes (0: sizes that are refused).
+ */
+size_t ra_page_reserve_workspace_size(int B, int tokens, int page);
+ra_status_t ra_page_reserve(void* pool, int64_t page_stride, int64_t page_bytes, int32_t* table, const int32_t* length,
+                            int32_t* uses, const int32_t* count, int32_t* granted, void* workspace, int B, int M,
+                            int tokens, int pages, int page, void* stream);
+
+/*
+ * ra_page_compact -- the pages in use moved together: the r-th page with uses > 0 becomes page r of pool_out.
+ *   table_out, uses_out, live   [B, M], [pages_out], [1] int32 (written): the table renumbered, the uses, how many pages are
+ *                 in use.  Where live > pages_out the last ones are not moved, and the table has -1 for them.
+ *   page_bytes    bytes of a page that are copied (a multiple of 16).  Pages of pool_out from `live` on are left as they are.
+ *   workspace     ra_page_compact_workspace_size(pages) bytes.
+ * Outputs must not overlap inputs.
+ */
+size_t ra_page_compact_workspace_size(int pages);
+ra_status_t ra_page_compact(const void* pool, int64_t page_stride, const int32_t* table, const int32_t* uses,
+                            void* pool_out, int64_t page_stride_out, int32_t* table_out, int32_t* uses_out,
+                            int32_t* live, void* workspace, int64_t page_bytes, int B, int M, int pages, int pages_out,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,9 @@ section 3 "Rational Attention & Softmax":
 around it, for positions and for serving (serving.py):
     ra_qk_norm_rope(qkv, ...)          per-head norm and rotation of q and k, autograd-aware
     ra_cache_append, ra_attention_decode, ra_cache_evict, RaCache        single tokens against a cache
+and for a cache in pages of 4-bit entries (paging.py):
+    ra_page_write, ra_page_read, ra_attention_decode_paged               entries in, out, and attended to
+    ra_page_fork, ra_page_reserve, ra_page_compact, RaPagedCache         whose pages are whose
 plus the explicit forward/backward entry points used by tests and benchmarks.
 """
 from __future__ import annotations
@@ -26,7 +29,8 @@ __all__ = [
     "RaError", "lib", "ra_softmax", "ra_softmax_backward", "ra_attention", "ra_attention_forward", "RaAttention",
     "ra_attention_backward", "pack_attn_mask", "device_status", "set_wait_limit_ns", "exported_symbols", "LIB_PATH",
     "debug_kernel_events", "ra_rope_frequencies", "ra_qk_norm_rope", "ra_qk_norm_rope_backward", "ra_cache_append",
-    "ra_attention_decode", "ra_cache_evict", "RaCache",
+    "ra_attention_decode", "ra_cache_evict", "RaCache", "ra_page_pool", "ra_page_write", "ra_page_read",
+    "ra_attention_decode_paged", "ra_page_fork", "ra_page_reserve", "ra_page_compact", "RaPagedCache",
 ]
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -71,6 +75,15 @@ _SIGNATURES = {
     "ra_attention_decode_workspace_size": ([_i32] * 7, ctypes.c_size_t),
     "ra_attention_decode": ([_vp] * 9 + [_i32] * 6 + [_f32, _i32, _vp], _i32),
     "ra_cache_evict": ([_vp] * 9 + [_i32] * 8 + [_vp], _i32),
+    "ra_page_write": ([_vp] * 5 + [_i64] + [_vp] * 5 + [_i32] * 8 + [_vp], _i32),
+    "ra_page_read": ([_vp, _i64] + [_vp] * 5 + [_i32] * 8 + [_vp], _i32),
+    "ra_attention_decode_paged_workspace_size": ([_i32] * 6, ctypes.c_size_t),
+    "ra_attention_decode_paged": ([_vp, _vp, _i64] + [_vp] * 4 + [_i32] * 7 + [_f32, _i32, _vp], _i32),
+    "ra_page_fork": ([_vp] * 4 + [_i32] * 3 + [_vp], _i32),
+    "ra_page_reserve_workspace_size": ([_i32] * 3, ctypes.c_size_t),
+    "ra_page_reserve": ([_vp, _i64, _i64] + [_vp] * 6 + [_i32] * 5 + [_vp], _i32),
+    "ra_page_compact_workspace_size": ([_i32], ctypes.c_size_t),
+    "ra_page_compact": ([_vp, _i64, _vp, _vp, _vp, _i64] + [_vp] * 4 + [_i64] + [_i32] * 4 + [_vp], _i32),
     "ra_device_status": ([_vp], _i32),
     "ra_set_wait_limit_ns": ([_u64], None),
     "ra_debug_force_timeout": ([_i32], None),
@@ -322,6 +335,8 @@ def ra_attention(q, k, v, attn_mask=None, is_causal=False, scale=None):
 
 from .serving import (RaCache, ra_attention_decode, ra_cache_append, ra_cache_evict, ra_qk_norm_rope,  # noqa: E402
                       ra_qk_norm_rope_backward, ra_rope_frequencies)
+from .paging import (RaPagedCache, ra_attention_decode_paged, ra_page_compact, ra_page_fork, ra_page_pool,  # noqa: E402
+                     ra_page_read, ra_page_reserve, ra_page_write)
 
 
 class RaAttention(torch.nn.Module):
@@ -336,7 +351,7 @@ class RaAttention(torch.nn.Module):
     projection.  The two projections are plain library GEMMs (torch Linear, cuBLAS).
     Dropout is not part of this path: attn_drop and proj_drop must be 0.
 
-    Serving (causal modules): new_cache, then prefill for a prompt and decode for single tokens.
+    Serving (causal modules): new_cache, then prefill for prompts and decode for single tokens.
     """
 
     def __init__(self, dim, num_heads=8, qkv_bias=False, qk_norm=False, attn_drop=0.0, proj_drop=0.0,
@@ -409,8 +424,16 @@ class RaAttention(torch.nn.Module):
         o = ra_attention(q, k, v, is_causal=self.causal)
         return self.proj(o.transpose(1, 2).reshape(B, N, C))
 
-    def new_cache(self, batch, capacity, *, prefix=None, track_weight=False, dtype=None):
-        """An empty RaCache for this module, of its dtype or (under autocast, the projection's) the one given."""
+    def new_cache(self, batch, capacity, *, prefix=None, track_weight=False, dtype=None, page_size=None, pages=None):
+        """An empty RaCache for this module, of its dtype or (under autocast, the projection's) the one given;
+        with page_size an empty RaPagedCache, whose entries take 4 bits an element (head dimension 64 or 128)."""
+        if page_size is not None:
+            if prefix is not None or track_weight:
+                raise ValueError("a paged cache has no prefix (sequences share pages after fork) and tracks no weights")
+            return RaPagedCache(batch, self.num_heads, capacity, self.head_dim, page_size=page_size, pages=pages,
+                                device=self.proj.weight.device, dtype=dtype or self.proj.weight.dtype)
+        if pages is not None:
+            raise ValueError("pages need page_size")
         return RaCache(batch, self.num_heads, capacity, self.head_dim, prefix=prefix, track_weight=track_weight,
                        device=self.proj.weight.device, dtype=dtype or self.proj.weight.dtype)
 
@@ -418,9 +441,14 @@ class RaAttention(torch.nn.Module):
     def prefill(self, x, cache, positions=None, count=None):
         """forward of a prompt x [B, N, dim] whose keys and values go into an empty cache; returns y.
         count: optional int32 [B], the tokens of a padded batch (rows of y behind them mean nothing).
-        Behind a prefix the prompt attends to it too (bf16 only: a masked attention call)."""
+        Behind a prefix the prompt attends to it too (bf16 only: a masked attention call).
+
+        A paged cache: the prompt attends to its keys and values as the cache holds them, as later single tokens do,
+        and a cache that holds entries already is continued (bf16 only, likewise)."""
         if not self.causal:
             raise ValueError("serving needs a causal module")
+        if isinstance(cache, RaPagedCache):
+            return self._prefill_paged(x, cache, positions, count)
         if cache.bound:
             raise ValueError("prefill needs an empty cache")
         B, N, _ = x.shape
@@ -445,6 +473,28 @@ class RaAttention(torch.nn.Module):
         v = torch.cat([cache.prefix_v.expand(B, -1, -1, -1), v], 2)
         seen = torch.ones(N, P + N, dtype=torch.bool, device=x.device).tril(P)
         return self._merge(ra_attention(q, k, v, attn_mask=seen))
+
+    def _prefill_paged(self, x, cache, positions, count):
+        B, N, _ = x.shape
+        if cache.table.shape[0] != B or cache.num_kv_heads != self.num_heads or cache.head_dim != self.head_dim:
+            raise ValueError("the cache must have the batch size, heads and head dimension of x in this module")
+        qkv = self.qkv(x)
+        if cache.dtype != qkv.dtype:
+            raise ValueError(f"the cache must have the projection's dtype, {qkv.dtype}")
+        if cache.bound and qkv.dtype != torch.bfloat16:
+            raise NotImplementedError("continuing a cache that holds entries takes bf16 modules only")
+        if self.rope_sections and positions is None:
+            positions = cache.position.view(B, 1) + torch.arange(N, device=x.device, dtype=torch.int32)
+        before = cache.length.clone() if cache.bound else None
+        how = self._how(positions, qkv.dtype)
+        if before is None:
+            q, k, v = cache.append(qkv, self.num_heads, count=count, held=True, **how)
+            return self._merge(ra_attention(q, k, v, is_causal=True))
+        q = cache.append(qkv, self.num_heads, count=count, **how)
+        k, v = cache.read(cache.bound)
+        slot = torch.arange(cache.bound, device=x.device)
+        seen = slot <= (before.view(B, 1, 1) + torch.arange(N, device=x.device).view(1, N, 1))
+        return self._merge(ra_attention(q, k, v, attn_mask=seen.unsqueeze(1)))
 
     @torch.no_grad()
     def decode(self, x, cache, positions=None):

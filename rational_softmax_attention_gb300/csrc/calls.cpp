@@ -377,6 +377,204 @@ PyObject* cache_evict(PyObject* const* a) {
   return tuple({ko, vo, wo, new_length, index});
 }
 
+// ---- pages in 4 bits ----------------------------------------------------------------------------
+// uint8 [pages, H_kv, 2, page, row]: a layer's slice of a larger tensor will do, pages may lie apart.
+struct Pool {
+  const Tensor* t;
+  int pages, Hkv, page, D;
+  int64_t stride, bytes;   // from page to page; of a page
+
+  Pool(PyObject* o, const char* name) : t(&tensor(o, name)) {
+    std::ostringstream s;
+    if (t->dim() != 5 || t->scalar_type() != at::kByte || !t->is_cuda() || t->size(2) != 2 ||
+        (t->size(4) != 36 && t->size(4) != 72)) {
+      s << name << " must be a CUDA uint8 tensor [pages, num_kv_heads, 2, page_size, head_dim / 2 + head_dim / 16], head_dim 64 or 128";
+      refuse(s.str());
+    }
+    pages = size32(t->size(0));
+    Hkv = size32(t->size(1));
+    page = size32(t->size(3));
+    D = t->size(4) == 36 ? 64 : 128;
+    if (pages < 1 || Hkv < 1 || (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)) {
+      s << name << " must have pages of 16, 32, 64, 128 or 256 tokens, and no size 0";
+      refuse(s.str());
+    }
+    const int64_t part = t->size(3) * t->size(4);
+    bytes = 2 * Hkv * part;
+    stride = pages > 1 ? t->stride(0) : bytes;
+    if (t->stride(4) != 1 || t->stride(3) != t->size(4) || t->stride(2) != part || (Hkv > 1 && t->stride(1) != 2 * part) ||
+        stride < bytes || stride % 16 || reinterpret_cast<uintptr_t>(t->data_ptr()) & 15) {
+      s << name << " must hold each page without gaps, pages a multiple of 16 bytes apart, at a 16-byte address";
+      refuse(s.str());
+    }
+  }
+  at::Device device() const { return t->device(); }
+  void* data() const { return t->data_ptr(); }
+};
+// int32 [B, M] on the pool's device
+const Tensor& table_of(PyObject* o, const at::Device& device) {
+  const Tensor& t = tensor(o, "table");
+  if (t.dim() != 2 || t.size(0) < 1 || t.size(1) < 1) refuse("table must be [sequences, pages], and no size 0");
+  check("table", t, {t.size(0), t.size(1)}, at::kInt, device);
+  size32(t.size(0));
+  size32(t.size(1));
+  return t;
+}
+const int32_t* ints(const Tensor* t) { return static_cast<const int32_t*>(address(t)); }
+int32_t* ints(const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+const Tensor* per_sequence(PyObject* o, const char* name, int B, const at::Device& device) {
+  const Tensor* t = optional_tensor(o, name);
+  if (t) check(name, *t, {B}, at::kInt, device);
+  return t;
+}
+Tensor rows_for(const Tensor& x, int vec) {   // as the kernel reads them, whatever view of another tensor they are
+  if (x.stride(3) != 1 || x.stride(0) % vec || x.stride(1) % vec || x.stride(2) % vec ||
+      reinterpret_cast<uintptr_t>(x.data_ptr()) & 15)
+    return x.clone(at::MemoryFormat::Contiguous);
+  return x;
+}
+
+// k, v, pool, table, start, count, held
+PyObject* page_write(PyObject* const* a) {
+  const Tensor &k0 = tensor(a[0], "k"), &v0 = tensor(a[1], "v");
+  const Pool pool(a[2], "pool");
+  const Tensor& table = table_of(a[3], pool.device());
+  const int B = size32(table.size(0)), M = size32(table.size(1));
+  const ra_dtype_t code = dtype_code(k0);
+  if (k0.dim() != 4 || k0.size(2) < 1) refuse("k must be [B, num_kv_heads, N, head_dim] with N >= 1");
+  const int N = size32(k0.size(2));
+  for (const Tensor* t : {&k0, &v0})
+    if (t->sizes() != at::IntArrayRef({B, pool.Hkv, N, pool.D}) || t->scalar_type() != k0.scalar_type() || t->device() != pool.device()) {
+      std::ostringstream s;
+      s << "k and v must be [B, num_kv_heads, N, head_dim] = " << at::IntArrayRef({B, pool.Hkv, N, pool.D})
+        << " of one dtype on the pool's device";
+      refuse(s.str());
+    }
+  const Tensor *start = per_sequence(a[4], "start", B, pool.device()), *count = per_sequence(a[5], "count", B, pool.device());
+  const int truth = PyObject_IsTrue(a[6]);
+  if (truth < 0) throw Refusal{nullptr, ""};
+  const int vec = code == RA_BF16 ? 8 : 4;
+  const Tensor k = rows_for(k0, vec), v = rows_for(v0, vec);
+  Tensor kh, vh;
+  if (truth) {
+    kh = make({B, pool.Hkv, N, pool.D}, k.scalar_type(), pool.device());
+    vh = make({B, pool.Hkv, N, pool.D}, k.scalar_type(), pool.device());
+  }
+  const int64_t ks[3] = {k.stride(0), k.stride(1), k.stride(2)}, vs[3] = {v.stride(0), v.stride(1), v.stride(2)};
+  check_status("ra_page_write", on_stream(pool.device(), [&](cudaStream_t st) {
+                 return ra_page_write(k.data_ptr(), v.data_ptr(), ks, vs, pool.data(), pool.stride, ints(table), ints(start),
+                                      ints(count), truth ? kh.data_ptr() : nullptr, truth ? vh.data_ptr() : nullptr, B, N,
+                                      pool.Hkv, pool.D, pool.pages, pool.page, M, code, st);
+               }));
+  if (truth) return tuple({kh, vh});
+  Py_RETURN_NONE;
+}
+
+// pool, table, length, tokens, start, dtype (a code)
+PyObject* page_read(PyObject* const* a) {
+  const Pool pool(a[0], "pool");
+  const Tensor& table = table_of(a[1], pool.device());
+  const int B = size32(table.size(0)), M = size32(table.size(1)), N = integer(a[3]);
+  const Tensor *length = per_sequence(a[2], "length", B, pool.device()), *start = per_sequence(a[4], "start", B, pool.device());
+  if (N < 1) refuse("tokens must be at least 1");
+  const ra_dtype_t code = integer(a[5]) == RA_BF16 ? RA_BF16 : RA_F32;
+  const at::ScalarType dtype = code == RA_BF16 ? at::kBFloat16 : at::kFloat;
+  const Tensor k = make({B, pool.Hkv, N, pool.D}, dtype, pool.device()), v = make({B, pool.Hkv, N, pool.D}, dtype, pool.device());
+  check_status("ra_page_read", on_stream(pool.device(), [&](cudaStream_t st) {
+                 return ra_page_read(pool.data(), pool.stride, ints(table), ints(start), ints(length), k.data_ptr(), v.data_ptr(),
+                                     B, N, pool.Hkv, pool.D, pool.pages, pool.page, M, code, st);
+               }));
+  return tuple({k, v});
+}
+
+// q, pool, table, length, scale
+PyObject* attention_decode_paged(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q");
+  if (q.dim() != 3) refuse("q must be [B, H, D]");
+  if (!q.is_cuda() || !q.is_contiguous()) refuse("q must be a contiguous CUDA tensor (there is no CPU path)");
+  const Pool pool(a[1], "pool");
+  const Tensor& table = table_of(a[2], pool.device());
+  const ra_dtype_t code = dtype_code(q);
+  const int B = size32(table.size(0)), M = size32(table.size(1)), Hq = size32(q.size(1));
+  if (q.device() != pool.device() || q.size(0) != B || q.size(2) != pool.D || Hq < 1 || Hq % pool.Hkv)
+    refuse("q must be [B, H, head_dim] on the pool's device, with H a multiple of the key heads, B as in the table");
+  const Tensor& length = tensor(a[3], "length");
+  check("length", length, {B}, at::kInt, pool.device());
+  const float scale = a[4] == Py_None ? 0.0f : number(a[4]);
+  // an address that the kernels cannot read as it is
+  const Tensor in = reinterpret_cast<uintptr_t>(q.data_ptr()) & 15 ? q.clone(at::MemoryFormat::Contiguous) : q;
+  const Tensor o = make({B, Hq, pool.D}, q.scalar_type(), pool.device());
+  const Tensor ws = make({static_cast<int64_t>(ra_attention_decode_paged_workspace_size(B, Hq, pool.Hkv, M, pool.page, pool.D)) + 16},
+                         at::kByte, pool.device());
+  check_status("ra_attention_decode_paged", on_stream(pool.device(), [&](cudaStream_t st) {
+                 return ra_attention_decode_paged(in.data_ptr(), pool.data(), pool.stride, ints(table), ints(length), o.data_ptr(),
+                                                  ws.data_ptr(), B, Hq, pool.Hkv, pool.D, pool.pages, pool.page, M, scale, code, st);
+               }));
+  return THPVariable_Wrap(o);
+}
+
+// table, length, uses, parent
+PyObject* page_fork(PyObject* const* a) {
+  const Tensor& first = tensor(a[0], "table");
+  if (!first.is_cuda()) refuse("table must be a CUDA tensor (there is no CPU path)");
+  const at::Device device = first.device();
+  const Tensor &table = table_of(a[0], device), &length = tensor(a[1], "length"), &uses = tensor(a[2], "uses"),
+               &parent = tensor(a[3], "parent");
+  const int B = size32(table.size(0)), M = size32(table.size(1));
+  if (uses.dim() != 1 || uses.size(0) < 1) refuse("uses must be [pages]");
+  check("length", length, {B}, at::kInt, device);
+  check("uses", uses, {uses.size(0)}, at::kInt, device);
+  check("parent", parent, {B}, at::kInt, device);
+  const int pages = size32(uses.size(0));
+  check_status("ra_page_fork", on_stream(device, [&](cudaStream_t st) {
+                 return ra_page_fork(ints(table), ints(length), ints(uses), ints(parent), B, M, pages, st);
+               }));
+  Py_RETURN_NONE;
+}
+
+// pool, table, length, uses, tokens, count
+PyObject* page_reserve(PyObject* const* a) {
+  const Pool pool(a[0], "pool");
+  const at::Device device = pool.device();
+  const Tensor &table = table_of(a[1], device), &length = tensor(a[2], "length"), &uses = tensor(a[3], "uses");
+  const int B = size32(table.size(0)), M = size32(table.size(1)), tokens = integer(a[4]);
+  check("length", length, {B}, at::kInt, device);
+  check("uses", uses, {pool.pages}, at::kInt, device);
+  const Tensor* count = per_sequence(a[5], "count", B, device);
+  if (tokens < 1) refuse("tokens must be at least 1");
+  const Tensor granted = make({B}, at::kInt, device);
+  const Tensor ws = make({static_cast<int64_t>(ra_page_reserve_workspace_size(B, tokens, pool.page)) + 16}, at::kByte, device);
+  check_status("ra_page_reserve", on_stream(device, [&](cudaStream_t st) {
+                 return ra_page_reserve(pool.data(), pool.stride, pool.bytes, ints(table), ints(length), ints(uses), ints(count),
+                                        ints(granted), ws.data_ptr(), B, M, tokens, pool.pages, pool.page, st);
+               }));
+  return THPVariable_Wrap(granted);
+}
+
+// pool, table, uses, out
+PyObject* page_compact(PyObject* const* a) {
+  const Pool pool(a[0], "pool"), out(a[3], "out");
+  const at::Device device = pool.device();
+  const Tensor &table = table_of(a[1], device), &uses = tensor(a[2], "uses");
+  const int B = size32(table.size(0)), M = size32(table.size(1));
+  check("uses", uses, {pool.pages}, at::kInt, device);
+  if (out.device() != device || out.Hkv != pool.Hkv || out.page != pool.page || out.D != pool.D)
+    refuse("out must be a pool of the same heads, pages' size and head_dim on the same device");
+  const char *p0 = static_cast<const char*>(pool.data()), *p1 = p0 + (pool.pages - 1) * pool.stride + pool.bytes;
+  const char *o0 = static_cast<const char*>(out.data()), *o1 = o0 + (out.pages - 1) * out.stride + out.bytes;
+  // slices of one tensor may interleave (layers); what must not happen is that a page of one lies in a page of the other
+  const int64_t apart = ((o0 - p0) % pool.stride + pool.stride) % pool.stride;
+  const bool interleaved = pool.stride == out.stride && apart >= pool.bytes && apart + pool.bytes <= pool.stride;
+  if (o0 < p1 && p0 < o1 && !interleaved) refuse("out must not share memory with pool");
+  const Tensor table_out = make({B, M}, at::kInt, device), uses_out = make({out.pages}, at::kInt, device), live = make({1}, at::kInt, device);
+  const Tensor ws = make({static_cast<int64_t>(ra_page_compact_workspace_size(pool.pages)) + 16}, at::kByte, device);
+  check_status("ra_page_compact", on_stream(device, [&](cudaStream_t st) {
+                 return ra_page_compact(pool.data(), pool.stride, ints(table), ints(uses), out.data(), out.stride, ints(table_out),
+                                        ints(uses_out), ints(live), ws.data_ptr(), pool.bytes, B, M, pool.pages, out.pages, st);
+               }));
+  return tuple({table_out, uses_out, live});
+}
+
 template <PyObject* (*F)(PyObject* const*), int COUNT>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -402,6 +600,12 @@ PyMethodDef methods[] = {method<norm_rope, kLead>("norm_rope"),
                          method<cache_append, kLead + 4>("cache_append"),
                          method<attention_decode, 8>("attention_decode"),
                          method<cache_evict, 7>("cache_evict"),
+                         method<page_write, 7>("page_write"),
+                         method<page_read, 6>("page_read"),
+                         method<attention_decode_paged, 5>("attention_decode_paged"),
+                         method<page_fork, 4>("page_fork"),
+                         method<page_reserve, 6>("page_reserve"),
+                         method<page_compact, 4>("page_compact"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -42,15 +42,14 @@
 // 16 bytes for four FMAs, and the keys anew for every 16 rows (B32 H8 D64 C64 P16384: 128 us, 8 TFLOP/s).
 #include <climits>
 
-#include "decode_split.cuh"
+#include "decode_parts.cuh"
 
 namespace raattn {
 namespace {
 
-constexpr int kThreads = kDecodeThreads, kWarps = kThreads / 32, kCtasPerSm = kDecodeCtasPerSm;
-constexpr int kRows = kDecodeRows;
-using Split = DecodeSplit;
-constexpr float kInf = __builtin_huge_valf();
+using namespace decode;
+
+constexpr int kCtasPerSm = kDecodeCtasPerSm;
 
 template <typename T, int D>
 struct Cfg {
@@ -65,213 +64,6 @@ struct Cfg {
   static constexpr int kStageV = kBlockBytes + kRows * kScoreStride * 4;
 };
 
-__device__ __forceinline__ float phi_fast(float d) {   // bf16 inputs: 1 ulp reciprocal, exactly 1 at d = 0
-  const float q = fmaxf(16.0f - d, 0.0f) * rcp_approx(16.0f + d);
-  const float q2 = q * q, q4 = q2 * q2;
-  return q4 * q4;
-}
-__device__ __forceinline__ float phi_exact(float d) {   // fp32 inputs: IEEE division
-  const bool in = !(d >= 16.0f);   // NaN stays NaN
-  d = in ? d : 0.0f;   // always a plain quotient: a division's special cases are slow
-  const float q = in ? (16.0f - d) / (16.0f + d) : 0.0f;
-  const float q2 = q * q, q4 = q2 * q2;
-  return q4 * q4;
-}
-template <typename T>
-__device__ __forceinline__ float phi_t(float d) {
-  return sizeof(T) == 2 ? phi_fast(d) : phi_exact(d);
-}
-
-// ---------------------------------------------------------------------------------------------
-// the split
-// ---------------------------------------------------------------------------------------------
-// The sequences' entries and own blocks: cum[b] = blocks per stream of the sequences before b, for
-// b <= B, and behind it their lengths.  All threads.
-template <int KEYS>
-__device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a, int* most_blocks) {
-  __shared__ int sums[kWarps], longest[kWarps];
-  int* len = cum + a.B + 1;
-  const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
-  int mine = 0, most = 0;
-  for (int i = b0; i < b0 + per && i < a.B; ++i) {
-    const int n = decode_own_length(a, i), blocks = (n + KEYS - 1) / KEYS;
-    len[i] = n;
-    mine += blocks;
-    most = max(most, blocks);
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if ((threadIdx.x & 31) == 0) longest[threadIdx.x >> 5] = most;
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if ((threadIdx.x & 31) >= o) inc += v;
-  }
-  if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = inc;
-  __syncthreads();
-  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) inc += sums[w];
-  int run = inc - mine;
-  for (int i = b0; i < b0 + per && i < a.B; ++i) {
-    cum[i] = run;
-    run += (len[i] + KEYS - 1) / KEYS;
-  }
-  if (b0 < a.B && b0 + per >= a.B) cum[a.B] = run;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) most = max(most, longest[w]);
-  *most_blocks = most;
-  return decode_split(a, cum[a.B], most);
-}
-
-// A stream's part in a run.
-struct Part {
-  int first, count;    // blocks of the stream
-  int keys;            // keys of the stream
-  int slot;            // its place among a row's partial results
-  int kv, b;           // key head; sequence, or -1: shared keys
-  int row0, rows;      // rows: within the head's G (own) or the batch's B G (shared)
-};
-
-// The part that begins at block u of run `run`, which ends at `end`.
-__device__ __forceinline__ Part get_part(int u, int run, int end, const int* cum, const Split& s, const DecodeArgs& a) {
-  Part p;
-  int stream0, blocks, stream;   // the stream's first block among all; its blocks
-  if (u < s.own0) {
-    blocks = a.pblocks;
-    stream = u / blocks;
-    stream0 = stream * blocks;
-    p.kv = stream / a.shared_rowblocks;
-    p.b = -1;
-    p.keys = a.P;
-    p.row0 = (stream - p.kv * a.shared_rowblocks) * kRows;
-    p.rows = min(a.B * a.G - p.row0, kRows);
-    p.slot = 0;
-  } else {
-    const int streams = a.Hkv * a.own_rowblocks, x = u - s.own0, c = x / streams;
-    int lo = 0, hi = a.B - 1;   // the last b with cum[b] <= c: c lies in its blocks
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cum[mid] <= c) lo = mid; else hi = mid - 1;
-    }
-    blocks = cum[lo + 1] - cum[lo];
-    const int seq0 = cum[lo] * streams;
-    stream = (x - seq0) / blocks;
-    stream0 = s.own0 + seq0 + stream * blocks;
-    p.kv = a.own_rowblocks == 1 ? stream : stream / a.own_rowblocks;
-    p.b = lo;
-    p.keys = cum[a.B + 1 + lo];
-    p.row0 = (stream - p.kv * a.own_rowblocks) * kRows;
-    p.rows = min(a.G - p.row0, kRows);
-    p.slot = a.pslots;
-  }
-  p.first = u - stream0;
-  p.count = min(blocks - p.first, end - u);
-  p.slot += run - stream0 / s.per;
-  return p;
-}
-
-// With a run per CTA: run `run` of the streams in order, each cut for itself; false where there is none.  All
-// lanes; few streams, so few sequences: two per lane.
-__device__ __forceinline__ bool get_run(int run, const int* cum, const Split& s, const DecodeArgs& a, Part& p) {
-  int blocks, i;   // the stream's blocks; the run's place in it
-  const int shared_runs = (a.pblocks + s.per - 1) / s.per, shared_streams = a.Hkv * a.shared_rowblocks;
-  if (run < shared_runs * shared_streams) {
-    const int stream = run / shared_runs;
-    i = run - stream * shared_runs;
-    blocks = a.pblocks;
-    p.kv = stream / a.shared_rowblocks;
-    p.b = -1;
-    p.keys = a.P;
-    p.row0 = (stream - p.kv * a.shared_rowblocks) * kRows;
-    p.rows = min(a.B * a.G - p.row0, kRows);
-    p.slot = i;
-  } else {
-    const int lane = threadIdx.x & 31, streams = a.Hkv * a.own_rowblocks;
-    int at = run - shared_runs * shared_streams;
-    int b = -1, n = 0, seq0 = 0;   // the sequence, its runs per stream and all before it
-    for (int b0 = 0; b0 < a.B && b < 0; b0 += 32) {
-      const int mine = b0 + lane < a.B ? (cum[b0 + lane + 1] - cum[b0 + lane] + s.per - 1) / s.per : 0;
-      int upto = mine * streams;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, seq0 + upto > at);
-      const int l = past ? __ffs(past) - 1 : 31;
-      n = __shfl_sync(0xffffffffu, mine, l);
-      if (past) {
-        b = b0 + l;
-        seq0 += __shfl_sync(0xffffffffu, upto, l) - n * streams;
-      } else {
-        seq0 += __shfl_sync(0xffffffffu, upto, 31);
-      }
-    }
-    if (b < 0) return false;
-    at -= seq0;
-    const int stream = at / n;
-    i = at - stream * n;
-    blocks = cum[b + 1] - cum[b];
-    p.kv = stream / a.own_rowblocks;
-    p.b = b;
-    p.keys = cum[a.B + 1 + b];
-    p.row0 = (stream - p.kv * a.own_rowblocks) * kRows;
-    p.rows = min(a.G - p.row0, kRows);
-    p.slot = a.pslots + i;
-  }
-  p.first = i * s.per;
-  p.count = min(blocks - p.first, s.per);
-  return true;
-}
-
-// A short prefix counts for more blocks than it has, see plan_decode: those that it has of them.
-__device__ __forceinline__ void clip(Part& p, const DecodeArgs& a) {
-  if (p.b < 0) p.count = max(min(p.count, (a.P + a.block - 1) / a.block - p.first), 0);
-}
-
-// f(part) for the parts of this team's run.
-template <int TW, typename F>
-__device__ __forceinline__ void each_part(int team, const int* cum, const Split& s, const DecodeArgs& a, F f) {
-  if constexpr (TW == 1) {   // runs go to the CTAs in turn, so that few runs spread over the SMs
-    const int run = team * gridDim.x + blockIdx.x, end = min((run + 1) * s.per, s.total);
-    for (int u = run * s.per; u < end;) {
-      Part p = get_part(u, run, end, cum, s, a);
-      u += p.count;
-      clip(p, a);
-      f(p);
-    }
-  } else {
-    Part p;
-    if (get_run(blockIdx.x, cum, s, a, p)) {
-      clip(p, a);
-      f(p);
-    }
-  }
-}
-
-// Teams of TW warps.  Blocks of a part that this warp takes: every TW-th.
-template <int TW>
-__device__ __forceinline__ int warp_of_team() { return static_cast<int>(threadIdx.x >> 5) % TW; }
-template <int TW>
-__device__ __forceinline__ int blocks_of_warp(const Part& p) { return (p.count - warp_of_team<TW>() + TW - 1) / TW; }
-template <int TW>
-__device__ __forceinline__ void team_sync() {
-  static_assert(TW == 1 || TW == kWarps, "a warp or the CTA");
-  if (TW == 1) __syncwarp();
-  else __syncthreads();
-}
-
-// Row r of a part (its last one for those past it) as an index into [B, H_q].
-__device__ __forceinline__ int row_of(const Part& p, int r, const DecodeArgs& a) {
-  const int x = p.row0 + min(r, p.rows - 1);
-  if (p.b >= 0) return p.b * a.Hq + p.kv * a.G + x;
-  const int b = x / a.G;
-  return b * a.Hq + p.kv * a.G + x - b * a.G;
-}
-__device__ __forceinline__ float* score_row(const Part& p, int row, const DecodeArgs& a) {
-  return p.b >= 0 ? a.s_own + static_cast<int64_t>(row) * a.own_width
-                  : a.s_pre + static_cast<int64_t>(row) * a.pre_width;
-}
 template <typename T, int D>
 __device__ __forceinline__ const char* stream_of(const Part& p, const void* own, const void* pre, const DecodeArgs& a) {
   const T* x = p.b >= 0 ? static_cast<const T*>(own) + (static_cast<int64_t>(p.b) * a.Hkv + p.kv) * a.C * D
@@ -282,22 +74,6 @@ __device__ __forceinline__ const char* stream_of(const Part& p, const void* own,
 // ---------------------------------------------------------------------------------------------
 // asynchronous copies
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {   // zeros when not in
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-// The same without the choice, for keys and values: no later kernel reads them, so they are the first to leave
-// L2, where the scores had better stay (B64 H32/8 D128 C2048, whole call: 111.5 us -> 99.0).  So too where several
-// row blocks read them, close to one another in time: with the ordinary policy B8 H32/1 D128 C32768 takes 50.8 us
-// instead of 44.8, B1 H24/1 D128 C524288 94.5 instead of 88.4, fp32 B32 H8 D64 P16384 130.5 instead of 128.5.
-__device__ __forceinline__ void copy16_once(uint32_t dst, const void* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Where chunk c of row r of a block stands.  K16, V16: the bf16 fragment reads of eight lanes
 // (two keys by four chunks; four keys by two chunks); F32: eight keys by one chunk.
 enum Layout { K16, V16, F32 };
@@ -337,12 +113,6 @@ struct Fetch {
     }
   }
 };
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 u;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(addr));
-  return u;
-}
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -528,37 +298,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_scores_kernel(con
 // ---------------------------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------------------------
-// A row's values v[] over its slots, folded by f over N neighbouring lanes, of which this is lane t;
-// x0 is neutral.  Eight loads at a time are in flight.
-template <int N, typename F>
-__device__ __forceinline__ float fold_slots(const float* v, int shared, int own, int pslots, int t, float x0, F f) {
-  float x = x0;
-  for (int i0 = t; i0 < shared + own; i0 += 8 * N) {
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * N;
-      y[j] = i < shared + own ? __ldcg(v + (i < shared ? i : pslots + i - shared)) : x0;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x = f(x, y[j]);
-  }
-#pragma unroll
-  for (int o = 1; o < N; o <<= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-// The maxima of a part's rows, each by 2 TW of the team's threads.
-template <int TW>
-__device__ __forceinline__ void part_maxima(float* rowm, const Part& p, const int* cum, const Split& s,
-                                            const DecodeArgs& a) {
-  const int tt = threadIdx.x % (32 * TW), r = tt / (2 * TW), row = row_of(p, r, a), b = row / a.Hq;
-  int shared, own;
-  decode_row_slots(b, p.kv, row - b * a.Hq - p.kv * a.G, cum[b], cum[b + 1], s, a, shared, own);
-  const float m = fold_slots<2 * TW>(a.row_max + static_cast<int64_t>(row) * a.slots, shared, own, a.pslots,
-                                     tt % (2 * TW), -kInf, [](float x, float y) { return fmaxf(x, y); });
-  if (tt % (2 * TW) == 0) rowm[r] = m;
-}
-
 // Where piece c (four keys) of row r's scores stands: in bf16 so that the reads of sixteen lanes (four
 // rows, eight keys) meet no bank conflict.
 template <bool BF>
@@ -1015,6 +754,26 @@ __global__ void __launch_bounds__(kThreads) decode_join_kernel(const DecodeArgs 
   }
 }
 
+template <typename T, int D>
+cudaError_t join(const DecodeArgs& a, cudaStream_t st) {
+  const cudaError_t e = set_up_kernel<decode_join_kernel<T, D>>(0, true);
+  if (e != cudaSuccess) return e;
+  // Few CTAs: a weight CTA takes as many keys, up to 4096, as leave about six per SM (starting the
+  // 6144 CTAs of one row or 512 keys each took most of 15 us at B64 H32/8 C4096).
+  // A CTA per row where rows are few and their partial results many.
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
+  const int row_warps = rows <= 2 * kSms && a.slots > 8 * (128 / D) ? kWarps : 1;
+  int64_t ctas = (rows * row_warps + kWarps - 1) / kWarps;
+  int weight_keys = kWeightKeys;
+  if (a.weight) {
+    const int64_t streams = static_cast<int64_t>(a.B) * a.Hkv;
+    while (weight_keys < 8 * kWeightKeys && streams * ((a.C + weight_keys - 1) / weight_keys) > 6 * kSms) weight_keys *= 2;
+    ctas += streams * ((a.C + weight_keys - 1) / weight_keys);
+  }
+  return launch_dependent(decode_join_kernel<T, D>, static_cast<unsigned>(ctas), kThreads, a.weight ? a.G * 8 : 0, st, a,
+                          row_warps, weight_keys);
+}
+
 template <typename T, int D, int TW>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
   using C = Cfg<T, D>;
@@ -1027,7 +786,6 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   cudaError_t e = set_up_kernel<decode_scores_kernel<T, D, TW>>(kWarps * C::kStages * C::kStageK + kMostCum, true);
   if (e == cudaSuccess)
     e = set_up_kernel<decode_values_kernel<T, D, TW>>(kWarps * C::kStages * C::kStageV + kMostCum, true);
-  if (e == cudaSuccess) e = set_up_kernel<decode_join_kernel<T, D>>(0, true);
   if (e != cudaSuccess) return e;
   // CTAs for the runs that there can be
   const int64_t shared_streams = static_cast<int64_t>(a.Hkv) * a.shared_rowblocks,
@@ -1047,20 +805,7 @@ cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx
   if (a.tc && (e = launch_decode_prefix(maps, a, true, ctx, st)) != cudaSuccess) return e;
   e = launch_dependent(decode_values_kernel<T, D, TW>, grid, kThreads, smem_values, st, a);
   if (e != cudaSuccess) return e;
-  // Few CTAs: a weight CTA takes as many keys, up to 4096, as leave about six per SM (starting the
-  // 6144 CTAs of one row or 512 keys each took most of 15 us at B64 H32/8 C4096).
-  // A CTA per row where rows are few and their partial results many.
-  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
-  const int row_warps = rows <= 2 * kSms && a.slots > 8 * (128 / D) ? kWarps : 1;
-  int64_t join = (rows * row_warps + kWarps - 1) / kWarps;
-  int weight_keys = kWeightKeys;
-  if (a.weight) {
-    const int64_t streams = static_cast<int64_t>(a.B) * a.Hkv;
-    while (weight_keys < 8 * kWeightKeys && streams * ((a.C + weight_keys - 1) / weight_keys) > 6 * kSms) weight_keys *= 2;
-    join += streams * ((a.C + weight_keys - 1) / weight_keys);
-  }
-  return launch_dependent(decode_join_kernel<T, D>, static_cast<unsigned>(join), kThreads, a.weight ? a.G * 8 : 0, st, a,
-                          row_warps, weight_keys);
+  return join<T, D>(a, st);
 }
 template <typename T, int D>
 cudaError_t go(const DecodeArgs& a, const PrefixMaps& maps, const LaunchCtx& ctx, cudaStream_t st) {
@@ -1131,6 +876,11 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   a->part_o = reinterpret_cast<float*>(piece(rows * a->slots * a->D));
   a->cum = reinterpret_cast<int*>(piece(a->B + 2));
   return at;
+}
+
+cudaError_t launch_decode_join(const DecodeArgs& a, bool bf16, cudaStream_t st) {
+  if (bf16) return a.D == 64 ? join<__nv_bfloat16, 64>(a, st) : join<__nv_bfloat16, 128>(a, st);
+  return a.D == 64 ? join<float, 64>(a, st) : join<float, 128>(a, st);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, const PrefixMaps& maps, const LaunchCtx& ctx,

@@ -217,6 +217,70 @@ cudaError_t launch_decode(const DecodeArgs& a, bool bf16, const PrefixMaps& maps
 cudaError_t launch_decode_prefix(const PrefixMaps& maps, const DecodeArgs& a, bool values, const LaunchCtx& ctx,
                                  cudaStream_t st);
 
+// Pages of a cache held in 4 bits (the layout: paged.cuh).
+struct PagePool {
+  uint8_t* base;
+  int64_t page_stride;          // bytes from page to page
+  int part;                     // bytes of a head's keys or values in a page
+  int pages, Hkv, D;
+  int page, shift;              // tokens of a page, 2^shift
+};
+// Keys and values quantised into pages, or read from them (page_rows.cu).
+struct PageRows {
+  PagePool pool;
+  const int32_t* table;         // [B, M] pages, -1: none
+  int M;
+  const int32_t *start, *limit; // [B]: token n of sequence b has slot start[b] + n (null: n); write: tokens from
+                                // limit[b] on are not stored; read: slots from limit[b] on are zeros (null: no limit)
+  const void *k, *v;            // write: [B, Hkv, N, D] with these strides (elements)
+  int64_t k_stride[3], v_stride[3];
+  void *k_out, *v_out;          // [B, Hkv, N, D] dense; write: what the cache holds, or null
+  int B, N;
+};
+cudaError_t launch_page_write(const PageRows& a, bool bf16, cudaStream_t st);
+cudaError_t launch_page_read(const PageRows& a, bool bf16, cudaStream_t st);
+
+// The page table (page_table.cu): rows replaced by others, pages handed out, pages moved together.
+struct PageFork {
+  int32_t *table, *length, *uses;
+  const int32_t* parent;
+  int B, M, pages;
+};
+struct PageReserve {
+  PagePool pool;
+  int32_t *table, *uses, *granted;
+  const int32_t *length, *count;
+  int B, M, tokens;
+  int per_row;                  // pages that a sequence's tokens may touch
+  int64_t page_bytes;
+  int32_t *place, *freed, *copy;   // workspace: [B per_row] ranks, as many free pages, [B][2] pages to copy from and to
+};
+struct PageCompact {
+  const uint8_t* from;
+  uint8_t* to;
+  int64_t from_stride, to_stride, page_bytes;
+  const int32_t *table, *uses;
+  int32_t *table_out, *uses_out, *live;
+  int B, M, pages, pages_out;
+  int32_t *rank, *order;        // workspace: [pages] each
+};
+constexpr int kMostForkRows = 8192;
+cudaError_t launch_page_fork(const PageFork& a, cudaStream_t st);
+cudaError_t launch_page_reserve(const PageReserve& a, cudaStream_t st);
+cudaError_t launch_page_compact(const PageCompact& a, cudaStream_t st);
+
+// One query token per sequence against its pages (decode_paged.cu).  a.C: the most tokens of a table row.
+struct PagedDecodeArgs {
+  DecodeArgs a;
+  PagePool pool;
+  const int32_t* table;
+  int M;
+};
+size_t plan_decode_paged(PagedDecodeArgs* p, char* base);
+cudaError_t launch_decode_paged(const PagedDecodeArgs& p, bool bf16, cudaStream_t st);
+// The join of a decode without weights (decode.cu).
+cudaError_t launch_decode_join(const DecodeArgs& a, bool bf16, cudaStream_t st);
+
 // From api.cu: where a launch reports timeouts, and the tensor map of a [BH, N, D] bf16 tensor
 // (box 64 x 128 rows, 128-byte swizzle).
 ra_status_t launch_context(LaunchCtx* ctx);

@@ -1,0 +1,328 @@
+// The page table of a paged cache: whose pages are whose.
+//
+//   table [B, M] pages of each sequence in order, -1: none;  uses [pages], in how many places of the table a page
+//   stands, 0: free.
+//
+//   fork     row b becomes what row parent[b] was, or empty; the uses follow.  Any reordering, in place: a CTA holds
+//            a few columns of the whole table in shared memory.  Counts are integers, so the atomics' order does not show.
+//   reserve  every page that the next tokens of a sequence touch and that is missing or has other users is replaced by a
+//            free one: the lowest free pages in the order of the sequences and their pages.  Of a shared page that
+//            holds tokens already the content is copied.  One cluster counts and ranks wants and free pages (the prefix
+//            sums cross its CTAs through distributed shared memory) and hands the pages out; a second launch copies.
+//   compact  the pages in use, in order, into another pool; ranks by the same cluster, then copies over the whole GPU.
+//
+// Bound: reserve by latency (a few dependent loads and three cluster barriers), the copies by HBM.
+#include "paged.cuh"
+
+namespace raattn {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32, kCluster = 8;
+constexpr int kCopyThreads = 256, kCopyAhead = 4;
+constexpr int kChunk = kCopyThreads * kCopyAhead * 16;   // bytes of a page that a CTA copies at a time
+
+__device__ __forceinline__ bool is_page(int id, int pages) { return static_cast<unsigned>(id) < static_cast<unsigned>(pages); }
+
+// ---------------------------------------------------------------------------------------------
+// fork
+// ---------------------------------------------------------------------------------------------
+template <int W>   // columns of a CTA
+__global__ void __launch_bounds__(kCopyThreads) page_fork_kernel(const PageFork a) {
+  extern __shared__ int old[];   // [B][W], then the lengths of all in the first CTA
+  const int c0 = blockIdx.x * W, n = a.B * W;
+  for (int i = threadIdx.x; i < n; i += kCopyThreads) {
+    const int b = i / W, c = c0 + i % W;
+    old[i] = c < a.M ? a.table[static_cast<int64_t>(b) * a.M + c] : -1;
+  }
+  int* lengths = old + n;
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.B; b += kCopyThreads) lengths[b] = a.length[b];
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kCopyThreads) {
+    const int b = i / W, c = c0 + i % W, from = a.parent[b];
+    if (c >= a.M || from == b) continue;
+    const int was = old[i], is = is_page(from, a.B) ? old[from * W + i % W] : -1;
+    if (was == is) continue;
+    a.table[static_cast<int64_t>(b) * a.M + c] = is;
+    if (is_page(was, a.pages)) atomicSub(a.uses + was, 1);
+    if (is_page(is, a.pages)) atomicAdd(a.uses + is, 1);
+  }
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < a.B; b += kCopyThreads) {
+      const int from = a.parent[b];
+      if (from != b) a.length[b] = is_page(from, a.B) ? lengths[from] : 0;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// ranks over a cluster
+// ---------------------------------------------------------------------------------------------
+// Exclusive prefix sums of two counts per warp over the warps of a cluster, and their totals.  All threads; counts are the same in
+// all lanes of a warp.
+struct ClusterSums {
+  int2 warp[kWarps];
+  int2 total;
+};
+__device__ __forceinline__ int2 cluster_exclusive(ClusterSums& s, int2 mine, int2* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if (lane == 0) s.warp[w] = mine;
+  __syncthreads();
+  int2 inc = s.warp[lane];
+  const int2 own = inc;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc.x, o), y = __shfl_up_sync(0xffffffffu, inc.y, o);
+    if (lane >= o) {
+      inc.x += x;
+      inc.y += y;
+    }
+  }
+  if (threadIdx.x == 31) s.total = inc;
+  int2 before = make_int2(__shfl_sync(0xffffffffu, inc.x - own.x, w), __shfl_sync(0xffffffffu, inc.y - own.y, w));
+  cluster_sync();
+  const uint32_t at = smem_u32(&s.total), rank = cluster_ctarank();
+  *total = make_int2(0, 0);
+#pragma unroll
+  for (uint32_t r = 0; r < kCluster; ++r) {
+    int x, y;
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(mapa_shared(at, r)) : "memory");
+    if (r < rank) {
+      before.x += x;
+      before.y += y;
+    }
+    total->x += x;
+    total->y += y;
+  }
+  return before;
+}
+
+// A warp's contiguous share [first, last) of n items, in whole steps of 32 R items.
+template <int R>
+__device__ __forceinline__ int2 share_of(int n) {
+  const int warps = kCluster * kWarps, w = static_cast<int>(cluster_ctarank()) * kWarps + (threadIdx.x >> 5);
+  const int64_t steps = (static_cast<int64_t>(n) + 32 * R - 1) / (32 * R), per = (steps + warps - 1) / warps * (32 * R);
+  const int64_t first = w * per;
+  return make_int2(static_cast<int>(first < n ? first : n), static_cast<int>(first + per < n ? first + per : n));
+}
+constexpr int kPer = 8;   // loads of a lane in flight
+
+// How many of a warp's pages are free (or, with LIVE, in use).
+template <bool LIVE>
+__device__ __forceinline__ int count_pages(const int32_t* uses, int2 range) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+  for (int p0 = range.x; p0 < range.y; p0 += 32 * kPer) {
+    int u[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = p0 + 32 * i + lane;
+      u[i] = p < range.y ? uses[p] : LIVE ? 0 : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) n += LIVE ? u[i] > 0 : u[i] == 0;
+  }
+  return __reduce_add_sync(0xffffffffu, n);
+}
+// f(page, uses, whether it counts, its rank) for a warp's pages; `rank`: of the warp's first that counts.
+template <bool LIVE, typename F>
+__device__ __forceinline__ void each_page(const int32_t* uses, int2 range, int rank, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int p0 = range.x; p0 < range.y; p0 += 32 * kPer) {
+    int u[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = p0 + 32 * i + lane;
+      u[i] = p < range.y ? uses[p] : LIVE ? 0 : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = p0 + 32 * i + lane;
+      const bool counts = LIVE ? u[i] > 0 : u[i] == 0;
+      const unsigned all = __ballot_sync(0xffffffffu, counts);
+      if (p < range.y) f(p, u[i], counts, rank + __popc(all & ((1u << lane) - 1u)));
+      rank += __popc(all);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// reserve
+// ---------------------------------------------------------------------------------------------
+// Place k of sequence b among the pages that its new tokens touch.
+struct Want {
+  int b, k, at, length, tokens;
+  int old;        // the page there, or -1
+  bool touched, wanted;
+};
+__device__ __forceinline__ Want want_of(const PageReserve& a, int item) {
+  Want w;
+  w.b = item / a.per_row;
+  w.k = item - w.b * a.per_row;
+  const int64_t most = static_cast<int64_t>(a.M) << a.pool.shift;
+  w.length = static_cast<int>(min(static_cast<int64_t>(max(a.length[w.b], 0)), most));
+  w.tokens = a.count ? min(max(a.count[w.b], 0), a.tokens) : a.tokens;
+  w.at = (w.length >> a.pool.shift) + w.k;
+  w.touched = w.tokens > 0 && w.at < a.M && (static_cast<int64_t>(w.at) << a.pool.shift) < static_cast<int64_t>(w.length) + w.tokens;
+  w.old = w.touched ? paged::page_at(a.pool, a.table + static_cast<int64_t>(w.b) * a.M, w.at) : -1;
+  return w;
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) page_reserve_kernel(const PageReserve a) {
+  __shared__ ClusterSums sums;
+  const int lane = threadIdx.x & 31, items = a.B * a.per_row;
+  const int2 mine = share_of<1>(items), pages = share_of<kPer>(a.pool.pages);
+  release_dependents();
+  // wants, left in the workspace as ranks within the warp's share: the uses that they go by change below
+  int wants = 0;
+  for (int i0 = mine.x; i0 < mine.y; i0 += 32) {
+    const int item = i0 + lane;
+    bool wanted = false;
+    if (item < mine.y) {
+      const Want w = want_of(a, item);
+      wanted = w.touched && (w.old < 0 || a.uses[w.old] > 1);
+      if (w.k == 0) {
+        const int64_t room = (static_cast<int64_t>(a.M) << a.pool.shift) - w.length;
+        a.granted[w.b] = static_cast<int>(min(static_cast<int64_t>(w.tokens), room));
+        a.copy[2 * w.b] = -1;
+      }
+    }
+    const unsigned all = __ballot_sync(0xffffffffu, wanted);
+    if (item < mine.y) a.place[item] = wanted ? wants + __popc(all & ((1u << lane) - 1u)) : -1;
+    wants += __popc(all);
+  }
+  int2 total;
+  const int2 before = cluster_exclusive(sums, make_int2(wants, count_pages<false>(a.uses, pages)), &total);
+  if (total.x > 0) {   // the same in all CTAs
+    each_page<false>(a.uses, pages, before.y, [&](int p, int, bool free, int rank) {
+      if (free && rank < total.x) a.freed[rank] = p;
+    });
+    cluster_sync();
+    for (int i0 = mine.x; i0 < mine.y; i0 += 32) {
+      const int item = i0 + lane;
+      if (item >= mine.y || a.place[item] < 0) continue;
+      const int rank = before.x + a.place[item];
+      const Want w = want_of(a, item);   // its own place in the table, which no other thread changes
+      if (rank < total.y) {
+        const int id = __ldcg(a.freed + rank);
+        a.table[static_cast<int64_t>(w.b) * a.M + w.at] = id;
+        a.uses[id] = 1;
+        if (w.old >= 0) {
+          atomicSub(a.uses + w.old, 1);
+          if (w.k == 0 && (w.length & (a.pool.page - 1))) {   // tokens that stay
+            a.copy[2 * w.b + 1] = id;
+            a.copy[2 * w.b] = w.old;
+          }
+        }
+      } else {
+        atomicMin(a.granted + w.b, max(static_cast<int>((static_cast<int64_t>(w.at) << a.pool.shift) - w.length), 0));
+      }
+    }
+  }
+  cluster_sync();   // no CTA ends while another reads its counts
+}
+
+// ---------------------------------------------------------------------------------------------
+// copies
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy_chunk(uint8_t* to, const uint8_t* from, int64_t at, int64_t bytes) {
+  uint4 x[kCopyAhead];
+#pragma unroll
+  for (int i = 0; i < kCopyAhead; ++i) {
+    const int64_t o = at + (i * kCopyThreads + threadIdx.x) * 16;
+    if (o < bytes) x[i] = __ldcs(reinterpret_cast<const uint4*>(from + o));
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyAhead; ++i) {
+    const int64_t o = at + (i * kCopyThreads + threadIdx.x) * 16;
+    if (o < bytes) __stcs(reinterpret_cast<uint4*>(to + o), x[i]);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageReserve a, int chunks) {
+  await_previous();
+  const int64_t items = static_cast<int64_t>(a.B) * chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int b = static_cast<int>(item / chunks);
+    const int from = __ldcg(a.copy + 2 * b);
+    if (from < 0) continue;
+    const int to = __ldcg(a.copy + 2 * b + 1);
+    copy_chunk(a.pool.base + to * a.pool.page_stride, a.pool.base + from * a.pool.page_stride,
+               (item - static_cast<int64_t>(b) * chunks) * kChunk, a.page_bytes);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------------------------
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) page_rank_kernel(const PageCompact a) {
+  __shared__ ClusterSums sums;
+  const int2 pages = share_of<kPer>(a.pages);
+  release_dependents();
+  int2 total;
+  const int2 before = cluster_exclusive(sums, make_int2(count_pages<true>(a.uses, pages), 0), &total);
+  each_page<true>(a.uses, pages, before.x, [&](int p, int uses, bool live, int rank) {
+    a.rank[p] = live && rank < a.pages_out ? rank : -1;
+    if (live && rank < a.pages_out) {
+      a.order[rank] = p;
+      a.uses_out[rank] = uses;
+    }
+  });
+  const int here = static_cast<int>(cluster_ctarank()) * kThreads + threadIdx.x;
+  for (int64_t p = static_cast<int64_t>(total.x) + here; p < a.pages_out; p += kCluster * kThreads) a.uses_out[p] = 0;
+  if (here == 0) a.live[0] = total.x;
+  cluster_sync();   // no CTA ends while another reads its counts
+}
+
+__global__ void __launch_bounds__(kCopyThreads) page_move_kernel(const PageCompact a, int chunks) {
+  await_previous();
+  const int64_t places = static_cast<int64_t>(a.B) * a.M;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; i < places;
+       i += static_cast<int64_t>(gridDim.x) * kCopyThreads) {
+    const int id = a.table[i];
+    a.table_out[i] = is_page(id, a.pages) ? __ldcg(a.rank + id) : -1;
+  }
+  const int64_t items = static_cast<int64_t>(min(__ldcg(a.live), a.pages_out)) * chunks;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int page = static_cast<int>(item / chunks);
+    copy_chunk(a.to + page * a.to_stride, a.from + __ldcg(a.order + page) * a.from_stride,
+               (item - static_cast<int64_t>(page) * chunks) * kChunk, a.page_bytes);
+  }
+}
+
+int chunks_of(int64_t page_bytes) { return static_cast<int>((page_bytes + kChunk - 1) / kChunk); }
+unsigned copy_grid(int64_t items) { return static_cast<unsigned>(items < 1 ? 1 : items < 8 * kSms ? items : 8 * kSms); }
+
+}  // namespace
+
+cudaError_t launch_page_fork(const PageFork& a, cudaStream_t st) {
+  constexpr int kWide = 8, kNarrow = 4;
+  constexpr int kMost = 220 * 1024;   // bytes of shared memory: W columns and the lengths
+  static_assert((kNarrow + 1) * kMostForkRows * 4 <= kMost, "every table fits");
+  const bool wide = (kWide + 1) * a.B * 4 <= kMost;
+  cudaError_t e = wide ? set_up_kernel<page_fork_kernel<kWide>>(kMost, false) : set_up_kernel<page_fork_kernel<kNarrow>>(kMost, false);
+  if (e != cudaSuccess) return e;
+  const int W = wide ? kWide : kNarrow, grid = (a.M + W - 1) / W, smem = (W + 1) * a.B * 4;
+  if (wide) page_fork_kernel<kWide><<<grid, kCopyThreads, smem, st>>>(a);
+  else page_fork_kernel<kNarrow><<<grid, kCopyThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_page_reserve(const PageReserve& a, cudaStream_t st) {
+  page_reserve_kernel<<<kCluster, kThreads, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int chunks = chunks_of(a.page_bytes);
+  return launch_dependent(page_copy_kernel, copy_grid(static_cast<int64_t>(a.B) * chunks), kCopyThreads, 0, st, a, chunks);
+}
+
+cudaError_t launch_page_compact(const PageCompact& a, cudaStream_t st) {
+  page_rank_kernel<<<kCluster, kThreads, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int chunks = chunks_of(a.page_bytes);
+  const int64_t most = a.pages < a.pages_out ? a.pages : a.pages_out, table = (static_cast<int64_t>(a.B) * a.M + kCopyThreads - 1) / kCopyThreads;
+  const int64_t items = most * chunks;
+  return launch_dependent(page_move_kernel, copy_grid(items > table ? items : table), kCopyThreads, 0, st, a, chunks);
+}
+
+}  // namespace raattn
