@@ -463,7 +463,7 @@ ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, co
 /*
  * A cache whose keys and values lie in pages, held in 4 bits.
  *
- * Pool.  `pages` pages, page_stride bytes apart (a multiple of 16), each [H_KV][2 (keys, values)] parts without
+ * Pool.  `pages` pages, page_stride bytes apart (a multiple of 16 below 2^31), each [H_KV][2 (keys, values)] parts without
  * gaps; a part holds `page` (16, 32, 64, 128 or 256) tokens in page * row bytes, row = D / 2 + D / 16, D = 64 or
  * 128.  A token's row of D elements is cut into G = D / 64 groups of 64 dimensions; a group is held as
  *   lo   the largest bfloat16 number that is not above its minimum (never -0),

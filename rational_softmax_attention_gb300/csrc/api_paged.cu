@@ -27,8 +27,8 @@ ra_status_t pool_of(PagePool* p, const void* pool, int64_t page_stride, int page
   if (shift_of(page) < 0 || (D != 64 && D != 128)) return RA_ERR_UNSUPPORTED;
   const int part = page * paged::row_bytes(D);
   if (Hkv > INT_MAX / (2 * part) || (pages > 1 && page_stride < static_cast<int64_t>(2) * Hkv * part)) return RA_ERR_ARG;
-  if (static_cast<int64_t>(M) * page > kMostTokens) return RA_ERR_ARG;
-  *p = PagePool{static_cast<uint8_t*>(const_cast<void*>(pool)), page_stride, part, pages, Hkv, D, page, shift_of(page)};
+  if (static_cast<int64_t>(M) * page > kMostTokens || page_stride > INT_MAX) return RA_ERR_ARG;
+  *p = PagePool{static_cast<uint8_t*>(const_cast<void*>(pool)), static_cast<int>(pages > 1 ? page_stride : 0), part, pages, Hkv, D, page, shift_of(page)};
   return RA_OK;
 }
 
@@ -112,7 +112,9 @@ ra_status_t ra_page_read(const void* pool, int64_t page_stride, const int32_t* t
 
 size_t ra_attention_decode_paged_workspace_size(int B, int H_Q, int H_KV, int M, int page, int D) {
   PagedDecodeArgs p{};
-  return decode_of(&p, B, H_Q, H_KV, M, page, D) == RA_OK ? plan_decode_paged(&p, nullptr) : 0;
+  if (decode_of(&p, B, H_Q, H_KV, M, page, D) != RA_OK) return 0;
+  const size_t wide = plan_decode_paged(&p, false, nullptr), narrow = plan_decode_paged(&p, true, nullptr);   // of either dtype
+  return wide > narrow ? wide : narrow;
 }
 
 ra_status_t ra_attention_decode_paged(const void* q, const void* pool, int64_t page_stride, const int32_t* table,
@@ -136,7 +138,7 @@ ra_status_t ra_attention_decode_paged(const void* q, const void* pool, int64_t p
   p.a.o = o;
   p.a.length = length;
   p.a.scale = scale;
-  if (plan_decode_paged(&p, static_cast<char*>(workspace)) == 0) return RA_ERR_UNSUPPORTED;
+  if (plan_decode_paged(&p, dtype == RA_BF16, static_cast<char*>(workspace)) == 0) return RA_ERR_UNSUPPORTED;
   return launch_decode_paged(p, dtype == RA_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? RA_OK : RA_ERR_LAUNCH;
 }
 
@@ -166,11 +168,12 @@ ra_status_t ra_page_reserve(void* pool, int64_t page_stride, int64_t page_bytes,
   if (!aligned(pool, 16) || !aligned(workspace, 16) || page_stride % 16 || page_bytes % 16 || page_bytes < 16) return RA_ERR_ARG;
   if (B < 1 || M < 1 || tokens < 1 || pages < 1 || page < 1 || (pages > 1 && page_stride < page_bytes)) return RA_ERR_ARG;
   if (!fits(B, M) || static_cast<int64_t>(M) * page > kMostTokens || tokens > kMostTokens) return RA_ERR_ARG;
+  if (page_stride > INT_MAX) return RA_ERR_ARG;
   if (shift_of(page) < 0) return RA_ERR_UNSUPPORTED;
   const int per_row = per_row_of(tokens, page);
   if (!fits(B, per_row)) return RA_ERR_ARG;
   PageReserve a{};
-  a.pool = PagePool{static_cast<uint8_t*>(pool), page_stride, 0, pages, 0, 0, page, shift_of(page)};
+  a.pool = PagePool{static_cast<uint8_t*>(pool), static_cast<int>(page_stride), 0, pages, 0, 0, page, shift_of(page)};
   a.table = table;
   a.uses = uses;
   a.granted = granted;

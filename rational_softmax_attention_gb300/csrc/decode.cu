@@ -878,11 +878,6 @@ size_t plan_decode(DecodeArgs* a, bool bf16, char* base) {
   return at;
 }
 
-cudaError_t launch_decode_join(const DecodeArgs& a, bool bf16, cudaStream_t st) {
-  if (bf16) return a.D == 64 ? join<__nv_bfloat16, 64>(a, st) : join<__nv_bfloat16, 128>(a, st);
-  return a.D == 64 ? join<float, 64>(a, st) : join<float, 128>(a, st);
-}
-
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, const PrefixMaps& maps, const LaunchCtx& ctx,
                           cudaStream_t st) {
   if (bf16) return a.D == 64 ? go<__nv_bfloat16, 64>(a, maps, ctx, st) : go<__nv_bfloat16, 128>(a, maps, ctx, st);

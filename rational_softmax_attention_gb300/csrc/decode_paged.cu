@@ -16,8 +16,9 @@
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
 //            by byte.  phi s goes in as fp16 times a power of two that follows the largest scale met so far (11 bits: 2^-11 of a weight
 //            at most, an eighth of what the output's rounding to bf16 costs, and the weights' errors differ); fp32 as two fp16.
-// Three launches, as in decode.cu, whose split, join and partial results these kernels share.  The scores of sixteen
+// Two launches, scores and values, with decode.cu's split; the last part of a row to be done joins them.  The scores of sixteen
 // keys stand in the workspace as the value products want them: key t at 4 (t % 4) + t / 4.
+#include <algorithm>
 #include <climits>
 #include <cuda_fp16.h>
 
@@ -30,8 +31,8 @@ namespace {
 using namespace decode;
 using namespace paged;
 
-constexpr int kCtasPerSm = 5, kCtas = kSms * kCtasPerSm;
 constexpr int kKeys = 32;                        // of a block: two products' M, or K
+constexpr int64_t kPrefetched = 1 << 18;          // numbers of a table that is fetched ahead: 1 MB
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 template <int D>
@@ -40,33 +41,38 @@ struct Cfg {
   static constexpr int kCodes = kKeys * D / 2;            // bytes of a block's codes
   static constexpr int kMeta = 4 * G;                     // bytes of a key's scales and minima
   static constexpr int kBlock = kKeys * row_bytes(D);
-  static constexpr int kStagesK = 4, kStagesV = 3;
+  static constexpr int kStagesK = 3, kStagesV = 3;
 };
-// CTAs of an SM that the registers have to leave room for: two fp16 for each weight or sixteen rows take more.
-template <typename T, int NT>
-__host__ __device__ constexpr int resident() { return sizeof(T) == 2 && NT == 1 ? kCtasPerSm : 3; }
+// CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
+// C16384, both kernels: 137 us with 4, 161 with 5, 166 with 6); two fp16 for each weight, or sixteen rows, take more registers.
+__host__ __device__ constexpr int resident(bool bf16, int tiles) { return bf16 && tiles == 1 ? 4 : 3; }
 // A stage of the values: the block, then eight or sixteen rows of scores.
 template <int D, int NT>
 __host__ __device__ constexpr int stage_values() { return Cfg<D>::kBlock + 8 * NT * kKeys * 4; }
+// A warp's ring of them, and behind it a block's scales and minima in fp32.
+template <int D, int NT>
+__host__ __device__ constexpr int ring_values() { return Cfg<D>::kStagesV * stage_values<D, NT>() + kKeys * 2 * Cfg<D>::kMeta; }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t u;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(addr));
-  return u;
+// The same with nothing to add to.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 u;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(addr));
-  return u;
-}
+// Loads that the compiler may move, unlike volatile ones: products and loads of neighbouring tiles mix.
+template <typename V>
+__device__ __forceinline__ V get(const char* p) { return *reinterpret_cast<const V*>(p); }
 __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -100,15 +106,15 @@ __host__ __device__ constexpr float code_unit() { return sizeof(T) == 4 ? 1.0f :
 template <int G>
 struct Meta {
   float s[G], lo[G];
-  __device__ __forceinline__ explicit Meta(uint32_t addr) {
+  __device__ __forceinline__ explicit Meta(const char* p) {
     if constexpr (G == 2) {
-      const uint2 u = lds64(addr);
+      const uint2 u = get<uint2>(p);
       s[0] = bf16_low(u.x);
       s[1] = bf16_high(u.x);
       lo[0] = bf16_low(u.y);
       lo[1] = bf16_high(u.y);
     } else {
-      const uint32_t u = lds32(addr);
+      const uint32_t u = get<uint32_t>(p);
       s[0] = bf16_low(u);
       lo[0] = bf16_high(u);
     }
@@ -116,15 +122,105 @@ struct Meta {
 };
 
 // ---------------------------------------------------------------------------------------------
+// the split
+// ---------------------------------------------------------------------------------------------
+// A team (a warp, or a CTA's four) has a run of blocks for one key head and up to sixteen of its query rows.
+// The blocks of all sequences, in order, are cut into runs of `per`, or with CUT each sequence for itself; every run
+// has a team for each head, next to one another, since the heads' parts of a page lie together: a warp
+// that moves from page to page on its own meets a new one for every 4.6 KB.
+struct PagedPart {
+  int b, kv, row0, rows;   // sequence, key head; rows within the head's G
+  int first, count, keys;  // blocks of the sequence; its keys
+  int slot, parts;         // its place among the sequence's parts
+};
+template <bool CUT>
+__device__ __forceinline__ int blocks_per_run(const PagedDecodeArgs& p, const int* cum, int longest) {
+  const DecodeArgs& a = p.a;
+  int per = max((cum[a.B] + a.runs - 1) / a.runs, 1);
+  per = max(per, (longest + a.slots - 2) / (a.slots - 1));   // a sequence of n blocks meets at most ceil(n / per) + 1 runs
+  return CUT && a.team > 1 ? (per + a.team - 1) / a.team * a.team : per;   // as many for each warp
+}
+// f(part) for the parts of this team's run.  All lanes.
+template <int TW, bool CUT, typename F>
+__device__ __forceinline__ void each_paged_part(const PagedDecodeArgs& pa, const int* cum, int per, F f) {
+  const DecodeArgs& a = pa.a;
+  const int heads = a.Hkv * a.own_rowblocks;
+  const int task = TW == 1 ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x, run = task / heads, head = task - run * heads;
+  PagedPart p;
+  p.kv = a.own_rowblocks == 1 ? head : head / a.own_rowblocks;
+  p.row0 = (head - p.kv * a.own_rowblocks) * kRows;
+  p.rows = min(a.G - p.row0, kRows);
+  if constexpr (CUT) {   // few sequences: 32 at a time
+    const int lane = threadIdx.x & 31;
+    int b = -1, i = run;
+    for (int b0 = 0; b0 < a.B && b < 0; b0 += 32) {
+      const int mine = b0 + lane < a.B ? (cum[b0 + lane + 1] - cum[b0 + lane] + per - 1) / per : 0;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, upto > i);
+      const int l = past ? __ffs(past) - 1 : 31;
+      const int before = __shfl_sync(0xffffffffu, upto - mine, l), all = __shfl_sync(0xffffffffu, upto, 31);
+      if (past) {
+        b = b0 + l;
+        i -= before;
+      } else {
+        i -= all;
+      }
+    }
+    if (b < 0) return;
+    const int blocks = cum[b + 1] - cum[b];
+    p.b = b;
+    p.keys = cum[a.B + 1 + b];
+    p.first = i * per;
+    p.count = min(blocks - p.first, per);
+    p.slot = i;
+    p.parts = (blocks + per - 1) / per;
+    f(p);
+  } else {
+    const int total = cum[a.B], end = static_cast<int>(min(static_cast<int64_t>(run + 1) * per, static_cast<int64_t>(total)));
+    for (int64_t u0 = static_cast<int64_t>(run) * per; u0 < end;) {
+      const int u = static_cast<int>(u0);
+      int lo = 0, hi = a.B - 1;   // the last b with cum[b] <= u: u lies in its blocks
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= u) lo = mid; else hi = mid - 1;
+      }
+      const int c0 = cum[lo], c1 = cum[lo + 1];
+      p.b = lo;
+      p.keys = cum[a.B + 1 + lo];
+      p.first = u - c0;
+      p.count = min(c1, end) - u;
+      p.slot = run - c0 / per;
+      p.parts = (c1 - 1) / per - c0 / per + 1;
+      u0 += p.count;
+      f(p);
+    }
+  }
+}
+template <int TW>
+__device__ __forceinline__ int blocks_of_warp(const PagedPart& p) { return (p.count - warp_of_team<TW>() + TW - 1) / TW; }
+// Row r of a part (its last one for those past it) as an index into [B, H_q], and its scores.
+__device__ __forceinline__ int row_of(const PagedPart& p, int r, const DecodeArgs& a) {
+  return p.b * a.Hq + p.kv * a.G + p.row0 + min(r, p.rows - 1);
+}
+__device__ __forceinline__ float* score_row(int row, const DecodeArgs& a) { return a.s_own + static_cast<int64_t>(row) * a.own_width; }
+
+// ---------------------------------------------------------------------------------------------
 // a warp's blocks into its ring
 // ---------------------------------------------------------------------------------------------
-__device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, int bytes) {   // zeros behind `bytes`
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, int bytes, uint64_t policy) {   // zeros behind `bytes`
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes), "l"(policy)
+               : "memory");
 }
 
-// Blocks first, first + step, .. of a part.  A page is at least sixteen keys, so a block's halves lie in a page
-// each: lane l holds the page of half l % 2 of block i0 + l / 2, and those of the next sixteen blocks are on
-// their way.  What no page holds and what lies behind the last key arrives as zeros: scales and minima of 0.
+// Blocks first, first + step, .. of a part.  The page numbers of their halves (a page is at least sixteen keys) come
+// through shared memory, sixteen blocks at a time and sixteen to thirty-two ahead.  What no page holds and what lies behind the
+// last key arrives as zeros: scales and minima of 0.
+constexpr int kIds = 32;   // blocks whose pages a warp has
 template <int D>
 struct Fetch {
   static constexpr int kLanesPerKey = D / 32;        // 16-byte chunks of a key's codes
@@ -133,47 +229,59 @@ struct Fetch {
   static constexpr int kMetaLanes = kKeys * Cfg<D>::kMeta / 16, kKeysPerChunk = 16 / Cfg<D>::kMeta;
   const PagePool& pool;
   const int32_t* row;
-  const uint8_t* base;
+  const uint8_t* base;   // with this lane's place in a block's codes
+  const int2* ids;       // pages of block i's halves: place i % kIds
   int first, step, blocks, keys, lane;
-  int now, next;
+  uint64_t policy;       // keys and values leave L2 first: the scores had better stay
 
-  __device__ __forceinline__ Fetch(const PagedDecodeArgs& p, const Part& part, int which, int warp, int warps, int blocks_)
-      : pool(p.pool), row(p.table + static_cast<int64_t>(part.b) * p.M), base(part_of(p.pool, 0, part.kv, which)),
-        first((part.first + warp) * kKeys), step(warps * kKeys), blocks(blocks_), keys(part.keys), lane(threadIdx.x & 31) {
-    now = pages(0);
-    next = pages(16);
+  // ids: kIds of this warp's, which nobody reads any more.  await() comes before the first block.
+  __device__ __forceinline__ Fetch(const PagedDecodeArgs& p, const PagedPart& part, int which, int warp, int warps, int blocks_,
+                                   const int2* ids_)
+      : pool(p.pool), row(p.table + static_cast<int64_t>(part.b) * p.M), ids(ids_), first((part.first + warp) * kKeys),
+        step(warps * kKeys), blocks(blocks_), keys(part.keys), lane(threadIdx.x & 31) {
+    base = part_of(p.pool, 0, part.kv, which) + lane * 16;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    pages(0);
+    pages(kIds / 2);
+    copy_commit();
   }
-  __device__ __forceinline__ int pages(int i0) const {
-    const int i = i0 + (lane >> 1), key = first + i * step + (lane & 1) * 16;
-    return i < blocks && key < keys ? page_at(pool, row, key >> pool.shift) : -1;
+  __device__ __forceinline__ void await() const {
+    copy_wait<0>();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void pages(int i0) const {   // lane l: half l % 2 of block i0 + l / 2
+    const int i = i0 + (lane >> 1), key = min(first + i * step + (lane & 1) * 16, keys - 1);
+    if (i < blocks)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(ids + i % kIds) + (lane & 1) * 4),
+                   "l"(row + (key >> pool.shift))
+                   : "memory");
   }
   __device__ __forceinline__ void operator()(uint32_t stage, int i) {
-    if ((i & 15) == 0 && i) {
-      now = next;
-      next = pages(i + 16);
-    }
-    const int key0 = first + i * step, mask = pool.page - 1;
-    const uint8_t* src[2];
-    int slot[2], left[2];   // the half's first slot in its page; keys of it that there are
+    if ((i & (kIds / 2 - 1)) == 0 && i) pages(i + kIds / 2);   // the other half is in use
+    stage += lane * 16;
+    const int key0 = first + i * step, slot = key0 & (pool.page - 1);
+    const int2 id = ids[i % kIds];
+    if (pool.page >= kKeys && key0 + kKeys <= keys && static_cast<unsigned>(id.x) < static_cast<unsigned>(pool.pages)) {
+      const uint8_t* src = base + static_cast<int64_t>(id.x) * pool.page_stride;
+      const uint8_t* codes = src + slot * (D / 2);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int id = __shfl_sync(0xffffffffu, now, 2 * (i & 15) + h);
-      src[h] = base + max(id, 0) * pool.page_stride;
-      slot[h] = (key0 + 16 * h) & mask;
-      left[h] = id < 0 ? 0 : keys - key0 - 16 * h;
-    }
+      for (int c = 0; c < kCopies; ++c) copy16_once(stage + c * 512, codes + c * 512, policy);
+      if (lane < kMetaLanes) copy16_once(stage + Cfg<D>::kCodes, src + pool.page * (D / 2) + slot * Cfg<D>::kMeta, policy);
+    } else {
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) {
-      constexpr int kPerHalf = kCopies / 2;
-      const int h = c / kPerHalf, key = c % kPerHalf * kKeysPerCopy + lane / kLanesPerKey;
-      copy16_part(stage + (c * 32 + lane) * 16, src[h] + slot[h] * (D / 2) + (c % kPerHalf * 32 + lane) * 16,
-                  key < left[h] ? 16 : 0);
-    }
-    if (lane < kMetaLanes) {
-      const int h = lane >= kMetaLanes / 2, key = (lane - h * (kMetaLanes / 2)) * kKeysPerChunk;
-      const int bytes = min(max(((h ? left[1] : left[0]) - key) * Cfg<D>::kMeta, 0), 16);
-      copy16_part(stage + Cfg<D>::kCodes + lane * 16,
-                  (h ? src[1] : src[0]) + pool.page * (D / 2) + ((h ? slot[1] : slot[0]) + key) * Cfg<D>::kMeta, bytes);
+      for (int h = 0; h < 2; ++h) {   // the block's halves
+        const int at = h ? id.y : id.x, in_page = (key0 + 16 * h) & (pool.page - 1);
+        const bool there = static_cast<unsigned>(at) < static_cast<unsigned>(pool.pages);
+        const int left = there ? keys - key0 - 16 * h : 0;   // keys of it that there are
+        const uint8_t* src = base + static_cast<int64_t>(there ? at : 0) * pool.page_stride;
+#pragma unroll
+        for (int c = 0; c < kCopies / 2; ++c)
+          copy16_part(stage + (h * (kCopies / 2) + c) * 512, src + in_page * (D / 2) + c * 512,
+                      c * kKeysPerCopy + lane / kLanesPerKey < left ? 16 : 0, policy);
+        if (lane < kMetaLanes / 2)
+          copy16_part(stage + Cfg<D>::kCodes + h * (kMetaLanes / 2) * 16, src + pool.page * (D / 2) + in_page * Cfg<D>::kMeta,
+                      min(max((left - lane * kKeysPerChunk) * Cfg<D>::kMeta, 0), 16), policy);
+      }
     }
   }
 };
@@ -189,24 +297,41 @@ struct Query {
   static constexpr int G = D / kGroup;
   static constexpr bool TWO = sizeof(T) == 4;
   uint32_t b[NT][G][4][2], rest[NT][G][TWO ? 4 : 1][2];
-  float sum[NT][G][2], unit[NT][2];   // of query rows 2 j, 2 j + 1: their sums over a group, and a score's unit
+  float sum[NT][G][2];   // of query rows 2 j, 2 j + 1: their sums over a group
 
-  __device__ __forceinline__ Query(const Part& p, const DecodeArgs& a) {
+  static constexpr int kWords = 16 * sizeof(T) / 16;   // 16-byte words of sixteen elements
+  struct Raw {
+    uint4 u[NT][G][kWords];
+    __device__ __forceinline__ Raw(const PagedPart& p, const DecodeArgs& a) {
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(row_of(p, t * 8 + (lane >> 2), a)) * D + 16 * (lane & 3);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) u[t][g][i] = __ldg(reinterpret_cast<const uint4*>(q + g * kGroup) + i);
+      }
+    }
+  };
+
+  // The rows' units go to `units`: what a score of 1 stands for, the same in all parts of a row.
+  __device__ __forceinline__ Query(const Raw& raw, const PagedPart& p, const DecodeArgs& a, float* units) {
     const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const T* q = static_cast<const T*>(a.q) + static_cast<int64_t>(row_of(p, t * 8 + r, a)) * D + 16 * j;
       float x[G][16], most = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        load(q + g * kGroup, x[g]);
+        values(raw.u[t][g], x[g]);
 #pragma unroll
         for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(x[g][i]));
       }
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
       most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const int e = max(static_cast<int>(__float_as_uint(most) >> 23) - 126, -100);   // most < 2^e
-      const float to = power_of_2(14 - e), of = power_of_2(e - 14 + (TWO ? 0 : 24));
+      const float to = power_of_2(14 - e);
+      if (j == 0 && t * 8 + r < p.rows) units[row_of(p, t * 8 + r, a)] = power_of_2(e - 14 + (TWO ? 0 : 24));
       float total[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -229,17 +354,15 @@ struct Query {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int from = 8 * j + 4 * c;
-        unit[t][c] = __shfl_sync(0xffffffffu, of, from);
 #pragma unroll
         for (int g = 0; g < G; ++g) sum[t][g][c] = __shfl_sync(0xffffffffu, total[g], from) * code_unit<T>();
       }
     }
   }
-  static __device__ __forceinline__ void load(const __nv_bfloat16* q, float (&x)[16]) {
+  static __device__ __forceinline__ void values(const uint4 (&u)[2], float (&x)[16]) {   // bf16
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 u = reinterpret_cast<const uint4*>(q)[i];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         x[8 * i + 2 * k] = bf16_low(w[k]);
@@ -247,78 +370,79 @@ struct Query {
       }
     }
   }
-  static __device__ __forceinline__ void load(const float* q, float (&x)[16]) {
+  static __device__ __forceinline__ void values(const uint4 (&u)[4], float (&x)[16]) {   // fp32
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 u = reinterpret_cast<const float4*>(q)[i];
-      x[4 * i] = u.x;
-      x[4 * i + 1] = u.y;
-      x[4 * i + 2] = u.z;
-      x[4 * i + 3] = u.w;
+      x[4 * i] = __uint_as_float(u[i].x);
+      x[4 * i + 1] = __uint_as_float(u[i].y);
+      x[4 * i + 2] = __uint_as_float(u[i].z);
+      x[4 * i + 3] = __uint_as_float(u[i].w);
     }
   }
 };
 
 template <typename T, int D, int TW, int NT>
-__device__ __forceinline__ void part_scores(const Part& p, const PagedDecodeArgs& pa, uint32_t ring, float* best_s) {
+__device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int2* ids, float* best_s) {
   using C = Cfg<D>;
   constexpr int G = C::G;
   constexpr bool TWO = sizeof(T) == 4;
   const DecodeArgs& a = pa.a;
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
   const int mine = blocks_of_warp<TW>(p);
-  Fetch<D> fetch(pa, p, 0, warp_of_team<TW>(), TW, mine);
+  Fetch<D> fetch(pa, p, 0, warp_of_team<TW>(), TW, mine, ids);
+  const typename Query<T, D, NT>::Raw raw(p, a);
+  fetch.await();
 #pragma unroll
   for (int i = 0; i < C::kStagesK - 1; ++i) {
-    if (i < mine) fetch(ring + i * C::kBlock, i);
+    if (i < mine) fetch(smem_u32(ring) + i * C::kBlock, i);
     copy_commit();
   }
-  const Query<T, D, NT> q(p, a);
+  const Query<T, D, NT> q(raw, p, a, pa.unit);
   const int first = (p.first + warp_of_team<TW>()) * kKeys, at = (r & 3) * 4 + (r >> 2);
   float* out[NT][2];
+  bool there[NT][2];
   float best[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      out[t][c] = score_row(p, row_of(p, t * 8 + 2 * j + c, a), a) + at;
+      out[t][c] = score_row(row_of(p, t * 8 + 2 * j + c, a), a) + first + at;
+      there[t][c] = t * 8 + 2 * j + c < p.rows;
       best[t][c] = -kInf;
     }
   // this lane's 16 bytes (D = 128) or 8 of key r: the halves' order depends on the key's bit 1, which is r's
   const int chunk = r * (D / 2) + (G == 2 ? (16 * j) ^ ((r & 2) << 4) : 8 * j), meta = C::kCodes + r * C::kMeta;
-  for (int i = 0; i < mine; ++i) {
+  int left = p.keys - first;   // keys from the block's first on
+  const char *stage = ring, *to = ring + (C::kStagesK - 1) * C::kBlock;
+  for (int i = 0; i < mine; ++i, left -= TW * kKeys) {
     copy_wait<C::kStagesK - 2>();
     __syncwarp();   // block i has landed for all lanes, and all have read block i - 1
-    const int ahead = i + C::kStagesK - 1;
-    if (ahead < mine) fetch(ring + ahead % C::kStagesK * C::kBlock, ahead);
+    if (i + C::kStagesK - 1 < mine) fetch(smem_u32(to), i + C::kStagesK - 1);
     copy_commit();
-    const uint32_t stage = ring + i % C::kStagesK * C::kBlock;
-    const int key0 = first + i * (TW * kKeys);
+    to = to == ring + (C::kStagesK - 1) * C::kBlock ? ring : to + C::kBlock;
+    float z[kKeys / 16][NT][4];
 #pragma unroll
     for (int tile = 0; tile < kKeys / 16; ++tile) {
       uint32_t x[2][G][2];   // keys r, r + 8; words 2 j, 2 j + 1 of the groups
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t src = stage + chunk + (tile * 16 + h * 8) * (D / 2);
+        const char* src = stage + chunk + (tile * 16 + h * 8) * (D / 2);
         if constexpr (G == 2) {
-          const uint4 u = lds128(src);
+          const uint4 u = get<uint4>(src);
           x[h][0][0] = u.x;
           x[h][1][0] = u.y;
           x[h][0][1] = u.z;
           x[h][1][1] = u.w;
         } else {
-          const uint2 u = lds64(src);
+          const uint2 u = get<uint2>(src);
           x[h][0][0] = u.x;
           x[h][0][1] = u.y;
         }
       }
       const Meta<G> m0(stage + meta + tile * 16 * C::kMeta), m1(stage + meta + (tile * 16 + 8) * C::kMeta);
-      float z[NT][4];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float acc[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t u = x[0][g][k >> 1] >> (k & 1) * 8, v = x[1][g][k >> 1] >> (k & 1) * 8;
@@ -326,7 +450,8 @@ __device__ __forceinline__ void part_scores(const Part& p, const PagedDecodeArgs
                          a3 = codes2<TWO>(v, kHigh);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma_f16(acc[t], a0, a1, a2, a3, q.b[t][g][k][0], q.b[t][g][k][1]);
+            if (k == 0) mma_f16_first(acc[t], a0, a1, a2, a3, q.b[t][g][k][0], q.b[t][g][k][1]);
+            else mma_f16(acc[t], a0, a1, a2, a3, q.b[t][g][k][0], q.b[t][g][k][1]);
             if constexpr (TWO) mma_f16(acc[t], a0, a1, a2, a3, q.rest[t][g][k][0], q.rest[t][g][k][1]);
           }
         }
@@ -335,20 +460,37 @@ __device__ __forceinline__ void part_scores(const Part& p, const PagedDecodeArgs
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float lo = e < 2 ? m0.lo[g] : m1.lo[g], s = e < 2 ? m0.s[g] : m1.s[g], w = q.sum[t][g][e & 1];
-            z[t][e] = g ? fmaf(s, acc[t][e], fmaf(lo, w, z[t][e])) : fmaf(s, acc[t][e], lo * w);
+            z[tile][t][e] = g ? fmaf(s, acc[t][e], fmaf(lo, w, z[tile][t][e])) : fmaf(s, acc[t][e], lo * w);
           }
       }
-      const int key = key0 + tile * 16;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = e & 1, h = e >> 1;
-          const float s = key + r + 8 * h < p.keys ? z[t][e] * q.unit[t][c] : -kInf;
-          best[t][c] = fmaxf(best[t][c], s);
-          if (t * 8 + 2 * j + c < p.rows) out[t][c][key + 2 * h] = s;
-        }
     }
+    if (left < kKeys) {   // the last block may have fewer
+#pragma unroll
+      for (int tile = 0; tile < kKeys / 16; ++tile)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (tile * 16 + r + 8 * (e >> 1) >= left) z[tile][t][e] = -kInf;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int tile = 0; tile < kKeys / 16; ++tile) {
+          best[t][c] = fmaxf(best[t][c], fmaxf(z[tile][t][c], z[tile][t][2 + c]));
+          if (there[t][c]) {
+            out[t][c][tile * 16] = z[tile][t][c];
+            out[t][c][tile * 16 + 2] = z[tile][t][2 + c];
+          }
+        }
+      }
+    stage = stage == ring + (C::kStagesK - 1) * C::kBlock ? ring : stage + C::kBlock;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) out[t][c] += TW * kKeys;
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -360,23 +502,23 @@ __device__ __forceinline__ void part_scores(const Part& p, const PagedDecodeArgs
     }
 }
 
-template <typename T, int D, int TW, int NT>
-__global__ void __launch_bounds__(kThreads, resident<T, NT>()) paged_scores_kernel(const PagedDecodeArgs pa) {
+template <typename T, int D, int TW, int NT, bool CUT>
+__global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_scores_kernel(const PagedDecodeArgs pa) {
   extern __shared__ uint4 dyn[];
   constexpr int kRing = Cfg<D>::kStagesK * Cfg<D>::kBlock;
   const DecodeArgs& a = pa.a;
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
+  __shared__ int2 ids[kWarps][kIds];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   release_dependents();   // the next kernel's first values are on their way while this one ends
-  int longest;
-  const Split s = make_split<kKeys>(cum, a, &longest);
-  if (blockIdx.x == 0) {   // for the join
-    for (int b = threadIdx.x; b <= a.B; b += kThreads) a.cum[b] = cum[b];
-    if (threadIdx.x == 0) a.cum[a.B + 1] = longest;
-  }
-  each_part<TW>(team, cum, s, a, [&](const Part& p) {
-    part_scores<T, D, TW, NT>(p, pa, smem_u32(dyn) + warp * kRing, best);
+  // the page numbers, if they are few, are on their way while the split is made
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 32, table = static_cast<int64_t>(a.B) * pa.M;
+  if (at < table && table <= kPrefetched) asm volatile("prefetch.global.L2 [%0];" ::"l"(pa.table + at));
+  const int per = blocks_per_run<CUT>(pa, cum, count_blocks<kKeys>(cum, a));
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.B * a.Hkv * a.own_rowblocks; i += gridDim.x * kThreads) pa.done[i] = 0;
+  each_paged_part<TW, CUT>(pa, cum, per, [&](const PagedPart& p) {
+    part_scores<T, D, TW, NT>(p, pa, reinterpret_cast<char*>(dyn) + warp * kRing, ids[warp], best);
     team_sync<TW>();
     if (tt < p.rows) {
       float m = best[team * TW * kRows + tt];
@@ -391,24 +533,23 @@ __global__ void __launch_bounds__(kThreads, resident<T, NT>()) paged_scores_kern
 // ---------------------------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------------------------
-// phi of four scores, from their distances to the maximum: w = (1 + u) / 2 by a saturating FMA, so that -inf gives
-// w = 1; q = 1 / w - 1 with one reciprocal for two (phi.cuh).
-__device__ __forceinline__ void phi4(const float4& z, float m, float c2, float (&f)[4]) {
-  const float2 A = make_float2(fma_sat(m - z.x, c2, 0.5f), fma_sat(m - z.y, c2, 0.5f));
-  const float2 B = make_float2(fma_sat(m - z.z, c2, 0.5f), fma_sat(m - z.w, c2, 0.5f));
+// phi of four scores z, from their distances to the maximum m: w = (1 + u) / 2 by a saturating FMA, so that -inf gives
+// w = 1; q = 1 / w - 1 with one reciprocal for two (phi.cuh).  c2: scale / 32 in units of the scores.
+__device__ __forceinline__ void phi4(const float4& z, float m, float c2, float2& x, float2& y) {
+  const float2 minus1 = make_float2(-1.0f, -1.0f), mm = make_float2(m, m);
+  const float2 d = __ffma2_rn(make_float2(z.x, z.y), minus1, mm), e = __ffma2_rn(make_float2(z.z, z.w), minus1, mm);
+  const float2 A = make_float2(fma_sat(d.x, c2, 0.5f), fma_sat(d.y, c2, 0.5f));
+  const float2 B = make_float2(fma_sat(e.x, c2, 0.5f), fma_sat(e.y, c2, 0.5f));
   const float2 P = __fmul2_rn(A, B);
-  const float2 R = make_float2(rcp_approx(P.x), rcp_approx(P.y)), minus1 = make_float2(-1.0f, -1.0f);
-  float2 x = __ffma2_rn(R, B, minus1), y = __ffma2_rn(R, A, minus1);
+  const float2 R = make_float2(rcp_approx(P.x), rcp_approx(P.y));
+  x = __ffma2_rn(R, B, minus1);
+  y = __ffma2_rn(R, A, minus1);
   x = __fmul2_rn(x, x);
   y = __fmul2_rn(y, y);
   x = __fmul2_rn(x, x);
   y = __fmul2_rn(y, y);
   x = __fmul2_rn(x, x);
   y = __fmul2_rn(y, y);
-  f[0] = x.x;
-  f[1] = x.y;
-  f[2] = y.x;
-  f[3] = y.y;
 }
 
 // Where piece c (four keys) of row r's scores stands: the reads of eight lanes (two rows by four pieces) meet no
@@ -419,69 +560,76 @@ __device__ __forceinline__ int piece_of(int r, int c) { return c ^ ((r & 1) << 2
 // rows r and r + 8 of the A operand of product n stand for dimensions 8 r + 2 n and 8 r + 2 n + 1, the latter sixteen times as
 // large.  The weights of query row r at the same keys are the B operand.
 template <typename T, int D, int TW, int NT>
-__device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs& pa, const Split& s, const int* cum,
-                                            uint32_t ring, char* ring_ptr, float* rowm, float* sums) {
+__device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int2* ids, float* rowm,
+                                            float* sums) {
   using C = Cfg<D>;
   constexpr int G = C::G, kStage = stage_values<D, NT>(), S = C::kStagesV;
   constexpr bool TWO = sizeof(T) == 4;
   const DecodeArgs& a = pa.a;
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
   const int mine = blocks_of_warp<TW>(p), first = (p.first + warp_of_team<TW>()) * kKeys;
-  Fetch<D> fetch(pa, p, 1, warp_of_team<TW>(), TW, mine);
+  Fetch<D> fetch(pa, p, 1, warp_of_team<TW>(), TW, mine, ids);
   const float* score[2 * NT];   // lane's piece of rows lane / 8 + 4 i
 #pragma unroll
-  for (int i = 0; i < 2 * NT; ++i) score[i] = score_row(p, row_of(p, (lane >> 3) + 4 * i, a), a) + first + (lane & 7) * 4;
+  for (int i = 0; i < 2 * NT; ++i) score[i] = score_row(row_of(p, (lane >> 3) + 4 * i, a), a) + first + (lane & 7) * 4;
   auto fetch_scores = [&](uint32_t stage, int i) {
 #pragma unroll
     for (int k = 0; k < 2 * NT; ++k) {
       const int row = (lane >> 3) + 4 * k;
       if (row < p.rows)
-        copy16_part(stage + C::kBlock + (row * 8 + piece_of(row, lane & 7)) * 16, score[k] + i * (TW * kKeys), 16);
+        copy16(stage + C::kBlock + (row * 8 + piece_of(row, lane & 7)) * 16, score[k] + i * (TW * kKeys), true);
     }
   };
+  fetch.await();
   // the first blocks of a part do not wait for the scores
 #pragma unroll
   for (int i = 0; i < S - 1; ++i)
-    if (i < mine) fetch(ring + i * kStage, i);
+    if (i < mine) fetch(smem_u32(ring) + i * kStage, i);
   await_previous();
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) {
-    if (i < mine) fetch_scores(ring + i * kStage, i);
+    if (i < mine) fetch_scores(smem_u32(ring) + i * kStage, i);
     copy_commit();
   }
-  part_maxima<TW>(rowm, p, cum, s, a);
+  {   // the rows' maxima over all parts, each by 2 TW of the team's threads
+    const int tt = threadIdx.x % (32 * TW), row = tt / (2 * TW);
+    const float most = fold_slots<2 * TW>(a.row_max + static_cast<int64_t>(row_of(p, row, a)) * a.slots, 0, p.parts, 0,
+                                          tt % (2 * TW), -kInf, [](float x, float y) { return fmaxf(x, y); });
+    if (tt % (2 * TW) == 0) rowm[row] = most;
+  }
   team_sync<TW>();
-  float m[NT], total[NT], low[NT][G], acc[NT][G][4][4];
+  float m[NT], c2[NT], total[NT], acc[NT][G][4][4];
+  float2 low[NT];   // of the groups (D = 64: the first)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     m[t] = rowm[t * 8 + r];
     if (m[t] == -kInf) m[t] = 0.0f;
+    c2[t] = a.scale * (TWO ? 1.0f : 0.03125f) * __ldcg(pa.unit + row_of(p, t * 8 + r, a));
     total[t] = 0.0f;
+    low[t] = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      low[t][g] = 0.0f;
+    for (int g = 0; g < G; ++g)
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[t][g][n][0] = acc[t][g][n][1] = acc[t][g][n][2] = acc[t][g][n][3] = 0.0f;
-    }
   }
-  const float c2 = a.scale * 0.03125f;
   int exponent = -100;   // every scale met so far is below 2^exponent
-  float unit = power_of_2(14 - exponent);
   const int word = word_offset<G>(0, r, j);   // the halves' order: bit 1 of the key's slot is j's
+  float* metas = reinterpret_cast<float*>(ring + S * kStage);
+  const char *stage = ring, *to = ring + (S - 1) * kStage;
   for (int i = 0; i < mine; ++i) {
     copy_wait<S - 2>();
     __syncwarp();
-    const int ahead = i + S - 1;
-    if (ahead < mine) {
-      fetch(ring + ahead % S * kStage, ahead);
-      fetch_scores(ring + ahead % S * kStage, ahead);
+    if (i + S - 1 < mine) {
+      fetch(smem_u32(to), i + S - 1);
+      fetch_scores(smem_u32(to), i + S - 1);
     }
     copy_commit();
-    const uint32_t stage = ring + i % S * kStage;
-    {   // bits of bf16 scales, which are not negative, are in their order
-      const uint32_t w = lds32(stage + C::kCodes + lane * C::kMeta);
-      const uint32_t most = __reduce_max_sync(0xffffffffu, G == 2 ? max(w & 0xffffu, w >> 16) : w & 0xffffu);
-      const int e = static_cast<int>(most >> 7) - 126;
+    to = to == ring + (S - 1) * kStage ? ring : to + kStage;
+    {   // a key's scales, times a power of two, and minima by each lane
+      const Meta<G> meta(stage + C::kCodes + lane * C::kMeta);
+      // the bits of scales, which are not negative, are in their order
+      const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(G == 2 ? fmaxf(meta.s[0], meta.s[1]) : meta.s[0]));
+      const int e = static_cast<int>(most >> 23) - 126;
       if (e > exponent) {
         const float f = power_of_2(exponent - e);
 #pragma unroll
@@ -493,55 +641,70 @@ __device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs
 #pragma unroll
               for (int k = 0; k < 4; ++k) acc[t][g][n][k] *= f;
         exponent = e;
-        unit = power_of_2(14 - e);
       }
+      const float unit = power_of_2(14 - exponent);
+      if constexpr (G == 2)
+        reinterpret_cast<float4*>(metas)[lane] = make_float4(meta.s[0] * unit, meta.s[1] * unit, meta.lo[0], meta.lo[1]);
+      else
+        reinterpret_cast<float2*>(metas)[lane] = make_float2(meta.s[0] * unit, meta.lo[0]);
+      __syncwarp();
     }
+    float f[kKeys / 16][NT][4];
+    bool live = false;   // some weight that is not 0 (a NaN is not)
 #pragma unroll
-    for (int tile = 0; tile < kKeys / 16; ++tile) {
-      float f[NT][4];
-      bool live = false;   // some weight that is not 0 (a NaN is not)
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int tile = 0; tile < kKeys / 16; ++tile) {
+        float* w = f[tile][t];
+        w[0] = w[1] = w[2] = w[3] = 0.0f;
         if (t * 8 + r < p.rows) {
-          const uint4 u = lds128(stage + C::kBlock + ((t * 8 + r) * 8 + piece_of(r, tile * 4 + j)) * 16);
-          const float4 z = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+          const float4 z = get<float4>(stage + C::kBlock + ((t * 8 + r) * 8 + piece_of(r, tile * 4 + j)) * 16);
           if constexpr (TWO) {
-            f[t][0] = phi_exact((m[t] - z.x) * a.scale);
-            f[t][1] = phi_exact((m[t] - z.y) * a.scale);
-            f[t][2] = phi_exact((m[t] - z.z) * a.scale);
-            f[t][3] = phi_exact((m[t] - z.w) * a.scale);
+            w[0] = phi_exact((m[t] - z.x) * c2[t]);
+            w[1] = phi_exact((m[t] - z.y) * c2[t]);
+            w[2] = phi_exact((m[t] - z.z) * c2[t]);
+            w[3] = phi_exact((m[t] - z.w) * c2[t]);
           } else {
-            phi4(z, m[t], c2, f[t]);
+            float2 x, y;
+            phi4(z, m[t], c2[t], x, y);
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = y.x;
+            w[3] = y.y;
           }
-        } else {
-          f[t][0] = f[t][1] = f[t][2] = f[t][3] = 0.0f;
         }
-        const float all = (f[t][0] + f[t][1]) + (f[t][2] + f[t][3]);
+        const float all = (w[0] + w[1]) + (w[2] + w[3]);
         total[t] += all;
         live |= all != 0.0f;
       }
-      if (!__any_sync(0xffffffffu, live)) continue;
+    }
+    const bool any = __any_sync(0xffffffffu, live);
+#pragma unroll
+    for (int tile = 0; any && tile < kKeys / 16; ++tile) {
       uint32_t x[4][G];
-      float weight[NT][G][4];
+      float2 weight[NT][4];   // of the groups
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int key = tile * 16 + j + 4 * k;
-        const uint32_t src = stage + key * (D / 2) + word;
+        const char* src = stage + key * (D / 2) + word;
         if constexpr (G == 2) {
-          const uint2 u = lds64(src);
+          const uint2 u = get<uint2>(src);
           x[k][0] = u.x;
           x[k][1] = u.y;
+          const float4 meta = reinterpret_cast<const float4*>(metas)[key];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float2 ff = make_float2(f[tile][t][k], f[tile][t][k]);
+            weight[t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
+            low[t] = __ffma2_rn(ff, make_float2(meta.z, meta.w), low[t]);
+          }
         } else {
-          x[k][0] = lds32(src);
-        }
-        const Meta<G> meta(stage + C::kCodes + key * C::kMeta);
+          x[k][0] = get<uint32_t>(src);
+          const float2 meta = reinterpret_cast<const float2*>(metas)[key];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float fu = f[t][k] * unit;
-#pragma unroll
-          for (int g = 0; g < G; ++g) {
-            weight[t][g][k] = fu * meta.s[g];
-            low[t][g] = fmaf(f[t][k], meta.lo[g], low[t][g]);
+          for (int t = 0; t < NT; ++t) {
+            weight[t][k].x = f[tile][t][k] * meta.x;
+            low[t].x = fmaf(f[tile][t][k], meta.y, low[t].x);
           }
         }
       }
@@ -550,8 +713,9 @@ __device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs
         uint32_t b[NT][2], rest[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          split_half2<TWO>(weight[t][g][0], weight[t][g][1], b[t][0], rest[t][0]);
-          split_half2<TWO>(weight[t][g][2], weight[t][g][3], b[t][1], rest[t][1]);
+          const float2* w = weight[t];
+          split_half2<TWO>(g ? w[0].y : w[0].x, g ? w[1].y : w[1].x, b[t][0], rest[t][0]);
+          split_half2<TWO>(g ? w[2].y : w[2].x, g ? w[3].y : w[3].x, b[t][1], rest[t][1]);
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -563,8 +727,8 @@ __device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             if constexpr (TWO) {
-              float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_f16(c, a0, a1, a2, a3, rest[t][0], rest[t][1]);
+              float c[4];
+              mma_f16_first(c, a0, a1, a2, a3, rest[t][0], rest[t][1]);
               mma_f16(c, a0, a1, a2, a3, b[t][0], b[t][1]);
 #pragma unroll
               for (int k = 0; k < 4; ++k) acc[t][g][n][k] += c[k];
@@ -575,19 +739,20 @@ __device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs
         }
       }
     }
+    stage = stage == ring + (S - 1) * kStage ? ring : stage + kStage;
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       total[t] += __shfl_xor_sync(0xffffffffu, total[t], o);
-#pragma unroll
-      for (int g = 0; g < G; ++g) low[t][g] += __shfl_xor_sync(0xffffffffu, low[t][g], o);
+      low[t].x += __shfl_xor_sync(0xffffffffu, low[t].x, o);
+      if (G == 2) low[t].y += __shfl_xor_sync(0xffffffffu, low[t].y, o);
     }
     if (j == 0) sums[(threadIdx.x >> 5) * kRows + t * 8 + r] = total[t];
   }
   __syncwarp();   // this warp's blocks have been read: its sums into their place
-  float* out = reinterpret_cast<float*>(ring_ptr);
+  float* out = reinterpret_cast<float*>(ring);
   const float back = power_of_2(exponent), undo = 0x1p-14f / code_unit<T>();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -596,7 +761,7 @@ __device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int row = t * 8 + 2 * j + c;
-        const float lo = __shfl_sync(0xffffffffu, low[t][g], 8 * j + 4 * c);
+        const float lo = __shfl_sync(0xffffffffu, g ? low[t].y : low[t].x, 8 * j + 4 * c);
         float y[8];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -611,96 +776,160 @@ __device__ __forceinline__ void part_values(const Part& p, const PagedDecodeArgs
       }
 }
 
-template <typename T, int D, int TW, int NT>
-__global__ void __launch_bounds__(kThreads, resident<T, NT>()) paged_values_kernel(const PagedDecodeArgs pa) {
+template <typename T>
+__device__ __forceinline__ void put4(void* o, int64_t at, const float4& f, float inv) {
+  if constexpr (sizeof(T) == 2)
+    static_cast<uint2*>(o)[at] = make_uint2(pack_bf16x2(f.x * inv, f.y * inv), pack_bf16x2(f.z * inv, f.w * inv));
+  else
+    static_cast<float4*>(o)[at] = make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
+}
+__device__ __forceinline__ float4 add4(const float4& x, const float4& y) {
+  return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+}
+
+// The output rows of a stream from its parts' sums, in their order, by the team of the last part to be done.
+template <typename T, int D, int TW>
+__device__ __forceinline__ void join_rows(const PagedPart& p, const DecodeArgs& a, int parts) {
+  constexpr int kRowThreads = D / 4;   // of a row
+  const int tt = threadIdx.x % (32 * TW);
+  for (int e = tt; e < p.rows * kRowThreads; e += 32 * TW) {
+    const int row = row_of(p, e / kRowThreads, a), c = e % kRowThreads;
+    const int64_t at = static_cast<int64_t>(row) * a.slots;
+    const float4* x = reinterpret_cast<const float4*>(a.part_o + at * D) + c;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float total = 0.0f;
+    for (int i0 = 0; i0 < parts; i0 += 8) {   // eight parts at a time in flight
+      float4 y[8];
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = i0 + i < parts;
+        y[i] = in ? __ldcg(x + static_cast<int64_t>(i0 + i) * kRowThreads) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        f[i] = in ? __ldcg(a.part_sum + at + i0 + i) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum = add4(sum, y[i]);
+        total += f[i];
+      }
+    }
+    put4<T>(a.o, static_cast<int64_t>(row) * kRowThreads + c, sum, total != 0.0f ? 1.0f / total : 0.0f);
+  }
+}
+
+template <typename T, int D, int TW, int NT, bool CUT>
+__global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_values_kernel(const PagedDecodeArgs pa) {
   extern __shared__ uint4 dyn[];
-  constexpr int kRing = Cfg<D>::kStagesV * stage_values<D, NT>();
+  constexpr int kRing = ring_values<D, NT>();
   static_assert(kRing >= 8 * NT * D * 4, "a warp's partial sums fit its ring");
   const DecodeArgs& a = pa.a;
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float rowm_s[kWarps / TW * kRows], sums[kWarps * kRows];
+  __shared__ int2 ids[kWarps][kIds];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
-  int longest;
-  const Split s = make_split<kKeys>(cum, a, &longest);
-  each_part<TW>(team, cum, s, a, [&](const Part& p) {
-    part_values<T, D, TW, NT>(p, pa, s, cum, smem_u32(ring), ring, rowm_s + team * kRows, sums);
+  const int per = blocks_per_run<CUT>(pa, cum, count_blocks<kKeys>(cum, a));
+  __shared__ int last_s[kWarps / TW];
+  each_paged_part<TW, CUT>(pa, cum, per, [&](const PagedPart& p) {
+    part_values<T, D, TW, NT>(p, pa, ring, ids[warp], rowm_s + team * kRows, sums);
+    const int parts = p.parts;
     team_sync<TW>();
-    if (tt < p.rows) {
-      float f = sums[team * TW * kRows + tt];
+    const auto sum_of = [&](int row) {
+      float f = sums[team * TW * kRows + row];
 #pragma unroll
-      for (int w = 1; w < TW; ++w) f += sums[(team * TW + w) * kRows + tt];
-      a.part_sum[static_cast<int64_t>(row_of(p, tt, a)) * a.slots + p.slot] = f;
-    }
+      for (int w = 1; w < TW; ++w) f += sums[(team * TW + w) * kRows + row];
+      return f;
+    };
+    if (parts > 1 && tt < p.rows) a.part_sum[static_cast<int64_t>(row_of(p, tt, a)) * a.slots + p.slot] = sum_of(tt);
     for (int e = tt; e < p.rows * (D / 4); e += 32 * TW) {
       const int row = e / (D / 4), c = e % (D / 4);
       float4 f = reinterpret_cast<const float4*>(rings)[e];
 #pragma unroll
-      for (int w = 1; w < TW; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(rings + w * kRing + e * 16);
-        f.x += x.x;
-        f.y += x.y;
-        f.z += x.z;
-        f.w += x.w;
+      for (int w = 1; w < TW; ++w) f = add4(f, *reinterpret_cast<const float4*>(rings + w * kRing + e * 16));
+      if (parts == 1) {
+        const float total = sum_of(row);
+        put4<T>(a.o, static_cast<int64_t>(row_of(p, row, a)) * (D / 4) + c, f, total != 0.0f ? 1.0f / total : 0.0f);
+      } else {
+        reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, row, a)) * a.slots + p.slot) * D)[c] = f;
       }
-      reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, row, a)) * a.slots + p.slot) * D)[c] = f;
+    }
+    if (parts > 1) {
+      __threadfence();   // this thread's sums are there before the part counts as done
+      team_sync<TW>();
+      if (tt == 0)
+        last_s[team] = atomicAdd(pa.done + (p.b * a.Hkv + p.kv) * a.own_rowblocks + p.row0 / kRows, 1) == parts - 1;
+      team_sync<TW>();
+      if (last_s[team]) {
+        __threadfence();
+        join_rows<T, D, TW>(p, a, parts);
+      }
     }
     team_sync<TW>();
   });
-  release_dependents();
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)   // sequences without any key
+    if (cum[a.B + 1 + b] == 0)
+      for (int i = threadIdx.x; i < a.Hq * (D / 4); i += kThreads)
+        put4<T>(a.o, static_cast<int64_t>(b) * a.Hq * (D / 4) + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
   // Whoever awaits this kernel awaits the scores too: a CTA without a part sees to it.
   if (blockIdx.x == gridDim.x - 1) await_previous();
 }
 
-template <typename T, int D, int TW, int NT>
+template <typename T, int D, int TW, int NT, bool CUT>
 cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
   const DecodeArgs& a = p.a;
   constexpr int kScores = kWarps * Cfg<D>::kStagesK * Cfg<D>::kBlock;
-  constexpr int kValues = kWarps * Cfg<D>::kStagesV * stage_values<D, NT>();
+  constexpr int kValues = kWarps * ring_values<D, NT>();
   constexpr int kMostCum = (2 * kDecodeMaxBatch + 1) * 4;
   const int cum = (2 * a.B + 1) * 4;
-  cudaError_t e = set_up_kernel<paged_scores_kernel<T, D, TW, NT>>(kScores + kMostCum, true);
-  if (e == cudaSuccess) e = set_up_kernel<paged_values_kernel<T, D, TW, NT>>(kValues + kMostCum, true);
+  cudaError_t e = set_up_kernel<paged_scores_kernel<T, D, TW, NT, CUT>>(kScores + kMostCum, true);
+  if (e == cudaSuccess) e = set_up_kernel<paged_values_kernel<T, D, TW, NT, CUT>>(kValues + kMostCum, true);
   if (e != cudaSuccess) return e;
-  // CTAs for the runs that there can be
-  const int64_t streams = static_cast<int64_t>(a.B) * a.Hkv * a.own_rowblocks, own = a.own_width / a.block;
-  const int64_t ctas = TW == 1 ? streams * own : streams * ((own + TW - 1) / TW);
-  const int grid = static_cast<int>(ctas < kCtas ? ctas : kCtas);
-  paged_scores_kernel<T, D, TW, NT><<<grid, kThreads, kScores + cum, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;   // the next kernels read what this one leaves
-  e = launch_dependent(paged_values_kernel<T, D, TW, NT>, grid, kThreads, kValues + cum, st, p);
-  if (e != cudaSuccess) return e;
-  return launch_decode_join(a, sizeof(T) == 2, st);
+  // teams for the runs that there can be, one for each head
+  const int64_t heads = static_cast<int64_t>(a.Hkv) * a.own_rowblocks, blocks = static_cast<int64_t>(a.B) * (a.own_width / a.block);
+  const int64_t runs = CUT ? std::min<int64_t>(a.runs + a.B, blocks) : std::min<int64_t>(a.runs, blocks);
+  const unsigned grid = static_cast<unsigned>((runs * heads + kWarps / TW - 1) / (kWarps / TW));
+  paged_scores_kernel<T, D, TW, NT, CUT><<<grid, kThreads, kScores + cum, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;   // the next kernel reads what this one leaves
+  return launch_dependent(paged_values_kernel<T, D, TW, NT, CUT>, grid, kThreads, kValues + cum, st, p);
+}
+template <typename T, int D, int NT>
+cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
+  if (p.a.team == kWarps) return p.cut ? go<T, D, kWarps, NT, true>(p, st) : go<T, D, kWarps, NT, false>(p, st);
+  return p.cut ? go<T, D, 1, NT, true>(p, st) : go<T, D, 1, NT, false>(p, st);
 }
 template <typename T, int D>
 cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
-  if (p.a.G > 8) return p.a.team == kWarps ? go<T, D, kWarps, 2>(p, st) : go<T, D, 1, 2>(p, st);
-  return p.a.team == kWarps ? go<T, D, kWarps, 1>(p, st) : go<T, D, 1, 1>(p, st);
+  return p.a.G > 8 ? go<T, D, 2>(p, st) : go<T, D, 1>(p, st);
 }
 
 }  // namespace
 
-// The split of decode.cu without shared keys: equal runs, one per warp, with many streams; one per CTA, each stream
-// for itself, with few.
-size_t plan_decode_paged(PagedDecodeArgs* p, char* base) {
+// The split: `runs` runs for every head, as many as teams that are resident at a time.  Where streams are few, or
+// a warp would have few blocks, a run belongs to a CTA, whose warps' sums meet in shared memory (a row then has a quarter of the
+// parts; with a warp's runs / with a CTA's: B32 H32/8 C2048 26.5 us / 23.6, B16 H64/8 C8192 50.8 / 32.8, but B64 H8
+// C4096 44.7 / 51.7), and each sequence is cut for itself where that leaves enough runs.
+constexpr int kMostTeamStreams = 400, kMostCutStreams = 1024, kFewBlocks = 24;
+size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   DecodeArgs* a = &p->a;
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
   a->G = a->Hq / a->Hkv;
   a->block = kKeys;
   a->own_rowblocks = (a->G + kRows - 1) / kRows;
-  a->shared_rowblocks = 1;
   const int own = (a->C + kKeys - 1) / kKeys;
   a->own_width = own * kKeys;
-  a->tc = a->pblocks = a->pre_width = a->pchunk = a->pslots = 0;
-  const int64_t streams = static_cast<int64_t>(a->B) * a->Hkv * a->own_rowblocks, total = streams * own;
-  if (total > INT_MAX / 2) return 0;
-  a->team = streams < 64 || (streams <= 128 && total < 10 * kCtas * kWarps) ? kWarps : 1;
-  a->runs = a->team == 1 ? kCtas * kWarps : kCtas - static_cast<int>(streams);
-  const int64_t even = total / a->runs;
-  const int64_t full = even < a->team ? a->team : even > 8 * a->team ? 8 * a->team : even;
-  a->slots = static_cast<int>((own + full - 1) / full + 1);
-  a->least = 1;
+  const int64_t heads = static_cast<int64_t>(a->Hkv) * a->own_rowblocks, streams = heads * a->B, blocks = static_cast<int64_t>(a->B) * own;
+  if (streams * own > INT_MAX / 2) return 0;
+  const int64_t ctas = kSms * resident(bf16, a->G > 8 ? 2 : 1);
+  const bool few = streams * own < kFewBlocks * ctas * kWarps;
+  a->team = streams < 64 || (streams <= kMostTeamStreams && few) ? kWarps : 1;
+  int64_t runs = (a->team == 1 ? ctas * kWarps : ctas) / heads;   // of each head
+  p->cut = runs >= 2 * a->B && (a->team > 1 || (streams <= kMostCutStreams && few));
+  if (p->cut) runs -= a->B;   // cut for itself, a sequence has one more at most
+  a->runs = static_cast<int>(std::max<int64_t>(runs, 1));
+  // the most parts of a sequence: as if a run had eight blocks a warp at most
+  const int64_t even = blocks / a->runs, full = std::min<int64_t>(std::max<int64_t>(even, a->team), 8 * a->team);
+  a->slots = static_cast<int>((own + full - 1) / full + 2);
   size_t at = 0;
   auto piece = [&](int64_t floats) {
     char* q = base + at;
@@ -713,6 +942,8 @@ size_t plan_decode_paged(PagedDecodeArgs* p, char* base) {
   a->part_sum = reinterpret_cast<float*>(piece(rows * a->slots));
   a->part_o = reinterpret_cast<float*>(piece(rows * a->slots * a->D));
   a->cum = reinterpret_cast<int*>(piece(a->B + 2));
+  p->unit = reinterpret_cast<float*>(piece(rows));
+  p->done = reinterpret_cast<int*>(piece(streams));
   return at;
 }
 

@@ -33,9 +33,9 @@ __device__ __forceinline__ float phi_t(float d) {
 // the split
 // ---------------------------------------------------------------------------------------------
 // The sequences' entries and own blocks: cum[b] = blocks per stream of the sequences before b, for
-// b <= B, and behind it their lengths.  All threads.
+// b <= B, and behind it their lengths; returns the most blocks of one.  All threads.
 template <int KEYS>
-__device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a, int* most_blocks) {
+__device__ __forceinline__ int count_blocks(int* cum, const DecodeArgs& a) {
   __shared__ int sums[kWarps], longest[kWarps];
   int* len = cum + a.B + 1;
   const int per = (a.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
@@ -66,8 +66,12 @@ __device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a, int* 
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) most = max(most, longest[w]);
-  *most_blocks = most;
-  return decode_split(a, cum[a.B], most);
+  return most;
+}
+template <int KEYS>
+__device__ __forceinline__ Split make_split(int* cum, const DecodeArgs& a, int* most_blocks) {
+  *most_blocks = count_blocks<KEYS>(cum, a);
+  return decode_split(a, cum[a.B], *most_blocks);
 }
 
 // A stream's part in a run.

@@ -220,7 +220,7 @@ cudaError_t launch_decode_prefix(const PrefixMaps& maps, const DecodeArgs& a, bo
 // Pages of a cache held in 4 bits (the layout: paged.cuh).
 struct PagePool {
   uint8_t* base;
-  int64_t page_stride;          // bytes from page to page
+  int page_stride;              // bytes from page to page
   int part;                     // bytes of a head's keys or values in a page
   int pages, Hkv, D;
   int page, shift;              // tokens of a page, 2^shift
@@ -269,17 +269,18 @@ cudaError_t launch_page_fork(const PageFork& a, cudaStream_t st);
 cudaError_t launch_page_reserve(const PageReserve& a, cudaStream_t st);
 cudaError_t launch_page_compact(const PageCompact& a, cudaStream_t st);
 
-// One query token per sequence against its pages (decode_paged.cu).  a.C: the most tokens of a table row.
+// One query token per sequence against its pages (decode_paged.cu).
 struct PagedDecodeArgs {
-  DecodeArgs a;
+  DecodeArgs a;                 // C: the most tokens of a table row; own keys only
   PagePool pool;
   const int32_t* table;
   int M;
+  int cut;                      // each sequence is cut for itself
+  float* unit;                  // [B Hq] what a score of 1 in the workspace stands for
+  int* done;                    // [B Hkv own_rowblocks] parts whose sums are there
 };
-size_t plan_decode_paged(PagedDecodeArgs* p, char* base);
+size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base);
 cudaError_t launch_decode_paged(const PagedDecodeArgs& p, bool bf16, cudaStream_t st);
-// The join of a decode without weights (decode.cu).
-cudaError_t launch_decode_join(const DecodeArgs& a, bool bf16, cudaStream_t st);
 
 // From api.cu: where a launch reports timeouts, and the tensor map of a [BH, N, D] bf16 tensor
 // (box 64 x 128 rows, 128-byte swizzle).

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageReser
     const int from = __ldcg(a.copy + 2 * b);
     if (from < 0) continue;
     const int to = __ldcg(a.copy + 2 * b + 1);
-    copy_chunk(a.pool.base + to * a.pool.page_stride, a.pool.base + from * a.pool.page_stride,
+    copy_chunk(a.pool.base + static_cast<int64_t>(to) * a.pool.page_stride, a.pool.base + static_cast<int64_t>(from) * a.pool.page_stride,
                (item - static_cast<int64_t>(b) * chunks) * kChunk, a.page_bytes);
   }
 }

@@ -26,7 +26,7 @@ __host__ __device__ constexpr int row_bytes(int D) { return D / 2 + D / 16; }
 
 // The part of head h (which: 0 keys, 1 values) of a page.
 __device__ __forceinline__ uint8_t* part_of(const PagePool& p, int64_t page, int h, int which) {
-  return p.base + page * p.page_stride + static_cast<int64_t>(2 * h + which) * p.part;
+  return p.base + page * p.page_stride + (2 * h + which) * p.part;   // a page's bytes fit 32 bits
 }
 // Page `at` of a table row, or -1: none, or no page of the pool.
 __device__ __forceinline__ int page_at(const PagePool& p, const int32_t* row, int at) {
