@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_
   __shared__ float best[kWarps * kRows];
   __shared__ int2 ids[kWarps][kIds];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
+  await_previous();
   release_dependents();   // the next kernel's first values are on their way while this one ends
   // the page numbers, if they are few, are on their way while the split is made
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 32, table = static_cast<int64_t>(a.B) * pa.M;
@@ -889,8 +890,8 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
   const int64_t heads = static_cast<int64_t>(a.Hkv) * a.own_rowblocks, blocks = static_cast<int64_t>(a.B) * (a.own_width / a.block);
   const int64_t runs = CUT ? std::min<int64_t>(a.runs + a.B, blocks) : std::min<int64_t>(a.runs, blocks);
   const unsigned grid = static_cast<unsigned>((runs * heads + kWarps / TW - 1) / (kWarps / TW));
-  paged_scores_kernel<T, D, TW, NT, CUT><<<grid, kThreads, kScores + cum, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;   // the next kernel reads what this one leaves
+  e = launch_dependent(paged_scores_kernel<T, D, TW, NT, CUT>, grid, kThreads, kScores + cum, st, p);
+  if (e != cudaSuccess) return e;   // the next kernel reads what this one leaves
   return launch_dependent(paged_values_kernel<T, D, TW, NT, CUT>, grid, kThreads, kValues + cum, st, p);
 }
 template <typename T, int D, int NT>

@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, 6) page_write_kernel(const RowsArgs 
   constexpr int G = D / kGroup;
   const PageRows& a = ra.a;
   const int w = threadIdx.x & 7, token = (threadIdx.x & 31) >> 3, warps = gridDim.x * (kThreads / 32);
+  await_previous();
+  release_dependents();
   for (int64_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < ra.items; item += warps) {
     const Chunk c(ra, static_cast<int>(item));
     if (c.n >= a.N) continue;
@@ -351,6 +353,8 @@ __global__ void __launch_bounds__(kThreads) page_read_kernel(const RowsArgs ra) 
   constexpr int G = D / kGroup;
   const PageRows& a = ra.a;
   const int w = threadIdx.x & 7, token = (threadIdx.x & 31) >> 3, warps = gridDim.x * (kThreads / 32);
+  await_previous();
+  release_dependents();
   for (int64_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < ra.items; item += warps) {
     const Chunk c(ra, static_cast<int>(item));
     if (c.n >= a.N) continue;
@@ -397,9 +401,8 @@ __global__ void __launch_bounds__(kThreads) page_read_kernel(const RowsArgs ra) 
 template <bool WRITE, typename T, int D>
 cudaError_t go(const RowsArgs& ra, cudaStream_t st) {
   const int need = (ra.items - 1) / (kThreads / 32) + 1, most = 32 * kSms, grid = need < most ? need : most;
-  if constexpr (WRITE) page_write_kernel<T, D><<<grid, kThreads, 0, st>>>(ra);
-  else page_read_kernel<T, D><<<grid, kThreads, 0, st>>>(ra);
-  return cudaGetLastError();
+  if constexpr (WRITE) return launch_dependent(page_write_kernel<T, D>, grid, kThreads, 0, st, ra);
+  else return launch_dependent(page_read_kernel<T, D>, grid, kThreads, 0, st, ra);
 }
 template <bool WRITE>
 cudaError_t launch(const PageRows& a, bool bf16, cudaStream_t st) {

@@ -533,3 +533,73 @@ def test_two_streams_at_once():
                 got[s].append(ra.ra_attention_decode_paged(*sets[s]))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[s]) for s in range(2) for o in got[s])
+
+
+def test_every_call_after_joined_streams_and_copies_in_a_graph():
+    """The calls start early behind a kernel of the same stream; behind a copy, a set or an event of another stream, in
+    a graph and outside, they wait for all of it."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    B, H, D, page, N = 3, 2, 64, 16, 40
+    k0, v0 = (torch.randn(B, H, N, D, generator=g, device="cuda") for _ in range(2))
+    q0 = torch.randn(B, 4, D, generator=g, device="cuda")
+
+    def state():
+        return dict(k=torch.zeros_like(k0), v=torch.zeros_like(v0), q=torch.zeros_like(q0),
+                    pool=torch.full((30, H, 2, page, 36), 255, dtype=torch.uint8, device="cuda"),
+                    table=torch.full((B, 4), -1, dtype=torch.int32, device="cuda"), uses=torch.zeros(30, dtype=torch.int32, device="cuda"),
+                    length=torch.zeros(B, dtype=torch.int32, device="cuda"), parent=torch.zeros(B, dtype=torch.int32, device="cuda"),
+                    big=torch.zeros(1 << 24, device="cuda"))
+
+    def work(s, stream, other):
+        """Every call right behind something that is not one of the library's kernels."""
+        out = []
+        def join():                                # a slow kernel on another stream, then a copy and a set on this one
+            other.wait_stream(stream)
+            with torch.cuda.stream(other):
+                s["big"].add_(1.0).mul_(1.0)
+                s["k"].copy_(k0)
+                s["v"].copy_(v0)
+            stream.wait_stream(other)
+        s["length"].zero_()
+        join()
+        granted = ra.ra_page_reserve(s["pool"], s["table"], s["length"], s["uses"], N)
+        join()
+        out += ra.ra_page_write(s["k"], s["v"], s["pool"], s["table"], s["length"], count=granted, held=True)
+        s["length"].fill_(N)
+        out += ra.ra_page_read(s["pool"], s["table"], s["length"], N, dtype=torch.float32)
+        s["q"].copy_(q0)
+        out.append(ra.ra_attention_decode_paged(s["q"], s["pool"], s["table"], s["length"]))
+        s["parent"].copy_(torch.arange(B, device="cuda", dtype=torch.int32).flip(0))
+        join()
+        ra.ra_page_fork(s["table"], s["length"], s["uses"], s["parent"])
+        join()
+        small = torch.zeros(12, H, 2, page, 36, dtype=torch.uint8, device="cuda")
+        out += ra.ra_page_compact(s["pool"], s["table"], s["uses"], small)
+        out.append(ra.ra_attention_decode_paged(s["q"], small, out[-3], s["length"]))
+        s["parent"].fill_(-1)
+        ra.ra_page_fork(s["table"], s["length"], s["uses"], s["parent"])
+        return out + [small, s["uses"].clone()]
+
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = state(), state()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        want = work(a, main, other)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        got = work(b, main, other)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        b["k"].zero_()
+        b["q"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    z = torch.matmul(q0.view(B, H, 2, D), want[0].transpose(-1, -2)) / 8.0
+    u = ((z.amax(-1, keepdim=True) - z) / 16.0).clamp(max=1.0)
+    p = ((1 - u) / (1 + u)) ** 8
+    o = torch.matmul(p / p.sum(-1, keepdim=True), want[1]).view(B, 4, D)
+    # fp32 on both sides, matmuls of torch possibly with fewer bits: far from what a missing wait would give
+    assert (want[4] - o).abs().max() < 2e-2
