@@ -16,7 +16,7 @@
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
 //            by byte.  phi s goes in as fp16 times a power of two that follows the largest scale met so far (11 bits: 2^-11 of a weight
 //            at most, an eighth of what the output's rounding to bf16 costs, and the weights' errors differ); fp32 as two fp16.
-// Two launches, scores and values, with decode.cu's split; the last part of a row to be done joins them.  The scores of sixteen
+// Two launches, scores and values; the last part of a row to be done joins them, or a third launch where they are many.  The scores of sixteen
 // keys stand in the workspace as the value products want them: key t at 4 (t % 4) + t / 4.
 #include <algorithm>
 #include <climits>
@@ -31,16 +31,18 @@ namespace {
 using namespace decode;
 using namespace paged;
 
-constexpr int kKeys = 32;                        // of a block: two products' M, or K
+constexpr int kKeys = 32;                        // of a block: products' M, or K, of sixteen
 constexpr int64_t kPrefetched = 1 << 18;          // numbers of a table that is fetched ahead: 1 MB
 constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
 
 template <int D>
 struct Cfg {
   static constexpr int G = D / kGroup;
+  static constexpr int kTiles = kKeys / 16;
   static constexpr int kCodes = kKeys * D / 2;            // bytes of a block's codes
   static constexpr int kMeta = 4 * G;                     // bytes of a key's scales and minima
   static constexpr int kBlock = kKeys * row_bytes(D);
+  
   static constexpr int kStagesK = 3, kStagesV = 3;
 };
 // CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
@@ -133,12 +135,26 @@ struct PagedPart {
   int first, count, keys;  // blocks of the sequence; its keys
   int slot, parts;         // its place among the sequence's parts
 };
+// CUT: the least (a multiple of the team, so that its warps have as many each) with which the sequences' runs are
+// a.runs in all; 32 of them are tried at once, by counts that are never too low.  Beyond, what is enough for any lengths.
 template <bool CUT>
 __device__ __forceinline__ int blocks_per_run(const PagedDecodeArgs& p, const int* cum, int longest) {
   const DecodeArgs& a = p.a;
-  int per = max((cum[a.B] + a.runs - 1) / a.runs, 1);
-  per = max(per, (longest + a.slots - 2) / (a.slots - 1));   // a sequence of n blocks meets at most ceil(n / per) + 1 runs
-  return CUT && a.team > 1 ? (per + a.team - 1) / a.team * a.team : per;   // as many for each warp
+  const int least = (longest + a.slots - 2) / (a.slots - 1);   // a sequence of n blocks meets at most ceil(n / per) + 1 runs
+  const int total = cum[a.B];
+  if (!CUT) return max(max((total + a.runs - 1) / a.runs, least), 1);
+  const auto whole = [&](int per) { return (max(per, 1) + a.team - 1) / a.team * a.team; };
+  const int first = whole(max((total + a.runs - 1) / a.runs, least)), mine = first + static_cast<int>(threadIdx.x & 31) * a.team;
+  const float inv = 1.0f / mine;
+  int runs = 0;
+  for (int b = 0; b < a.B; ++b) runs += static_cast<int>(ceilf(static_cast<float>(cum[b + 1] - cum[b]) * inv * 1.000001f));
+  const unsigned fits = __ballot_sync(0xffffffffu, runs <= a.runs);
+  return fits ? first + (__ffs(fits) - 1) * a.team : max(first, whole((total + a.runs - a.B - 1) / (a.runs - a.B)));
+}
+// Parts of a sequence whose blocks are c0 .. c1 - 1 of all.
+template <bool CUT>
+__device__ __forceinline__ int parts_of(int c0, int c1, int per) {
+  return c0 == c1 ? 0 : CUT ? (c1 - c0 + per - 1) / per : (c1 - 1) / per - c0 / per + 1;
 }
 // f(part) for the parts of this team's run.  All lanes.
 template <int TW, bool CUT, typename F>
@@ -178,7 +194,7 @@ __device__ __forceinline__ void each_paged_part(const PagedDecodeArgs& pa, const
     p.first = i * per;
     p.count = min(blocks - p.first, per);
     p.slot = i;
-    p.parts = (blocks + per - 1) / per;
+    p.parts = parts_of<CUT>(cum[b], cum[b + 1], per);
     f(p);
   } else {
     const int total = cum[a.B], end = static_cast<int>(min(static_cast<int64_t>(run + 1) * per, static_cast<int64_t>(total)));
@@ -195,7 +211,7 @@ __device__ __forceinline__ void each_paged_part(const PagedDecodeArgs& pa, const
       p.first = u - c0;
       p.count = min(c1, end) - u;
       p.slot = run - c0 / per;
-      p.parts = (c1 - 1) / per - c0 / per + 1;
+      p.parts = parts_of<CUT>(c0, c1, per);
       u0 += p.count;
       f(p);
     }
@@ -217,26 +233,28 @@ __device__ __forceinline__ void copy16_part(uint32_t dst, const void* src, int b
                : "memory");
 }
 
-// Blocks first, first + step, .. of a part.  The page numbers of their halves (a page is at least sixteen keys) come
-// through shared memory, sixteen blocks at a time and sixteen to thirty-two ahead.  What no page holds and what lies behind the
+// Blocks first, first + step, .. of a part.  The page numbers of their tiles (a page is at least sixteen keys) come
+// through shared memory, half of kIds blocks at a time and that many ahead.  What no page holds and what lies behind the
 // last key arrives as zeros: scales and minima of 0.
-constexpr int kIds = 32;   // blocks whose pages a warp has
 template <int D>
 struct Fetch {
+  using C = Cfg<D>;
+  static constexpr int kIds = 2 * 32 / C::kTiles;    // blocks whose pages a warp has
   static constexpr int kLanesPerKey = D / 32;        // 16-byte chunks of a key's codes
   static constexpr int kKeysPerCopy = 32 / kLanesPerKey;
-  static constexpr int kCopies = kKeys / kKeysPerCopy;
-  static constexpr int kMetaLanes = kKeys * Cfg<D>::kMeta / 16, kKeysPerChunk = 16 / Cfg<D>::kMeta;
+  static constexpr int kCopies = kKeys / kKeysPerCopy, kTileCopies = 16 / kKeysPerCopy;
+  static constexpr int kMetaLanes = kKeys * C::kMeta / 16, kKeysPerChunk = 16 / C::kMeta;
+  static_assert(kMetaLanes <= 32, "one copy");
   const PagePool& pool;
   const int32_t* row;
   const uint8_t* base;   // with this lane's place in a block's codes
-  const int2* ids;       // pages of block i's halves: place i % kIds
+  const int* ids;        // pages of block i's tiles: from (i % kIds) * kTiles on
   int first, step, blocks, keys, lane;
   uint64_t policy;       // keys and values leave L2 first: the scores had better stay
 
-  // ids: kIds of this warp's, which nobody reads any more.  await() comes before the first block.
+  // ids: of this warp's, which nobody reads any more.  await() comes before the first block.
   __device__ __forceinline__ Fetch(const PagedDecodeArgs& p, const PagedPart& part, int which, int warp, int warps, int blocks_,
-                                   const int2* ids_)
+                                   const int* ids_)
       : pool(p.pool), row(p.table + static_cast<int64_t>(part.b) * p.M), ids(ids_), first((part.first + warp) * kKeys),
         step(warps * kKeys), blocks(blocks_), keys(part.keys), lane(threadIdx.x & 31) {
     base = part_of(p.pool, 0, part.kv, which) + lane * 16;
@@ -249,38 +267,39 @@ struct Fetch {
     copy_wait<0>();
     __syncwarp();
   }
-  __device__ __forceinline__ void pages(int i0) const {   // lane l: half l % 2 of block i0 + l / 2
-    const int i = i0 + (lane >> 1), key = min(first + i * step + (lane & 1) * 16, keys - 1);
+  __device__ __forceinline__ void pages(int i0) const {   // lane l: tile l % kTiles of block i0 + l / kTiles
+    const int i = i0 + lane / C::kTiles, key = min(first + i * step + lane % C::kTiles * 16, keys - 1);
     if (i < blocks)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(ids + i % kIds) + (lane & 1) * 4),
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(ids + i % kIds * C::kTiles + lane % C::kTiles)),
                    "l"(row + (key >> pool.shift))
                    : "memory");
   }
+  __device__ __forceinline__ bool there(int id) const { return static_cast<unsigned>(id) < static_cast<unsigned>(pool.pages); }
   __device__ __forceinline__ void operator()(uint32_t stage, int i) {
     if ((i & (kIds / 2 - 1)) == 0 && i) pages(i + kIds / 2);   // the other half is in use
     stage += lane * 16;
     const int key0 = first + i * step, slot = key0 & (pool.page - 1);
-    const int2 id = ids[i % kIds];
-    if (pool.page >= kKeys && key0 + kKeys <= keys && static_cast<unsigned>(id.x) < static_cast<unsigned>(pool.pages)) {
-      const uint8_t* src = base + static_cast<int64_t>(id.x) * pool.page_stride;
+    const int* id = ids + i % kIds * C::kTiles;
+    if (pool.page >= kKeys && key0 + kKeys <= keys && there(id[0])) {
+      const uint8_t* src = base + static_cast<int64_t>(id[0]) * pool.page_stride;
       const uint8_t* codes = src + slot * (D / 2);
 #pragma unroll
       for (int c = 0; c < kCopies; ++c) copy16_once(stage + c * 512, codes + c * 512, policy);
-      if (lane < kMetaLanes) copy16_once(stage + Cfg<D>::kCodes, src + pool.page * (D / 2) + slot * Cfg<D>::kMeta, policy);
+      if (lane < kMetaLanes) copy16_once(stage + C::kCodes, src + pool.page * (D / 2) + slot * C::kMeta, policy);
     } else {
+#pragma unroll 1
+      for (int h = 0; h < C::kTiles; ++h) {
+        const int at = id[h], in_page = (key0 + 16 * h) & (pool.page - 1);
+        const bool in = there(at);
+        const int left = in ? keys - key0 - 16 * h : 0;   // keys of the tile that there are
+        const uint8_t* src = base + static_cast<int64_t>(in ? at : 0) * pool.page_stride;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {   // the block's halves
-        const int at = h ? id.y : id.x, in_page = (key0 + 16 * h) & (pool.page - 1);
-        const bool there = static_cast<unsigned>(at) < static_cast<unsigned>(pool.pages);
-        const int left = there ? keys - key0 - 16 * h : 0;   // keys of it that there are
-        const uint8_t* src = base + static_cast<int64_t>(there ? at : 0) * pool.page_stride;
-#pragma unroll
-        for (int c = 0; c < kCopies / 2; ++c)
-          copy16_part(stage + (h * (kCopies / 2) + c) * 512, src + in_page * (D / 2) + c * 512,
+        for (int c = 0; c < kTileCopies; ++c)
+          copy16_part(stage + (h * kTileCopies + c) * 512, src + in_page * (D / 2) + c * 512,
                       c * kKeysPerCopy + lane / kLanesPerKey < left ? 16 : 0, policy);
-        if (lane < kMetaLanes / 2)
-          copy16_part(stage + Cfg<D>::kCodes + h * (kMetaLanes / 2) * 16, src + pool.page * (D / 2) + in_page * Cfg<D>::kMeta,
-                      min(max((left - lane * kKeysPerChunk) * Cfg<D>::kMeta, 0), 16), policy);
+        if (lane < kMetaLanes / C::kTiles)
+          copy16_part(stage + C::kCodes + h * (kMetaLanes / C::kTiles) * 16, src + pool.page * (D / 2) + in_page * C::kMeta,
+                      min(max((left - lane * kKeysPerChunk) * C::kMeta, 0), 16), policy);
       }
     }
   }
@@ -382,7 +401,7 @@ struct Query {
 };
 
 template <typename T, int D, int TW, int NT>
-__device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int2* ids, float* best_s) {
+__device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int* ids, float* best_s) {
   using C = Cfg<D>;
   constexpr int G = C::G;
   constexpr bool TWO = sizeof(T) == 4;
@@ -399,7 +418,7 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
   }
   const Query<T, D, NT> q(raw, p, a, pa.unit);
   const int first = (p.first + warp_of_team<TW>()) * kKeys, at = (r & 3) * 4 + (r >> 2);
-  float* out[NT][2];
+  float* out[NT][2];   // sixteen keys' scores stand as the value products want them
   bool there[NT][2];
   float best[NT][2];
 #pragma unroll
@@ -420,9 +439,9 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
     if (i + C::kStagesK - 1 < mine) fetch(smem_u32(to), i + C::kStagesK - 1);
     copy_commit();
     to = to == ring + (C::kStagesK - 1) * C::kBlock ? ring : to + C::kBlock;
-    float z[kKeys / 16][NT][4];
+    float z[C::kTiles][NT][4];
 #pragma unroll
-    for (int tile = 0; tile < kKeys / 16; ++tile) {
+    for (int tile = 0; tile < C::kTiles; ++tile) {
       uint32_t x[2][G][2];   // keys r, r + 8; words 2 j, 2 j + 1 of the groups
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -466,7 +485,7 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
     }
     if (left < kKeys) {   // the last block may have fewer
 #pragma unroll
-      for (int tile = 0; tile < kKeys / 16; ++tile)
+      for (int tile = 0; tile < C::kTiles; ++tile)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -478,7 +497,7 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int tile = 0; tile < kKeys / 16; ++tile) {
+        for (int tile = 0; tile < C::kTiles; ++tile) {
           best[t][c] = fmaxf(best[t][c], fmaxf(z[tile][t][c], z[tile][t][2 + c]));
           if (there[t][c]) {
             out[t][c][tile * 16] = z[tile][t][c];
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_
   const DecodeArgs& a = pa.a;
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
-  __shared__ int2 ids[kWarps][kIds];
+  __shared__ int ids[kWarps][64];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   await_previous();
   release_dependents();   // the next kernel's first values are on their way while this one ends
@@ -518,6 +537,8 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_
   if (at < table && table <= kPrefetched) asm volatile("prefetch.global.L2 [%0];" ::"l"(pa.table + at));
   const int per = blocks_per_run<CUT>(pa, cum, count_blocks<kKeys>(cum, a));
   for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.B * a.Hkv * a.own_rowblocks; i += gridDim.x * kThreads) pa.done[i] = 0;
+  if (pa.join && blockIdx.x == 0)   // for the join
+    for (int b = threadIdx.x; b < a.B; b += kThreads) a.cum[b] = parts_of<CUT>(cum[b], cum[b + 1], per);
   each_paged_part<TW, CUT>(pa, cum, per, [&](const PagedPart& p) {
     part_scores<T, D, TW, NT>(p, pa, reinterpret_cast<char*>(dyn) + warp * kRing, ids[warp], best);
     team_sync<TW>();
@@ -559,26 +580,32 @@ __device__ __forceinline__ int piece_of(int r, int c) { return c ^ ((r & 1) << 2
 
 // Lane (r, j) reads, of keys j, j + 4, j + 8 and j + 12 of sixteen, word r of every group (dimensions 8 r .. 8 r + 7):
 // rows r and r + 8 of the A operand of product n stand for dimensions 8 r + 2 n and 8 r + 2 n + 1, the latter sixteen times as
-// large.  The weights of query row r at the same keys are the B operand.
-template <typename T, int D, int TW, int NT>
-__device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int2* ids, float* rowm,
+// large.  The weights of query row r at the same keys are the B operand.  FOLD, up to four rows: columns 0 .. 3 take the weights at a
+// block's first sixteen keys and columns 4 .. 7 those at its other sixteen, so that no lane forms weights for nothing; the
+// columns are added at the end.
+template <typename T, int D, int TW, int NT, bool FOLD>
+__device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int* ids, float* rowm,
                                             float* sums) {
   using C = Cfg<D>;
   constexpr int G = C::G, kStage = stage_values<D, NT>(), S = C::kStagesV;
   constexpr bool TWO = sizeof(T) == 4;
   const DecodeArgs& a = pa.a;
+  static_assert(!FOLD || (NT == 1 && C::kTiles == 2), "two tiles for eight columns");
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+  const int row8 = FOLD ? r & 3 : r, half = r >> 2;   // this lane's row of eight (FOLD: of four), and of which tile
   const int mine = blocks_of_warp<TW>(p), first = (p.first + warp_of_team<TW>()) * kKeys;
   Fetch<D> fetch(pa, p, 1, warp_of_team<TW>(), TW, mine, ids);
-  const float* score[2 * NT];   // lane's piece of rows lane / 8 + 4 i
-#pragma unroll
-  for (int i = 0; i < 2 * NT; ++i) score[i] = score_row(row_of(p, (lane >> 3) + 4 * i, a), a) + first + (lane & 7) * 4;
+  // the scores: kKeys / 4 pieces of a row; a warp copies kRowsPerCopy rows at a time
+  constexpr int kPieces = kKeys / 4, kRowsPerCopy = 32 / kPieces;
+  const int score_at = lane / kPieces, piece = lane % kPieces;
+  const float* score = score_row(row_of(p, 0, a) + score_at, a) + first + piece * 4;
   auto fetch_scores = [&](uint32_t stage, int i) {
+    const float* src = score + i * (TW * kKeys);
 #pragma unroll
-    for (int k = 0; k < 2 * NT; ++k) {
-      const int row = (lane >> 3) + 4 * k;
-      if (row < p.rows)
-        copy16(stage + C::kBlock + (row * 8 + piece_of(row, lane & 7)) * 16, score[k] + i * (TW * kKeys), true);
+    for (int k = 0; k < 8 * NT / kRowsPerCopy; ++k) {
+      const int row = score_at + k * kRowsPerCopy;
+      if (row < p.rows) copy16(stage + C::kBlock + (row * kPieces + piece_of(row, piece)) * 16, src, true);
+      src += kRowsPerCopy * static_cast<int64_t>(a.own_width);
     }
   };
   fetch.await();
@@ -603,9 +630,9 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
   float2 low[NT];   // of the groups (D = 64: the first)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t] = rowm[t * 8 + r];
+    m[t] = rowm[t * 8 + row8];
     if (m[t] == -kInf) m[t] = 0.0f;
-    c2[t] = a.scale * (TWO ? 1.0f : 0.03125f) * __ldcg(pa.unit + row_of(p, t * 8 + r, a));
+    c2[t] = a.scale * (TWO ? 1.0f : 0.03125f) * __ldcg(pa.unit + row_of(p, t * 8 + row8, a));
     total[t] = 0.0f;
     low[t] = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -614,6 +641,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
       for (int n = 0; n < 4; ++n) acc[t][g][n][0] = acc[t][g][n][1] = acc[t][g][n][2] = acc[t][g][n][3] = 0.0f;
   }
   int exponent = -100;   // every scale met so far is below 2^exponent
+  float unit = power_of_2(14 - exponent);
   const int word = word_offset<G>(0, r, j);   // the halves' order: bit 1 of the key's slot is j's
   float* metas = reinterpret_cast<float*>(ring + S * kStage);
   const char *stage = ring, *to = ring + (S - 1) * kStage;
@@ -626,11 +654,15 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
     }
     copy_commit();
     to = to == ring + (S - 1) * kStage ? ring : to + kStage;
-    {   // a key's scales, times a power of two, and minima by each lane
-      const Meta<G> meta(stage + C::kCodes + lane * C::kMeta);
+    {   // the keys' scales, times a power of two, and minima, a lane for each of 32
+      float most = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kKeys; k += 32) {
+        const Meta<G> meta(stage + C::kCodes + (k + lane) * C::kMeta);
+        most = fmaxf(most, G == 2 ? fmaxf(meta.s[0], meta.s[G - 1]) : meta.s[0]);
+      }
       // the bits of scales, which are not negative, are in their order
-      const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(G == 2 ? fmaxf(meta.s[0], meta.s[1]) : meta.s[0]));
-      const int e = static_cast<int>(most >> 23) - 126;
+      const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 126;
       if (e > exponent) {
         const float f = power_of_2(exponent - e);
 #pragma unroll
@@ -642,24 +674,30 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
 #pragma unroll
               for (int k = 0; k < 4; ++k) acc[t][g][n][k] *= f;
         exponent = e;
+        unit = power_of_2(14 - e);
       }
-      const float unit = power_of_2(14 - exponent);
-      if constexpr (G == 2)
-        reinterpret_cast<float4*>(metas)[lane] = make_float4(meta.s[0] * unit, meta.s[1] * unit, meta.lo[0], meta.lo[1]);
-      else
-        reinterpret_cast<float2*>(metas)[lane] = make_float2(meta.s[0] * unit, meta.lo[0]);
+#pragma unroll
+      for (int k = 0; k < kKeys; k += 32) {
+        const Meta<G> meta(stage + C::kCodes + (k + lane) * C::kMeta);
+        if constexpr (G == 2)
+          reinterpret_cast<float4*>(metas)[k + lane] = make_float4(meta.s[0] * unit, meta.s[1] * unit, meta.lo[0], meta.lo[1]);
+        else
+          reinterpret_cast<float2*>(metas)[k + lane] = make_float2(meta.s[0] * unit, meta.lo[0]);
+      }
       __syncwarp();
     }
-    float f[kKeys / 16][NT][4];
+    constexpr int FT = FOLD ? 1 : C::kTiles;   // tiles for which a lane forms weights
+    float f[FT][NT][4];
     bool live = false;   // some weight that is not 0 (a NaN is not)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int tile = 0; tile < kKeys / 16; ++tile) {
+      for (int tile = 0; tile < FT; ++tile) {
         float* w = f[tile][t];
         w[0] = w[1] = w[2] = w[3] = 0.0f;
-        if (t * 8 + r < p.rows) {
-          const float4 z = get<float4>(stage + C::kBlock + ((t * 8 + r) * 8 + piece_of(r, tile * 4 + j)) * 16);
+        if (t * 8 + row8 < p.rows) {
+          const float4 z = get<float4>(stage + C::kBlock +
+                                       ((t * 8 + row8) * kPieces + piece_of(row8, (FOLD ? half : tile) * 4 + j)) * 16);
           if constexpr (TWO) {
             w[0] = phi_exact((m[t] - z.x) * c2[t]);
             w[1] = phi_exact((m[t] - z.y) * c2[t]);
@@ -679,62 +717,83 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
         live |= all != 0.0f;
       }
     }
-    const bool any = __any_sync(0xffffffffu, live);
+    if (__any_sync(0xffffffffu, live)) {
+      // the weights times the scales, as operands, and times the minima
+      uint32_t wb[FT][NT][G][2], rest[FT][NT][G][2];
 #pragma unroll
-    for (int tile = 0; any && tile < kKeys / 16; ++tile) {
-      uint32_t x[4][G];
-      float2 weight[NT][4];   // of the groups
+      for (int tile = 0; tile < FT; ++tile) {
+        float2 weight[NT][4];   // of the groups
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = tile * 16 + j + 4 * k;
-        const char* src = stage + key * (D / 2) + word;
-        if constexpr (G == 2) {
-          const uint2 u = get<uint2>(src);
-          x[k][0] = u.x;
-          x[k][1] = u.y;
-          const float4 meta = reinterpret_cast<const float4*>(metas)[key];
+        for (int k = 0; k < 4; ++k) {
+          const int key = (FOLD ? half : tile) * 16 + j + 4 * k;
+          if constexpr (G == 2) {
+            const float4 meta = reinterpret_cast<const float4*>(metas)[key];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float2 ff = make_float2(f[tile][t][k], f[tile][t][k]);
-            weight[t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
-            low[t] = __ffma2_rn(ff, make_float2(meta.z, meta.w), low[t]);
-          }
-        } else {
-          x[k][0] = get<uint32_t>(src);
-          const float2 meta = reinterpret_cast<const float2*>(metas)[key];
+            for (int t = 0; t < NT; ++t) {
+              const float2 ff = make_float2(f[tile][t][k], f[tile][t][k]);
+              weight[t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
+              low[t] = __ffma2_rn(ff, make_float2(meta.z, meta.w), low[t]);
+            }
+          } else {
+            const float2 meta = reinterpret_cast<const float2*>(metas)[key];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            weight[t][k].x = f[tile][t][k] * meta.x;
-            low[t].x = fmaf(f[tile][t][k], meta.y, low[t].x);
+            for (int t = 0; t < NT; ++t) {
+              weight[t][k].x = f[tile][t][k] * meta.x;
+              low[t].x = fmaf(f[tile][t][k], meta.y, low[t].x);
+            }
           }
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float2* w = weight[t];
+            split_half2<TWO>(g ? w[0].y : w[0].x, g ? w[1].y : w[1].x, wb[tile][t][g][0], rest[tile][t][g][0]);
+            split_half2<TWO>(g ? w[2].y : w[2].x, g ? w[3].y : w[3].x, wb[tile][t][g][1], rest[tile][t][g][1]);
+          }
       }
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        uint32_t b[NT][2], rest[NT][2];
+      for (int tile = 0; tile < C::kTiles; ++tile) {
+        uint32_t x[4][G];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float2* w = weight[t];
-          split_half2<TWO>(g ? w[0].y : w[0].x, g ? w[1].y : w[1].x, b[t][0], rest[t][0]);
-          split_half2<TWO>(g ? w[2].y : w[2].x, g ? w[3].y : w[3].x, b[t][1], rest[t][1]);
+        for (int k = 0; k < 4; ++k) {
+          const char* src = stage + (tile * 16 + j + 4 * k) * (D / 2) + word;
+          if constexpr (G == 2) {
+            const uint2 u = get<uint2>(src);
+            x[k][0] = u.x;
+            x[k][1] = u.y;
+          } else {
+            x[k][0] = get<uint32_t>(src);
+          }
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t sel = n < 2 ? 0x5410u : 0x7632u;
-          const uint32_t u = __byte_perm(x[0][g], x[1][g], sel) >> (n & 1) * 8;
-          const uint32_t v = __byte_perm(x[2][g], x[3][g], sel) >> (n & 1) * 8;
-          const uint32_t a0 = codes2<TWO>(u, kLow), a1 = codes2<TWO>(u, kHigh), a2 = codes2<TWO>(v, kLow),
-                         a3 = codes2<TWO>(v, kHigh);
+        for (int g = 0; g < G; ++g) {
+          uint32_t b[NT][2], br[NT][2];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            if constexpr (TWO) {
-              float c[4];
-              mma_f16_first(c, a0, a1, a2, a3, rest[t][0], rest[t][1]);
-              mma_f16(c, a0, a1, a2, a3, b[t][0], b[t][1]);
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) acc[t][g][n][k] += c[k];
-            } else {
-              mma_f16(acc[t][g][n], a0, a1, a2, a3, b[t][0], b[t][1]);
+            for (int h = 0; h < 2; ++h) {
+              b[t][h] = !FOLD ? wb[FOLD ? 0 : tile][t][g][h] : half == tile ? wb[0][t][g][h] : 0u;
+              if constexpr (TWO) br[t][h] = !FOLD ? rest[FOLD ? 0 : tile][t][g][h] : half == tile ? rest[0][t][g][h] : 0u;
+            }
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t sel = n < 2 ? 0x5410u : 0x7632u;
+            const uint32_t u = __byte_perm(x[0][g], x[1][g], sel) >> (n & 1) * 8;
+            const uint32_t v = __byte_perm(x[2][g], x[3][g], sel) >> (n & 1) * 8;
+            const uint32_t a0 = codes2<TWO>(u, kLow), a1 = codes2<TWO>(u, kHigh), a2 = codes2<TWO>(v, kLow),
+                           a3 = codes2<TWO>(v, kHigh);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              if constexpr (TWO) {
+                float c[4];
+                mma_f16_first(c, a0, a1, a2, a3, br[t][0], br[t][1]);
+                mma_f16(c, a0, a1, a2, a3, b[t][0], b[t][1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[t][g][n][k] += c[k];
+              } else {
+                mma_f16(acc[t][g][n], a0, a1, a2, a3, b[t][0], b[t][1]);
+              }
             }
           }
         }
@@ -749,6 +808,17 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
       total[t] += __shfl_xor_sync(0xffffffffu, total[t], o);
       low[t].x += __shfl_xor_sync(0xffffffffu, low[t].x, o);
       if (G == 2) low[t].y += __shfl_xor_sync(0xffffffffu, low[t].y, o);
+    }
+    if constexpr (FOLD) {   // rows r and r + 4, columns c and c + 4 are one
+      total[t] += __shfl_xor_sync(0xffffffffu, total[t], 16);
+      low[t].x += __shfl_xor_sync(0xffffffffu, low[t].x, 16);
+      if (G == 2) low[t].y += __shfl_xor_sync(0xffffffffu, low[t].y, 16);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[t][g][n][k] += __shfl_xor_sync(0xffffffffu, acc[t][g][n][k], 2);
     }
     if (j == 0) sums[(threadIdx.x >> 5) * kRows + t * 8 + r] = total[t];
   }
@@ -769,7 +839,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
           y[2 * n] = fmaf(acc[t][g][n][c] * undo, back, lo);
           y[2 * n + 1] = fmaf(acc[t][g][n][2 + c] * (undo * 0.0625f), back, lo);
         }
-        if (row < p.rows) {
+        if (row < p.rows) {   // FOLD: lanes with j < 2
           float4* o = reinterpret_cast<float4*>(out + row * D + g * kGroup + r * 8);
           o[0] = make_float4(y[0], y[1], y[2], y[3]);
           o[1] = make_float4(y[4], y[5], y[6], y[7]);
@@ -818,7 +888,7 @@ __device__ __forceinline__ void join_rows(const PagedPart& p, const DecodeArgs& 
   }
 }
 
-template <typename T, int D, int TW, int NT, bool CUT>
+template <typename T, int D, int TW, int NT, bool CUT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_values_kernel(const PagedDecodeArgs pa) {
   extern __shared__ uint4 dyn[];
   constexpr int kRing = ring_values<D, NT>();
@@ -826,14 +896,14 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_
   const DecodeArgs& a = pa.a;
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float rowm_s[kWarps / TW * kRows], sums[kWarps * kRows];
-  __shared__ int2 ids[kWarps][kIds];
+  __shared__ int ids[kWarps][64];
   const int warp = threadIdx.x >> 5, team = warp / TW, tt = threadIdx.x % (32 * TW);
   char* ring = reinterpret_cast<char*>(dyn) + warp * kRing;
   const char* rings = reinterpret_cast<const char*>(dyn) + team * TW * kRing;   // the team's
   const int per = blocks_per_run<CUT>(pa, cum, count_blocks<kKeys>(cum, a));
   __shared__ int last_s[kWarps / TW];
   each_paged_part<TW, CUT>(pa, cum, per, [&](const PagedPart& p) {
-    part_values<T, D, TW, NT>(p, pa, ring, ids[warp], rowm_s + team * kRows, sums);
+    part_values<T, D, TW, NT, FOLD>(p, pa, ring, ids[warp], rowm_s + team * kRows, sums);
     const int parts = p.parts;
     team_sync<TW>();
     const auto sum_of = [&](int row) {
@@ -855,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_
         reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(row_of(p, row, a)) * a.slots + p.slot) * D)[c] = f;
       }
     }
-    if (parts > 1) {
+    if (parts > 1 && !pa.join) {
       __threadfence();   // this thread's sums are there before the part counts as done
       team_sync<TW>();
       if (tt == 0)
@@ -872,11 +942,52 @@ __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_
     if (cum[a.B + 1 + b] == 0)
       for (int i = threadIdx.x; i < a.Hq * (D / 4); i += kThreads)
         put4<T>(a.o, static_cast<int64_t>(b) * a.Hq * (D / 4) + i, make_float4(0.0f, 0.0f, 0.0f, 0.0f), 0.0f);
+  release_dependents();
   // Whoever awaits this kernel awaits the scores too: a CTA without a part sees to it.
   if (blockIdx.x == gridDim.x - 1) await_previous();
 }
 
-template <typename T, int D, int TW, int NT, bool CUT>
+// A CTA per row: D / 4 threads across, the others over the parts.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const DecodeArgs a) {
+  constexpr int L = D / 4, KS = kThreads / L;
+  __shared__ float4 sums[KS][L];
+  __shared__ float totals[KS];
+  const int row = blockIdx.x, c = threadIdx.x % L, ks = threadIdx.x / L;
+  await_previous();
+  const int parts = __ldcg(a.cum + row / a.Hq);
+  if (parts <= 1) return;   // written already
+  const int64_t at = static_cast<int64_t>(row) * a.slots;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float total = 0.0f;
+  for (int i0 = ks; i0 < parts; i0 += 8 * KS) {   // eight parts at a time in flight
+    float4 x[8];
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool in = i0 + i * KS < parts;
+      x[i] = in ? __ldcg(reinterpret_cast<const float4*>(a.part_o + (at + i0 + i * KS) * D) + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      f[i] = in ? __ldcg(a.part_sum + at + i0 + i * KS) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum = add4(sum, x[i]);
+      total += f[i];
+    }
+  }
+  sums[ks][c] = sum;
+  if (c == 0) totals[ks] = total;
+  __syncthreads();
+  if (ks) return;
+#pragma unroll
+  for (int i = 1; i < KS; ++i) {
+    sum = add4(sum, sums[i][c]);
+    total += totals[i];
+  }
+  put4<T>(a.o, static_cast<int64_t>(row) * L + c, sum, total != 0.0f ? 1.0f / total : 0.0f);
+}
+
+template <typename T, int D, int TW, int NT, bool FOLD, bool CUT>
 cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
   const DecodeArgs& a = p.a;
   constexpr int kScores = kWarps * Cfg<D>::kStagesK * Cfg<D>::kBlock;
@@ -884,24 +995,26 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
   constexpr int kMostCum = (2 * kDecodeMaxBatch + 1) * 4;
   const int cum = (2 * a.B + 1) * 4;
   cudaError_t e = set_up_kernel<paged_scores_kernel<T, D, TW, NT, CUT>>(kScores + kMostCum, true);
-  if (e == cudaSuccess) e = set_up_kernel<paged_values_kernel<T, D, TW, NT, CUT>>(kValues + kMostCum, true);
+  if (e == cudaSuccess) e = set_up_kernel<paged_values_kernel<T, D, TW, NT, CUT, FOLD>>(kValues + kMostCum, true);
   if (e != cudaSuccess) return e;
   // teams for the runs that there can be, one for each head
   const int64_t heads = static_cast<int64_t>(a.Hkv) * a.own_rowblocks, blocks = static_cast<int64_t>(a.B) * (a.own_width / a.block);
-  const int64_t runs = CUT ? std::min<int64_t>(a.runs + a.B, blocks) : std::min<int64_t>(a.runs, blocks);
+  const int64_t runs = std::min<int64_t>(a.runs, blocks);
   const unsigned grid = static_cast<unsigned>((runs * heads + kWarps / TW - 1) / (kWarps / TW));
   e = launch_dependent(paged_scores_kernel<T, D, TW, NT, CUT>, grid, kThreads, kScores + cum, st, p);
   if (e != cudaSuccess) return e;   // the next kernel reads what this one leaves
-  return launch_dependent(paged_values_kernel<T, D, TW, NT, CUT>, grid, kThreads, kValues + cum, st, p);
+  e = launch_dependent(paged_values_kernel<T, D, TW, NT, CUT, FOLD>, grid, kThreads, kValues + cum, st, p);
+  if (e != cudaSuccess || !p.join) return e;
+  return launch_dependent(paged_join_kernel<T, D>, static_cast<unsigned>(a.B) * a.Hq, kThreads, 0, st, a);
 }
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool FOLD>
 cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
-  if (p.a.team == kWarps) return p.cut ? go<T, D, kWarps, NT, true>(p, st) : go<T, D, kWarps, NT, false>(p, st);
-  return p.cut ? go<T, D, 1, NT, true>(p, st) : go<T, D, 1, NT, false>(p, st);
+  if (p.a.team == kWarps) return p.cut ? go<T, D, kWarps, NT, FOLD, true>(p, st) : go<T, D, kWarps, NT, FOLD, false>(p, st);
+  return p.cut ? go<T, D, 1, NT, FOLD, true>(p, st) : go<T, D, 1, NT, FOLD, false>(p, st);
 }
 template <typename T, int D>
 cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
-  return p.a.G > 8 ? go<T, D, 2>(p, st) : go<T, D, 1>(p, st);
+  return p.a.G > 8 ? go<T, D, 2, false>(p, st) : p.a.G > 4 ? go<T, D, 1, false>(p, st) : go<T, D, 1, true>(p, st);
 }
 
 }  // namespace
@@ -910,6 +1023,9 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
 // a warp would have few blocks, a run belongs to a CTA, whose warps' sums meet in shared memory (a row then has a quarter of the
 // parts; with a warp's runs / with a CTA's: B32 H32/8 C2048 26.5 us / 23.6, B16 H64/8 C8192 50.8 / 32.8, but B64 H8
 // C4096 44.7 / 51.7), and each sequence is cut for itself where that leaves enough runs.
+// More parts than kMostJoined are joined by CTAs of their own: the last team of a part would take eight at a time (B2 H24/1
+// D64 C131072, 100 parts: 29.3 us against 20.0).
+constexpr int kMostJoined = 32;
 constexpr int kMostTeamStreams = 400, kMostCutStreams = 1024, kFewBlocks = 24;
 size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   DecodeArgs* a = &p->a;
@@ -917,8 +1033,8 @@ size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   a->G = a->Hq / a->Hkv;
   a->block = kKeys;
   a->own_rowblocks = (a->G + kRows - 1) / kRows;
-  const int own = (a->C + kKeys - 1) / kKeys;
-  a->own_width = own * kKeys;
+  const int own = (a->C + a->block - 1) / a->block;
+  a->own_width = own * a->block;
   const int64_t heads = static_cast<int64_t>(a->Hkv) * a->own_rowblocks, streams = heads * a->B, blocks = static_cast<int64_t>(a->B) * own;
   if (streams * own > INT_MAX / 2) return 0;
   const int64_t ctas = kSms * resident(bf16, a->G > 8 ? 2 : 1);
@@ -926,11 +1042,11 @@ size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   a->team = streams < 64 || (streams <= kMostTeamStreams && few) ? kWarps : 1;
   int64_t runs = (a->team == 1 ? ctas * kWarps : ctas) / heads;   // of each head
   p->cut = runs >= 2 * a->B && (a->team > 1 || (streams <= kMostCutStreams && few));
-  if (p->cut) runs -= a->B;   // cut for itself, a sequence has one more at most
   a->runs = static_cast<int>(std::max<int64_t>(runs, 1));
   // the most parts of a sequence: as if a run had eight blocks a warp at most
   const int64_t even = blocks / a->runs, full = std::min<int64_t>(std::max<int64_t>(even, a->team), 8 * a->team);
   a->slots = static_cast<int>((own + full - 1) / full + 2);
+  p->join = a->slots > kMostJoined;
   size_t at = 0;
   auto piece = [&](int64_t floats) {
     char* q = base + at;

@@ -276,6 +276,7 @@ struct PagedDecodeArgs {
   const int32_t* table;
   int M;
   int cut;                      // each sequence is cut for itself
+  int join;                     // rows of several parts are joined by a kernel of their own
   float* unit;                  // [B Hq] what a score of 1 in the workspace stands for
   int* done;                    // [B Hkv own_rowblocks] parts whose sums are there
 };
