@@ -192,11 +192,12 @@ class RaPagedCache:
         self.shared = True
 
     def free(self, sequences):
-        """Empties these sequences (integers) and gives their pages back."""
+        """Empties these sequences (integers) and gives their pages back; reads the lengths of the others back."""
         parent = torch.arange(self.length.numel(), dtype=torch.int32)
         parent[list(sequences)] = -1
         ra_page_fork(self.table, self.length, self.uses, parent.to(self.length.device))
         self.position.mul_((parent >= 0).to(self.position.device))
+        self.bound = int(self.length.clamp(0, self.capacity).max())
 
     def compact(self, pages=None):
         """Moves the cache into a pool of `pages` pages (those in use when not given; their number is read back)."""

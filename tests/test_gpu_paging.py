@@ -246,6 +246,12 @@ CASES = [  # B, Hq, Hkv, D, page, M, sigma, lengths
     (8192, 1, 1, 64, 16, 1, 1.0, [i % 4 for i in range(8192)]),   # as many sequences as there may be
     (1, 1024, 1, 64, 32, 3, 1.0, [69]),                     # and as many query heads per key head
     (70, 2, 1, 64, 16, 300, 1.0, [4700 if i == 9 else i % 5 for i in range(70)]),
+    # a warp's runs, each sequence cut for itself or not; a CTA's runs over several sequences
+    (70, 8, 8, 64, 16, 20, 1.0, [(37 * i) % 321 for i in range(70)]),
+    (300, 4, 4, 64, 16, 5, 1.0, [i % 71 for i in range(300)]),
+    (310, 24, 4, 128, 32, 1, 1.0, [i % 31 for i in range(310)]),
+    (50, 16, 8, 128, 32, 6, 1.0, [150 - 3 * i for i in range(50)]),
+    (45, 72, 8, 64, 16, 8, 2.0, [11 + i % 100 for i in range(45)]),
 ]
 
 
@@ -489,6 +495,55 @@ def test_module_generation_with_forks():
     assert c.length.tolist() == [101, 0, 101, 0] and c.position.tolist() == [101, 0, 101, 0]
     c.free([0, 2])
     assert (c.uses == 0).all() and (c.table == -1).all()
+
+
+def test_a_freed_cache_takes_prompts_again():
+    """Also in fp32, where only an empty cache does."""
+    m = make_module(torch.float32)
+    x = torch.randn(2, 9, 256, device="cuda")
+    c = m.new_cache(2, 16, page_size=16)
+    want = m.prefill(x, c)
+    with pytest.raises(NotImplementedError, match="bf16"):
+        m.prefill(x[:, :2], c)
+    c.free([0, 1])
+    assert c.bound == 0 and torch.equal(m.prefill(x, c), want)
+    with pytest.raises(ValueError, match="no room"):
+        for _ in range(8):
+            m.decode(x[:, :1], c)
+    assert c.length.tolist() == [16, 16]
+
+
+def test_refusals_on_the_device():
+    """What the host's checks let through only as far as the device's tensors."""
+    pool, table = ra.ra_page_pool(4, 2, 64, 16), torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    n, k = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, 2, 5, 64, device="cuda")
+    uses = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for call in (lambda: ra.ra_page_write(k[:, :1], k[:, :1], pool, table), lambda: ra.ra_page_write(k, k.bfloat16(), pool, table),
+                 lambda: ra.ra_page_write(k, k, pool, table.long()), lambda: ra.ra_page_write(k, k, pool, table[:1]),
+                 lambda: ra.ra_page_write(k, k, pool, table, n[:1]), lambda: ra.ra_page_write(k, k, pool, table, n.cpu()),
+                 lambda: ra.ra_page_write(k, k, pool.transpose(0, 1), table), lambda: ra.ra_page_write(k, k, pool[..., :35], table),
+                 lambda: ra.ra_page_write(k, k, pool[:, :, :, ::2], table), lambda: ra.ra_page_write(k, k, pool[:1].expand(4, -1, -1, -1, -1), table),
+                 lambda: ra.ra_page_read(pool, table, n, 0), lambda: ra.ra_page_read(pool, table.t(), n, 1),
+                 lambda: ra.ra_attention_decode_paged(torch.zeros(2, 3, 64, device="cuda"), pool, table, n),
+                 lambda: ra.ra_attention_decode_paged(torch.zeros(2, 4, 128, device="cuda"), pool, table, n),
+                 lambda: ra.ra_attention_decode_paged(torch.zeros(1, 4, 64, device="cuda"), pool, table, n),
+                 lambda: ra.ra_attention_decode_paged(torch.zeros(2, 64, 4, device="cuda").transpose(1, 2), pool, table, n),
+                 lambda: ra.ra_page_fork(table, n, uses, uses), lambda: ra.ra_page_fork(table, n, uses.float(), n),
+                 lambda: ra.ra_page_reserve(pool, table, n, uses[:3], 1), lambda: ra.ra_page_reserve(pool, table, n, uses, 0),
+                 lambda: ra.ra_page_compact(pool, table, uses, pool), lambda: ra.ra_page_compact(pool, table, uses, pool[2:]),
+                 lambda: ra.ra_page_compact(pool, table, uses, ra.ra_page_pool(4, 2, 128, 16)),
+                 lambda: ra.ra_page_compact(pool, table, uses, ra.ra_page_pool(4, 1, 64, 16))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        ra.ra_page_write(k.half(), k.half(), pool, table)
+    with pytest.raises(ra.RaError):
+        ra.ra_attention_decode_paged(torch.zeros(2, 4, 64, device="cuda"), pool, table, n, scale=float("inf"))
+    with pytest.raises(ra.RaError):
+        ra.ra_page_fork(torch.zeros(8193, 1, dtype=torch.int32, device="cuda"), torch.zeros(8193, dtype=torch.int32, device="cuda"), uses,
+                        torch.zeros(8193, dtype=torch.int32, device="cuda"))
+    layers = torch.zeros(4, 3, 2, 2, 16, 36, dtype=torch.uint8, device="cuda")
+    ra.ra_page_compact(layers[:, 0], table, uses, layers[:, 2])          # layers of one tensor do not overlap
 
 
 def test_a_captured_step_replays():
