@@ -16,6 +16,10 @@
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
 //            by byte.  phi s goes in as fp16 times a power of two that follows the largest scale met so far (11 bits: 2^-11 of a weight
 //            at most, an eighth of what the output's rounding to bf16 costs, and the weights' errors differ); fp32 as two fp16.
+// Bound: HBM, and behind it the latency of a warp's chain of loads, masks and products.  bf16 H32/8 D128, whole call in a
+// graph: B64, 7700 keys each, 567 MB in 125.6 us, 4.5 TB/s (the scores kernel alone 5.2); B1, up to 131072 keys, 21.8 us.  A warp spends 48 of about 160
+// instructions for sixteen values of 128 dimensions on taking codes apart.  Below that latency: B1 C512 7.4 us, two
+// launches of a few dependent loads (lengths, page numbers, pages) each.
 // Two launches, scores and values; the last part of a row to be done joins them, or a third launch where they are many.  The scores of sixteen
 // keys stand in the workspace as the value products want them: key t at 4 (t % 4) + t / 4.
 #include <algorithm>
@@ -46,7 +50,7 @@ struct Cfg {
   static constexpr int kStagesK = 3, kStagesV = 3;
 };
 // CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
-// C16384, both kernels: 137 us with 4, 161 with 5, 166 with 6); two fp16 for each weight, or sixteen rows, take more registers.
+// C16384, whole call: 131 us with 4 and 128 registers, 152 with 4 and 96, 149 with 5); two fp16 for each weight, or sixteen rows, take more registers.
 __host__ __device__ constexpr int resident(bool bf16, int tiles) { return bf16 && tiles == 1 ? 4 : 3; }
 // A stage of the values: the block, then eight or sixteen rows of scores.
 template <int D, int NT>
@@ -599,6 +603,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
   constexpr int kPieces = kKeys / 4, kRowsPerCopy = 32 / kPieces;
   const int score_at = lane / kPieces, piece = lane % kPieces;
   const float* score = score_row(row_of(p, 0, a) + score_at, a) + first + piece * 4;
+  const float* used = score_row(row_of(p, lane, a), a) + first;   // lanes below p.rows
   auto fetch_scores = [&](uint32_t stage, int i) {
     const float* src = score + i * (TW * kKeys);
 #pragma unroll
@@ -648,6 +653,8 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
   for (int i = 0; i < mine; ++i) {
     copy_wait<S - 2>();
     __syncwarp();
+    // nobody reads these scores again: a line of L2 less to be written back (B64 H32/8 D128 C16384 131 us -> 125.6)
+    if (lane < p.rows) asm volatile("discard.global.L2 [%0], 128;" ::"l"(used + i * (TW * kKeys)) : "memory");
     if (i + S - 1 < mine) {
       fetch(smem_u32(to), i + S - 1);
       fetch_scores(smem_u32(to), i + S - 1);
