@@ -5,23 +5,29 @@
 //   phi_j as in decode.cu;  o_d = [sum_j (phi_j s_jg) u_jd + sum_j phi_j lo_jg] / sum_j phi_j,  g the group of d
 //
 // so the products run on the codes themselves and a scale is applied once per key and group (scores) or once per
-// weight and group (values).  A code is an fp16 subnormal as it stands: the bits 0000 0000 0000 uuuu are u 2^-24, and four
-// bits further left 16 u 2^-24, exactly.  So a mask makes an operand out of two codes: five integer instructions for
-// eight codes, no conversion.  The factors 16 and 2^-24 are powers of two and go into the query (scores) and the end
+// weight and group (values).  A code is an fp16 subnormal as it stands: the bits 0000 0000 0000 uuuu are u 2^-24, and
+// four bits further left 16 u 2^-24, exactly.  So a mask makes an operand out of two codes: five integer instructions
+// for eight codes, no conversion.  The factors 16 and 2^-24 are powers of two and go into the query (scores) and the end
 // (values).  The tensor cores align products by their operands' exponent fields, so a subnormal's leading zeros cost
-// up to six of the sum's 24 bits: nothing beside bf16's eight.  fp32 calls make normal numbers of the codes (1024 + u in fp16, minus
-// 1024), and add the products of each block of keys to fp32 sums: the tensor cores truncate theirs.
+// up to six of the sum's 24 bits: nothing beside bf16's eight, but 2.6e-5 of an fp32 output.  fp32 calls make normal
+// numbers of the codes (1024 + u in fp16, minus 1024), and add the products of each block of keys to fp32 sums, since
+// the tensor cores truncate theirs.
 //   scores   m16n8k16: sixteen keys as M, eight query heads as N.  The query goes in as fp16 times a power of two of
 //            its row (11 bits, bf16's 8 exactly, down to 2^-28 of the largest); fp32 queries as two fp16 (22 bits).
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
-//            by byte.  phi s goes in as fp16 times a power of two that follows the largest scale met so far (11 bits: 2^-11 of a weight
-//            at most, an eighth of what the output's rounding to bf16 costs, and the weights' errors differ); fp32 as two fp16.
+//            by byte.  phi s goes in as fp16 times a power of two that follows the largest scale met so far (11 bits:
+//            2^-11 of a weight at most, an eighth of what the output's rounding to bf16 costs, and the weights' errors
+//            differ); fp32 as two fp16.
+// A few rows of queries against many keys leave the fifth generation's products, 128 rows at a time, empty; their
+// operands would have to be unpacked into shared memory first.
+// Two launches, scores and values, around the rows' maxima; the last part of a row to be done joins them, or a third
+// launch where they are many.  The scores of sixteen keys stand in the workspace as the value products want them: key t
+// at 4 (t % 4) + t / 4.
+//
 // Bound: HBM, and behind it the latency of a warp's chain of loads, masks and products.  bf16 H32/8 D128, whole call in a
-// graph: B64, 7700 keys each, 567 MB in 125.6 us, 4.5 TB/s (the scores kernel alone 5.2); B1, up to 131072 keys, 21.8 us.  A warp spends 48 of about 160
-// instructions for sixteen values of 128 dimensions on taking codes apart.  Below that latency: B1 C512 7.4 us, two
-// launches of a few dependent loads (lengths, page numbers, pages) each.
-// Two launches, scores and values; the last part of a row to be done joins them, or a third launch where they are many.  The scores of sixteen
-// keys stand in the workspace as the value products want them: key t at 4 (t % 4) + t / 4.
+// graph: B64, 7700 keys each, 567 MB in 125.6 us, 4.5 TB/s (the scores kernel alone 5.2); B1, up to 131072 keys, 21.8 us.
+// A warp spends 48 of about 160 instructions for sixteen values of 128 dimensions on taking codes apart.  Below that
+// latency: B1 C512 7.4 us, two launches of a few dependent loads (lengths, page numbers, pages) each.
 #include <algorithm>
 #include <climits>
 #include <cuda_fp16.h>
@@ -46,7 +52,6 @@ struct Cfg {
   static constexpr int kCodes = kKeys * D / 2;            // bytes of a block's codes
   static constexpr int kMeta = 4 * G;                     // bytes of a key's scales and minima
   static constexpr int kBlock = kKeys * row_bytes(D);
-  
   static constexpr int kStagesK = 3, kStagesV = 3;
 };
 // CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
@@ -139,8 +144,9 @@ struct PagedPart {
   int first, count, keys;  // blocks of the sequence; its keys
   int slot, parts;         // its place among the sequence's parts
 };
-// CUT: the least (a multiple of the team, so that its warps have as many each) with which the sequences' runs are
-// a.runs in all; 32 of them are tried at once, by counts that are never too low.  Beyond, what is enough for any lengths.
+// CUT: of few sequences the least (a multiple of the team, so that its warps have as many each) with which their runs
+// are a.runs in all, of eight; else what is enough whatever the lengths.
+constexpr int kFewSequences = 64;
 template <bool CUT>
 __device__ __forceinline__ int blocks_per_run(const PagedDecodeArgs& p, const int* cum, int longest) {
   const DecodeArgs& a = p.a;
@@ -148,12 +154,18 @@ __device__ __forceinline__ int blocks_per_run(const PagedDecodeArgs& p, const in
   const int total = cum[a.B];
   if (!CUT) return max(max((total + a.runs - 1) / a.runs, least), 1);
   const auto whole = [&](int per) { return (max(per, 1) + a.team - 1) / a.team * a.team; };
-  const int first = whole(max((total + a.runs - 1) / a.runs, least)), mine = first + static_cast<int>(threadIdx.x & 31) * a.team;
+  const int first = whole(max((total + a.runs - 1) / a.runs, least));
+  const int enough = max(first, whole((total + a.runs - a.B - 1) / (a.runs - a.B)));   // one more run a sequence at most
+  if (a.B > kFewSequences || total + first >= 1 << 20) return enough;
+  // lane (c, g) counts candidate c's runs of every fourth sequence; the quotients are exact below 2^21
+  const int lane = threadIdx.x & 31, mine = first + (lane & 7) * a.team;
   const float inv = 1.0f / mine;
   int runs = 0;
-  for (int b = 0; b < a.B; ++b) runs += static_cast<int>(ceilf(static_cast<float>(cum[b + 1] - cum[b]) * inv * 1.000001f));
-  const unsigned fits = __ballot_sync(0xffffffffu, runs <= a.runs);
-  return fits ? first + (__ffs(fits) - 1) * a.team : max(first, whole((total + a.runs - a.B - 1) / (a.runs - a.B)));
+  for (int b = lane >> 3; b < a.B; b += 4) runs += static_cast<int>((static_cast<float>(cum[b + 1] - cum[b] + mine - 1) + 0.5f) * inv);
+  runs += __shfl_xor_sync(0xffffffffu, runs, 8);
+  runs += __shfl_xor_sync(0xffffffffu, runs, 16);
+  const unsigned fits = __ballot_sync(0xffffffffu, runs <= a.runs) & 0xffu;
+  return fits ? first + (__ffs(fits) - 1) * a.team : enough;
 }
 // Parts of a sequence whose blocks are c0 .. c1 - 1 of all.
 template <bool CUT>
@@ -1027,9 +1039,11 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
 }  // namespace
 
 // The split: `runs` runs for every head, as many as teams that are resident at a time.  Where streams are few, or
-// a warp would have few blocks, a run belongs to a CTA, whose warps' sums meet in shared memory (a row then has a quarter of the
-// parts; with a warp's runs / with a CTA's: B32 H32/8 C2048 26.5 us / 23.6, B16 H64/8 C8192 50.8 / 32.8, but B64 H8
-// C4096 44.7 / 51.7), and each sequence is cut for itself where that leaves enough runs.
+// a warp would have few blocks, a run belongs to a CTA, whose warps' sums meet in shared memory: a row then has a quarter of
+// the parts (with a warp's runs / with a CTA's: B32 H32/8 C2048 25.6 us / 22.4, B16 H64/8 C8192 34.4 / 32.1, but B64 H8
+// C2048 28.5 / 32.7).  Where blocks are few each sequence is cut for itself if that leaves enough runs, so that no team starts
+// twice (cut / not, B32 H32/8 C2048 with a warp's runs 25.6 / 27.0; with many blocks the even split is worth more:
+// B64 H32/8 C16384 129.4 / 124.5).
 // More parts than kMostJoined are joined by CTAs of their own: the last team of a part would take eight at a time (B2 H24/1
 // D64 C131072, 100 parts: 29.3 us against 20.0).
 constexpr int kMostJoined = 32;
