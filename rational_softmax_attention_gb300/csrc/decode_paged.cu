@@ -1044,9 +1044,10 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
 // C2048 28.5 / 32.7).  Where blocks are few each sequence is cut for itself if that leaves enough runs, so that no team starts
 // twice (cut / not, B32 H32/8 C2048 with a warp's runs 25.6 / 27.0; with many blocks the even split is worth more:
 // B64 H32/8 C16384 129.4 / 124.5).
-// More parts than kMostJoined are joined by CTAs of their own: the last team of a part would take eight at a time (B2 H24/1
-// D64 C131072, 100 parts: 29.3 us against 20.0).
-constexpr int kMostJoined = 32;
+// Rows of more than kMostJoined parts, when sequences are full, are joined by CTAs of their own: the team of the last part
+// takes eight parts at a time (by it / by a kernel: B64 H8 C2048, 5 parts, 25.8 us / 28.4; B16 H32/8 C16384, 19 parts, 47.0 /
+// 39.6; B2 H24/1 D64 C131072, 100 parts, 29.3 / 20.0).
+constexpr int kMostJoined = 8;
 constexpr int kMostTeamStreams = 400, kMostCutStreams = 1024, kFewBlocks = 24;
 size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   DecodeArgs* a = &p->a;
@@ -1067,7 +1068,7 @@ size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   // the most parts of a sequence: as if a run had eight blocks a warp at most
   const int64_t even = blocks / a->runs, full = std::min<int64_t>(std::max<int64_t>(even, a->team), 8 * a->team);
   a->slots = static_cast<int>((own + full - 1) / full + 2);
-  p->join = a->slots > kMostJoined;
+  p->join = own > kMostJoined * std::max<int64_t>(even, a->team);   // a full sequence's parts
   size_t at = 0;
   auto piece = [&](int64_t floats) {
     char* q = base + at;
