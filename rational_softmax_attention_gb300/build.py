@@ -74,7 +74,7 @@ def _build_calls(force):
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
            *(x for d in include for x in ("-isystem", d)), CALLS_SRC, "-o", tmp, "-L", PKG_DIR, "-l:libraattn.so",
-           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{res.stderr[-4000:]}")

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -71,8 +72,10 @@ void check(const char* name, const Tensor& t, at::IntArrayRef shape, at::ScalarT
   refuse(s.str());
 }
 void* address(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
+// at::empty without its dispatch, 0.35 us less each (page_write B64 5.55 us a call -> 4.85, page_compact 10.2 -> 8.8, norm and rotation
+// 7.2 -> 6.2).
 Tensor make(at::IntArrayRef shape, at::ScalarType dtype, const at::Device& device) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+  return Tensor(at::detail::empty_cuda(shape, dtype, device, c10::nullopt));
 }
 
 // f(stream) on the current stream of `device`, which is the current one meanwhile.

@@ -157,6 +157,7 @@ __device__ __forceinline__ int blocks_per_run(const PagedDecodeArgs& p, const in
   const int first = whole(max((total + a.runs - 1) / a.runs, least));
   const int enough = max(first, whole((total + a.runs - a.B - 1) / (a.runs - a.B)));   // one more run a sequence at most
   if (a.B > kFewSequences || total + first >= 1 << 20) return enough;
+  if (total + a.B * (first - 1) <= a.runs * first) return first;   // it fits whatever the lengths
   // lane (c, g) counts candidate c's runs of every fourth sequence; the quotients are exact below 2^21
   const int lane = threadIdx.x & 31, mine = first + (lane & 7) * a.team;
   const float inv = 1.0f / mine;
