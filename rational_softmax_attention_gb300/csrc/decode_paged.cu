@@ -52,17 +52,21 @@ struct Cfg {
   static constexpr int kCodes = kKeys * D / 2;            // bytes of a block's codes
   static constexpr int kMeta = 4 * G;                     // bytes of a key's scales and minima
   static constexpr int kBlock = kKeys * row_bytes(D);
-  static constexpr int kStagesK = 3, kStagesV = 3;
+  static constexpr int kStages = 3;                       // of a warp's ring; four or five gave nothing
 };
 // CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
 // C16384, whole call: 131 us with 4 and 128 registers, 152 with 4 and 96, 149 with 5); two fp16 for each weight, or sixteen rows, take more registers.
 __host__ __device__ constexpr int resident(bool bf16, int tiles) { return bf16 && tiles == 1 ? 4 : 3; }
-// A stage of the values: the block, then eight or sixteen rows of scores.
-template <int D, int NT>
-__host__ __device__ constexpr int stage_values() { return Cfg<D>::kBlock + 8 * NT * kKeys * 4; }
+// A stage of the values: the block, then its rows of scores (FOLD: four at most).
+template <int NT, bool FOLD>
+__host__ __device__ constexpr int score_rows() { return FOLD ? 4 : 8 * NT; }
+template <int D, int NT, bool FOLD>
+__host__ __device__ constexpr int stage_values() { return Cfg<D>::kBlock + score_rows<NT, FOLD>() * kKeys * 4; }
 // A warp's ring of them, and behind it a block's scales and minima in fp32.
-template <int D, int NT>
-__host__ __device__ constexpr int ring_values() { return Cfg<D>::kStagesV * stage_values<D, NT>() + kKeys * 2 * Cfg<D>::kMeta; }
+template <int D, int NT, bool FOLD>
+__host__ __device__ constexpr int ring_values() {
+  return Cfg<D>::kStages * stage_values<D, NT, FOLD>() + kKeys * 2 * Cfg<D>::kMeta;
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -429,7 +433,7 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
   const typename Query<T, D, NT>::Raw raw(p, a);
   fetch.await();
 #pragma unroll
-  for (int i = 0; i < C::kStagesK - 1; ++i) {
+  for (int i = 0; i < C::kStages - 1; ++i) {
     if (i < mine) fetch(smem_u32(ring) + i * C::kBlock, i);
     copy_commit();
   }
@@ -449,13 +453,13 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
   // this lane's 16 bytes (D = 128) or 8 of key r: the halves' order depends on the key's bit 1, which is r's
   const int chunk = r * (D / 2) + (G == 2 ? (16 * j) ^ ((r & 2) << 4) : 8 * j), meta = C::kCodes + r * C::kMeta;
   int left = p.keys - first;   // keys from the block's first on
-  const char *stage = ring, *to = ring + (C::kStagesK - 1) * C::kBlock;
+  const char *stage = ring, *to = ring + (C::kStages - 1) * C::kBlock;
   for (int i = 0; i < mine; ++i, left -= TW * kKeys) {
-    copy_wait<C::kStagesK - 2>();
+    copy_wait<C::kStages - 2>();
     __syncwarp();   // block i has landed for all lanes, and all have read block i - 1
-    if (i + C::kStagesK - 1 < mine) fetch(smem_u32(to), i + C::kStagesK - 1);
+    if (i + C::kStages - 1 < mine) fetch(smem_u32(to), i + C::kStages - 1);
     copy_commit();
-    to = to == ring + (C::kStagesK - 1) * C::kBlock ? ring : to + C::kBlock;
+    to = to == ring + (C::kStages - 1) * C::kBlock ? ring : to + C::kBlock;
     float z[C::kTiles][NT][4];
 #pragma unroll
     for (int tile = 0; tile < C::kTiles; ++tile) {
@@ -522,7 +526,7 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
           }
         }
       }
-    stage = stage == ring + (C::kStagesK - 1) * C::kBlock ? ring : stage + C::kBlock;
+    stage = stage == ring + (C::kStages - 1) * C::kBlock ? ring : stage + C::kBlock;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -541,7 +545,7 @@ __device__ __forceinline__ void part_scores(const PagedPart& p, const PagedDecod
 template <typename T, int D, int TW, int NT, bool CUT>
 __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_scores_kernel(const PagedDecodeArgs pa) {
   extern __shared__ uint4 dyn[];
-  constexpr int kRing = Cfg<D>::kStagesK * Cfg<D>::kBlock;
+  constexpr int kRing = Cfg<D>::kStages * Cfg<D>::kBlock;
   const DecodeArgs& a = pa.a;
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float best[kWarps * kRows];
@@ -604,7 +608,7 @@ template <typename T, int D, int TW, int NT, bool FOLD>
 __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int* ids, float* rowm,
                                             float* sums) {
   using C = Cfg<D>;
-  constexpr int G = C::G, kStage = stage_values<D, NT>(), S = C::kStagesV;
+  constexpr int G = C::G, kStage = stage_values<D, NT, FOLD>(), S = C::kStages;
   constexpr bool TWO = sizeof(T) == 4;
   const DecodeArgs& a = pa.a;
   static_assert(!FOLD || (NT == 1 && C::kTiles == 2), "two tiles for eight columns");
@@ -620,7 +624,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
   auto fetch_scores = [&](uint32_t stage, int i) {
     const float* src = score + i * (TW * kKeys);
 #pragma unroll
-    for (int k = 0; k < 8 * NT / kRowsPerCopy; ++k) {
+    for (int k = 0; k < score_rows<NT, FOLD>() / kRowsPerCopy; ++k) {
       const int row = score_at + k * kRowsPerCopy;
       if (row < p.rows) copy16(stage + C::kBlock + (row * kPieces + piece_of(row, piece)) * 16, src, true);
       src += kRowsPerCopy * static_cast<int64_t>(a.own_width);
@@ -911,8 +915,8 @@ __device__ __forceinline__ void join_rows(const PagedPart& p, const DecodeArgs& 
 template <typename T, int D, int TW, int NT, bool CUT, bool FOLD>
 __global__ void __launch_bounds__(kThreads, resident(sizeof(T) == 2, NT)) paged_values_kernel(const PagedDecodeArgs pa) {
   extern __shared__ uint4 dyn[];
-  constexpr int kRing = ring_values<D, NT>();
-  static_assert(kRing >= 8 * NT * D * 4, "a warp's partial sums fit its ring");
+  constexpr int kRing = ring_values<D, NT, FOLD>();
+  static_assert(kRing >= score_rows<NT, FOLD>() * D * 4, "a warp's partial sums fit its ring");
   const DecodeArgs& a = pa.a;
   int* cum = reinterpret_cast<int*>(reinterpret_cast<char*>(dyn) + kWarps * kRing);
   __shared__ float rowm_s[kWarps / TW * kRows], sums[kWarps * kRows];
@@ -1010,8 +1014,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const DecodeArgs a
 template <typename T, int D, int TW, int NT, bool FOLD, bool CUT>
 cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
   const DecodeArgs& a = p.a;
-  constexpr int kScores = kWarps * Cfg<D>::kStagesK * Cfg<D>::kBlock;
-  constexpr int kValues = kWarps * ring_values<D, NT>();
+  constexpr int kScores = kWarps * Cfg<D>::kStages * Cfg<D>::kBlock;
+  constexpr int kValues = kWarps * ring_values<D, NT, FOLD>();
   constexpr int kMostCum = (2 * kDecodeMaxBatch + 1) * 4;
   const int cum = (2 * a.B + 1) * 4;
   cudaError_t e = set_up_kernel<paged_scores_kernel<T, D, TW, NT, CUT>>(kScores + kMostCum, true);
@@ -1070,7 +1074,8 @@ size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   const int64_t even = blocks / a->runs, full = std::min<int64_t>(std::max<int64_t>(even, a->team), 8 * a->team);
   a->slots = static_cast<int>((own + full - 1) / full + 2);
   p->join = own > kMostJoined * std::max<int64_t>(even, a->team);   // a full sequence's parts
-  size_t at = 0;
+  // whole lines, since scores are discarded by the line: up to a line of the workspace in front, too
+  size_t at = static_cast<size_t>(-reinterpret_cast<intptr_t>(base)) & 127;
   auto piece = [&](int64_t floats) {
     char* q = base + at;
     at += (static_cast<size_t>(floats) * 4 + 255) & ~static_cast<size_t>(255);
@@ -1084,7 +1089,7 @@ size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   a->cum = reinterpret_cast<int*>(piece(a->B + 2));
   p->unit = reinterpret_cast<float*>(piece(rows));
   p->done = reinterpret_cast<int*>(piece(streams));
-  return at;
+  return base ? at : at + 128;
 }
 
 cudaError_t launch_decode_paged(const PagedDecodeArgs& p, bool bf16, cudaStream_t st) {

@@ -339,6 +339,26 @@ def test_decode_long_context_and_layers():
         assert torch.equal(o, ra.ra_attention_decode_paged(q, pool, table, torch.tensor([N], dtype=torch.int32, device="cuda")))
 
 
+def test_decode_with_a_workspace_at_any_16_bytes():
+    """The C call takes a workspace at a 16-byte address, and stays inside it."""
+    L = ra.lib()
+    g = torch.Generator().manual_seed(12)
+    pool, table, n = filled(g, [500, 90, 0], 2, 16, 128, 40)
+    for G in (4, 8, 16):
+        q = torch.randn(3, 2 * G, 128, generator=g).bfloat16().cuda()
+        want = ra.ra_attention_decode_paged(q, pool, table, n)
+        size = L.ra_attention_decode_paged_workspace_size(3, 2 * G, 2, 40, 16, 128)
+        ws = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        for off in (16, 48, 112, 128):
+            o = torch.zeros_like(q)
+            code = L.ra_attention_decode_paged(q.data_ptr(), pool.data_ptr(), pool.stride(0), table.data_ptr(), n.data_ptr(), o.data_ptr(),
+                                               ws.data_ptr() + off, 3, 2 * G, 2, 128, pool.shape[0], 16, 40, 0.0, 1,
+                                               torch.cuda.current_stream().cuda_stream)
+            torch.cuda.synchronize()
+            assert code == 0 and torch.equal(o, want)
+            assert (ws[:16] == 0xA5).all() and (ws[off + size:] == 0xA5).all()
+
+
 # ---- the table ------------------------------------------------------------------------------------------------
 def same(*pairs):
     for got, want in pairs:
