@@ -444,7 +444,8 @@ class RaAttention(torch.nn.Module):
         Behind a prefix the prompt attends to it too (bf16 only: a masked attention call).
 
         A paged cache: the prompt attends to its keys and values as the cache holds them, as later single tokens do,
-        and a cache that holds entries already is continued (bf16 only, likewise)."""
+        and a cache that holds entries already is continued (bf16 only, likewise; reads the longest length back).
+        A captured call goes on from whatever the cache holds in a replay if it held entries at the capture."""
         if not self.causal:
             raise ValueError("serving needs a causal module")
         if isinstance(cache, RaPagedCache):
@@ -485,14 +486,18 @@ class RaAttention(torch.nn.Module):
             raise NotImplementedError("continuing a cache that holds entries takes bf16 modules only")
         if self.rope_sections and positions is None:
             positions = cache.position.view(B, 1) + torch.arange(N, device=x.device, dtype=torch.int32)
+        captured = x.is_cuda and torch.cuda.is_current_stream_capturing()
+        if cache.bound and not captured:
+            cache.recount()   # replays of a graph may have stored more than the host has counted
         before = cache.length.clone() if cache.bound else None
         how = self._how(positions, qkv.dtype)
         if before is None:
             q, k, v = cache.append(qkv, self.num_heads, count=count, held=True, **how)
             return self._merge(ra_attention(q, k, v, is_causal=True))
         q = cache.append(qkv, self.num_heads, count=count, **how)
-        k, v = cache.read(cache.bound)
-        slot = torch.arange(cache.bound, device=x.device)
+        most = cache.capacity if captured else cache.bound
+        k, v = cache.read(most)
+        slot = torch.arange(most, device=x.device)
         seen = slot <= (before.view(B, 1, 1) + torch.arange(N, device=x.device).view(1, N, 1))
         return self._merge(ra_attention(q, k, v, attn_mask=seen.unsqueeze(1)))
 

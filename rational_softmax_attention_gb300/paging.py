@@ -93,7 +93,7 @@ class RaPagedCache:
 
     `bound` is the host's count of the entries of the longest sequence, or more.  A captured graph of append and
     attend advances length and position when it is replayed, but not `bound`: whoever replays it sees to it that there is
-    room (tokens without a page are not stored, and not counted).  compact changes which tensors the cache uses, so graphs of it
+    room (tokens without a page are not stored, and not counted), and calls recount before append again.  compact changes which tensors the cache uses, so graphs of it
     are captured anew afterwards."""
 
     def __init__(self, batch, num_kv_heads, capacity, head_dim, *, page_size=64, pages=None, device="cuda",
@@ -102,7 +102,7 @@ class RaPagedCache:
         if min(batch, capacity) < 1:
             raise ValueError("batch and capacity must be at least 1")
         _dtype_code(dtype)
-        row = -(-capacity // page_size)
+        row = -(-capacity // page_size) if page_size else 1   # a size of 0 is refused with the others
         self.pool = ra_page_pool(int(pages) if pages is not None else batch * row, int(num_kv_heads), head_dim, page_size,
                                  device=device)
         self.table = torch.full((batch, row), -1, device=device, dtype=torch.int32)
@@ -169,12 +169,19 @@ class RaPagedCache:
         self.require_room(tokens, count)
         with torch.no_grad():
             q, k, v = ra_qk_norm_rope(qkv, num_heads, self.num_kv_heads, **how)
+        if k.shape != (self.table.shape[0], self.num_kv_heads, tokens, self.head_dim) or k.device != self.pool.device:
+            raise ValueError("qkv must have the cache's batch size, head dimension and device")   # before any page is taken
         granted = ra_page_reserve(self.pool, self.table, self.length, self.uses, tokens, count=count)
         kept = ra_page_write(k, v, self.pool, self.table, self.length, count=granted, held=held)
         self.length.add_(granted)
         self.position.add_(granted)
         self.bound = min(self.bound + tokens, self.capacity)
         return (q, *kept) if held else q
+
+    def recount(self):
+        """Reads the length of the longest sequence back into `bound`, and returns it."""
+        self.bound = int(self.length.clamp(0, self.capacity).max())
+        return self.bound
 
     def attend(self, q, scale=None):
         """ra_attention_decode_paged of q [B, H, head_dim] against everything this cache holds."""
@@ -197,7 +204,7 @@ class RaPagedCache:
         parent[list(sequences)] = -1
         ra_page_fork(self.table, self.length, self.uses, parent.to(self.length.device))
         self.position.mul_((parent >= 0).to(self.position.device))
-        self.bound = int(self.length.clamp(0, self.capacity).max())
+        self.recount()
 
     def compact(self, pages=None):
         """Moves the cache into a pool of `pages` pages (those in use when not given; their number is read back)."""

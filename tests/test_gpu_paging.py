@@ -591,6 +591,52 @@ def test_a_captured_step_replays():
     assert torch.equal(a.length, b.length) and torch.equal(a.pool, b.pool) and torch.equal(a.table, b.table)
 
 
+def test_prompts_after_replays():
+    """Entries that a graph's replays stored count, for a prompt outside and for one that is replayed itself."""
+    m = make_module()
+    x = torch.randn(2, 40, 256, device="cuda").bfloat16()
+    want = m.prefill(x, m.new_cache(2, 64, page_size=16))
+    c = m.new_cache(2, 64, page_size=16)
+    static, prompt = x[:, 5:6].clone(), x[:, 10:20].clone()
+    m.prefill(x[:, :4], c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        static.copy_(x[:, 4:5])
+        m.decode(static, c)
+        one, ten = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(one, stream=side):
+            m.decode(static, c)
+    torch.cuda.current_stream().wait_stream(side)
+    for i in range(5, 10):
+        static.copy_(x[:, i:i + 1])
+        one.replay()
+    got = [m.prefill(prompt, c)]
+    assert c.length.tolist() == [20, 20] and c.bound == 20
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(ten, stream=side):
+        y = m.prefill(prompt, c)
+    torch.cuda.current_stream().wait_stream(side)
+    for i in (20, 30):
+        prompt.copy_(x[:, i:i + 10])
+        ten.replay()
+        got.append(y.clone())
+    # both sides round to bf16 once per projection and output, as above
+    for i, z in enumerate(got):
+        assert (z.float() - want[:, 10 * i + 10:10 * i + 20].float()).abs().max() < 6e-2, i
+    assert c.recount() == 40 and c.position.tolist() == [40, 40]
+
+
+def test_an_append_of_other_shapes_takes_no_page():
+    c = ra.RaPagedCache(2, 2, 64, 64, page_size=16)
+    for shape in ((3, 20, 6 * 64), (2, 20, 6 * 128), (1, 20, 6 * 64)):
+        with pytest.raises(ValueError, match="batch size"):
+            c.append(torch.zeros(shape, device="cuda"), 2, norm="none")
+    with pytest.raises(ValueError):
+        c.append(torch.zeros(2, 20, 6 * 64, device="cuda"), 2, norm="none", count=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert (c.uses == 0).all() and (c.table == -1).all() and c.bound == 0
+
+
 def test_two_streams_at_once():
     g = torch.Generator().manual_seed(2)
     sets = []

@@ -118,8 +118,9 @@ def test_binding_refuses_before_the_library_is_called():
 def test_cache_and_module_refuse_on_the_host():
     with pytest.raises(ValueError, match="head_dim"):
         ra.RaPagedCache(2, 2, 64, 32, device="cpu")
-    with pytest.raises(ValueError, match="page_size"):
-        ra.RaPagedCache(2, 2, 64, 64, page_size=10, device="cpu")
+    for size in (0, 10):
+        with pytest.raises(ValueError, match="page_size"):
+            ra.RaPagedCache(2, 2, 64, 64, page_size=size, device="cpu")
     with pytest.raises(ValueError, match="at least 1"):
         ra.RaPagedCache(0, 2, 64, 64, device="cpu")
     with pytest.raises(TypeError, match="dtype"):
