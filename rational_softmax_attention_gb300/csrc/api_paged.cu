@@ -28,7 +28,8 @@ ra_status_t pool_of(PagePool* p, const void* pool, int64_t page_stride, int page
   const int part = page * paged::row_bytes(D);
   if (Hkv > INT_MAX / (2 * part) || (pages > 1 && page_stride < static_cast<int64_t>(2) * Hkv * part)) return RA_ERR_ARG;
   if (static_cast<int64_t>(M) * page > kMostTokens || page_stride > INT_MAX) return RA_ERR_ARG;
-  *p = PagePool{static_cast<uint8_t*>(const_cast<void*>(pool)), static_cast<int>(pages > 1 ? page_stride : 0), part, pages, Hkv, D, page, shift_of(page)};
+  *p = PagePool{static_cast<uint8_t*>(const_cast<void*>(pool)), static_cast<int>(pages > 1 ? page_stride : 0), part, pages, Hkv, D,
+                page, shift_of(page)};
   return RA_OK;
 }
 

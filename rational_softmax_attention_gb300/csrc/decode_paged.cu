@@ -55,7 +55,9 @@ struct Cfg {
   static constexpr int kStages = 3;                       // of a warp's ring; four or five gave nothing
 };
 // CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
-// C16384, whole call: 131 us with 4 and 128 registers, 152 with 4 and 96, 149 with 5); two fp16 for each weight, or sixteen rows, take more registers.
+// C16384, whole call: 131 us with 4 and 128 registers, 152 with 4 and 96, 149 with 5; 96 for the scores with a CTA's runs alone,
+// which leaves room for a CTA of the values beside them: B32 H32/8 C2048 21.2 us -> 21.6).  Two fp16 for each weight, or
+// sixteen rows, take more registers.
 __host__ __device__ constexpr int resident(bool bf16, int tiles) { return bf16 && tiles == 1 ? 4 : 3; }
 // A stage of the values: the block, then its rows of scores (FOLD: four at most).
 template <int NT, bool FOLD>

@@ -93,8 +93,8 @@ class RaPagedCache:
 
     `bound` is the host's count of the entries of the longest sequence, or more.  A captured graph of append and
     attend advances length and position when it is replayed, but not `bound`: whoever replays it sees to it that there is
-    room (tokens without a page are not stored, and not counted), and calls recount before append again.  compact changes which tensors the cache uses, so graphs of it
-    are captured anew afterwards."""
+    room (tokens without a page are not stored, and not counted), and calls recount before append again.  compact
+    changes which tensors the cache uses, so graphs of it are captured anew afterwards."""
 
     def __init__(self, batch, num_kv_heads, capacity, head_dim, *, page_size=64, pages=None, device="cuda",
                  dtype=torch.bfloat16):
