@@ -15,9 +15,9 @@
 //   scores   m16n8k16: sixteen keys as M, eight query heads as N.  The query goes in as fp16 times a power of two of
 //            its row (11 bits, bf16's 8 exactly, down to 2^-28 of the largest); fp32 queries as two fp16 (22 bits).
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
-//            by byte.  phi s goes in as fp16 times a power of two that follows the largest scale met so far (11 bits:
-//            2^-11 of a weight at most, an eighth of what the output's rounding to bf16 costs, and the weights' errors
-//            differ); fp32 as two fp16.
+//            by byte.  phi s goes in as two fp16 (22 bits; with one, 11 bits, the errors of bf16 outputs against 64 bits
+//            were 1.74e-3 of their size instead of the output's rounding alone, 1.66e-3; B64 H32/8 C16384 126.3 us with one, 129.4
+//            with two) times a power of two that follows the largest scale met so far.
 // A few rows of queries against many keys leave the fifth generation's products, 128 rows at a time, empty; their
 // operands would have to be unpacked into shared memory first.
 // Two launches, scores and values, around the rows' maxima; the last part of a row to be done joins them, or a third
@@ -603,9 +603,10 @@ __device__ __forceinline__ int piece_of(int r, int c) { return c ^ ((r & 1) << 2
 
 // Lane (r, j) reads, of keys j, j + 4, j + 8 and j + 12 of sixteen, word r of every group (dimensions 8 r .. 8 r + 7):
 // rows r and r + 8 of the A operand of product n stand for dimensions 8 r + 2 n and 8 r + 2 n + 1, the latter sixteen times as
-// large.  The weights of query row r at the same keys are the B operand.  FOLD, up to four rows: columns 0 .. 3 take the weights at a
-// block's first sixteen keys and columns 4 .. 7 those at its other sixteen, so that no lane forms weights for nothing; the
-// columns are added at the end.
+// large.  The weights of query row r at the same keys are the B operand.  FOLD, up to four rows: the lanes of columns 0 .. 3 form the
+// weights at a block's first sixteen keys and those of columns 4 .. 7 the ones at its other sixteen, so that no lane forms weights for
+// nothing, and where one half's columns take the first fp16 of its weights the other's take the second: no product more than with one
+// fp16.  The columns are added at the end.
 template <typename T, int D, int TW, int NT, bool FOLD>
 __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecodeArgs& pa, char* ring, const int* ids, float* rowm,
                                             float* sums) {
@@ -774,9 +775,15 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             const float2* w = weight[t];
-            split_half2<TWO>(g ? w[0].y : w[0].x, g ? w[1].y : w[1].x, wb[tile][t][g][0], rest[tile][t][g][0]);
-            split_half2<TWO>(g ? w[2].y : w[2].x, g ? w[3].y : w[3].x, wb[tile][t][g][1], rest[tile][t][g][1]);
+            split_half2<true>(g ? w[0].y : w[0].x, g ? w[1].y : w[1].x, wb[tile][t][g][0], rest[tile][t][g][0]);
+            split_half2<true>(g ? w[2].y : w[2].x, g ? w[3].y : w[3].x, wb[tile][t][g][1], rest[tile][t][g][1]);
           }
+      }
+      if constexpr (FOLD) {   // the other half's second fp16 of the same row
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) rest[0][0][g][h] = __shfl_xor_sync(0xffffffffu, rest[0][0][g][h], 16);
       }
 #pragma unroll
       for (int tile = 0; tile < C::kTiles; ++tile) {
@@ -794,14 +801,12 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          uint32_t b[NT][2], br[NT][2];
+          uint32_t b[NT][2];
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              b[t][h] = !FOLD ? wb[FOLD ? 0 : tile][t][g][h] : half == tile ? wb[0][t][g][h] : 0u;
-              if constexpr (TWO) br[t][h] = !FOLD ? rest[FOLD ? 0 : tile][t][g][h] : half == tile ? rest[0][t][g][h] : 0u;
-            }
+            for (int h = 0; h < 2; ++h)
+              b[t][h] = FOLD ? half == tile ? wb[0][t][g][h] : rest[0][t][g][h] : wb[FOLD ? 0 : tile][t][g][h];
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
             const uint32_t sel = n < 2 ? 0x5410u : 0x7632u;
@@ -811,13 +816,19 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
                            a3 = codes2<TWO>(v, kHigh);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+              const uint32_t* second = rest[FOLD ? 0 : tile][t][g];
               if constexpr (TWO) {
                 float c[4];
-                mma_f16_first(c, a0, a1, a2, a3, br[t][0], br[t][1]);
-                mma_f16(c, a0, a1, a2, a3, b[t][0], b[t][1]);
+                if constexpr (FOLD) {
+                  mma_f16_first(c, a0, a1, a2, a3, b[t][0], b[t][1]);
+                } else {
+                  mma_f16_first(c, a0, a1, a2, a3, second[0], second[1]);
+                  mma_f16(c, a0, a1, a2, a3, b[t][0], b[t][1]);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[t][g][n][k] += c[k];
               } else {
+                if constexpr (!FOLD) mma_f16(acc[t][g][n], a0, a1, a2, a3, second[0], second[1]);
                 mma_f16(acc[t][g][n], a0, a1, a2, a3, b[t][0], b[t][1]);
               }
             }
