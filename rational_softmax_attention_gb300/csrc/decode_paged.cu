@@ -17,7 +17,9 @@
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
 //            by byte.  phi s goes in as two fp16 (22 bits; with one, 11 bits, the errors of bf16 outputs against 64 bits
 //            were 1.74e-3 of their size instead of the output's rounding alone, 1.66e-3; B64 H32/8 C16384 126.3 us with one, 129.4
-//            with two) times a power of two that follows the largest scale met so far.
+//            with two) times a power of two that follows the largest phi s met so far, of each row and group: with one power for
+//            all, a group or a key of much larger values, even one outside the support, took the others' bits (B64 H32/8 C16384
+//            129.4 -> 132.0 us).
 // A few rows of queries against many keys leave the fifth generation's products, 128 rows at a time, empty; their
 // operands would have to be unpacked into shared memory first.
 // Two launches, scores and values, around the rows' maxima; the last part of a row to be done joins them, or a third
@@ -107,6 +109,7 @@ __device__ __forceinline__ void split_half2(float x, float y, uint32_t& hi, uint
 __device__ __forceinline__ float power_of_2(int e) {   // inf above fp32's range, 0 below
   return __uint_as_float(static_cast<uint32_t>(min(max(e + 127, 0), 255)) << 23);
 }
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>(__float_as_uint(x) >> 23) - 127; }   // x >= 0
 
 // Two codes as an operand: the fp16 of them times 2^-24 or, with TWO, themselves.
 template <bool TWO>
@@ -652,6 +655,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
   }
   team_sync<TW>();
   float m[NT], c2[NT], total[NT], acc[NT][G][4][4];
+  float unit[NT][G];   // the power of two of this lane's row and group: every weight met so far, times it, is below 2^15
   float2 low[NT];   // of the groups (D = 64: the first)
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -661,12 +665,12 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
     total[t] = 0.0f;
     low[t] = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int g = 0; g < G; ++g)
+    for (int g = 0; g < G; ++g) {
+      unit[t][g] = 0x1p114f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) acc[t][g][n][0] = acc[t][g][n][1] = acc[t][g][n][2] = acc[t][g][n][3] = 0.0f;
+    }
   }
-  int exponent = -100;   // every scale met so far is below 2^exponent
-  float unit = power_of_2(14 - exponent);
   const int word = word_offset<G>(0, r, j);   // the halves' order: bit 1 of the key's slot is j's
   float* metas = reinterpret_cast<float*>(ring + S * kStage);
   const char *stage = ring, *to = ring + (S - 1) * kStage;
@@ -681,36 +685,13 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
     }
     copy_commit();
     to = to == ring + (S - 1) * kStage ? ring : to + kStage;
-    {   // the keys' scales, times a power of two, and minima, a lane for each of 32
-      float most = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kKeys; k += 32) {
-        const Meta<G> meta(stage + C::kCodes + (k + lane) * C::kMeta);
-        most = fmaxf(most, G == 2 ? fmaxf(meta.s[0], meta.s[G - 1]) : meta.s[0]);
-      }
-      // the bits of scales, which are not negative, are in their order
-      const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 126;
-      if (e > exponent) {
-        const float f = power_of_2(exponent - e);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) acc[t][g][n][k] *= f;
-        exponent = e;
-        unit = power_of_2(14 - e);
-      }
-#pragma unroll
-      for (int k = 0; k < kKeys; k += 32) {
-        const Meta<G> meta(stage + C::kCodes + (k + lane) * C::kMeta);
-        if constexpr (G == 2)
-          reinterpret_cast<float4*>(metas)[k + lane] = make_float4(meta.s[0] * unit, meta.s[1] * unit, meta.lo[0], meta.lo[1]);
-        else
-          reinterpret_cast<float2*>(metas)[k + lane] = make_float2(meta.s[0] * unit, meta.lo[0]);
-      }
+    {   // the keys' scales and minima, a lane for each of 32
+      static_assert(kKeys == 32, "a lane for each key");
+      const Meta<G> meta(stage + C::kCodes + lane * C::kMeta);
+      if constexpr (G == 2)
+        reinterpret_cast<float4*>(metas)[lane] = make_float4(meta.s[0], meta.s[1], meta.lo[0], meta.lo[1]);
+      else
+        reinterpret_cast<float2*>(metas)[lane] = make_float2(meta.s[0], meta.lo[0]);
       __syncwarp();
     }
     constexpr int FT = FOLD ? 1 : C::kTiles;   // tiles for which a lane forms weights
@@ -745,11 +726,10 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
       }
     }
     if (__any_sync(0xffffffffu, live)) {
-      // the weights times the scales, as operands, and times the minima
-      uint32_t wb[FT][NT][G][2], rest[FT][NT][G][2];
+      // the weights times the scales and times the minima
+      float2 weight[FT][NT][4];   // of the groups (D = 64: the first)
 #pragma unroll
-      for (int tile = 0; tile < FT; ++tile) {
-        float2 weight[NT][4];   // of the groups
+      for (int tile = 0; tile < FT; ++tile)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int key = (FOLD ? half : tile) * 16 + j + 4 * k;
@@ -758,27 +738,66 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const float2 ff = make_float2(f[tile][t][k], f[tile][t][k]);
-              weight[t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
+              weight[tile][t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
               low[t] = __ffma2_rn(ff, make_float2(meta.z, meta.w), low[t]);
             }
           } else {
             const float2 meta = reinterpret_cast<const float2*>(metas)[key];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-              weight[t][k].x = f[tile][t][k] * meta.x;
+              weight[tile][t][k].x = f[tile][t][k] * meta.x;
               low[t].x = fmaf(f[tile][t][k], meta.y, low[t].x);
             }
           }
         }
+      // the rows' powers of two follow their largest weights, those of a group apart from the other's
+      float most[NT][G];
+      bool over = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          most[t][g] = 0.0f;
+#pragma unroll
+          for (int tile = 0; tile < FT; ++tile)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) most[t][g] = fmaxf(most[t][g], g ? weight[tile][t][k].y : weight[tile][t][k].x);
+          over |= most[t][g] * unit[t][g] >= 0x1p15f;
+        }
+      if (__any_sync(0xffffffffu, over)) {   // a few times in a part
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            const float2* w = weight[t];
-            split_half2<true>(g ? w[0].y : w[0].x, g ? w[1].y : w[1].x, wb[tile][t][g][0], rest[tile][t][g][0]);
-            split_half2<true>(g ? w[2].y : w[2].x, g ? w[3].y : w[3].x, wb[tile][t][g][1], rest[tile][t][g][1]);
+            float w = most[t][g];
+            w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 1));
+            w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 2));
+            if constexpr (FOLD) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, 16));
+            const int now = exponent_of(unit[t][g]), e = w * unit[t][g] >= 0x1p15f ? 13 - exponent_of(w) : now;
+            unit[t][g] = power_of_2(e);
+            const float by = power_of_2(e - now);
+            const float f0 = __shfl_sync(0xffffffffu, by, 8 * j), f1 = __shfl_sync(0xffffffffu, by, 8 * j + 4);   // of the sums' columns
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              acc[t][g][n][0] *= f0;
+              acc[t][g][n][1] *= f1;
+              acc[t][g][n][2] *= f0;
+              acc[t][g][n][3] *= f1;
+            }
           }
       }
+      uint32_t wb[FT][NT][G][2], rest[FT][NT][G][2];   // as operands
+#pragma unroll
+      for (int tile = 0; tile < FT; ++tile)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float2* w = weight[tile][t];
+            const float u = unit[t][g];
+            split_half2<true>((g ? w[0].y : w[0].x) * u, (g ? w[1].y : w[1].x) * u, wb[tile][t][g][0], rest[tile][t][g][0]);
+            split_half2<true>((g ? w[2].y : w[2].x) * u, (g ? w[3].y : w[3].x) * u, wb[tile][t][g][1], rest[tile][t][g][1]);
+          }
       if constexpr (FOLD) {   // the other half's second fp16 of the same row
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -861,7 +880,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
   }
   __syncwarp();   // this warp's blocks have been read: its sums into their place
   float* out = reinterpret_cast<float*>(ring);
-  const float back = power_of_2(exponent), undo = 0x1p-14f / code_unit<T>();
+  constexpr float undo = 0x1p-14f / code_unit<T>();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -870,6 +889,7 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
       for (int c = 0; c < 2; ++c) {
         const int row = t * 8 + 2 * j + c;
         const float lo = __shfl_sync(0xffffffffu, g ? low[t].y : low[t].x, 8 * j + 4 * c);
+        const float back = power_of_2(14 - exponent_of(__shfl_sync(0xffffffffu, unit[t][g], 8 * j + 4 * c)));
         float y[8];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {

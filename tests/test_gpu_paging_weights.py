@@ -96,3 +96,36 @@ def test_more_than_eleven_bits_of_a_weight(N, heads, dtype):
     k, v = (torch.randn(4, H, N, 64, generator=g).repeat_interleave(2, 2)[:, :, :N] for _ in range(2))
     v[:, :, 1::2] *= -1.0
     check(one_hot_queries(g, 4, Hq, 64), k, v, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("apart", [-60, -40, -30, 30, 40, 60])
+def test_groups_of_very_different_values(apart, heads, dtype):
+    """A token's second group of values 2^apart times its first."""
+    g = torch.Generator().manual_seed(heads[0] + apart)
+    Hq, H = heads
+    k, v = torch.randn(2, H, 45, 128, generator=g), torch.randn(2, H, 45, 128, generator=g)
+    v[..., 64:] *= 2.0 ** apart
+    check(one_hot_queries(g, 2, Hq, 128), k, v, dtype, [45, 13])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values_outside_the_support(D, heads, dtype):
+    """Keys with values 2^45 times the others', which no row or only every other row of a key head sees: their weights are exactly 0
+    in the others, before, after and among the keys that count."""
+    g = torch.Generator().manual_seed(D + heads[0])
+    Hq, H = heads
+    N = 150
+    k, v = torch.randn(3, H, N, D, generator=g) * 0.5, torch.randn(3, H, N, D, generator=g)
+    far = [0, 33, 70, 149]
+    v[:, :, far] *= 2.0 ** 45
+    k[..., 0] = torch.rand(3, H, N, generator=g) * 8.0
+    k[:, :, far, 0] = -40.0                                 # 40 and more below the others for q = 1 in dimension 0
+    q = torch.zeros(3, Hq, D)
+    q[..., 0] = 1.0
+    check(q, k, v, dtype)
+    q[:, 1::2, 0] = -1.0                                    # these rows see nothing but the large ones
+    check(q, k, v, dtype)
