@@ -515,8 +515,9 @@ ra_status_t ra_page_read(const void* pool, int64_t page_stride, const int32_t* t
  *   scale         score scale; <= 0 means 1/sqrt(D).
  * Scores, maxima and sums are fp32.  RA_BF16: queries enter the products as fp16 times a power of two (exact down to
  * 2^-28 of the row's largest), RA_F32: as two fp16 (2^-22 lost of each element at most); weights times scales as two fp16 times a
- * power of two (2^-22 of each, or 2^-38 of the largest of its row and group of 64 dimensions).  A query, scale or minimum that is not finite makes the output of its heads not finite; so may
- * scales or queries beyond 2^117.
+ * power of two (2^-22 of each, or 2^-38 of the largest of its row and group of 64 dimensions).
+ * A query, or a key's scale or minimum, that is not finite makes the output of its heads not finite, a value's minimum the 64
+ * dimensions of its group, whatever its weight (ra_page_write gives finite scales); so may scales or queries beyond 2^117.
  * Errors: the common ones, H_Q no multiple of H_KV, a scale that is not finite (RA_ERR_ARG); B > 8192, more than 1024 query
  * heads per key head, or sizes whose blocks of 32 keys by 16 query rows number more than 2^30
  * (RA_ERR_UNSUPPORTED).  The size query returns 0 for such sizes.

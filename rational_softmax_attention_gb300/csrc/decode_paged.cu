@@ -725,46 +725,47 @@ __device__ __forceinline__ void part_values(const PagedPart& p, const PagedDecod
         live |= all != 0.0f;
       }
     }
-    if (__any_sync(0xffffffffu, live)) {
-      // the weights times the scales and times the minima
-      float2 weight[FT][NT][4];   // of the groups (D = 64: the first)
+    // the weights times the scales and times the minima, which show a NaN whatever the weights
+    float2 weight[FT][NT][4];   // of the groups (D = 64: the first)
 #pragma unroll
-      for (int tile = 0; tile < FT; ++tile)
+    for (int tile = 0; tile < FT; ++tile)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = (FOLD ? half : tile) * 16 + j + 4 * k;
-          if constexpr (G == 2) {
-            const float4 meta = reinterpret_cast<const float4*>(metas)[key];
+      for (int k = 0; k < 4; ++k) {
+        const int key = (FOLD ? half : tile) * 16 + j + 4 * k;
+        if constexpr (G == 2) {
+          const float4 meta = reinterpret_cast<const float4*>(metas)[key];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const float2 ff = make_float2(f[tile][t][k], f[tile][t][k]);
-              weight[tile][t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
-              low[t] = __ffma2_rn(ff, make_float2(meta.z, meta.w), low[t]);
-            }
-          } else {
-            const float2 meta = reinterpret_cast<const float2*>(metas)[key];
+          for (int t = 0; t < NT; ++t) {
+            const float2 ff = make_float2(f[tile][t][k], f[tile][t][k]);
+            weight[tile][t][k] = __fmul2_rn(ff, make_float2(meta.x, meta.y));
+            low[t] = __ffma2_rn(ff, make_float2(meta.z, meta.w), low[t]);
+          }
+        } else {
+          const float2 meta = reinterpret_cast<const float2*>(metas)[key];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              weight[tile][t][k].x = f[tile][t][k] * meta.x;
-              low[t].x = fmaf(f[tile][t][k], meta.y, low[t].x);
-            }
+          for (int t = 0; t < NT; ++t) {
+            weight[tile][t][k].x = f[tile][t][k] * meta.x;
+            low[t].x = fmaf(f[tile][t][k], meta.y, low[t].x);
           }
         }
-      // the rows' powers of two follow their largest weights, those of a group apart from the other's
-      float most[NT][G];
-      bool over = false;
+      }
+    // the rows' powers of two follow their largest weights, those of a group apart from the other's
+    float most[NT][G];
+    bool over = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          most[t][g] = 0.0f;
+      for (int g = 0; g < G; ++g) {
+        most[t][g] = 0.0f;
 #pragma unroll
-          for (int tile = 0; tile < FT; ++tile)
+        for (int tile = 0; tile < FT; ++tile)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) most[t][g] = fmaxf(most[t][g], g ? weight[tile][t][k].y : weight[tile][t][k].x);
-          over |= most[t][g] * unit[t][g] >= 0x1p15f;
-        }
-      if (__any_sync(0xffffffffu, over)) {   // a few times in a part
+          for (int k = 0; k < 4; ++k) most[t][g] = fmaxf(most[t][g], g ? weight[tile][t][k].y : weight[tile][t][k].x);
+        over |= most[t][g] * unit[t][g] >= 0x1p15f;
+      }
+    const unsigned state = __reduce_max_sync(0xffffffffu, over ? 2u : live ? 1u : 0u);
+    if (state) {   // no products where all weights are 0: codes are finite
+      if (state == 2) {   // a few times in a part
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll

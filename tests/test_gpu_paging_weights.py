@@ -129,3 +129,27 @@ def test_large_values_outside_the_support(D, heads, dtype):
     check(q, k, v, dtype)
     q[:, 1::2, 0] = -1.0                                    # these rows see nothing but the large ones
     check(q, k, v, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+def test_a_value_that_is_not_finite_shows_whatever_its_weight(heads, dtype):
+    """0 NaN is NaN: also where all the weights of a block's 32 keys are exactly 0, as where there are others beside it.  It shows in
+    every dimension of its group, in the rows of its key head and sequence, and nowhere else."""
+    g = torch.Generator().manual_seed(11)
+    Hq, H = heads
+    B, N, D, G = 4, 100, 128, Hq // H
+    k, v = torch.randn(B, H, N, D, generator=g) * 0.25, torch.randn(B, H, N, D, generator=g)
+    k[:, :, :, 0] = 30.0
+    k[:, :, 32:64, 0] = 0.0                                 # 30 below: a block of weights that are 0
+    k[:, :, 70, 0] = 0.0
+    v[0, 0, 40, 3], v[1, H - 1, 70, 100], v[2, 0, 63, 64] = float("nan"), float("inf"), -float("inf")
+    q = torch.zeros(B, Hq, D)
+    q[..., 0] = 1.0
+    pool, table = hold(k, v)
+    o = ra.ra_attention_decode_paged(q.to(dtype).cuda(), pool, table, torch.full((B,), N, dtype=torch.int32, device="cuda"), scale=1.0)
+    want = torch.zeros(B, Hq, D, dtype=torch.bool)
+    want[0, :G, :64] = True
+    want[1, Hq - G:, 64:] = True
+    want[2, :G, 64:] = True
+    assert torch.equal(~torch.isfinite(o).cpu(), want)
