@@ -445,7 +445,8 @@ class RaAttention(torch.nn.Module):
 
         A paged cache: the prompt attends to its keys and values as the cache holds them, as later single tokens do,
         and a cache that holds entries already is continued (bf16 only, likewise; reads the longest length back).
-        A captured call goes on from whatever the cache holds in a replay if it held entries at the capture."""
+        A captured call goes on from whatever the cache holds in a replay if it held entries at the capture, as the host
+        counts them (cache.recount() where replays came before); else it is one for an empty cache."""
         if not self.causal:
             raise ValueError("serving needs a causal module")
         if isinstance(cache, RaPagedCache):
@@ -487,7 +488,7 @@ class RaAttention(torch.nn.Module):
         if self.rope_sections and positions is None:
             positions = cache.position.view(B, 1) + torch.arange(N, device=x.device, dtype=torch.int32)
         captured = x.is_cuda and torch.cuda.is_current_stream_capturing()
-        if cache.bound and not captured:
+        if (cache.bound or cache.captured) and not captured:
             cache.recount()   # replays of a graph may have stored more than the host has counted
         before = cache.length.clone() if cache.bound else None
         how = self._how(positions, qkv.dtype)

@@ -112,6 +112,7 @@ class RaPagedCache:
         self.dtype = dtype
         self.bound = 0            # no sequence holds more entries than this
         self.shared = False       # whether pages may have several users
+        self.captured = False     # whether an append is part of a graph, whose replays `bound` does not count
 
     @property
     def pages(self):
@@ -176,6 +177,8 @@ class RaPagedCache:
         self.length.add_(granted)
         self.position.add_(granted)
         self.bound = min(self.bound + tokens, self.capacity)
+        if self.length.is_cuda and torch.cuda.is_current_stream_capturing():
+            self.captured = True
         return (q, *kept) if held else q
 
     def recount(self):
