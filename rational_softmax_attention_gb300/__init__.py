@@ -483,13 +483,13 @@ class RaAttention(torch.nn.Module):
         qkv = self.qkv(x)
         if cache.dtype != qkv.dtype:
             raise ValueError(f"the cache must have the projection's dtype, {qkv.dtype}")
+        captured = x.is_cuda and torch.cuda.is_current_stream_capturing()
+        if x.is_cuda and not captured and (cache.bound or cache.captured):
+            cache.recount()   # replays of a graph may have stored more than the host has counted, a fork emptied it
         if cache.bound and qkv.dtype != torch.bfloat16:
             raise NotImplementedError("continuing a cache that holds entries takes bf16 modules only")
         if self.rope_sections and positions is None:
             positions = cache.position.view(B, 1) + torch.arange(N, device=x.device, dtype=torch.int32)
-        captured = x.is_cuda and torch.cuda.is_current_stream_capturing()
-        if (cache.bound or cache.captured) and not captured:
-            cache.recount()   # replays of a graph may have stored more than the host has counted
         before = cache.length.clone() if cache.bound else None
         how = self._how(positions, qkv.dtype)
         if before is None:

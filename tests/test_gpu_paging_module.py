@@ -35,3 +35,15 @@ def test_a_prompt_after_a_freed_cache_and_replays(captured):
     assert torch.equal(m.prefill(x[:, n:20], c), m.prefill(x[:, n:20], plain))
     assert c.length.tolist() == [20, 20] and c.bound == 20
     assert torch.equal(c.pool, plain.pool)
+
+
+def test_a_cache_emptied_by_a_fork_takes_prompts():
+    """In fp32 too, where only an empty cache does: the lengths decide, not the host's count."""
+    m = make_module(torch.float32)
+    x = torch.randn(2, 9, 256, device="cuda")
+    c = m.new_cache(2, 16, page_size=16)
+    want = m.prefill(x, c)
+    with pytest.raises(NotImplementedError, match="bf16"):
+        m.prefill(x[:, :2], c)
+    c.fork(torch.full((2,), -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(m.prefill(x, c), want) and c.length.tolist() == [9, 9]
