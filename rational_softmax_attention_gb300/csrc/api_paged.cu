@@ -131,8 +131,8 @@ ra_status_t ra_attention_decode_paged(const void* q, const void* pool, int64_t p
   if (s == RA_ERR_ARG) return s;
   const ra_status_t sp = pool_of(&p.pool, pool, page_stride, pages, page, H_KV, D, M);
   if (sp != RA_OK) return sp;
-  if (!(scale > 0.0f)) scale = 1.0f / std::sqrt(static_cast<float>(D));
-  if (!std::isfinite(scale)) return RA_ERR_ARG;
+  if (!std::isfinite(scale)) return RA_ERR_ARG;   // NaN is no default
+  if (scale <= 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(D));
   if (s != RA_OK) return s;
   p.table = table;
   p.a.q = q;

@@ -166,3 +166,9 @@ def test_room_is_counted_in_entries_and_pages():
     c.uses[4] = 1
     c.require_room(2)
     assert c.bound == 30
+
+
+def test_a_scale_that_is_not_finite_is_refused(lib):
+    """NaN too, which is not above 0 either and would pass for the default."""
+    for scale in (float("nan"), float("-inf"), float("inf")):
+        assert _decode(lib, scale=scale) == ARG, scale
