@@ -210,7 +210,10 @@ class RaPagedCache:
         self.recount()
 
     def compact(self, pages=None):
-        """Moves the cache into a pool of `pages` pages (those in use when not given; their number is read back)."""
+        """Moves the cache into a pool of `pages` pages (those in use when not given; their number is read back).
+
+        The default leaves no page free: an append that crosses a page's border, or meets a page with several users, is refused until
+        the cache has moved into a larger pool."""
         used = int((self.uses > 0).sum())
         pages = max(used, 1) if pages is None else int(pages)
         if pages < max(used, 1):

@@ -101,3 +101,21 @@ def test_a_cache_emptied_by_a_fork_takes_prompts():
         m.prefill(x[:, :2], c)
     c.fork(torch.full((2,), -1, dtype=torch.int32, device="cuda"))
     assert torch.equal(m.prefill(x, c), want) and c.length.tolist() == [9, 9]
+
+
+def test_a_compacted_cache_goes_on_in_a_pool_with_room():
+    """compact() keeps no free page: tokens fit up to the page's border; compact(more) makes room."""
+    m = make_module()
+    x = torch.randn(2, 40, 256, device="cuda").bfloat16()
+    c, plain = (m.new_cache(2, 64, page_size=16) for _ in range(2))
+    for cache in (c, plain):
+        m.prefill(x[:, :30], cache)
+    c.compact()
+    assert c.pages == 4 and (c.uses == 1).all()
+    for i in (30, 31):
+        assert torch.equal(m.decode(x[:, i:i + 1], c), m.decode(x[:, i:i + 1], plain))
+    with pytest.raises(ValueError, match="0 free pages of 4: 2 are needed"):
+        m.decode(x[:, 32:33], c)
+    c.compact(6)
+    for i in range(32, 40):
+        assert torch.equal(m.decode(x[:, i:i + 1], c), m.decode(x[:, i:i + 1], plain))
