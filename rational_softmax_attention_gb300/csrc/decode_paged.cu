@@ -1077,17 +1077,20 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
 
 }  // namespace
 
-// The split: `runs` runs for every head, as many as teams that are resident at a time.  Where streams are few, or
-// a warp would have few blocks, a run belongs to a CTA, whose warps' sums meet in shared memory: a row then has a quarter of
-// the parts (with a warp's runs / with a CTA's: B32 H32/8 C2048 25.6 us / 22.4, B16 H64/8 C8192 34.4 / 32.1, but B64 H8
-// C2048 28.5 / 32.7).  Where blocks are few each sequence is cut for itself if that leaves enough runs, so that no team starts
-// twice (cut / not, B32 H32/8 C2048 with a warp's runs 25.6 / 27.0; with many blocks the even split is worth more:
-// B64 H32/8 C16384 129.4 / 124.5).
+// The split: `runs` runs for every head, as many as teams that are resident at a time.  Where streams are few, and a warp
+// would have few blocks, a run belongs to a CTA, whose warps' sums meet in shared memory: a row then has a quarter of the
+// parts.  That is so up to half as many streams as CTAs, where each sequence can still be cut for itself and no CTA starts twice
+// (a CTA's runs / a warp's, H32/8 D128, us: B16 C2048 15.1 / 15.4, B32 19.6 / 21.5, B36 21.1 / 22.2; B40, 320 streams for 608
+// CTAs, 30.1 / 26.2, B50 31.0 / 27.7; fp32, 456 CTAs: B28 22.2 / 24.2, B32 31.9 / 28.9).  kFewBlocks of a warp: B32 C6144, 20 of
+// them, 38.3 by CTAs and 38.2 by warps that are not cut, C10240, 34, 53.4 / 52.0.
+// With a warp's runs too each sequence is cut for itself if that leaves enough of them and blocks are few (cut / not: B64 H32/8
+// C512 17.2 / 21.5, C2048, 13 blocks a warp, 28.9 / 32.9, C6144, 40, 58.4 / 59.5; B128, 1024 streams: C512 24.6 / 26.6, C1536, 20,
+// 46.5 / 41.1, C2048, 27, 57.1 / 46.2; B64 C16384 129.4 / 124.5).
 // Rows of more than kMostJoined parts, when sequences are full, are joined by CTAs of their own: the team of the last part
 // takes eight parts at a time (by it / by a kernel: B64 H8 C2048, 5 parts, 25.8 us / 28.4; B16 H32/8 C16384, 19 parts, 47.0 /
 // 39.6; B2 H24/1 D64 C131072, 100 parts, 29.3 / 20.0).
 constexpr int kMostJoined = 8;
-constexpr int kMostTeamStreams = 400, kMostCutStreams = 1024, kFewBlocks = 24;
+constexpr int kMostCutStreams = 1024, kFewBlocks = 24;
 size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   DecodeArgs* a = &p->a;
   const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
@@ -1100,7 +1103,7 @@ size_t plan_decode_paged(PagedDecodeArgs* p, bool bf16, char* base) {
   if (streams * own > INT_MAX / 2) return 0;
   const int64_t ctas = kSms * resident(bf16, a->G > 8 ? 2 : 1);
   const bool few = streams * own < kFewBlocks * ctas * kWarps;
-  a->team = streams < 64 || (streams <= kMostTeamStreams && few) ? kWarps : 1;
+  a->team = streams < 64 || (2 * streams <= ctas && few) ? kWarps : 1;
   int64_t runs = (a->team == 1 ? ctas * kWarps : ctas) / heads;   // of each head
   p->cut = runs >= 2 * a->B && (a->team > 1 || (streams <= kMostCutStreams && few));
   a->runs = static_cast<int>(std::max<int64_t>(runs, 1));
