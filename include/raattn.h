@@ -490,8 +490,8 @@ ra_status_t ra_cache_evict(const void* k, const void* v, const float* weight, co
  *   k, v          [B, H_KV, N, D] of dtype; strides (of batch, head, token) in elements, multiples of 16 bytes.
  *   start, count  [B] int32 or NULL: token n goes to slot start[b] + n (NULL: n), for n < count[b] (NULL: all)
  *                 and slots in [0, M page).  Nothing else of the pool changes.  No two tokens of a call may share a slot.
- *   k_held, v_held  NULL, or [B, H_KV, N, D] of dtype (written): what k and v are held as, rounded once to dtype,
- *                 for every token, stored or not.
+ *   k_held, v_held  NULL, or [B, H_KV, N, D] of dtype (written): what k and v are held as, lo + s u in fp32,
+ *                 then rounded to dtype, for every token, stored or not.
  */
 ra_status_t ra_page_write(const void* k, const void* v, const int64_t* k_strides, const int64_t* v_strides, void* pool,
                           int64_t page_stride, const int32_t* table, const int32_t* start, const int32_t* count,
@@ -500,7 +500,7 @@ ra_status_t ra_page_write(const void* k, const void* v, const int64_t* k_strides
 
 /*
  * ra_page_read -- what slots start[b] + n (start NULL: n), n < N, hold: k, v [B, H_KV, N, D] of dtype (written),
- * rounded once.  Slots that are negative, at or past length[b] (NULL: no limit) or without a page give zeros.
+ * lo + s u in fp32, then rounded to dtype.  Slots that are negative, at or past length[b] (NULL: no limit) or without a page give zeros.
  */
 ra_status_t ra_page_read(const void* pool, int64_t page_stride, const int32_t* table, const int32_t* start,
                          const int32_t* length, void* k, void* v, int B, int N, int H_KV, int D, int pages, int page,
@@ -514,7 +514,7 @@ ra_status_t ra_page_read(const void* pool, int64_t page_stride, const int32_t* t
  *   workspace     ra_attention_decode_paged_workspace_size() bytes.
  *   scale         score scale; <= 0 means 1/sqrt(D).
  * Scores, maxima and sums are fp32.  RA_BF16: queries enter the products as fp16 times a power of two (exact down to
- * 2^-28 of the row's largest), RA_F32: as two fp16 (2^-22 lost of each element at most); weights times scales as two fp16 times a
+ * 2^-26 of the row's largest), RA_F32: as two fp16 (2^-22 lost of each element at most); weights times scales as two fp16 times a
  * power of two (2^-22 of each, or 2^-38 of the largest of its row and group of 64 dimensions).
  * A query, or a key's scale or minimum, that is not finite makes the output of its heads not finite, a value's minimum the 64
  * dimensions of its group, whatever its weight (ra_page_write gives finite scales); so may scales or queries beyond 2^117.

@@ -13,7 +13,8 @@
 // numbers of the codes (1024 + u in fp16, minus 1024), and add the products of each block of keys to fp32 sums, since
 // the tensor cores truncate theirs.
 //   scores   m16n8k16: sixteen keys as M, eight query heads as N.  The query goes in as fp16 times a power of two of
-//            its row (11 bits, bf16's 8 exactly, down to 2^-28 of the largest); fp32 queries as two fp16 (22 bits).
+//            its row (11 bits, bf16's 8 exactly, down to 2^-26 of the largest: it is below 2^14, every other dimension a sixteenth,
+//            and fp16 ends at 2^-24); fp32 queries as two fp16 (22 bits).
 //   values   m16n8k16: sixteen dimensions as M, eight heads as N, sixteen keys as K; two keys' words are put together
 //            by byte.  phi s goes in as two fp16 (22 bits; with one, 11 bits, the errors of bf16 outputs against 64 bits
 //            were 1.74e-3 of their size instead of the output's rounding alone, 1.66e-3; B64 H32/8 C16384 126.3 us with one, 129.4
@@ -27,9 +28,9 @@
 // at 4 (t % 4) + t / 4.
 //
 // Bound: HBM, and behind it the latency of a warp's chain of loads, masks and products.  bf16 H32/8 D128, whole call in a
-// graph: B64, 7700 keys each, 567 MB in 125.6 us, 4.5 TB/s (the scores kernel alone 5.2); B1, up to 131072 keys, 21.8 us.
-// A warp spends 48 of about 160 instructions for sixteen values of 128 dimensions on taking codes apart.  Below that
-// latency: B1 C512 7.4 us, two launches of a few dependent loads (lengths, page numbers, pages) each.
+// graph: B64, up to 16384 keys each, 567 MB in 130.7 us, 4.3 TB/s (the scores kernel alone 5.2); B1, 131072 keys, 42.5 us, 3.6 TB/s.
+// For 32 keys of 128 dimensions a warp issues 271 instructions in the scores and 392 in the values, about 100 of either to take codes
+// apart, at 55 % of the issue slots.  Below that latency: B1 C512 7.3 us, two launches of a few dependent loads (lengths, page numbers, pages) each.
 #include <algorithm>
 #include <climits>
 #include <cuda_fp16.h>
@@ -57,8 +58,8 @@ struct Cfg {
   static constexpr int kStages = 3;                       // of a warp's ring; four or five gave nothing
 };
 // CTAs of an SM.  More, with fewer registers each, lose more in spills and part starts than they hide (B64 H32/8 D128
-// C16384, whole call: 131 us with 4 and 128 registers, 152 with 4 and 96, 149 with 5; 96 for the scores with a CTA's runs alone,
-// which leaves room for a CTA of the values beside them: B32 H32/8 C2048 21.2 us -> 21.6).  Two fp16 for each weight, or
+// C16384, whole call, with one fp16 for a weight: 131 us with 4 and 128 registers, 152 with 4 and 96, 149 with 5; 96 for the scores with a CTA's runs alone,
+// which leaves room for a CTA of the values beside them: B32 H32/8 C2048 21.2 us -> 21.6).  fp32's operands and sums, or
 // sixteen rows, take more registers.
 __host__ __device__ constexpr int resident(bool bf16, int tiles) { return bf16 && tiles == 1 ? 4 : 3; }
 // A stage of the values: the block, then its rows of scores (FOLD: four at most).
@@ -1085,7 +1086,7 @@ cudaError_t go(const PagedDecodeArgs& p, cudaStream_t st) {
 // them, 38.3 by CTAs and 38.2 by warps that are not cut, C10240, 34, 53.4 / 52.0.
 // With a warp's runs too each sequence is cut for itself if that leaves enough of them and blocks are few (cut / not: B64 H32/8
 // C512 17.2 / 21.5, C2048, 13 blocks a warp, 28.9 / 32.9, C6144, 40, 58.4 / 59.5; B128, 1024 streams: C512 24.6 / 26.6, C1536, 20,
-// 46.5 / 41.1, C2048, 27, 57.1 / 46.2; B64 C16384 129.4 / 124.5).
+// 46.5 / 41.1, C2048, 27, 57.1 / 46.2; B64 C16384, 108, 130.5 / 130.7).
 // Rows of more than kMostJoined parts, when sequences are full, are joined by CTAs of their own: the team of the last part
 // takes eight parts at a time (by it / by a kernel: B64 H8 C2048, 5 parts, 25.8 us / 28.4; B16 H32/8 C16384, 19 parts, 47.0 /
 // 39.6; B2 H24/1 D64 C131072, 100 parts, 29.3 / 20.0).

@@ -74,7 +74,7 @@ struct Eight<__nv_bfloat16> {
       x[2 * i + 1] = bf16_high(w[i]);
     }
   }
-  // the one rounding of a bf16 output: half a step, 2^-8 relative at most
+  // a bf16 output's rounding, after the fp32 of lo + s u: half a step, 2^-8 relative at most
   static __device__ __forceinline__ void put(__nv_bfloat16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                                               pack_bf16x2(x[6], x[7]));

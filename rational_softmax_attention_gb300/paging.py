@@ -91,6 +91,9 @@ class RaPagedCache:
     held) and position int32 [B] (position of the next token), all on the device.  pages: pages of the pool, or enough for
     every sequence's capacity.  dtype: of the keys and values that are given and read.
 
+    A pool that is smaller than batch times the longest sequence's pages (and batch / 2 more after a fork) costs a read-back of the
+    counts at every append, which a capture refuses.
+
     `bound` is the host's count of the entries of the longest sequence, or more.  A captured graph of append and
     attend advances length and position when it is replayed, but not `bound`: whoever replays it sees to it that there is
     room (tokens without a page are not stored, and not counted), and calls recount before append again.  compact
