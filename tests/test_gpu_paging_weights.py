@@ -153,3 +153,48 @@ def test_a_value_that_is_not_finite_shows_whatever_its_weight(heads, dtype):
     want[1, Hq - G:, 64:] = True
     want[2, :G, 64:] = True
     assert torch.equal(~torch.isfinite(o).cpu(), want)
+
+
+def test_zeros_of_an_fp32_call_are_zeros():
+    """Groups with lo = -8, s = 1: a value of 0 is code 8, exactly.  Dimensions in which all values are 0 come out as 0, and dimensions in
+    which all keys are 0 do not move a score, however large the query is there."""
+    g = torch.Generator().manual_seed(21)
+    for Hq, H in HEADS:
+        k, v = (torch.randint(-8, 8, (2, H, 77, 128), generator=g).float() for _ in range(2))
+        for t in (k, v):
+            t[..., [0, 64]], t[..., [1, 65]] = -8.0, 7.0
+        k[..., 5:60], v[..., 70:120] = 0.0, 0.0
+        pool, table = hold(k, v)
+        n = torch.tensor([77, 40], dtype=torch.int32, device="cuda")
+        q = one_hot_queries(g, 2, Hq, 128) * 0.25
+        q[..., 5:60] = 0.0
+        large = q.clone()
+        large[..., 5:60] = torch.randn(2, Hq, 55, generator=g) * 1e4
+        o = ra.ra_attention_decode_paged(q.cuda(), pool, table, n, scale=1.0)
+        assert (o[..., 70:120] == 0).all() and (o[..., 121:] != 0).any()
+        # the large dimensions' products are exact zeros; the small ones are powers of two, 2^-9 at least beside 2^14 for the largest, and
+        # fp16 holds them: the scores are the same but for a power of two of the row
+        assert torch.equal(o, ra.ra_attention_decode_paged(large.cuda(), pool, table, n, scale=1.0))
+
+
+@pytest.mark.parametrize("shape", [(8, 3, 3, 64, 5000), (6, 6, 3, 64, 6000), (2, 24, 3, 64, 67), (16, 10, 2, 64, 3), (8, 3, 3, 128, 66), (2, 64, 8, 128, 191)], ids=str)
+def test_fp32_errors_are_those_of_a_plain_form(shape):
+    """The error against 64 bits over all outputs, next to that of fp32 products, sums and quotients of torch's on the held values: at most
+    twice as large."""
+    B, Hq, H, D, N = shape
+    g = torch.Generator().manual_seed(N)
+    k, v = torch.randn(B, H, N, D, generator=g), torch.randn(B, H, N, D, generator=g)
+    pool, table = hold(k, v)
+    q = torch.randn(B, Hq, D, generator=g).cuda()
+    n = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    kh, vh = ra.ra_page_read(pool, table, n, N, dtype=torch.float32)
+
+    def plain(q, kh, vh):
+        z = torch.matmul(q.view(B, H, Hq // H, D), kh.transpose(-1, -2)) * D ** -0.5
+        u = ((z.amax(-1, keepdim=True) - z) / 16.0).clamp(max=1.0)
+        p = ((1.0 - u) / (1.0 + u)) ** 8
+        return (torch.matmul(p, vh) / p.sum(-1, keepdim=True)).view(B, Hq, D)
+
+    want = plain(q.double(), kh.double(), vh.double())
+    own, other = ((x.double() - want).norm().item() for x in (ra.ra_attention_decode_paged(q, pool, table, n), plain(q, kh, vh)))
+    assert own <= 2.0 * other, own / other
